@@ -311,6 +311,67 @@ def mamba_decode(x, dt, A, Bm, Cm, h, *, Dskip=None, z=None):
     return y
 
 
+def mamba_scan(x, dt, A, Bm, Cm, *, lengths, Dskip=None, z=None, h0=None):
+    """The selective scan over packed sequences, token by token through mamba_decode. x, dt, z: [T, D]; Bm, Cm:
+    [T, N]; A: [D, N]; lengths: tokens of each sequence; h0: [S, D, N] or None (zero). Returns y [T, D] and the
+    final states [S, D, N]."""
+    x, dt, A, Bm, Cm = _f64(x), _f64(dt), _f64(A), _f64(Bm), _f64(Cm)
+    T, D = x.shape
+    h = np.zeros((len(lengths), D, A.shape[1])) if h0 is None else np.array(h0, dtype=np.float64)
+    y = np.zeros((T, D))
+    t = 0
+    for s, n in enumerate(lengths):
+        for t in range(t, t + n):
+            y[t:t + 1] = mamba_decode(x[t:t + 1], dt[t:t + 1], A, Bm[t:t + 1], Cm[t:t + 1], h[s:s + 1], Dskip=Dskip,
+                                      z=None if z is None else z[t:t + 1])
+        t = sum(lengths[:s + 1])
+    return y, h
+
+
+def mamba_scan_backward(x, dt, A, Bm, Cm, dy, *, lengths, Dskip=None, z=None, h0=None, dh_last=None):
+    """Gradients of mamba_scan's outputs contracted with dy [T, D] and dh_last [S, D, N]: a dict of dx, ddt, dz [T, D],
+    dBm, dCm [T, N], dA [D, N], dDskip [D], dh0 [S, D, N]. From the formulas, in fp64."""
+    x, dt, A, Bm, Cm, dy = _f64(x), _f64(dt), _f64(A), _f64(Bm), _f64(Cm), _f64(dy)
+    T, D = x.shape
+    N = A.shape[1]
+    S = len(lengths)
+    skip = np.zeros(D) if Dskip is None else _f64(Dskip)
+    out = {"dx": np.zeros((T, D)), "ddt": np.zeros((T, D)), "dBm": np.zeros((T, N)), "dCm": np.zeros((T, N)),
+           "dA": np.zeros((D, N)), "dz": np.zeros((T, D))}
+    dh0 = np.zeros((S, D, N)) if dh_last is None else np.array(dh_last, dtype=np.float64)
+    g = dy
+    if z is not None:
+        z = _f64(z)
+        sig = sigmoid(z)
+        g = dy * z * sig
+    out["dDskip"] = (g * x).sum(0)
+    at = 0
+    for s, n in enumerate(lengths):
+        states = np.zeros((n + 1, D, N))
+        if h0 is not None:
+            states[0] = h0[s]
+        decay = np.exp(dt[at:at + n, :, None] * A)
+        for i in range(n):
+            states[i + 1] = decay[i] * states[i] + (dt[at + i] * x[at + i])[:, None] * Bm[at + i]
+        for i in range(n - 1, -1, -1):
+            t = at + i
+            dh = dh0[s] + g[t][:, None] * Cm[t]
+            out["dCm"][t] = g[t] @ states[i + 1]
+            out["dBm"][t] = (dt[t] * x[t]) @ dh
+            dh0[s] = decay[i] * dh
+            w = dh0[s] * states[i]
+            du = dh @ Bm[t]
+            out["dx"][t] = dt[t] * du + skip * g[t]
+            out["ddt"][t] = x[t] * du + (A * w).sum(1)
+            out["dA"] += dt[t][:, None] * w
+            if z is not None:
+                pre = states[i + 1] @ Cm[t] + skip * x[t]
+                out["dz"][t] = dy[t] * pre * sig[t] * (1 + z[t] * (1 - sig[t]))
+        at += n
+    out["dh0"] = dh0
+    return out
+
+
 def gemv(x, W):
     """y [T, N] = x [T, Kd] . W[N, Kd]^T in fp64 (the decode projection)."""
     x, W = _f64(x), _f64(W)

@@ -12,6 +12,8 @@ Entry points (same names as the C ABI):
   gdn_decode_buffered      output-only decode that writes the state back once every L steps
   gdn_decode_fused         conv1d update -> delta step (per-key or per-head decay) -> gated RMSNorm
   mamba_selective_scan_decode  the Mamba-1 selective-scan decode step (a diagonal recurrence)
+  mamba_selective_scan     the same recurrence over whole sequences (prompts), packed end to end
+  mamba_selective_scan_backward  its gradients
 plus ``fused_recurrent_gated_delta_rule_packed_decode``, the packed call with the keyword names
 of "Microbenchmark: buffered output-only GDN decode (ReplaySSM Part A)" (_bench_cfg, run_packed).
 """
@@ -28,6 +30,8 @@ __all__ = [
     "gdn_decode_step", "gdn_decode_step_indexed", "gdn_decode_buffered", "gdn_decode_fused",
     "gdn_strerror", "split_mixed_qkv", "fused_recurrent_gated_delta_rule_packed_decode", "PreparedCall",
     "MambaArgs", "mamba_selective_scan_decode", "gdn_selftest_bounded_wait",
+    "MambaScanArgs", "MambaScanGradArgs", "mamba_selective_scan", "mamba_selective_scan_backward",
+    "mamba_scan_workspace",
     "GemvArgs", "gdn_gemv_bf16", "gemv_workspace",
     "GDN_F32", "GDN_BF16", "GDN_DEVERR_BAD_INDEX", "GDN_DEVERR_BAD_WRITE_POS", "GDN_DEVERR_TIMEOUT",
     "GDN_DEVERR_RANGE", "debug_lib", "using_debug_build",
@@ -41,14 +45,15 @@ GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1
 GDN_DEVERR_BAD_INDEX, GDN_DEVERR_BAD_WRITE_POS, GDN_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 GDN_DEVERR_RANGE = 0x8
 GDN_KERNEL = {"auto": 0, "tile": 1, "pipe": 2, "stage": 3}
-ABI_VERSION = 7
+ABI_VERSION = 8
 
 # every function the header declares
 EXPORTS = ("gdn_decode_step", "gdn_decode_step_indexed", "gdn_decode_buffered", "gdn_decode_fused",
            "gdn_strerror", "gdn_abi_struct_size", "gdn_abi_version", "mamba_selective_scan_decode",
            "gdn_selftest_bounded_wait", "gdn_gemv_bf16", "gdn_gemv_default_splits",
            "gdn_gemv_workspace_bytes", "gdn_gemv_bf16_noalloc", "gdn_decode_front",
-           "gdn_front_proj_width", "gdn_gemv_set_wait_limit", "gdn_decode_step_indexed_chained")
+           "gdn_front_proj_width", "gdn_gemv_set_wait_limit", "gdn_decode_step_indexed_chained",
+           "mamba_selective_scan", "mamba_selective_scan_backward", "mamba_scan_workspace_bytes")
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -93,6 +98,22 @@ class MambaArgs(ctypes.Structure):
                 ("z", _vp), ("h", _vp), ("h_out", _vp), ("y", _vp), ("err_flags", _vp)]
 
 
+class MambaScanArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("S", _i32), ("D", _i32), ("N", _i32), ("in_dtype", _i32), ("out_dtype", _i32),
+                ("x", _vp), ("x_stride", _i64), ("dt", _vp), ("dt_stride", _i64), ("A", _vp),
+                ("Bm", _vp), ("B_stride", _i64), ("Cm", _vp), ("C_stride", _i64), ("Dskip", _vp),
+                ("z", _vp), ("z_stride", _i64), ("cu_seqlens", _vp), ("state_indices", _vp),
+                ("num_states", _i32), ("h0", _vp), ("h_last", _vp), ("y", _vp), ("y_stride", _i64),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("err_flags", _vp)]
+
+
+class MambaScanGradArgs(ctypes.Structure):
+    _fields_ = [("s", MambaScanArgs), ("dy", _vp), ("dy_stride", _i64), ("dh_last", _vp),
+                ("dx", _vp), ("dx_stride", _i64), ("ddt", _vp), ("ddt_stride", _i64),
+                ("dz", _vp), ("dz_stride", _i64), ("dBm", _vp), ("dB_stride", _i64),
+                ("dCm", _vp), ("dC_stride", _i64), ("dA", _vp), ("dDskip", _vp), ("dh0", _vp)]
+
+
 class GemvArgs(ctypes.Structure):
     _fields_ = [("T", _i32), ("N", _i32), ("Kd", _i32), ("out_dtype", _i32), ("x", _vp),
                 ("x_stride", _i64), ("W", _vp), ("y", _vp), ("y_stride", _i64), ("splits", _i32),
@@ -128,6 +149,12 @@ def _load(path: str):
     L.gdn_decode_fused.argtypes = [ctypes.POINTER(GdnFusedArgs), _vp]
     L.mamba_selective_scan_decode.argtypes = [ctypes.POINTER(MambaArgs), _vp]
     L.mamba_selective_scan_decode.restype = ctypes.c_int
+    L.mamba_selective_scan.argtypes = [ctypes.POINTER(MambaScanArgs), _vp]
+    L.mamba_selective_scan.restype = ctypes.c_int
+    L.mamba_selective_scan_backward.argtypes = [ctypes.POINTER(MambaScanGradArgs), _vp]
+    L.mamba_selective_scan_backward.restype = ctypes.c_int
+    L.mamba_scan_workspace_bytes.argtypes = [_i32] * 6
+    L.mamba_scan_workspace_bytes.restype = ctypes.c_size_t
     L.gdn_selftest_bounded_wait.argtypes = [_vp, _i64, _i32, _vp]
     L.gdn_decode_front.argtypes = [ctypes.POINTER(GdnFrontArgs), _vp]
     L.gdn_decode_front.restype = ctypes.c_int
@@ -151,9 +178,9 @@ def _load(path: str):
     L.gdn_strerror.restype = ctypes.c_char_p
     L.gdn_abi_struct_size.argtypes = [ctypes.c_int]
     L.gdn_abi_struct_size.restype = ctypes.c_size_t
-    sizes = [L.gdn_abi_struct_size(i) for i in range(6)]
-    want = [ctypes.sizeof(GdnStepArgs), ctypes.sizeof(GdnRingArgs), ctypes.sizeof(GdnFusedArgs),
-            ctypes.sizeof(GemvArgs), ctypes.sizeof(GdnFrontArgs), ctypes.sizeof(MambaArgs)]
+    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7)]
+    want = [ctypes.sizeof(c) for c in (GdnStepArgs, GdnRingArgs, GdnFusedArgs, GemvArgs, GdnFrontArgs, MambaArgs,
+                                       MambaScanArgs, MambaScanGradArgs)]
     if sizes != want or L.gdn_abi_version() != ABI_VERSION:
         raise RuntimeError(f"libgdn_decode.so ABI mismatch: struct sizes {sizes} vs {want}")
     return L
@@ -614,6 +641,125 @@ def mamba_selective_scan_decode(x, dt, A, Bm, Cm, h, y, *, Dskip=None, z=None, h
     m.y = _ptr(_dense(y, "y"), "y")
     m.err_flags = _ptr(err_flags, "err_flags", torch.int32)
     return _run_or_prepare("mamba_selective_scan_decode", (ctypes.byref(m),), (m,), stream, prepare, y)
+
+
+def _token_rows(t, name: str, T: int, width: int, dtype=None):
+    """A [T, width] or [S, L, width] tensor whose T rows lie one stride apart: (pointer, row stride)."""
+    if t.dim() not in (2, 3) or t.shape[-1] != width or t.numel() != T * width:
+        raise ValueError(f"{name}: expected {T} rows of {width}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() == 0:
+        return _ptr(t, name), width
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: rows need unit inner stride")
+    stride = t.stride(-2) if t.shape[-2] > 1 else t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else width
+    if t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * stride:
+        raise ValueError(f"{name}: sequences must follow one another at the row stride")
+    return _ptr(t, name), stride
+
+
+def mamba_scan_workspace(T, D, N, *, sequences=1, uniform=True, backward=False, device=None):
+    """A workspace tensor for mamba_selective_scan (or its backward pass) over T token rows of
+    `sequences` sequences, of equal lengths (uniform) or given by cu_seqlens; None when the call needs none."""
+    nbytes = lib().mamba_scan_workspace_bytes(int(T), int(sequences), int(D), int(N), int(uniform), int(backward))
+    if nbytes == 0:
+        return None
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device or "cuda")
+
+
+def _scan_args(x, dt, A, Bm, Cm, *, Dskip, z, sequences, cu_seqlens, state_indices, h0, other_states, workspace,
+               err_flags):
+    torch = _torch()
+    D, N = A.shape
+    T = x.numel() // D if D else 0
+    m = MambaScanArgs()
+    m.T, m.D, m.N = T, D, N
+    if cu_seqlens is not None:
+        if sequences is not None:
+            raise ValueError("give cu_seqlens or sequences, not both")
+        m.S = cu_seqlens.numel() - 1
+    else:
+        m.S = sequences if sequences is not None else (x.shape[0] if x.dim() == 3 else 1)
+    m.in_dtype = _dtype_code(x)
+    m.x, m.x_stride = _token_rows(x, "x", T, D)
+    m.dt, m.dt_stride = _token_rows(dt, "dt", T, D, x.dtype)
+    m.Bm, m.B_stride = _token_rows(Bm, "Bm", T, N, x.dtype)
+    m.Cm, m.C_stride = _token_rows(Cm, "Cm", T, N, x.dtype)
+    if z is not None:
+        m.z, m.z_stride = _token_rows(z, "z", T, D, x.dtype)
+    m.A = _ptr(_dense(A, "A"), "A", torch.float32)
+    if Dskip is not None:
+        if Dskip.numel() != D:
+            raise ValueError(f"Dskip must have {D} entries")
+        m.Dskip = _ptr(_dense(Dskip, "Dskip"), "Dskip", torch.float32)
+    m.cu_seqlens = _ptr(None if cu_seqlens is None else _dense(cu_seqlens, "cu_seqlens"), "cu_seqlens", torch.int32)
+    if state_indices is not None:
+        if state_indices.numel() != m.S:
+            raise ValueError(f"state_indices must have {m.S} entries")
+        m.state_indices = _ptr(_dense(state_indices, "state_indices"), "state_indices", torch.int32)
+    states = [t for t in (h0, *other_states) if t is not None]
+    for t in states:
+        if t.dim() != 3 or t.shape != states[0].shape or tuple(t.shape[1:]) != (D, N):
+            raise ValueError(f"state buffers must be [num_states, {D}, {N}], all with the same num_states")
+        _ptr(_dense(t, "a state buffer"), "a state buffer", torch.float32)
+    m.num_states = states[0].shape[0] if states else 0
+    m.h0 = None if h0 is None else h0.data_ptr()
+    if workspace is not None:
+        m.workspace = _ptr(_dense(workspace, "workspace"), "workspace")
+        m.workspace_bytes = workspace.numel() * workspace.element_size()
+    m.err_flags = _ptr(err_flags, "err_flags", torch.int32)
+    return m, T, D, N
+
+
+def mamba_selective_scan(x, dt, A, Bm, Cm, y, *, Dskip=None, z=None, sequences=None, cu_seqlens=None,
+                         state_indices=None, h0=None, h_last=None, workspace=None, err_flags=None, stream=None,
+                         prepare=False):
+    """Mamba-1 selective scan over whole sequences (declared in include/mamba_scan.h). x, dt, z, y: [T, D] (or
+    [S, L, D]) and Bm, Cm: [T, N] row views, fp32 or bf16 (y of its own dtype); A: [D, N] and Dskip: [D] fp32. The T
+    rows are `sequences` equal sequences (default: x's first axis of three, else one), or those of cu_seqlens
+    (int32 [S + 1] on the device). h0 and h_last: [num_states, D, N] fp32 states at row state_indices[s] (int32;
+    default s) of sequence s; h_last may be h0. workspace: see mamba_scan_workspace."""
+    m, T, D, _ = _scan_args(x, dt, A, Bm, Cm, Dskip=Dskip, z=z, sequences=sequences, cu_seqlens=cu_seqlens,
+                            state_indices=state_indices, h0=h0, other_states=(h_last,), workspace=workspace,
+                            err_flags=err_flags)
+    m.out_dtype = _dtype_code(y)
+    m.y, m.y_stride = _token_rows(y, "y", T, D)
+    m.h_last = None if h_last is None else h_last.data_ptr()
+    keep = (m, x, dt, A, Bm, Cm, y, Dskip, z, cu_seqlens, state_indices, h0, h_last, workspace, err_flags)
+    return _run_or_prepare("mamba_selective_scan", (ctypes.byref(m),), keep, stream, prepare, y)
+
+
+def mamba_selective_scan_backward(x, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, sequences=None, cu_seqlens=None,
+                                  state_indices=None, h0=None, dh_last=None, dx=None, ddt=None, dz=None, dBm=None,
+                                  dCm=None, dA=None, dDskip=None, dh0=None, workspace=None, err_flags=None,
+                                  stream=None, prepare=False):
+    """Gradients of mamba_selective_scan (declared in include/mamba_scan.h). dy: [T, D], dh_last: [num_states, D, N]
+    fp32 or None (zero). Each gradient buffer given is written: dx, ddt, dz like x; dBm, dCm like Bm (all in the dtype
+    of x), dA [D, N], dDskip [D] and dh0 [num_states, D, N] fp32."""
+    torch = _torch()
+    m, T, D, N = _scan_args(x, dt, A, Bm, Cm, Dskip=Dskip, z=z, sequences=sequences, cu_seqlens=cu_seqlens,
+                            state_indices=state_indices, h0=h0, other_states=(dh_last, dh0), workspace=workspace,
+                            err_flags=err_flags)
+    a = MambaScanGradArgs()
+    a.s = m
+    a.dy, a.dy_stride = _token_rows(dy, "dy", T, D, x.dtype)
+    for t, name, width, stride in ((dx, "dx", D, "dx_stride"), (ddt, "ddt", D, "ddt_stride"), (dz, "dz", D, "dz_stride"),
+                                   (dBm, "dBm", N, "dB_stride"), (dCm, "dCm", N, "dC_stride")):
+        if t is not None:
+            p, st = _token_rows(t, name, T, width, x.dtype)
+            setattr(a, name, p)
+            setattr(a, stride, st)
+    for t, name, shape in ((dA, "dA", (D, N)), (dDskip, "dDskip", (D,))):
+        if t is not None:
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+            setattr(a, name, _ptr(_dense(t, name), name, torch.float32))
+    a.dh_last = None if dh_last is None else dh_last.data_ptr()
+    a.dh0 = None if dh0 is None else dh0.data_ptr()
+    keep = (a, x, dt, A, Bm, Cm, dy, Dskip, z, cu_seqlens, state_indices, h0, dh_last, dx, ddt, dz, dBm, dCm, dA,
+            dDskip, dh0, workspace, err_flags)
+    return _run_or_prepare("mamba_selective_scan_backward", (ctypes.byref(a),), keep, stream, prepare, None)
 
 
 def gdn_selftest_bounded_wait(err_flags, limit_cycles, arrive, stream=None):

@@ -9,10 +9,11 @@
 #include "gdn_gemv.h"
 #include "gdn_launch.h"
 #include "mamba_decode.h"
+#include "mamba_scan.h"
 
 namespace {
 
-constexpr int kAbiVersion = 7;
+constexpr int kAbiVersion = 8;
 
 bool k_supported(int K) { return K == 16 || K == 32 || K == 64 || K == 128; }
 bool dtype_ok(int d) { return d == GDN_F32 || d == GDN_BF16; }
@@ -277,6 +278,8 @@ size_t gdn_abi_struct_size(int which)
     case 3: return sizeof(gdn_gemv_args);
     case 4: return sizeof(gdn_front_args);
     case 5: return sizeof(mamba_decode_args);
+    case 6: return sizeof(mamba_scan_args);
+    case 7: return sizeof(mamba_scan_grad_args);
     default: return 0;
     }
 }

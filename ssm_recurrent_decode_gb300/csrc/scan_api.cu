@@ -1,0 +1,212 @@
+// scan_api.cu -- host checks, workspace layout and dispatch of the selective scan.
+#include <cstring>
+
+#include "scan_launch.h"
+
+namespace gdn {
+
+namespace {
+constexpr int kMaxState = 128;
+constexpr int kSms = 152;             // GB300
+constexpr size_t kWsAlign = 256;
+
+size_t round_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
+bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
+int tiles(int D, int N, bool backward)
+{
+    const int ch = (backward ? scan_shape_backward(N) : scan_shape(N)).channels;
+    return (D + ch - 1) / ch;
+}
+bool sizes_ok(int T, int S, int D, int N, bool uniform)
+{
+    return T >= 0 && S >= 1 && D >= 1 && N >= 1 && N <= kMaxState && (!uniform || T % S == 0);
+}
+
+// Takes consecutive pieces of a workspace (only counts when base is null).
+struct Carver {
+    unsigned char *base;
+    size_t used = 0;
+    template <typename T> T *take(size_t count)
+    {
+        T *p = base ? reinterpret_cast<T *>(base + used) : nullptr;
+        used += round_up(count * sizeof(T));
+        return p;
+    }
+};
+
+// Lays out the workspace of a call whose sizes, C, G, nct and W are set; returns its bytes.
+size_t carve(ScanLaunch &P, bool uniform, bool backward, unsigned char *base)
+{
+    Carver w{base};
+    const size_t dn = (size_t)P.a.D * P.a.N;
+    // one sequence per chunk, or all rows in one chunk: no state crosses a chunk border
+    const bool carried = P.G > 1 && !(uniform && P.C == P.L);
+    if (carried) {
+        P.info = w.take<int4>(P.G);
+        P.sumdt = w.take<float>((size_t)P.G * P.a.D);
+        P.hin = w.take<float>(P.G * dn);
+        if (!backward) P.init = w.take<float>(P.G * dn);
+    }
+    if (backward) {
+        if (carried) {
+            P.sumdt_head = w.take<float>((size_t)P.G * P.a.D);
+            P.ein = w.take<float>(P.G * dn);
+        }
+        P.part_bc = w.take<float>((size_t)P.nct * P.a.T * 2 * P.a.N);
+        P.part_a = w.take<float>(P.W * dn);
+        P.part_d = w.take<float>((size_t)P.W * P.a.D);
+    }
+    return w.used;
+}
+
+// C, G, nct and W of a call whose sizes are set
+void plan(ScanLaunch &P, bool uniform, bool backward)
+{
+    P.L = uniform ? P.a.T / P.a.S : 0;
+    P.nct = tiles(P.a.D, P.a.N, backward);
+    P.C = scan_chunk(P.a.T, P.a.S, P.a.D, P.a.N, uniform, backward);
+    P.G = P.a.T > 0 ? (int)(((int64_t)P.a.T + P.C - 1) / P.C) : 1;   // without rows: one chunk of empty sequences
+    P.W = 1;
+    if (backward) {
+        // about three CTAs per SM, each walking over chunks
+        const int64_t want = ((int64_t)3 * kSms + P.nct - 1) / P.nct;
+        P.W = (int)(want < P.G ? want : P.G);
+    }
+}
+
+int check(const mamba_scan_args &a, bool backward, bool states)
+{
+    const bool uniform = !a.cu_seqlens;
+    if (!sizes_ok(a.T, a.S, a.D, a.N, uniform)) return GDN_ERR_SHAPE;
+    if (a.in_dtype != GDN_F32 && a.in_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (!backward && a.out_dtype != GDN_F32 && a.out_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (states && a.num_states < 1) return GDN_ERR_SHAPE;
+    if (states && !a.state_indices && a.num_states < a.S) return GDN_ERR_SHAPE;
+    if (a.T > 0 && (!a.x || !a.dt || !a.A || !a.Bm || !a.Cm || (!backward && !a.y))) return GDN_ERR_NULL;
+    if (a.x_stride < a.D || a.dt_stride < a.D || (a.z && a.z_stride < a.D) || a.B_stride < a.N || a.C_stride < a.N ||
+        (!backward && a.y_stride < a.D))
+        return GDN_ERR_SHAPE;
+    const size_t es = a.in_dtype == GDN_BF16 ? 2 : 4;
+    if (!aligned(a.x, es) || !aligned(a.dt, es) || !aligned(a.z, es) || !aligned(a.Bm, es) || !aligned(a.Cm, es) ||
+        !aligned(a.A, 4) || !aligned(a.Dskip, 4) || !aligned(a.cu_seqlens, 4) || !aligned(a.state_indices, 4) ||
+        !aligned(a.h0, 4) || !aligned(a.h_last, 4) || !aligned(a.y, a.out_dtype == GDN_BF16 ? 2 : 4))
+        return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+int row_bit(const void *p, int64_t stride, size_t es, int bit)
+{
+    return p && aligned(p, 16) && (stride * (int64_t)es) % 16 == 0 ? bit : 0;
+}
+
+void set_inputs(ScanLaunch &P)
+{
+    const mamba_scan_args &a = P.a;
+    const size_t es = a.in_dtype == GDN_BF16 ? 2 : 4;
+    P.vec = row_bit(a.x, a.x_stride, es, kVecX) | row_bit(a.dt, a.dt_stride, es, kVecDt) |
+            row_bit(a.z, a.z_stride, es, kVecZ) | row_bit(a.Bm, a.B_stride, es, kVecB) |
+            row_bit(a.Cm, a.C_stride, es, kVecC);
+    if (a.N % 4 == 0 && aligned(a.A, 16) && aligned(a.h0, 16) && aligned(a.h_last, 16)) P.vec |= kVecState;
+}
+
+int check_workspace(const mamba_scan_args &a, size_t need)
+{
+    if (need == 0) return GDN_OK;
+    if (!a.workspace) return GDN_ERR_NULL;
+    if (a.workspace_bytes < need) return GDN_ERR_SHAPE;
+    return aligned(a.workspace, 16) ? GDN_OK : GDN_ERR_ALIGN;
+}
+}  // namespace
+
+int scan_chunk(int T, int S, int D, int N, bool uniform, bool backward)
+{
+    if (T < 1) return 1;
+    const int64_t nct = tiles(D, N, backward);
+    if (backward) return kScanBackChunk;
+    if (uniform && (S * nct >= 4 * kSms || T / S <= 128)) return T / S;
+    int C = 512;
+    while (C > 32 && ((int64_t)T + C - 1) / C * nct < 12 * kSms) C /= 2;
+    return C;
+}
+
+}  // namespace gdn
+
+extern "C" {
+
+size_t mamba_scan_workspace_bytes(int32_t T, int32_t S, int32_t D, int32_t N, int32_t uniform, int32_t backward)
+{
+    if (!gdn::sizes_ok(T, S, D, N, uniform != 0)) return 0;
+    gdn::ScanLaunch P;
+    std::memset(&P, 0, sizeof(P));
+    P.a.T = T;
+    P.a.S = S;
+    P.a.D = D;
+    P.a.N = N;
+    gdn::plan(P, uniform != 0, backward != 0);
+    return gdn::carve(P, uniform != 0, backward != 0, nullptr);
+}
+
+int mamba_selective_scan(const mamba_scan_args *args, gdn_stream_t stream)
+{
+    if (!args) return GDN_ERR_NULL;
+    const int rc = gdn::check(*args, false, args->h0 || args->h_last);
+    if (rc != GDN_OK || (args->T == 0 && !args->h_last)) return rc;
+    gdn::ScanLaunch P;
+    std::memset(&P, 0, sizeof(P));
+    P.a = *args;
+    const bool uniform = !args->cu_seqlens;
+    gdn::plan(P, uniform, false);
+    const size_t need = gdn::carve(P, uniform, false, nullptr);
+    const int wrc = gdn::check_workspace(*args, need);
+    if (wrc != GDN_OK) return wrc;
+    gdn::carve(P, uniform, false, static_cast<unsigned char *>(args->workspace));
+    gdn::set_inputs(P);
+    P.has_states = args->h0 || args->h_last;
+    const size_t os = args->out_dtype == GDN_BF16 ? 2 : 4;
+    if (gdn::aligned(args->y, 4 * os) && args->y_stride % 4 == 0) P.vec |= gdn::kVecY;
+    return gdn::launch_scan_forward(P, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mamba_selective_scan_backward(const mamba_scan_grad_args *args, gdn_stream_t stream)
+{
+    if (!args) return GDN_ERR_NULL;
+    const mamba_scan_grad_args &q = *args;
+    const bool states = q.s.h0 || q.dh_last || q.dh0;
+    const int rc = gdn::check(q.s, true, states);
+    if (rc != GDN_OK) return rc;
+    if ((q.dz && !q.s.z) || (q.dDskip && !q.s.Dskip)) return GDN_ERR_ARG;
+    if (q.s.T > 0 && !q.dy) return GDN_ERR_NULL;
+    const int64_t D = q.s.D, N = q.s.N;
+    if (q.dy_stride < D || (q.dx && q.dx_stride < D) || (q.ddt && q.ddt_stride < D) || (q.dz && q.dz_stride < D) ||
+        (q.dBm && q.dB_stride < N) || (q.dCm && q.dC_stride < N))
+        return GDN_ERR_SHAPE;
+    const size_t es = q.s.in_dtype == GDN_BF16 ? 2 : 4;
+    for (const void *p : {q.dy, (const void *)q.dx, (const void *)q.ddt, (const void *)q.dz, (const void *)q.dBm, (const void *)q.dCm})
+        if (!gdn::aligned(p, es)) return GDN_ERR_ALIGN;
+    for (const void *p : {(const void *)q.dh_last, (const void *)q.dA, (const void *)q.dDskip, (const void *)q.dh0})
+        if (!gdn::aligned(p, 4)) return GDN_ERR_ALIGN;
+    gdn::ScanLaunch P;
+    std::memset(&P, 0, sizeof(P));
+    P.a = q.s;
+    P.g = q;
+    const bool uniform = !q.s.cu_seqlens;
+    gdn::plan(P, uniform, true);
+    const size_t need = gdn::carve(P, uniform, true, nullptr);
+    const int wrc = gdn::check_workspace(q.s, need);
+    if (wrc != GDN_OK) return wrc;
+    gdn::carve(P, uniform, true, static_cast<unsigned char *>(q.s.workspace));
+    P.a.h_last = nullptr;
+    gdn::set_inputs(P);
+    if (!gdn::aligned(q.dh_last, 16) || !gdn::aligned(q.dh0, 16)) P.vec &= ~gdn::kVecState;
+    P.has_states = states;
+    P.vec |= gdn::row_bit(q.dy, q.dy_stride, es, gdn::kVecDy);
+    const auto out_bit = [&](const void *p, int64_t stride, int bit) {
+        if (p && gdn::aligned(p, 4 * es) && stride % 4 == 0) P.vec |= bit;
+    };
+    out_bit(q.dx, q.dx_stride, gdn::kVecDx);
+    out_bit(q.ddt, q.ddt_stride, gdn::kVecDdt);
+    out_bit(q.dz, q.dz_stride, gdn::kVecDz);
+    return gdn::launch_scan_backward(P, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,316 @@
+// scan_common.cuh -- what the selective scan's forward and backward kernels share (internal to
+// libgdn_decode.so): fp32-pair arithmetic, staging of token tiles, the walk over a chunk's sequences.
+//
+// Work split. The packed token rows are cut into chunks of C rows, the channels into tiles of
+// ScanShape::CB; one CTA of four warps owns a (chunk, channel tile) and walks its rows in order, each
+// thread keeping CPT channels x 4 state entries in registers. A chunk may hold pieces of several
+// sequences: the state is set anew where one begins, so ragged prompts cost what their tokens cost.
+// States cross chunk borders through a summary pass (the state each chunk would end with from zero,
+// and the sum of its dt: its decay is exp(A sum dt), one exp per entry and chunk) and a carry pass
+// over the chunks. The summary costs a second exp per state entry, so it is skipped where the
+// sequences alone fill the GPU (mamba_scan_plan).
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "gdn_chain.cuh"
+#include "gdn_common.cuh"
+#include "gdn_pipe.cuh"
+#include "mamba_scan.h"
+#include "scan_launch.h"
+
+namespace gdn {
+
+constexpr int kScanThreads = 128;
+constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kScanTile = 16;               // token rows staged at a time
+constexpr unsigned kScanFull = 0xFFFFFFFFu;
+
+// Lanes along the state: NL lanes x 4 entries cover a row of up to 4 NL entries (missing ones are
+// zeros); the other lanes, the warps and CPT lie along the channels.
+template <int NL_, int CPT_> struct ScanShape {
+    static constexpr int NL = NL_, CPT = CPT_;
+    static constexpr int NP = 4 * NL;                     // padded state size
+    static constexpr int CLN = 32 / NL;                   // channel lanes of a warp
+    static constexpr int CW = CLN * CPT;                  // channels of a warp
+    static constexpr int CB = CW * kScanWarps;            // channels of a CTA
+    static constexpr int YP = CB + 16;                    // row pitch of per-channel sums: rows two banks groups apart
+};
+
+// ---------------------------------------------------------------------------------------------
+// fp32 pairs (fma.rn.f32x2: half the issue slots of the scalar instructions at the same rate, each
+// element rounded alike)
+// ---------------------------------------------------------------------------------------------
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Decays close to one are multiplied over thousands of tokens, so a bias of their rounding grows
+// with the length of the memory. ex2.approx measured a mean error of -0.6e-8 for exponents of
+// -1e-4 .. -1e-3, -1.2e-8 for -1e-3 .. -1e-2 and about -2e-8 up to 1 (GB300, 2^18 arguments each);
+// an exponent larger by this constant takes the mean out where memories are long, at no cost (the
+// product dt A becomes a multiply-add).
+constexpr float kDecayBias = 0.9e-8f;
+
+// exp(dt A) of a pair of entries, A2 = A log2(e)
+__device__ __forceinline__ f2 decay2(f2 dtdt, f2 A2)
+{
+    const float2 y = unpack2(fma2(dtdt, A2, pack2(kDecayBias, kDecayBias)));
+    return pack2(ex2_approx(y.x), ex2_approx(y.y));
+}
+
+// silu and its parts on the fast reciprocal (relative error of a few 2^-23)
+__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// Sums v[0 .. M) over the NL lanes of a group, M values at once: each halving of the lanes halves
+// the values a lane keeps. Lane nl ends with values nl M / NL .. (M >= NL), or with value
+// nl / (NL / M) (M < NL, the same one in NL / M lanes).
+template <int M, int NL> __device__ __forceinline__ void group_reduce(float (&v)[M], int nl, int lane_step = 1)
+{
+    int m = M;
+#pragma unroll
+    for (int off = NL / 2; off > 0; off >>= 1) {
+        const bool hi = (nl & off) != 0;
+        if (m > 1) {
+            m /= 2;
+#pragma unroll
+            for (int i = 0; i < M / 2; ++i) {
+                if (i < m) {
+                    const float send = hi ? v[i] : v[i + m];
+                    const float keep = hi ? v[i + m] : v[i];
+                    v[i] = keep + __shfl_xor_sync(kScanFull, send, off * lane_step);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(kScanFull, v[0], off * lane_step);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// staging: R rows x W elements of a row-strided tensor into shared memory
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// rows >= n and columns >= ncols are filled with zeros. `src` is the first element of the tile;
+// vec: src and every row are 16-byte aligned (asynchronous 16-byte copies), else element by element.
+template <typename T, int W, int R = kScanTile>
+__device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t stride, int n, int ncols, bool vec, int tid)
+{
+    if (vec) {
+        constexpr int VE = 16 / (int)sizeof(T);
+        static_assert(W % VE == 0, "a staged row is whole 16-byte vectors");
+        constexpr int VPR = W / VE;
+#pragma unroll
+        for (int k = 0; k < (R * VPR + kScanThreads - 1) / kScanThreads; ++k) {
+            const int i = k * kScanThreads + tid;
+            const int r = i / VPR, v = i % VPR;
+            if (R * VPR % kScanThreads == 0 || r < R) {
+                int left = r < n ? (ncols - v * VE) * (int)sizeof(T) : 0;
+                left = left < 0 ? 0 : left > 16 ? 16 : left;
+                cp_async16(dst + r * W + v * VE, left ? src + r * stride + v * VE : src, left);
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int i = tid; i < R * W; i += kScanThreads) {
+            const int r = i / W, c = i % W;
+            dst[i] = r < n && c < ncols ? src[r * stride + c] : from_f32<T>(0.f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// sequences
+// ---------------------------------------------------------------------------------------------
+// first row of sequence s (s = S: the end of the last one)
+__device__ __forceinline__ int seq_bound(const ScanLaunch &P, int s)
+{
+    return P.a.cu_seqlens ? P.a.cu_seqlens[s] : s * P.L;
+}
+
+// The last sequence that begins at or before row pos (-1: none; S: pos lies behind the last one),
+// found by the whole CTA. Contains two barriers with cu_seqlens.
+__device__ __forceinline__ int find_seq(const ScanLaunch &P, int pos, int *scratch, int tid)
+{
+    if (!P.a.cu_seqlens) return P.L ? pos / P.L : 0;
+    int c = 0;
+    for (int i = tid; i <= P.a.S; i += kScanThreads) c += P.a.cu_seqlens[i] <= pos;
+    c = __reduce_add_sync(kScanFull, c);
+    __syncthreads();
+    if ((tid & 31) == 0) scratch[tid >> 5] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) c += scratch[w];
+    return c - 1;
+}
+
+// A staged tile: rows t0 .. t0 + n - 1 of one sequence (seq -1: rows of no sequence, or of one whose
+// state index is out of range: their outputs are zeros).
+struct ScanTile {
+    int t0, n;
+    int seq;
+    int64_t slot;     // its row in the state buffers
+    bool fresh;       // first tile of this sequence in the chunk
+    bool starts;      // holds the sequence's first row
+    bool ends;        // holds the sequence's last row
+};
+
+// Walks rows pos .. end - 1 in tiles that never span two sequences.
+struct ScanIter {
+    int pos, end, s, run_begin, run_end;
+    int64_t slot;
+    bool live;
+
+    __device__ __forceinline__ void init(int first, int last, int seq)
+    {
+        pos = first;
+        end = last;
+        s = seq;
+        run_end = first;
+        live = false;
+    }
+
+    __device__ __forceinline__ bool next(const ScanLaunch &P, ScanTile &t)
+    {
+        if (pos >= end) return false;
+        t.fresh = pos >= run_end;
+        if (t.fresh) {
+            if (s < 0 && seq_bound(P, 0) <= pos) s = 0;
+            while (s >= 0 && s < P.a.S && seq_bound(P, s + 1) <= pos) ++s;
+            live = s >= 0 && s < P.a.S;
+            run_begin = live ? seq_bound(P, s) : pos;
+            run_end = live ? seq_bound(P, s + 1) : s < 0 ? min(seq_bound(P, 0), end) : end;
+            if (live) {
+                slot = P.a.state_indices ? (int64_t)P.a.state_indices[s] : s;
+                if (P.has_states && (slot < 0 || slot >= P.a.num_states)) live = false;
+            }
+            if (!live) raise_flag(threadIdx.x == 0 ? P.a.err_flags : nullptr, GDN_DEVERR_BAD_INDEX);
+        }
+        t.t0 = pos;
+        t.n = min(kScanTile, min(run_end, end) - pos);
+        t.seq = live ? s : -1;
+        t.slot = slot;
+        t.starts = live && pos == run_begin;
+        t.ends = live && pos + t.n == run_end;
+        pos += t.n;
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------------------------
+// a thread's CPT x 4 entries of a [D, N] fp32 state row
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void load_entries(const float *row, int d, int D, int n0, int N, bool vec, f2 (&v)[2])
+{
+    float e[4] = {0.f, 0.f, 0.f, 0.f};
+    if (d < D) {
+        const float *p = row + (int64_t)d * N + n0;
+        if (vec && n0 < N) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n0 + j < N) e[j] = p[j];
+        }
+    }
+    v[0] = pack2(e[0], e[1]);
+    v[1] = pack2(e[2], e[3]);
+}
+__device__ __forceinline__ void store_entries(float *row, int d, int D, int n0, int N, bool vec, const f2 (&v)[2])
+{
+    if (d >= D) return;
+    float *p = row + (int64_t)d * N + n0;
+    const float2 lo = unpack2(v[0]), hi = unpack2(v[1]);
+    if (vec && n0 < N) {
+        *reinterpret_cast<float4 *>(p) = make_float4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+        const float e[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n0 + j < N) p[j] = e[j];
+    }
+}
+
+// A log2(e) of a thread's entries. An A of minus infinity (forget everything) becomes the lowest
+// finite value: the same decay of zero for every dt of a token, and still one for the dt of zero that
+// fills up a tile's missing rows.
+__device__ __forceinline__ float finite_rate(float a) { return a == -INFINITY ? -3.402823466e38f : a; }
+__device__ __forceinline__ void load_rates(const float *A, int d, int D, int n0, int N, bool vec, f2 (&v)[2])
+{
+    load_entries(A, d, D, n0, N, vec, v);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const float2 a = unpack2(v[p]);
+        v[p] = pack2(finite_rate(a.x * kLog2e), finite_rate(a.y * kLog2e));
+    }
+}
+
+// B and C rows of a staged tile as fp32: the tile itself for fp32 inputs
+__device__ __forceinline__ const float *as_f32(const float *raw, float *, int, int) { return raw; }
+__device__ __forceinline__ const float *as_f32(const bf16 *raw, float *wide, int count, int tid)
+{
+    for (int i = tid * 4; i < count; i += kScanThreads * 4)
+        *reinterpret_cast<float4 *>(wide + i) = load4(raw + i);
+    return wide;
+}
+
+// four elements of a row-strided output, as one access where the row allows it
+template <typename T>
+__device__ __forceinline__ void store_row4(T *p, float4 v, int left, bool vec)
+{
+    if (vec && left >= 4) {
+        store4(p, v);
+    } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) p[j] = from_f32<T>(e[j]);
+    }
+}
+
+}  // namespace gdn

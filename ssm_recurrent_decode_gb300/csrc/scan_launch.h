@@ -1,0 +1,65 @@
+// scan_launch.h -- launch parameters of the selective scan (internal to libgdn_decode.so).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "mamba_scan.h"
+
+namespace gdn {
+
+// 16-byte copies allowed for a row-strided tensor (bits of ScanLaunch::vec)
+enum { kVecX = 1, kVecDt = 2, kVecZ = 4, kVecB = 8, kVecC = 16, kVecDy = 32, kVecY = 64, kVecState = 128,
+       kVecDx = 256, kVecDdt = 512, kVecDz = 1024 };
+
+struct ScanLaunch {
+    mamba_scan_args a;
+    int L;              // rows per sequence without cu_seqlens
+    int C, G;           // rows per chunk, chunks
+    int nct;            // channel tiles
+    int vec;
+    int has_states;     // state indices are checked
+    // workspace
+    int4 *info;         // [G] x: sequence that goes on behind the chunk (-1: none), y: it begins inside,
+                        //         z: sequence that began before the chunk (-1: none), w: it ends inside
+    float *sumdt;       // [G, D] sum of dt over the rows of info.x's sequence
+    float *hin;         // [G, D, N] the state that chunk ends with from zero; then the state it starts from
+    float *init;        // [G, D, N] initial state of info.x's sequence, when it begins in the chunk
+    // backward only
+    mamba_scan_grad_args g;
+    float *sumdt_head;  // [G, D] sum of dt over the rows of info.z's sequence
+    float *ein;         // [G, D, N] e that the chunk sends to the row before it, from zero; then e at its last row
+    float *part_bc;     // [nct, T, 2 N] each channel tile's share of dBm and dCm
+    float *part_a;      // [W, D, N] each worker's share of dA
+    float *part_d;      // [W, D] each worker's share of dDskip
+    int W;              // workers per channel tile
+};
+
+// lanes along the state and channels per thread for a state size
+struct ScanTileShape { int NL, CPT; int channels; };
+inline ScanTileShape scan_shape(int N)
+{
+    const int nl = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32;
+    const int cpt = nl >= 16 ? 4 : 2;
+    return {nl, cpt, 4 * (32 / nl) * cpt};
+}
+
+inline ScanTileShape scan_shape_backward(int N)
+{
+    const int nl = scan_shape(N).NL;
+    return {nl, 2, 4 * (32 / nl) * 2};
+}
+
+constexpr int kScanBackChunk = 64;   // token rows per chunk of the backward pass
+
+// Rows per chunk of the forward and the backward call (a function of the sizes alone, so that the
+// workspace can be sized before the call).
+int scan_chunk(int T, int S, int D, int N, bool uniform, bool backward);
+
+// The carry pass over the chunks (forward; with both also the backward one, over e).
+cudaError_t launch_scan_carry(const ScanLaunch &P, bool both, cudaStream_t stream);
+
+int launch_scan_forward(const ScanLaunch &P, cudaStream_t stream);
+int launch_scan_backward(const ScanLaunch &P, cudaStream_t stream);
+
+}  // namespace gdn
