@@ -14,6 +14,8 @@ Entry points (same names as the C ABI):
   mamba_selective_scan_decode  the Mamba-1 selective-scan decode step (a diagonal recurrence)
   mamba_selective_scan     the same recurrence over whole sequences (prompts), packed end to end
   mamba_selective_scan_backward  its gradients
+  gdn_beam_select          the best K of beams x vocabulary by cumulative log-probability
+  gdn_beam_reorder         the chosen beams' states, moved within their slot pools
 plus ``fused_recurrent_gated_delta_rule_packed_decode``, the packed call with the keyword names
 of "Microbenchmark: buffered output-only GDN decode (ReplaySSM Part A)" (_bench_cfg, run_packed).
 """
@@ -32,6 +34,8 @@ __all__ = [
     "MambaArgs", "mamba_selective_scan_decode", "gdn_selftest_bounded_wait",
     "MambaScanArgs", "MambaScanGradArgs", "mamba_selective_scan", "mamba_selective_scan_backward",
     "mamba_scan_workspace",
+    "BeamSelectArgs", "BeamPool", "BeamReorderArgs", "gdn_beam_select", "beam_select_workspace",
+    "gdn_beam_reorder",
     "GemvArgs", "gdn_gemv_bf16", "gemv_workspace",
     "GDN_F32", "GDN_BF16", "GDN_DEVERR_BAD_INDEX", "GDN_DEVERR_BAD_WRITE_POS", "GDN_DEVERR_TIMEOUT",
     "GDN_DEVERR_RANGE", "debug_lib", "using_debug_build",
@@ -53,7 +57,8 @@ EXPORTS = ("gdn_decode_step", "gdn_decode_step_indexed", "gdn_decode_buffered", 
            "gdn_selftest_bounded_wait", "gdn_gemv_bf16", "gdn_gemv_default_splits",
            "gdn_gemv_workspace_bytes", "gdn_gemv_bf16_noalloc", "gdn_decode_front",
            "gdn_front_proj_width", "gdn_gemv_set_wait_limit", "gdn_decode_step_indexed_chained",
-           "mamba_selective_scan", "mamba_selective_scan_backward", "mamba_scan_workspace_bytes")
+           "mamba_selective_scan", "mamba_selective_scan_backward", "mamba_scan_workspace_bytes",
+           "gdn_beam_select", "gdn_beam_select_workspace_bytes", "gdn_beam_reorder")
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -120,6 +125,24 @@ class GemvArgs(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("err_flags", _vp)]
 
 
+class BeamSelectArgs(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("beams", _i32), ("vocab", _i32), ("K", _i32), ("logits_dtype", _i32),
+                ("num_rows", _i32), ("logits", _vp), ("row_stride", _i64), ("rows", _vp), ("scores", _vp),
+                ("finished", _vp), ("eos_token", _i32), ("out_scores", _vp), ("out_parents", _vp),
+                ("out_tokens", _vp), ("out_finished", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t), ("err_flags", _vp)]
+
+
+class BeamPool(ctypes.Structure):
+    _fields_ = [("base", _vp), ("slot_stride", _i64), ("slot_bytes", _i64)]
+
+
+class BeamReorderArgs(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("beams", _i32), ("num_slots", _i32), ("num_pools", _i32),
+                ("pools", ctypes.POINTER(BeamPool)), ("slots", _vp), ("parents", _vp), ("new_slots", _vp),
+                ("err_flags", _vp)]
+
+
 class GdnError(RuntimeError):
     """A non-zero status from the library (the message is gdn_strerror's)."""
 
@@ -155,6 +178,12 @@ def _load(path: str):
     L.mamba_selective_scan_backward.restype = ctypes.c_int
     L.mamba_scan_workspace_bytes.argtypes = [_i32] * 6
     L.mamba_scan_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_beam_select.argtypes = [ctypes.POINTER(BeamSelectArgs), _vp]
+    L.gdn_beam_select.restype = ctypes.c_int
+    L.gdn_beam_select_workspace_bytes.argtypes = [_i32] * 4
+    L.gdn_beam_select_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_beam_reorder.argtypes = [ctypes.POINTER(BeamReorderArgs), _vp]
+    L.gdn_beam_reorder.restype = ctypes.c_int
     L.gdn_selftest_bounded_wait.argtypes = [_vp, _i64, _i32, _vp]
     L.gdn_decode_front.argtypes = [ctypes.POINTER(GdnFrontArgs), _vp]
     L.gdn_decode_front.restype = ctypes.c_int
@@ -178,9 +207,9 @@ def _load(path: str):
     L.gdn_strerror.restype = ctypes.c_char_p
     L.gdn_abi_struct_size.argtypes = [ctypes.c_int]
     L.gdn_abi_struct_size.restype = ctypes.c_size_t
-    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7)]
+    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10)]
     want = [ctypes.sizeof(c) for c in (GdnStepArgs, GdnRingArgs, GdnFusedArgs, GemvArgs, GdnFrontArgs, MambaArgs,
-                                       MambaScanArgs, MambaScanGradArgs)]
+                                       MambaScanArgs, MambaScanGradArgs, BeamSelectArgs, BeamReorderArgs)]
     if sizes != want or L.gdn_abi_version() != ABI_VERSION:
         raise RuntimeError(f"libgdn_decode.so ABI mismatch: struct sizes {sizes} vs {want}")
     return L
@@ -760,6 +789,86 @@ def mamba_selective_scan_backward(x, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, s
     keep = (a, x, dt, A, Bm, Cm, dy, Dskip, z, cu_seqlens, state_indices, h0, dh_last, dx, ddt, dz, dBm, dCm, dA,
             dDskip, dh0, workspace, err_flags)
     return _run_or_prepare("mamba_selective_scan_backward", (ctypes.byref(a),), keep, stream, prepare, None)
+
+
+def beam_select_workspace(batch, beams, vocab, K, device=None):
+    """A workspace tensor for gdn_beam_select with these sizes."""
+    nbytes = lib().gdn_beam_select_workspace_bytes(int(batch), int(beams), int(vocab), int(K))
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device or "cuda")
+
+
+def _table(t, name, shape, dtype):
+    if t is None:
+        return None
+    if tuple(t.shape) != shape and t.numel() != shape[0] * shape[1]:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return _ptr(_dense(t, name), name, dtype)
+
+
+def gdn_beam_select(logits, scores, out_scores, out_parents, out_tokens, *, rows=None, finished=None, eos_token=-1,
+                    out_finished=None, workspace=None, err_flags=None, stream=None, prepare=False):
+    """One beam-search selection (declared in include/gdn_beam.h). logits: [num_rows, vocab] fp32 or bf16 row view;
+    scores: [batch, beams] fp32; rows: int32 [batch, beams], the logits row of each beam, or None (in order);
+    finished: uint8 or bool [batch, beams] or None; out_scores fp32, out_parents and out_tokens int32, out_finished uint8
+    or bool: [batch, K]. workspace: see beam_select_workspace."""
+    torch = _torch()
+    batch, beams = scores.shape
+    K = out_scores.shape[1]
+    a = BeamSelectArgs()
+    a.batch, a.beams, a.K = batch, beams, K
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected [rows, vocab] with unit inner stride")
+    a.num_rows, a.vocab = logits.shape
+    a.logits_dtype = _dtype_code(logits)
+    a.logits = _ptr(logits, "logits")
+    a.row_stride = logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    for t, name in ((finished, "finished"), (out_finished, "out_finished")):
+        if t is not None and t.dtype not in (torch.uint8, torch.bool):
+            raise TypeError(f"{name} must be uint8 or bool")
+    a.rows = _table(rows, "rows", (batch, beams), torch.int32)
+    a.scores = _table(scores, "scores", (batch, beams), torch.float32)
+    a.finished = _table(finished, "finished", (batch, beams), None)
+    a.eos_token = int(eos_token)
+    a.out_scores = _table(out_scores, "out_scores", (batch, K), torch.float32)
+    a.out_parents = _table(out_parents, "out_parents", (batch, K), torch.int32)
+    a.out_tokens = _table(out_tokens, "out_tokens", (batch, K), torch.int32)
+    a.out_finished = _table(out_finished, "out_finished", (batch, K), None)
+    if workspace is not None:
+        a.workspace = _ptr(_dense(workspace, "workspace"), "workspace")
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    a.err_flags = _ptr(err_flags, "err_flags", torch.int32)
+    keep = (a, logits, scores, out_scores, out_parents, out_tokens, rows, finished, out_finished, workspace, err_flags)
+    return _run_or_prepare("gdn_beam_select", (ctypes.byref(a),), keep, stream, prepare,
+                           (out_scores, out_parents, out_tokens))
+
+
+def gdn_beam_reorder(pools, slots, parents, new_slots, *, err_flags=None, stream=None, prepare=False):
+    """Moves the states of a beam search's chosen continuations (declared in include/gdn_beam.h). pools: tensors whose
+    first axis is the slot and whose slots are dense (any dtype: states, convolution taps, rings), updated in place;
+    slots, parents, new_slots: int32 [batch, beams]. new_slots gets each new beam's slot."""
+    torch = _torch()
+    batch, beams = slots.shape
+    a = BeamReorderArgs()
+    a.batch, a.beams = batch, beams
+    a.num_pools = len(pools)
+    table = (BeamPool * max(1, len(pools)))()
+    num_slots = pools[0].shape[0] if pools else 1
+    if any(t.dim() < 1 or t.shape[0] != num_slots for t in pools):
+        raise ValueError("every pool must have the same number of slots")
+    for q, t in zip(table, pools):
+        if t.shape[0] > 0 and not t[0].is_contiguous():
+            raise ValueError("a pool's slots must be dense")
+        q.base = _ptr(t, "a pool")
+        q.slot_bytes = t[0].numel() * t.element_size() if num_slots else 0
+        q.slot_stride = t.stride(0) * t.element_size() if num_slots > 1 else q.slot_bytes
+    a.num_slots = num_slots
+    a.pools = table
+    a.slots = _table(slots, "slots", (batch, beams), torch.int32)
+    a.parents = _table(parents, "parents", (batch, beams), torch.int32)
+    a.new_slots = _table(new_slots, "new_slots", (batch, beams), torch.int32)
+    a.err_flags = _ptr(err_flags, "err_flags", torch.int32)
+    keep = (a, table, pools, slots, parents, new_slots, err_flags)
+    return _run_or_prepare("gdn_beam_reorder", (ctypes.byref(a),), keep, stream, prepare, new_slots)
 
 
 def gdn_selftest_bounded_wait(err_flags, limit_cycles, arrive, stream=None):

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "gdn_beam.h"
 #include "gdn_front.h"
 #include "gdn_gemv.h"
 #include "gdn_launch.h"
@@ -280,6 +281,8 @@ size_t gdn_abi_struct_size(int which)
     case 5: return sizeof(mamba_decode_args);
     case 6: return sizeof(mamba_scan_args);
     case 7: return sizeof(mamba_scan_grad_args);
+    case 8: return sizeof(gdn_beam_select_args);
+    case 10: return sizeof(gdn_beam_reorder_args);
     default: return 0;
     }
 }
