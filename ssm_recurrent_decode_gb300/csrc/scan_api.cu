@@ -12,11 +12,7 @@ constexpr size_t kWsAlign = 256;
 
 size_t round_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
-int tiles(int D, int N, bool backward)
-{
-    const int ch = (backward ? scan_shape_backward(N) : scan_shape(N)).channels;
-    return (D + ch - 1) / ch;
-}
+int tiles(int D, int N) { return (D + scan_shape(N).channels - 1) / scan_shape(N).channels; }
 bool sizes_ok(int T, int S, int D, int N, bool uniform)
 {
     return T >= 0 && S >= 1 && D >= 1 && N >= 1 && N <= kMaxState && (!uniform || T % S == 0);
@@ -63,13 +59,13 @@ size_t carve(ScanLaunch &P, bool uniform, bool backward, unsigned char *base)
 void plan(ScanLaunch &P, bool uniform, bool backward)
 {
     P.L = uniform ? P.a.T / P.a.S : 0;
-    P.nct = tiles(P.a.D, P.a.N, backward);
+    P.nct = tiles(P.a.D, P.a.N);
     P.C = scan_chunk(P.a.T, P.a.S, P.a.D, P.a.N, uniform, backward);
     P.G = P.a.T > 0 ? (int)(((int64_t)P.a.T + P.C - 1) / P.C) : 1;   // without rows: one chunk of empty sequences
     P.W = 1;
     if (backward) {
-        // about three CTAs per SM, each walking over chunks
-        const int64_t want = ((int64_t)3 * kSms + P.nct - 1) / P.nct;
+        // two CTAs per SM (what their registers allow), each walking over chunks
+        const int64_t want = (int64_t)2 * kSms / P.nct > 0 ? (int64_t)2 * kSms / P.nct : 1;
         P.W = (int)(want < P.G ? want : P.G);
     }
 }
@@ -121,7 +117,7 @@ int check_workspace(const mamba_scan_args &a, size_t need)
 int scan_chunk(int T, int S, int D, int N, bool uniform, bool backward)
 {
     if (T < 1) return 1;
-    const int64_t nct = tiles(D, N, backward);
+    const int64_t nct = tiles(D, N);
     if (backward) return kScanBackChunk;
     if (uniform && (S * nct >= 4 * kSms || T / S <= 128)) return T / S;
     int C = 512;

@@ -20,35 +20,24 @@ template <typename Tin, class Sh> struct BackSmem {
     static constexpr int RX = R * Sh::CB * (int)sizeof(Tin);              // a staged x, dt, z or dy tile
     static constexpr int RB = R * Sh::NP * (int)sizeof(Tin);              // a staged B or C tile
     static constexpr int STAGE = 4 * RX + 2 * RB;
-    static constexpr int Q = R * Sh::CB * 16;                             // {dt, dt, u, u}
-    static constexpr int GG = R * Sh::CB * 8;                             // {g, g}
-    static constexpr int WIDE = sizeof(Tin) == 4 ? 0 : R * Sh::NP * 4;
-    static constexpr int SUMS = R * Sh::YP * 4;                           // per-channel sums of one kind
+    static constexpr int SUMS = kScanWarps * R * Sh::YP * 4;              // a value per row and channel
     static constexpr int PART = kScanWarps * R * 2 * Sh::NP * 4;          // dB and dC per warp
-    static constexpr int STATES = kBackTiles * Sh::CPT * kScanThreads * 16;
-    static constexpr int SUMMARY = 2 * STAGE + Q + GG + 2 * WIDE;
-    static constexpr int MAIN = 2 * STAGE + Q + GG + 2 * WIDE + 3 * SUMS + PART + STATES;
+    static constexpr int STATES = kBackTiles * 4 * kScanThreads * 16;
+    static constexpr int SUMMARY = 2 * STAGE + SUMS;
+    static constexpr int MAIN = 2 * STAGE + 4 * SUMS + PART + STATES;
 };
 
-// Staging, conversion and addressing that the summary and the gradient kernel share.
+// Staging that the summary and the gradient kernel share, and g = dy silu(z) of a tile.
 template <typename Tin, class Sh> struct BackTile {
     using Sm = BackSmem<Tin, Sh>;
     static constexpr int CB = Sh::CB, NP = Sh::NP, R = kBackTile;
     const ScanLaunch &P;
     unsigned char *smem;
     int tid, c0, ncols;
-    float4 *q;
-    f2 *gg;
-    float *wideB, *wideC;
-    const float *Bf, *Cf;
 
     __device__ __forceinline__ BackTile(const ScanLaunch &P_, unsigned char *s, int tid_, int c0_)
         : P(P_), smem(s), tid(tid_), c0(c0_), ncols(min(CB, P_.a.D - c0_))
     {
-        q = reinterpret_cast<float4 *>(smem + 2 * Sm::STAGE);
-        gg = reinterpret_cast<f2 *>(smem + 2 * Sm::STAGE + Sm::Q);
-        wideB = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::Q + Sm::GG);
-        wideC = wideB + Sm::WIDE / 4;
     }
     __device__ __forceinline__ Tin *raw(int b, int k) const      // k: 0 x, 1 dt, 2 z, 3 dy
     {
@@ -76,41 +65,38 @@ template <typename Tin, class Sh> struct BackTile {
                                    n, P.a.N, P.vec & kVecC, tid);
         }
     }
-    __device__ __forceinline__ void widen(int b, bool grads)
+    // g of this warp's channels into gs [R][YP]; the warp alone reads it
+    __device__ __forceinline__ void gate(int b, float *gs, int lane, int warp)
     {
-        const Tin *xs = raw(b, 0), *ds = raw(b, 1), *zs = raw(b, 2), *dys = raw(b, 3);
-        for (int i = tid * 4; i < R * CB; i += kScanThreads * 4) {
-            const float4 x4 = load4(xs + i), d4 = load4(ds + i);
-            const float u0 = d4.x * x4.x, u1 = d4.y * x4.y, u2 = d4.z * x4.z, u3 = d4.w * x4.w;
-            q[i] = make_float4(d4.x, d4.x, u0, u0);
-            q[i + 1] = make_float4(d4.y, d4.y, u1, u1);
-            q[i + 2] = make_float4(d4.z, d4.z, u2, u2);
-            q[i + 3] = make_float4(d4.w, d4.w, u3, u3);
-            if (grads) {
-                float4 g = load4(dys + i);
-                if (P.a.z) {
-                    const float4 z4 = load4(zs + i);
-                    g.x *= z4.x * fast_sigmoid(z4.x);
-                    g.y *= z4.y * fast_sigmoid(z4.y);
-                    g.z *= z4.z * fast_sigmoid(z4.z);
-                    g.w *= z4.w * fast_sigmoid(z4.w);
+        constexpr int CLN = Sh::CLN, NL = Sh::NL;
+        const int c = lane % CLN * 4;
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += NL) {
+            const int r = r0 + lane / CLN;
+            if (NL > R && r >= R) break;
+            f2 g[2], z[2];
+            load_pairs(raw(b, 3) + r * CB + warp * Sh::CW + c, g);
+            if (P.a.z) {
+                load_pairs(raw(b, 2) + r * CB + warp * Sh::CW + c, z);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float2 v = unpack2(z[p]);
+                    g[p] = mul2(g[p], pack2(v.x * fast_sigmoid(v.x), v.y * fast_sigmoid(v.y)));
                 }
-                *reinterpret_cast<float4 *>(gg + i) = make_float4(g.x, g.x, g.y, g.y);
-                *reinterpret_cast<float4 *>(gg + i + 2) = make_float4(g.z, g.z, g.w, g.w);
             }
+            *reinterpret_cast<ulonglong2 *>(gs + r * Sh::YP + c) = make_ulonglong2(g[0], g[1]);
         }
-        Bf = as_f32(raw_bc(b, 0), wideB, R * NP, tid);
-        if (grads) Cf = as_f32(raw_bc(b, 1), wideC, R * NP, tid);
     }
 };
 
 // (1) The summaries of chunk g: for the sequence that goes on behind the chunk its end state from
 // zero, for the sequence that began before it what its rows send back. Usually one and the same.
 template <typename Tin, int NL>
-__global__ void __launch_bounds__(kScanThreads) scan_back_summary_kernel(const __grid_constant__ ScanLaunch P)
+__global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(const __grid_constant__ ScanLaunch P)
 {
-    using Sh = ScanShape<NL, 2>;
-    constexpr int CPT = 2, R = kBackTile, NP = Sh::NP, CB = Sh::CB;
+    using Sh = ScanShape<NL, 4>;
+    using Sm = BackSmem<Tin, Sh>;
+    constexpr int R = kBackTile, NP = Sh::NP, CB = Sh::CB;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[kScanWarps];
     ordinary_launch_start();
@@ -119,10 +105,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_summary_kernel(const _
     const int nl = lane % NL, cl = lane / NL;
     const int ct = (int)(blockIdx.x % (unsigned)P.nct), g = (int)(blockIdx.x / (unsigned)P.nct);
     const int D = P.a.D, N = P.a.N, c0 = ct * CB;
-    const int n0 = 4 * nl, wc = warp * Sh::CW + cl;
+    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * 4, d0 = c0 + wc;
     const int64_t dn = (int64_t)D * N;
     const bool vst = (P.vec & kVecState) != 0;
-    const int row0 = g * P.C, row1 = min(P.a.T, row0 + P.C);
+    const int row0 = g * P.C, row1 = (int)min((int64_t)P.a.T, (int64_t)row0 + P.C);
 
     const int sh = find_seq(P, row0, scratch, tid), st = find_seq(P, row1 - 1, scratch, tid);
     const bool before = sh >= 0 && sh < P.a.S && seq_bound(P, sh) < row0;
@@ -133,20 +119,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_summary_kernel(const _
         P.info[g] = make_int4(behind ? st : -1, behind && seq_bound(P, st) >= row0, before ? sh : -1,
                               before && seq_bound(P, sh + 1) <= row1);
 
-    f2 A2[CPT][2], h[CPT][2], prod[CPT][2], e[CPT][2];
-    float dt_head[CPT], dt_tail[CPT];
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        load_rates(P.a.A, c0 + wc + c * Sh::CLN, D, n0, N, vst, A2[c]);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            h[c][p] = e[c][p] = 0ull;
-            prod[c][p] = pack2(1.f, 1.f);
-        }
-        dt_head[c] = dt_tail[c] = 0.f;
-    }
-
     BackTile<Tin, Sh> T(P, smem, tid, c0);
+    float *gs = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * R * Sh::YP;
     // rows row0 .. head_end - 1 (head) and tail_begin .. row1 - 1 (tail); tiles do not cross either border
     auto clip = [&](int pos) {
         int end = min(row1, pos + R);
@@ -158,6 +132,16 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_summary_kernel(const _
     int pos = first_at(row0), b = 0;
     if (pos < row1) T.stage(0, pos, clip(pos), true);
     cp_async_commit();
+
+    f2 A2[4][2], h[4][2], prod[4][2], e[4][2], dt_head[2] = {}, dt_tail[2] = {};
+    load_rates(P.a.A, d0, D, n0, N, vst, A2);
+    zero_entries(h);
+    zero_entries(e);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) prod[n][p] = pack2(1.f, 1.f);
+
     while (pos < row1) {
         const bool head = pos < head_end, tail = pos >= tail_begin;
         const int next = first_at(pos + clip(pos));
@@ -165,62 +149,70 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_summary_kernel(const _
         __syncthreads();
         if (next < row1) T.stage(b ^ 1, next, clip(next), true);
         cp_async_commit();
-        T.widen(b, true);
-        __syncthreads();
-        float dts[CPT] = {};
-#pragma unroll
+        T.gate(b, gs, lane, warp);
+        __syncwarp();
+        const Tin *xs = T.raw(b, 0), *ds = T.raw(b, 1), *Bs = T.raw_bc(b, 0), *Cs = T.raw_bc(b, 1);
+        f2 dts[2] = {};
+#pragma unroll 2
         for (int t = 0; t < R; ++t) {
-            const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(T.Bf + t * NP + n0);
-            const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(T.Cf + t * NP + n0);
+            f2 dt[2], u[2], gv[2], B[4], C[4];
+            load_pairs(ds + t * CB + wc, dt);
+            load_pairs(xs + t * CB + wc, u);
+            load_pairs(gs + t * Sh::YP + cl * 4, gv);
+            load_twice(Bs + t * NP + n0, B);
+            load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-                const int ch = t * CB + wc + c * Sh::CLN;
-                const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(T.q + ch);
-                const f2 g2 = T.gg[ch];
-                const f2 a0 = decay2(du.x, A2[c][0]), a1 = decay2(du.x, A2[c][1]);
-                dts[c] += unpack2(du.x).x;
-                if (tail) {
-                    h[c][0] = fma2(a0, h[c][0], mul2(du.y, B.x));
-                    h[c][1] = fma2(a1, h[c][1], mul2(du.y, B.y));
-                }
-                if (head) {
-                    prod[c][0] = mul2(prod[c][0], a0);
-                    prod[c][1] = mul2(prod[c][1], a1);
-                    e[c][0] = fma2(prod[c][0], mul2(C.x, g2), e[c][0]);
-                    e[c][1] = fma2(prod[c][1], mul2(C.y, g2), e[c][1]);
+            for (int p = 0; p < 2; ++p) {
+                dts[p] = add2(dts[p], dt[p]);
+                u[p] = mul2(u[p], dt[p]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const f2 a = decay2(dt[p], A2[n][p]);
+                    h[n][p] = fma2(a, h[n][p], mul2(u[p], B[n]));
+                    prod[n][p] = mul2(prod[n][p], a);
+                    e[n][p] = fma2(prod[n][p], mul2(C[n], gv[p]), e[n][p]);
                 }
             }
         }
+        if (!tail) zero_entries(h);          // the sequence that goes on behind the chunk has not begun
 #pragma unroll
-        for (int c = 0; c < CPT; ++c) {
-            if (head) dt_head[c] += dts[c];
-            if (tail) dt_tail[c] += dts[c];
+        for (int p = 0; p < 2; ++p) {
+            if (head) dt_head[p] = add2(dt_head[p], dts[p]);
+            if (tail) dt_tail[p] = add2(dt_tail[p], dts[p]);
         }
+        if (head && next >= head_end && before) store_entries(P.ein + g * dn, d0, D, n0, N, vst, e);
+        __syncwarp();
         pos = next;
         b ^= 1;
     }
+    if (behind) store_entries(P.hin + g * dn, d0, D, n0, N, vst, h);
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        const int d = c0 + wc + c * Sh::CLN;
-        if (behind) store_entries(P.hin + g * dn, d, D, n0, N, vst, h[c]);
-        if (before) store_entries(P.ein + g * dn, d, D, n0, N, vst, e[c]);
+    for (int p = 0; p < 2; ++p) {
+        const float2 ht = unpack2(dt_head[p]), tt = unpack2(dt_tail[p]);
+        const int d = d0 + 2 * p;
+        const int64_t o = (int64_t)g * D + d;
         if (nl == 0 && d < D) {
-            P.sumdt[(int64_t)g * D + d] = dt_tail[c];
-            P.sumdt_head[(int64_t)g * D + d] = dt_head[c];
+            P.sumdt[o] = tt.x;
+            P.sumdt_head[o] = ht.x;
+        }
+        if (nl == 0 && d + 1 < D) {
+            P.sumdt[o + 1] = tt.y;
+            P.sumdt_head[o + 1] = ht.y;
         }
     }
 }
 
 // (3) The gradients. A CTA owns a channel tile and walks the chunks w, w + W, ..., so that dA and dD
 // stay in registers. In a chunk it takes each sequence's rows forward once, keeping the state before
-// every tile in shared memory, then tile by tile backwards: the tile's states and decays again, now
-// kept in registers, and the recurrence of dh through them.
+// every tile in shared memory, then tile by tile backwards: the tile's states again, now kept in
+// registers, and the recurrence of dh through them (the decays a third time: one instruction pair
+// each, where keeping them would take another 128 registers).
 template <typename Tin, int NL>
-__global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_constant__ ScanLaunch P)
+__global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid_constant__ ScanLaunch P)
 {
-    using Sh = ScanShape<NL, 2>;
+    using Sh = ScanShape<NL, 4>;
     using Sm = BackSmem<Tin, Sh>;
-    constexpr int CPT = 2, R = kBackTile, NP = Sh::NP, CB = Sh::CB, CLN = Sh::CLN, YP = Sh::YP;
+    constexpr int R = kBackTile, NP = Sh::NP, CB = Sh::CB, CLN = Sh::CLN, YP = Sh::YP;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[kScanWarps];
     ordinary_launch_start();
@@ -229,23 +221,26 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_co
     const int nl = lane % NL, cl = lane / NL;
     const int ct = (int)(blockIdx.x % (unsigned)P.nct), w = (int)(blockIdx.x / (unsigned)P.nct);
     const int D = P.a.D, N = P.a.N, c0 = ct * CB;
-    const int n0 = 4 * nl, wc = warp * Sh::CW + cl;
+    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * 4, d0 = c0 + wc;
     const int64_t dn = (int64_t)D * N;
     const bool vst = (P.vec & kVecState) != 0;
 
     BackTile<Tin, Sh> T(P, smem, tid, c0);
-    float *sum_y = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::Q + Sm::GG + 2 * Sm::WIDE);
-    float *sum_u = sum_y + R * YP, *sum_w = sum_u + R * YP, *part = sum_w + R * YP;
+    // per warp [R][YP]: g, and sums over n of C h, B dh and A w
+    float *gs = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * R * YP;
+    float *sum_y = gs + Sm::SUMS / 4, *sum_u = sum_y + Sm::SUMS / 4, *sum_w = sum_u + Sm::SUMS / 4;
+    float *part = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + 4 * Sm::SUMS);
     ulonglong2 *states = reinterpret_cast<ulonglong2 *>(smem + Sm::MAIN - Sm::STATES);
 
-    f2 A2[CPT][2], dA[CPT][2];
+    f2 A2[4][2], dA[4][2];
+    zero_entries(A2);
+    zero_entries(dA);
+    if (P.a.T > 0) load_rates(P.a.A, d0, D, n0, N, vst, A2);
+    // a lane finishes four channels of every row it is given: the same ones in every tile
+    const int oc = warp * Sh::CW + lane % CLN * 4, orow = lane / CLN;
+    float skip[4], dD[4] = {};
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        A2[c][0] = A2[c][1] = dA[c][0] = dA[c][1] = 0ull;
-        if (P.a.T > 0) load_rates(P.a.A, c0 + wc + c * CLN, D, n0, N, vst, A2[c]);
-    }
-    float4 dD = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int ec = tid * 4 % CB;            // the four channels this thread finishes in every tile
+    for (int c = 0; c < 4; ++c) skip[c] = P.a.Dskip && oc + c < T.ncols ? P.a.Dskip[c0 + oc + c] : 0.f;
 
     // a gradient of the final state goes straight through an empty sequence
     if (P.g.dh0 && (P.a.cu_seqlens || P.L == 0)) {
@@ -269,7 +264,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_co
         int end = row1;
         int s = find_seq(P, row1 - 1, scratch, tid);
         while (end > row0) {
-            // the rows ra .. end - 1 of one sequence (or of none)
+            // the rows ra .. rb - 1 of one sequence (or of none)
             bool live = s >= 0 && s < P.a.S;
             const int first = live ? seq_bound(P, s) : s < 0 ? row0 : min(seq_bound(P, P.a.S), end - 1);
             const int ra = max(row0, min(first, end - 1));
@@ -285,18 +280,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_co
             s = s >= P.a.S ? P.a.S - 1 : s - 1;
             while (s >= 0 && seq_bound(P, s) >= end) --s;
 
-            f2 h[CPT][2], e[CPT][2];
-            {
-                const float *hf = starts ? (P.a.h0 && live ? P.a.h0 + slot * dn : nullptr) : P.hin ? P.hin + g * dn : nullptr;
-                const float *ef = ends ? (P.g.dh_last && live ? P.g.dh_last + slot * dn : nullptr) : P.ein ? P.ein + g * dn : nullptr;
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    h[c][0] = h[c][1] = e[c][0] = e[c][1] = 0ull;
-                    if (live && hf) load_entries(hf, c0 + wc + c * CLN, D, n0, N, vst, h[c]);
-                    if (live && ef) load_entries(ef, c0 + wc + c * CLN, D, n0, N, vst, e[c]);
-                }
-            }
-
             // jobs 0 .. nt - 2: tiles 0 .. nt - 2 forward; jobs nt - 1 .. 2 nt - 2: tiles nt - 1 .. 0 backward
             auto tile_of = [&](int j) { return j < nt - 1 ? j : 2 * nt - 2 - j; };
             auto stage_job = [&](int j, int buf) {
@@ -307,6 +290,17 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_co
             __syncthreads();                 // the buffers of the rows before are free
             stage_job(first_job, 0);
             cp_async_commit();
+
+            f2 h[4][2], e[4][2];
+            zero_entries(h);
+            zero_entries(e);
+            if (live) {
+                const float *hf = starts ? (P.a.h0 ? P.a.h0 + slot * dn : nullptr) : P.hin ? P.hin + g * dn : nullptr;
+                const float *ef = ends ? (P.g.dh_last ? P.g.dh_last + slot * dn : nullptr) : P.ein ? P.ein + g * dn : nullptr;
+                if (hf) load_entries(hf, d0, D, n0, N, vst, h);
+                if (ef) load_entries(ef, d0, D, n0, N, vst, e);
+            }
+
             int b = 0;
             for (int j = first_job; j < 2 * nt - 1; ++j, b ^= 1) {
                 const bool back = j >= nt - 1;
@@ -315,167 +309,169 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_co
                 __syncthreads();
                 if (j + 1 < 2 * nt - 1) stage_job(j + 1, b ^ 1);
                 cp_async_commit();
-                T.widen(b, back);
-                __syncthreads();
+                const Tin *xs = T.raw(b, 0), *ds = T.raw(b, 1), *zs = T.raw(b, 2), *dys = T.raw(b, 3);
+                const Tin *Bs = T.raw_bc(b, 0), *Cs = T.raw_bc(b, 1);
 
-                if (!back || tile == nt - 1) {
-#pragma unroll
-                    for (int c = 0; c < CPT; ++c)
-                        states[(tile * CPT + c) * kScanThreads + tid] = make_ulonglong2(h[c][0], h[c][1]);
-                }
                 if (!back) {
 #pragma unroll
+                    for (int q = 0; q < 4; ++q) states[(tile * 4 + q) * kScanThreads + tid] = make_ulonglong2(h[q][0], h[q][1]);
+#pragma unroll 2
                     for (int t = 0; t < R; ++t) {
-                        const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(T.Bf + t * NP + n0);
+                        f2 dt[2], u[2], B[4];
+                        load_pairs(ds + t * CB + wc, dt);
+                        load_pairs(xs + t * CB + wc, u);
+                        load_twice(Bs + t * NP + n0, B);
 #pragma unroll
-                        for (int c = 0; c < CPT; ++c) {
-                            const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(T.q + t * CB + wc + c * CLN);
-                            h[c][0] = fma2(decay2(du.x, A2[c][0]), h[c][0], mul2(du.y, B.x));
-                            h[c][1] = fma2(decay2(du.x, A2[c][1]), h[c][1], mul2(du.y, B.y));
+                        for (int p = 0; p < 2; ++p) {
+                            u[p] = mul2(u[p], dt[p]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) h[k][p] = fma2(decay2(dt[p], A2[k][p]), h[k][p], mul2(u[p], B[k]));
                         }
                     }
                     continue;
                 }
 
-                // the tile's states (before each row) and decays
-                f2 hp[R + 1][CPT][2], a[R][CPT][2];
+                T.gate(b, gs, lane, warp);
+                // the tile's states, hp[t] before row t
+                f2 hp[R + 1][4][2];
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const ulonglong2 v = states[(tile * CPT + c) * kScanThreads + tid];
-                    hp[0][c][0] = v.x;
-                    hp[0][c][1] = v.y;
+                for (int q = 0; q < 4; ++q) {
+                    if (tile == nt - 1 || !live) {
+                        hp[0][q][0] = h[q][0];
+                        hp[0][q][1] = h[q][1];
+                    } else {
+                        const ulonglong2 v = states[(tile * 4 + q) * kScanThreads + tid];
+                        hp[0][q][0] = v.x;
+                        hp[0][q][1] = v.y;
+                    }
                 }
 #pragma unroll
                 for (int t4 = 0; t4 < R; t4 += 4) {
-                    float acc[4 * CPT];
+                    float acc[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int t = t4 + k;
-                        const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(T.Bf + t * NP + n0);
-                        const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(T.Cf + t * NP + n0);
+                        f2 dt[2], u[2], B[4], C[4], y[2];
+                        load_pairs(ds + t * CB + wc, dt);
+                        load_pairs(xs + t * CB + wc, u);
+                        load_twice(Bs + t * NP + n0, B);
+                        load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-                        for (int c = 0; c < CPT; ++c) {
-                            const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(T.q + t * CB + wc + c * CLN);
-                            a[t][c][0] = decay2(du.x, A2[c][0]);
-                            a[t][c][1] = decay2(du.x, A2[c][1]);
-                            hp[t + 1][c][0] = fma2(a[t][c][0], hp[t][c][0], mul2(du.y, B.x));
-                            hp[t + 1][c][1] = fma2(a[t][c][1], hp[t][c][1], mul2(du.y, B.y));
-                            const float2 y = unpack2(fma2(C.y, hp[t + 1][c][1], mul2(C.x, hp[t + 1][c][0])));
-                            acc[k * CPT + c] = y.x + y.y;
+                        for (int p = 0; p < 2; ++p) {
+                            u[p] = mul2(u[p], dt[p]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                hp[t + 1][q][p] = fma2(decay2(dt[p], A2[q][p]), hp[t][q][p], mul2(u[p], B[q]));
+                                y[p] = q == 0 ? mul2(C[q], hp[t + 1][q][p]) : fma2(C[q], hp[t + 1][q][p], y[p]);
+                            }
+                            const float2 v = unpack2(y[p]);
+                            acc[k * 4 + 2 * p] = v.x;
+                            acc[k * 4 + 2 * p + 1] = v.y;
                         }
                     }
                     if (P.g.dz) {
-                        constexpr int M = 4 * CPT;
-                        group_reduce<M, NL>(acc, nl);
-                        constexpr int KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
+                        constexpr int KEEP = 16 >= NL ? 16 / NL : 1, REP = 16 >= NL ? 1 : NL / 16;
+                        group_reduce<16, NL>(acc, nl);
                         if (nl % REP == 0) {
 #pragma unroll
                             for (int i = 0; i < KEEP; ++i) {
                                 const int v = nl / REP * KEEP + i;
-                                sum_y[(t4 + v / CPT) * YP + wc + (v % CPT) * CLN] = acc[i];
+                                sum_y[(t4 + v / 4) * YP + cl * 4 + v % 4] = acc[i];
                             }
                         }
                     }
                 }
+                __syncwarp();
                 // backwards
 #pragma unroll
                 for (int t = R - 1; t >= 0; --t) {
-                    const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(T.Bf + t * NP + n0);
-                    const ulonglong2 C = *reinterpret_cast<const ulonglong2 *>(T.Cf + t * NP + n0);
-                    f2 db[2], dc[2];
-                    float uw[2 * CPT];
+                    f2 dt[2], u[2], gv[2], B[4], C[4], db[4], dc[4], us[2], ws[2];
+                    load_pairs(ds + t * CB + wc, dt);
+                    load_pairs(xs + t * CB + wc, u);
+                    load_pairs(gs + t * YP + cl * 4, gv);
+                    load_twice(Bs + t * NP + n0, B);
+                    load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-                    for (int c = 0; c < CPT; ++c) {
-                        const int ch = t * CB + wc + c * CLN;
-                        const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(T.q + ch);
-                        const f2 g2 = T.gg[ch];
-                        f2 us, ws;
+                    for (int p = 0; p < 2; ++p) {
+                        u[p] = mul2(u[p], dt[p]);
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const f2 Bp = p ? B.y : B.x, Cp = p ? C.y : C.x;
-                            const f2 dh = fma2(Cp, g2, e[c][p]);
-                            dc[p] = c == 0 ? mul2(g2, hp[t + 1][c][p]) : fma2(g2, hp[t + 1][c][p], dc[p]);
-                            db[p] = c == 0 ? mul2(du.y, dh) : fma2(du.y, dh, db[p]);
-                            us = p == 0 ? mul2(Bp, dh) : fma2(Bp, dh, us);
-                            e[c][p] = mul2(a[t][c][p], dh);
-                            const f2 wv = mul2(e[c][p], hp[t][c][p]);
-                            ws = p == 0 ? mul2(wv, A2[c][p]) : fma2(wv, A2[c][p], ws);
-                            dA[c][p] = fma2(wv, du.x, dA[c][p]);
+                        for (int q = 0; q < 4; ++q) {
+                            const f2 dh = fma2(C[q], gv[p], e[q][p]);
+                            dc[q] = p == 0 ? mul2(gv[p], hp[t + 1][q][p]) : fma2(gv[p], hp[t + 1][q][p], dc[q]);
+                            db[q] = p == 0 ? mul2(u[p], dh) : fma2(u[p], dh, db[q]);
+                            us[p] = q == 0 ? mul2(B[q], dh) : fma2(B[q], dh, us[p]);
+                            e[q][p] = mul2(decay2(dt[p], A2[q][p]), dh);
+                            const f2 wv = mul2(e[q][p], hp[t][q][p]);
+                            ws[p] = q == 0 ? mul2(wv, A2[q][p]) : fma2(wv, A2[q][p], ws[p]);
+                            dA[q][p] = fma2(wv, dt[p], dA[q][p]);
                         }
-                        const float2 u = unpack2(us), wsum = unpack2(ws);
-                        uw[c] = u.x + u.y;
-                        uw[CPT + c] = wsum.x + wsum.y;
                     }
                     {
-                        constexpr int M = 2 * CPT;
-                        group_reduce<M, NL>(uw, nl);
-                        constexpr int KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
+                        const float2 u0 = unpack2(us[0]), u1 = unpack2(us[1]), w0 = unpack2(ws[0]), w1 = unpack2(ws[1]);
+                        float v[8] = {u0.x, u0.y, u1.x, u1.y, w0.x, w0.y, w1.x, w1.y};
+                        constexpr int KEEP = 8 >= NL ? 8 / NL : 1, REP = 8 >= NL ? 1 : NL / 8;
+                        group_reduce<8, NL>(v, nl);
                         if (nl % REP == 0) {
 #pragma unroll
                             for (int i = 0; i < KEEP; ++i) {
-                                const int v = nl / REP * KEEP + i;
-                                (v < CPT ? sum_u : sum_w)[t * YP + wc + (v % CPT) * CLN] = uw[i];
+                                const int k = nl / REP * KEEP + i;      // 0 .. 3: sum of B dh, 4 .. 7: of A w
+                                (k < 4 ? sum_u : sum_w)[t * YP + cl * 4 + k % 4] = v[i];
                             }
                         }
                     }
                     {
-                        const float2 b0 = unpack2(db[0]), b1 = unpack2(db[1]), k0 = unpack2(dc[0]), k1 = unpack2(dc[1]);
-                        float bc[8] = {b0.x, b0.y, b1.x, b1.y, k0.x, k0.y, k1.x, k1.y};
-                        group_reduce<8, CLN>(bc, cl, NL);
+                        float v[8];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 x2 = unpack2(db[q]), y2 = unpack2(dc[q]);
+                            v[q] = x2.x + x2.y;
+                            v[4 + q] = y2.x + y2.y;
+                        }
                         constexpr int KEEP = 8 >= CLN ? 8 / CLN : 1, REP = 8 >= CLN ? 1 : CLN / 8;
+                        group_reduce<8, CLN>(v, cl, NL);
                         if (cl % REP == 0) {
 #pragma unroll
                             for (int i = 0; i < KEEP; ++i) {
-                                const int v = cl / REP * KEEP + i;      // 0 .. 3: dB, 4 .. 7: dC
-                                part[((warp * R + t) * 2 + v / 4) * NP + n0 + v % 4] = bc[i];
+                                const int k = cl / REP * KEEP + i;      // 0 .. 3: dB, 4 .. 7: dC
+                                part[((warp * R + t) * 2 + k / 4) * NP + n0 + k % 4] = v[i];
                             }
                         }
                     }
                 }
                 __syncthreads();
 
-                // per-channel gradients of the tile's rows
-                for (int i = tid * 4; i < n * CB; i += kScanThreads * 4) {
-                    const int r = i / CB;
-                    if (ec >= T.ncols) break;
-                    const float4 x4 = load4(T.raw(b, 0) + i), d4 = load4(T.raw(b, 1) + i), dy4 = load4(T.raw(b, 3) + i);
-                    const float4 u4 = *reinterpret_cast<const float4 *>(sum_u + r * YP + ec);
-                    const float4 w4 = *reinterpret_cast<const float4 *>(sum_w + r * YP + ec);
-                    const float xv[4] = {x4.x, x4.y, x4.z, x4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w},
-                                yv[4] = {dy4.x, dy4.y, dy4.z, dy4.w}, uv[4] = {u4.x, u4.y, u4.z, u4.w},
-                                wv[4] = {w4.x, w4.y, w4.z, w4.w};
-                    float zv[4] = {}, pre[4] = {}, dskip[4] = {}, gx[4], gt[4], gz[4] = {}, gd[4];
-                    if (P.a.z) {
-                        const float4 z4 = load4(T.raw(b, 2) + i);
-                        zv[0] = z4.x; zv[1] = z4.y; zv[2] = z4.z; zv[3] = z4.w;
-                        if (P.g.dz) {
-                            const float4 s4 = *reinterpret_cast<const float4 *>(sum_y + r * YP + ec);
-                            pre[0] = s4.x; pre[1] = s4.y; pre[2] = s4.z; pre[3] = s4.w;
-                        }
+                // this warp's per-channel gradients of the tile's rows
+#pragma unroll
+                for (int r0 = 0; r0 < R; r0 += NL) {
+                    const int r = r0 + orow;
+                    if (r >= n || oc >= T.ncols) continue;
+                    const int sc = r * YP + lane % CLN * 4;
+                    float gx[4], gt[4], gz[4] = {};
+                    f2 x2[2], d2[2], y2[2], z2[2];
+                    load_pairs(xs + r * CB + oc, x2);
+                    load_pairs(ds + r * CB + oc, d2);
+                    if (P.g.dz) {
+                        load_pairs(dys + r * CB + oc, y2);
+                        load_pairs(zs + r * CB + oc, z2);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (P.a.Dskip && ec + k < T.ncols) dskip[k] = P.a.Dskip[c0 + ec + k];
-                        float gk = yv[k];
-                        if (P.a.z) {
-                            const float sg = fast_sigmoid(zv[k]);
-                            gk = yv[k] * (zv[k] * sg);
-                            gz[k] = yv[k] * fmaf(dskip[k], xv[k], pre[k]) * (sg * fmaf(zv[k], 1.f - sg, 1.f));
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 xp = unpack2(x2[c / 2]), dp = unpack2(d2[c / 2]);
+                        const float x = c & 1 ? xp.y : xp.x, dtv = c & 1 ? dp.y : dp.x, gk = gs[sc + c], u = sum_u[sc + c];
+                        gx[c] = fmaf(u, dtv, skip[c] * gk);
+                        gt[c] = fmaf(u, x, kLn2 * sum_w[sc + c]);      // A2 = A log2(e)
+                        dD[c] = fmaf(gk, x, dD[c]);
+                        if (P.g.dz) {
+                            const float2 yp = unpack2(y2[c / 2]), zp = unpack2(z2[c / 2]);
+                            const float dy = c & 1 ? yp.y : yp.x, z = c & 1 ? zp.y : zp.x, sg = fast_sigmoid(z);
+                            gz[c] = dy * fmaf(skip[c], x, sum_y[sc + c]) * (sg * fmaf(z, 1.f - sg, 1.f));
                         }
-                        gx[k] = fmaf(uv[k], dv[k], dskip[k] * gk);
-                        gt[k] = fmaf(uv[k], xv[k], kLn2 * wv[k]);      // A2 = A log2(e)
-                        gd[k] = gk * xv[k];
-                        if (!live) gx[k] = gt[k] = gz[k] = gd[k] = 0.f;
                     }
-                    dD.x += gd[0]; dD.y += gd[1]; dD.z += gd[2]; dD.w += gd[3];
                     const int64_t row = t0 + r;
-                    const int left = T.ncols - ec, col = c0 + ec;
-                    if (P.g.dx)
-                        store_row4(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, make_float4(gx[0], gx[1], gx[2], gx[3]), left, P.vec & kVecDx);
-                    if (P.g.ddt)
-                        store_row4(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, make_float4(gt[0], gt[1], gt[2], gt[3]), left, P.vec & kVecDdt);
-                    if (P.g.dz)
-                        store_row4(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, make_float4(gz[0], gz[1], gz[2], gz[3]), left, P.vec & kVecDz);
+                    const int left = T.ncols - oc, col = c0 + oc;
+                    if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, P.vec & kVecDx);
+                    if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, P.vec & kVecDdt);
+                    if (P.g.dz) store_row(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, gz, left, P.vec & kVecDz);
                 }
                 // this channel tile's share of dB and dC: the warps' sums in order
                 for (int i = tid; i < n * 2 * NP; i += kScanThreads) {
@@ -484,30 +480,23 @@ __global__ void __launch_bounds__(kScanThreads) scan_back_kernel(const __grid_co
                     float v = 0.f;
 #pragma unroll
                     for (int q = 0; q < kScanWarps; ++q) v += part[((q * R + r) * 2 + k) * NP + nn];
-                    P.part_bc[((int64_t)ct * P.a.T + t0 + r) * 2 * N + k * N + nn] = live ? v : 0.f;
+                    P.part_bc[((int64_t)ct * P.a.T + t0 + r) * 2 * N + k * N + nn] = v;
                 }
             }
-            if (starts && live && P.g.dh0) {
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) store_entries(P.g.dh0 + slot * dn, c0 + wc + c * CLN, D, n0, N, vst, e[c]);
-            }
+            if (starts && live && P.g.dh0) store_entries(P.g.dh0 + slot * dn, d0, D, n0, N, vst, e);
         }
     }
 
+    store_entries(P.part_a + w * dn, d0, D, n0, N, vst, dA);
+    // dD: the lanes that share four channels
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) store_entries(P.part_a + w * dn, c0 + wc + c * CLN, D, n0, N, vst, dA[c]);
-    // dD: the threads that share four channels
-    __syncthreads();
-    reinterpret_cast<float4 *>(smem)[tid] = dD;
-    __syncthreads();
-    if (tid * 4 < CB) {
-        float v[4] = {};
-        for (int k = tid; k < kScanThreads; k += CB / 4) {
-            const float4 o = reinterpret_cast<const float4 *>(smem)[k];
-            v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
-        }
-        for (int k = 0; k < 4; ++k)
-            if (ec + k < T.ncols) P.part_d[(int64_t)w * D + c0 + ec + k] = v[k];
+    for (int off = CLN; off < 32; off <<= 1)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dD[c] += __shfl_xor_sync(kScanFull, dD[c], off);
+    if (orow == 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (oc + c < T.ncols) P.part_d[(int64_t)w * D + c0 + oc + c] = dD[c];
     }
 }
 
@@ -553,7 +542,7 @@ template <typename Kern> static cudaError_t launch_sized(Kern kern, int64_t ctas
 
 template <typename Tin, int NL> static int launch_shape(const ScanLaunch &P, cudaStream_t stream)
 {
-    using Sm = BackSmem<Tin, ScanShape<NL, 2>>;
+    using Sm = BackSmem<Tin, ScanShape<NL, 4>>;
     if (P.hin) {
         if (launch_sized(scan_back_summary_kernel<Tin, NL>, (int64_t)P.G * P.nct, Sm::SUMMARY, P, stream) != cudaSuccess)
             return GDN_ERR_LAUNCH;
@@ -568,7 +557,7 @@ template <typename Tin, int NL> static int launch_shape(const ScanLaunch &P, cud
 
 template <typename Tin> static int launch_typed(const ScanLaunch &P, cudaStream_t stream)
 {
-    switch (scan_shape_backward(P.a.N).NL) {
+    switch (scan_shape(P.a.N).NL) {
     case 2: return launch_shape<Tin, 2>(P, stream);
     case 4: return launch_shape<Tin, 4>(P, stream);
     case 8: return launch_shape<Tin, 8>(P, stream);

@@ -4,14 +4,16 @@
 
 namespace gdn {
 
+constexpr int kCarryThreads = 64;      // small CTAs: the loads in flight are spread over the SMs
+
 // One thread per state entry walks the chunks in order (blockIdx.y = 0) or backwards (1). Two loads
 // per chunk do not depend on the carry, so U chunks' values are in flight at a time; the traffic is
 // 12 bytes per entry and chunk.
-__global__ void __launch_bounds__(256) scan_carry_kernel(const __grid_constant__ ScanLaunch P)
+__global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const __grid_constant__ ScanLaunch P)
 {
     ordinary_launch_start();
     const int64_t dn = (int64_t)P.a.D * P.a.N;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * kCarryThreads + threadIdx.x;
     if (i >= dn) return;
     const bool back = blockIdx.y != 0;
     const int d = (int)(i / P.a.N);
@@ -20,7 +22,7 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const __grid_constant__
     const float *sums = back ? P.sumdt_head : P.sumdt;
     const float *boundary = back ? P.g.dh_last : P.a.h0;
     float carry = 0.f;
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int k0 = 0; k0 < P.G; k0 += U) {
         float loc[U], sum[U];
         int seq[U], edge[U];
@@ -60,7 +62,8 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const __grid_constant__
 cudaError_t launch_scan_carry(const ScanLaunch &P, bool both, cudaStream_t stream)
 {
     const int64_t dn = (int64_t)P.a.D * P.a.N;
-    return launch_ordinary(scan_carry_kernel, dim3((unsigned)((dn + 255) / 256), both ? 2 : 1), dim3(256), 0, stream, P);
+    return launch_ordinary(scan_carry_kernel, dim3((unsigned)((dn + kCarryThreads - 1) / kCarryThreads), both ? 2 : 1),
+                           dim3(kCarryThreads), 0, stream, P);
 }
 
 }  // namespace gdn

@@ -28,14 +28,17 @@ constexpr int kScanTile = 16;               // token rows staged at a time
 constexpr unsigned kScanFull = 0xFFFFFFFFu;
 
 // Lanes along the state: NL lanes x 4 entries cover a row of up to 4 NL entries (missing ones are
-// zeros); the other lanes, the warps and CPT lie along the channels.
+// zeros); the other lanes and the warps lie along the channels, CPT consecutive ones a thread. What
+// bounds the kernels besides the arithmetic is shared memory's 128 bytes a clock: a thread loads CPT
+// dt and x and 4 B and C per token for its 4 CPT entries, so a square 4 x 4 tile of entries per thread
+// loads least, and the operands stay in their own type until they are in registers.
 template <int NL_, int CPT_> struct ScanShape {
-    static constexpr int NL = NL_, CPT = CPT_;
+    static constexpr int NL = NL_, CPT = CPT_, P = CPT_ / 2;   // P pairs of channels
     static constexpr int NP = 4 * NL;                     // padded state size
     static constexpr int CLN = 32 / NL;                   // channel lanes of a warp
     static constexpr int CW = CLN * CPT;                  // channels of a warp
     static constexpr int CB = CW * kScanWarps;            // channels of a CTA
-    static constexpr int YP = CB + 16;                    // row pitch of per-channel sums: rows two banks groups apart
+    static constexpr int YP = CW + 8;                     // row pitch of a warp's per-channel sums (no bank conflicts)
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -242,75 +245,122 @@ struct ScanIter {
 };
 
 // ---------------------------------------------------------------------------------------------
-// a thread's CPT x 4 entries of a [D, N] fp32 state row
+// operands in shared memory
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ void load_entries(const float *row, int d, int D, int n0, int N, bool vec, f2 (&v)[2])
+// CPT consecutive channels of a staged row as pairs
+__device__ __forceinline__ void load_pairs(const float *p, f2 (&v)[1]) { v[0] = *reinterpret_cast<const f2 *>(p); }
+__device__ __forceinline__ void load_pairs(const float *p, f2 (&v)[2])
 {
-    float e[4] = {0.f, 0.f, 0.f, 0.f};
-    if (d < D) {
-        const float *p = row + (int64_t)d * N + n0;
-        if (vec && n0 < N) {
-            const float4 q = *reinterpret_cast<const float4 *>(p);
-            e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;
-        } else {
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(p);
+    v[0] = q.x;
+    v[1] = q.y;
+}
+__device__ __forceinline__ f2 widen2(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ void load_pairs(const bf16 *p, f2 (&v)[1]) { v[0] = widen2(*reinterpret_cast<const uint32_t *>(p)); }
+__device__ __forceinline__ void load_pairs(const bf16 *p, f2 (&v)[2])
+{
+    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+    v[0] = widen2(q.x);
+    v[1] = widen2(q.y);
+}
+// four consecutive state entries of a staged B or C row, each in both halves of a pair
+template <typename T> __device__ __forceinline__ void load_twice(const T *p, f2 (&v)[4])
+{
+    const float4 q = load4(p);
+    v[0] = pack2(q.x, q.x);
+    v[1] = pack2(q.y, q.y);
+    v[2] = pack2(q.z, q.z);
+    v[3] = pack2(q.w, q.w);
+}
+
+// ---------------------------------------------------------------------------------------------
+// a thread's entries of a [D, N] fp32 state row: v[n][p] holds entry n0 + n of channels d + 2 p, d + 2 p + 1
+// ---------------------------------------------------------------------------------------------
+template <int P> __device__ __forceinline__ void load_entries(const float *row, int d, int D, int n0, int N, bool vec, f2 (&v)[4][P])
+{
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n0 + j < N) e[j] = p[j];
+    for (int p = 0; p < P; ++p) {
+        float e[2][4] = {};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (d + 2 * p + c < D) {
+                const float *q = row + (int64_t)(d + 2 * p + c) * N + n0;
+                if (vec && n0 < N) {
+                    const float4 f = *reinterpret_cast<const float4 *>(q);
+                    e[c][0] = f.x; e[c][1] = f.y; e[c][2] = f.z; e[c][3] = f.w;
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (n0 + n < N) e[c][n] = q[n];
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) v[n][p] = pack2(e[0][n], e[1][n]);
+    }
+}
+template <int P> __device__ __forceinline__ void store_entries(float *row, int d, int D, int n0, int N, bool vec, const f2 (&v)[4][P])
+{
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const float2 e[4] = {unpack2(v[0][p]), unpack2(v[1][p]), unpack2(v[2][p]), unpack2(v[3][p])};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (d + 2 * p + c < D) {
+                float *q = row + (int64_t)(d + 2 * p + c) * N + n0;
+                const float f[4] = {c ? e[0].y : e[0].x, c ? e[1].y : e[1].x, c ? e[2].y : e[2].x, c ? e[3].y : e[3].x};
+                if (vec && n0 < N) {
+                    *reinterpret_cast<float4 *>(q) = make_float4(f[0], f[1], f[2], f[3]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (n0 + n < N) q[n] = f[n];
+                }
+            }
         }
     }
-    v[0] = pack2(e[0], e[1]);
-    v[1] = pack2(e[2], e[3]);
 }
-__device__ __forceinline__ void store_entries(float *row, int d, int D, int n0, int N, bool vec, const f2 (&v)[2])
+template <int P> __device__ __forceinline__ void zero_entries(f2 (&v)[4][P])
 {
-    if (d >= D) return;
-    float *p = row + (int64_t)d * N + n0;
-    const float2 lo = unpack2(v[0]), hi = unpack2(v[1]);
-    if (vec && n0 < N) {
-        *reinterpret_cast<float4 *>(p) = make_float4(lo.x, lo.y, hi.x, hi.y);
-    } else {
-        const float e[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n0 + j < N) p[j] = e[j];
-    }
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int p = 0; p < P; ++p) v[n][p] = 0ull;
 }
 
 // A log2(e) of a thread's entries. An A of minus infinity (forget everything) becomes the lowest
 // finite value: the same decay of zero for every dt of a token, and still one for the dt of zero that
 // fills up a tile's missing rows.
 __device__ __forceinline__ float finite_rate(float a) { return a == -INFINITY ? -3.402823466e38f : a; }
-__device__ __forceinline__ void load_rates(const float *A, int d, int D, int n0, int N, bool vec, f2 (&v)[2])
+template <int P> __device__ __forceinline__ void load_rates(const float *A, int d, int D, int n0, int N, bool vec, f2 (&v)[4][P])
 {
     load_entries(A, d, D, n0, N, vec, v);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const float2 a = unpack2(v[p]);
-        v[p] = pack2(finite_rate(a.x * kLog2e), finite_rate(a.y * kLog2e));
-    }
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float2 a = unpack2(v[n][p]);
+            v[n][p] = pack2(finite_rate(a.x * kLog2e), finite_rate(a.y * kLog2e));
+        }
 }
 
-// B and C rows of a staged tile as fp32: the tile itself for fp32 inputs
-__device__ __forceinline__ const float *as_f32(const float *raw, float *, int, int) { return raw; }
-__device__ __forceinline__ const float *as_f32(const bf16 *raw, float *wide, int count, int tid)
-{
-    for (int i = tid * 4; i < count; i += kScanThreads * 4)
-        *reinterpret_cast<float4 *>(wide + i) = load4(raw + i);
-    return wide;
-}
-
-// four elements of a row-strided output, as one access where the row allows it
+// a thread's consecutive elements of a row-strided output, as one access where the row allows it
 template <typename T>
-__device__ __forceinline__ void store_row4(T *p, float4 v, int left, bool vec)
+__device__ __forceinline__ void store_row(T *p, const float (&v)[4], int left, bool vec)
 {
     if (vec && left >= 4) {
-        store4(p, v);
+        store4(p, make_float4(v[0], v[1], v[2], v[3]));
     } else {
-        const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (j < left) p[j] = from_f32<T>(e[j]);
+            if (j < left) p[j] = from_f32<T>(v[j]);
     }
+}
+template <typename T>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[2], int left, bool)
+{
+    p[0] = from_f32<T>(v[0]);
+    if (left > 1) p[1] = from_f32<T>(v[1]);
 }
 
 }  // namespace gdn

@@ -6,25 +6,25 @@
 
 namespace gdn {
 
-// Shared memory of the scan kernels, in bytes.
+// Shared memory, in bytes.
 template <typename Tin, class Sh> struct ScanSmem {
     static constexpr int RX = kScanTile * Sh::CB * (int)sizeof(Tin);     // a staged x, dt or z tile
     static constexpr int RB = kScanTile * Sh::NP * (int)sizeof(Tin);     // a staged B or C tile
     static constexpr int STAGE = 3 * RX + 2 * RB;
-    static constexpr int Q = kScanTile * Sh::CB * 16;                    // {dt, dt, dt x, dt x}
-    static constexpr int WIDE = sizeof(Tin) == 4 ? 0 : kScanTile * Sh::NP * 4;
-    static constexpr int Y = kScanTile * Sh::YP * 4;
-    static constexpr int MAIN = 2 * STAGE + Q + 2 * WIDE + Y;
+    static constexpr int Y = kScanWarps * kScanTile * Sh::YP * 4;
+    static constexpr int MAIN = 2 * STAGE + Y;
+    static constexpr int SUMMARY = 2 * STAGE;
 };
 
 // One CTA: rows g C .. of channel tile ct. SUM: the summary pass (end state from zero and sum of dt
-// of the sequence that goes on behind the chunk); else the outputs.
+// of the sequence that goes on behind the chunk); else the outputs. Tiles of 16 rows are staged one
+// ahead by asynchronous copies; a warp's channels are its own, so only the staging needs barriers.
 template <typename Tin, int NL, int CPT, bool SUM>
-__global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
+__global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
 {
     using Sh = ScanShape<NL, CPT>;
     using Sm = ScanSmem<Tin, Sh>;
-    constexpr int CB = Sh::CB, NP = Sh::NP;
+    constexpr int CB = Sh::CB, NP = Sh::NP, PP = Sh::P, CLN = Sh::CLN;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[kScanWarps];
     ordinary_launch_start();
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
     const int ct = (int)(blockIdx.x % (unsigned)P.nct), g = (int)(blockIdx.x / (unsigned)P.nct);
     const int D = P.a.D, N = P.a.N;
     const int c0 = ct * CB, ncols = min(CB, D - c0);
-    const int n0 = 4 * nl, wc = warp * Sh::CW + cl;          // this thread's channels: wc + c CLN
+    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * CPT, d0 = c0 + wc;      // this thread's first entry and channel
     const int64_t dn = (int64_t)D * N;
     const bool vst = (P.vec & kVecState) != 0;
     const int row0 = (int)min((int64_t)g * P.C, (int64_t)P.a.T), row1 = (int)min((int64_t)(g + 1) * P.C, (int64_t)P.a.T);
@@ -67,19 +67,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
     }
     use = load;
 
-    f2 A2[CPT][2], h[CPT][2];
-    float dts[CPT];
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        A2[c][0] = A2[c][1] = h[c][0] = h[c][1] = 0ull;
-        if (row0 < row1) load_rates(P.a.A, c0 + wc + c * Sh::CLN, D, n0, N, vst, A2[c]);
-        dts[c] = 0.f;
-    }
-
-    float4 *q = reinterpret_cast<float4 *>(smem + 2 * Sm::STAGE);
-    float *wideB = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::Q), *wideC = wideB + Sm::WIDE / 4;
-    float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::Q + 2 * Sm::WIDE);
-
     auto stage_tile = [&](const ScanTile &t, int b) {
         Tin *xs = reinterpret_cast<Tin *>(smem + b * Sm::STAGE);
         Tin *ds = xs + kScanTile * CB, *zs = ds + kScanTile * CB;
@@ -94,10 +81,23 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
             stage_rows<Tin, NP>(Cs, static_cast<const Tin *>(P.a.Cm) + r * P.a.C_stride, P.a.C_stride, t.n, N, P.vec & kVecC, tid);
         }
     };
-
     ScanTile tl, nxt;
     if (load.next(P, nxt)) stage_tile(nxt, 0);
     cp_async_commit();
+
+    f2 A2[4][PP], h[4][PP], dts[PP];
+    zero_entries(A2);
+    zero_entries(h);
+    if (row0 < row1) load_rates(P.a.A, d0, D, n0, N, vst, A2);
+#pragma unroll
+    for (int p = 0; p < PP; ++p) dts[p] = 0ull;
+    // a lane finishes CPT channels of every row it is given: the same ones in every tile
+    const int oc = warp * Sh::CW + lane % CLN * CPT, orow = lane / CLN;
+    float skip[CPT];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) skip[c] = !SUM && P.a.Dskip && oc + c < ncols ? P.a.Dskip[c0 + oc + c] : 0.f;
+    float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * kScanTile * Sh::YP;
+
     int b = 0;
     while (use.next(P, tl)) {
         cp_async_wait<0>();
@@ -108,19 +108,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
         const Tin *xs = reinterpret_cast<const Tin *>(smem + b * Sm::STAGE);
         const Tin *ds = xs + kScanTile * CB, *zs = ds + kScanTile * CB;
         const Tin *Bs = zs + kScanTile * CB, *Cs = Bs + kScanTile * NP;
-#pragma unroll
-        for (int i = tid * 4; i < kScanTile * CB; i += kScanThreads * 4) {
-            const float4 x4 = load4(xs + i), d4 = load4(ds + i);
-            const float u0 = d4.x * x4.x, u1 = d4.y * x4.y, u2 = d4.z * x4.z, u3 = d4.w * x4.w;
-            q[i] = make_float4(d4.x, d4.x, u0, u0);
-            q[i + 1] = make_float4(d4.y, d4.y, u1, u1);
-            q[i + 2] = make_float4(d4.z, d4.z, u2, u2);
-            q[i + 3] = make_float4(d4.w, d4.w, u3, u3);
-        }
-        const float *Bf = as_f32(Bs, wideB, kScanTile * NP, tid);
-        const float *Cf = SUM ? nullptr : as_f32(Cs, wideC, kScanTile * NP, tid);
-        __syncthreads();
-
         if (tl.fresh) {
             const float *from = nullptr;
             if (!SUM && tl.seq >= 0)
@@ -129,16 +116,11 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
                 from = !tl.starts ? (P.hin ? P.hin + g * dn : nullptr)
                        : !P.a.h0  ? nullptr
                        : P.hin && g < P.G - 1 && P.info[g].x == tl.seq ? P.init + g * dn : P.a.h0 + tl.slot * dn;
-#pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-                h[c][0] = h[c][1] = 0ull;
-                if (from) load_entries(from, c0 + wc + c * Sh::CLN, D, n0, N, vst, h[c]);
-            }
+            zero_entries(h);
+            if (from) load_entries(from, d0, D, n0, N, vst, h);
         }
 
-        float dt_tile[CPT];
-#pragma unroll
-        for (int c = 0; c < CPT; ++c) dt_tile[c] = 0.f;
+        f2 dt_tile[PP] = {};
         // rows behind the tile's last are zeros: dt = 0 leaves h as it is
 #pragma unroll 1
         for (int t4 = 0; t4 < kScanTile; t4 += 4) {
@@ -146,84 +128,89 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int t = t4 + k;
-                const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(Bf + t * NP + n0);
-                ulonglong2 C = make_ulonglong2(0, 0);
-                if (!SUM) C = *reinterpret_cast<const ulonglong2 *>(Cf + t * NP + n0);
+                f2 dt[PP], u[PP], B[4], C[4], y[PP];
+                load_pairs(ds + t * CB + wc, dt);
+                load_pairs(xs + t * CB + wc, u);
+                load_twice(Bs + t * NP + n0, B);
+                if (!SUM) load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const ulonglong2 du = *reinterpret_cast<const ulonglong2 *>(q + t * CB + wc + c * Sh::CLN);
-                    h[c][0] = fma2(decay2(du.x, A2[c][0]), h[c][0], mul2(du.y, B.x));
-                    h[c][1] = fma2(decay2(du.x, A2[c][1]), h[c][1], mul2(du.y, B.y));
+                for (int p = 0; p < PP; ++p) {
+                    u[p] = mul2(dt[p], u[p]);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        h[n][p] = fma2(decay2(dt[p], A2[n][p]), h[n][p], mul2(u[p], B[n]));
+                        if (!SUM) y[p] = n == 0 ? mul2(C[n], h[n][p]) : fma2(C[n], h[n][p], y[p]);
+                    }
                     if (SUM) {
-                        dt_tile[c] += unpack2(du.x).x;
+                        dt_tile[p] = add2(dt_tile[p], dt[p]);
                     } else {
-                        const float2 s = unpack2(fma2(C.y, h[c][1], mul2(C.x, h[c][0])));
-                        acc[k * CPT + c] = s.x + s.y;
+                        const float2 v = unpack2(y[p]);
+                        acc[k * CPT + 2 * p] = v.x;
+                        acc[k * CPT + 2 * p + 1] = v.y;
                     }
                 }
             }
             if (!SUM) {
-                constexpr int M = 4 * CPT;
+                constexpr int M = 4 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
                 group_reduce<M, NL>(acc, nl);
-                if (M >= NL) {
+                if (nl % REP == 0) {
 #pragma unroll
-                    for (int i = 0; i < (M >= NL ? M / NL : 1); ++i) {
-                        const int v = nl * (M / NL) + i;
-                        ys[(t4 + v / CPT) * Sh::YP + wc + (v % CPT) * Sh::CLN] = acc[i];
+                    for (int i = 0; i < KEEP; ++i) {
+                        const int v = nl / REP * KEEP + i;
+                        ys[(t4 + v / CPT) * Sh::YP + cl * CPT + v % CPT] = acc[i];
                     }
-                } else {
-                    constexpr int R = M >= NL ? 1 : NL / M;
-                    const int v = nl / R;
-                    if (nl % R == 0) ys[(t4 + v / CPT) * Sh::YP + wc + (v % CPT) * Sh::CLN] = acc[0];
                 }
             }
         }
         if (SUM) {
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) dts[c] += dt_tile[c];
+            for (int p = 0; p < PP; ++p) dts[p] = add2(dts[p], dt_tile[p]);
         } else {
-            if (tl.ends && P.a.h_last) {
-#pragma unroll
-                for (int c = 0; c < CPT; ++c)
-                    store_entries(P.a.h_last + tl.slot * dn, c0 + wc + c * Sh::CLN, D, n0, N, vst, h[c]);
-            }
-            __syncthreads();
+            if (tl.ends && P.a.h_last) store_entries(P.a.h_last + tl.slot * dn, d0, D, n0, N, vst, h);
+            __syncwarp();
             // skip, gate and output of the tile's rows
-            for (int i = tid * 4; i < tl.n * CB; i += kScanThreads * 4) {
-                const int r = i / CB, c = i % CB;
-                if (c >= ncols) continue;
-                float4 y = *reinterpret_cast<const float4 *>(ys + r * Sh::YP + c);
-                if (P.a.Dskip) {
-                    const float4 x4 = load4(xs + i);
-                    const float *dp = P.a.Dskip + c0 + c;
-                    y.x = fmaf(dp[0], x4.x, y.x);
-                    if (c + 1 < ncols) y.y = fmaf(dp[1], x4.y, y.y);
-                    if (c + 2 < ncols) y.z = fmaf(dp[2], x4.z, y.z);
-                    if (c + 3 < ncols) y.w = fmaf(dp[3], x4.w, y.w);
+#pragma unroll
+            for (int r0 = 0; r0 < kScanTile; r0 += NL) {
+                const int r = r0 + orow;
+                if (r >= tl.n || oc >= ncols) continue;
+                float y[CPT];
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    const float2 v = *reinterpret_cast<const float2 *>(ys + r * Sh::YP + lane % CLN * CPT + 2 * p);
+                    y[2 * p] = v.x;
+                    y[2 * p + 1] = v.y;
                 }
-                if (P.a.z) {
-                    const float4 z4 = load4(zs + i);
-                    y.x *= z4.x * fast_sigmoid(z4.x);
-                    y.y *= z4.y * fast_sigmoid(z4.y);
-                    y.z *= z4.z * fast_sigmoid(z4.z);
-                    y.w *= z4.w * fast_sigmoid(z4.w);
+                f2 x2[PP], z2[PP];
+                load_pairs(xs + r * CB + oc, x2);
+                if (P.a.z) load_pairs(zs + r * CB + oc, z2);
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) {
+                    const float2 xv = unpack2(x2[c / 2]);
+                    y[c] = fmaf(skip[c], c & 1 ? xv.y : xv.x, y[c]);
+                    if (P.a.z) {
+                        const float2 zp = unpack2(z2[c / 2]);
+                        const float z = c & 1 ? zp.y : zp.x;
+                        y[c] *= z * fast_sigmoid(z);
+                    }
+                    if (tl.seq < 0) y[c] = 0.f;
                 }
-                if (tl.seq < 0) y = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int64_t o = (int64_t)(tl.t0 + r) * P.a.y_stride + c0 + c;
+                const int64_t o = (int64_t)(tl.t0 + r) * P.a.y_stride + c0 + oc;
                 if (P.a.out_dtype == GDN_BF16)
-                    store_row4(static_cast<bf16 *>(P.a.y) + o, y, ncols - c, P.vec & kVecY);
+                    store_row(static_cast<bf16 *>(P.a.y) + o, y, ncols - oc, P.vec & kVecY);
                 else
-                    store_row4(static_cast<float *>(P.a.y) + o, y, ncols - c, P.vec & kVecY);
+                    store_row(static_cast<float *>(P.a.y) + o, y, ncols - oc, P.vec & kVecY);
             }
+            __syncwarp();
         }
         b ^= 1;
     }
     if (SUM) {
+        store_entries(P.hin + g * dn, d0, D, n0, N, vst, h);
 #pragma unroll
-        for (int c = 0; c < CPT; ++c) {
-            const int d = c0 + wc + c * Sh::CLN;
-            store_entries(P.hin + g * dn, d, D, n0, N, vst, h[c]);
-            if (nl == 0 && d < D) P.sumdt[(int64_t)g * D + d] = dts[c];
+        for (int p = 0; p < PP; ++p) {
+            const float2 v = unpack2(dts[p]);
+            if (nl == 0 && d0 + 2 * p < D) P.sumdt[(int64_t)g * D + d0 + 2 * p] = v.x;
+            if (nl == 0 && d0 + 2 * p + 1 < D) P.sumdt[(int64_t)g * D + d0 + 2 * p + 1] = v.y;
         }
     }
 }
@@ -231,7 +218,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_forward_kernel(const __grid
 template <typename Tin, int NL, int CPT, bool SUM>
 static cudaError_t launch_one(const ScanLaunch &P, int chunks, cudaStream_t stream)
 {
-    constexpr int bytes = ScanSmem<Tin, ScanShape<NL, CPT>>::MAIN;
+    constexpr int bytes = SUM ? ScanSmem<Tin, ScanShape<NL, CPT>>::SUMMARY : ScanSmem<Tin, ScanShape<NL, CPT>>::MAIN;
     auto kern = scan_forward_kernel<Tin, NL, CPT, SUM>;
     if (bytes > 48 * 1024) {
         const cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -252,9 +239,9 @@ template <typename Tin, int NL, int CPT> static int launch_shape(const ScanLaunc
 template <typename Tin> static int launch_typed(const ScanLaunch &P, cudaStream_t stream)
 {
     switch (scan_shape(P.a.N).NL) {
-    case 2: return launch_shape<Tin, 2, 2>(P, stream);
-    case 4: return launch_shape<Tin, 4, 2>(P, stream);
-    case 8: return launch_shape<Tin, 8, 2>(P, stream);
+    case 2: return launch_shape<Tin, 2, 4>(P, stream);
+    case 4: return launch_shape<Tin, 4, 4>(P, stream);
+    case 8: return launch_shape<Tin, 8, 4>(P, stream);
     case 16: return launch_shape<Tin, 16, 4>(P, stream);
     default: return launch_shape<Tin, 32, 4>(P, stream);
     }

@@ -35,19 +35,12 @@ struct ScanLaunch {
     int W;              // workers per channel tile
 };
 
-// lanes along the state and channels per thread for a state size
+// lanes along the state, channels per thread and per CTA for a state size
 struct ScanTileShape { int NL, CPT; int channels; };
 inline ScanTileShape scan_shape(int N)
 {
     const int nl = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32;
-    const int cpt = nl >= 16 ? 4 : 2;
-    return {nl, cpt, 4 * (32 / nl) * cpt};
-}
-
-inline ScanTileShape scan_shape_backward(int N)
-{
-    const int nl = scan_shape(N).NL;
-    return {nl, 2, 4 * (32 / nl) * 2};
+    return {nl, 4, 4 * (32 / nl) * 4};
 }
 
 constexpr int kScanBackChunk = 64;   // token rows per chunk of the backward pass
