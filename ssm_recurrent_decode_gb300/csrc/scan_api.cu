@@ -12,7 +12,6 @@ constexpr size_t kWsAlign = 256;
 
 size_t round_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
-int tiles(int D, int N) { return (D + scan_shape(N).channels - 1) / scan_shape(N).channels; }
 bool sizes_ok(int T, int S, int D, int N, bool uniform)
 {
     return T >= 0 && S >= 1 && D >= 1 && N >= 1 && N <= kMaxState && (!uniform || T % S == 0);
@@ -55,13 +54,32 @@ size_t carve(ScanLaunch &P, bool uniform, bool backward, unsigned char *base)
     return w.used;
 }
 
-// C, G, nct and W of a call whose sizes are set
+// Splits a call whose sizes are set (by the sizes alone, so that the workspace can be sized before the
+// call): channels per thread, rows per chunk, workers.
 void plan(ScanLaunch &P, bool uniform, bool backward)
 {
+    const int64_t T = P.a.T;
     P.L = uniform ? P.a.T / P.a.S : 0;
-    P.nct = tiles(P.a.D, P.a.N);
-    P.C = scan_chunk(P.a.T, P.a.S, P.a.D, P.a.N, uniform, backward);
-    P.G = P.a.T > 0 ? (int)(((int64_t)P.a.T + P.C - 1) / P.C) : 1;   // without rows: one chunk of empty sequences
+    const auto tiles = [&](int cpt) { return (P.a.D + scan_channels(P.a.N, cpt) - 1) / scan_channels(P.a.N, cpt); };
+    P.cpt = 4;
+    P.nct = tiles(4);
+    if (backward) {
+        P.C = kScanBackChunk;
+    } else {
+        constexpr int64_t kSlots = 4 * kSms;     // resident CTAs
+        // Chunks of equal length that fill the GPU once, and no shorter than the 32 rows below which a
+        // chunk's own costs (its rates, states and launch) outweigh its rows.
+        int64_t C = (T * P.nct + kSlots - 1) / kSlots;
+        C = (C + 15) / 16 * 16;
+        P.C = (int)(C < 32 ? 32 : C);
+        if (C < 32 && T * tiles(2) <= 32 * kSlots) {
+            P.cpt = 2;                           // too few rows for that: more threads for each
+            P.nct = tiles(2);
+        }
+        // One pass over whole sequences where they are about as long as the chunks would be.
+        if (uniform && P.L > 0 && P.L <= 4 * P.C) P.C = P.L;
+    }
+    P.G = T > 0 ? (int)((T + P.C - 1) / P.C) : 1;   // without rows: one chunk of empty sequences
     P.W = 1;
     if (backward) {
         // two CTAs per SM (what their registers allow), each walking over chunks
@@ -113,17 +131,6 @@ int check_workspace(const mamba_scan_args &a, size_t need)
     return aligned(a.workspace, 16) ? GDN_OK : GDN_ERR_ALIGN;
 }
 }  // namespace
-
-int scan_chunk(int T, int S, int D, int N, bool uniform, bool backward)
-{
-    if (T < 1) return 1;
-    const int64_t nct = tiles(D, N);
-    if (backward) return kScanBackChunk;
-    if (uniform && (S * nct >= 4 * kSms || T / S <= 128)) return T / S;
-    int C = 512;
-    while (C > 32 && ((int64_t)T + C - 1) / C * nct < 12 * kSms) C /= 2;
-    return C;
-}
 
 }  // namespace gdn
 

@@ -557,7 +557,7 @@ template <typename Tin, int NL> static int launch_shape(const ScanLaunch &P, cud
 
 template <typename Tin> static int launch_typed(const ScanLaunch &P, cudaStream_t stream)
 {
-    switch (scan_shape(P.a.N).NL) {
+    switch (scan_lanes(P.a.N)) {
     case 2: return launch_shape<Tin, 2>(P, stream);
     case 4: return launch_shape<Tin, 4>(P, stream);
     case 8: return launch_shape<Tin, 8>(P, stream);

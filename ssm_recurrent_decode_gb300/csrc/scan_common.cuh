@@ -99,8 +99,13 @@ __device__ __forceinline__ f2 decay2(f2 dtdt, f2 A2)
     return pack2(ex2_approx(y.x), ex2_approx(y.y));
 }
 
-// silu and its parts on the fast reciprocal (relative error of a few 2^-23)
-__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// sigmoid on the fast reciprocal and exponential (relative error of a few 2^-23; exactly 0 where exp(-z) overflows)
+__device__ __forceinline__ float fast_sigmoid(float z)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * z)));
+    return r;
+}
 
 // Sums v[0 .. M) over the NL lanes of a group, M values at once: each halving of the lanes halves
 // the values a lane keeps. Lane nl ends with values nl M / NL .. (M >= NL), or with value
@@ -263,6 +268,8 @@ __device__ __forceinline__ void load_pairs(const bf16 *p, f2 (&v)[2])
     v[0] = widen2(q.x);
     v[1] = widen2(q.y);
 }
+__device__ __forceinline__ void store_pairs(float *p, const f2 (&v)[1]) { *reinterpret_cast<f2 *>(p) = v[0]; }
+__device__ __forceinline__ void store_pairs(float *p, const f2 (&v)[2]) { *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v[0], v[1]); }
 // four consecutive state entries of a staged B or C row, each in both halves of a pair
 template <typename T> __device__ __forceinline__ void load_twice(const T *p, f2 (&v)[4])
 {

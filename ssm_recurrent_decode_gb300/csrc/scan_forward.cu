@@ -6,12 +6,15 @@
 
 namespace gdn {
 
+constexpr int kScanHalf = 8;        // rows between two stores of outputs
+
 // Shared memory, in bytes.
 template <typename Tin, class Sh> struct ScanSmem {
     static constexpr int RX = kScanTile * Sh::CB * (int)sizeof(Tin);     // a staged x, dt or z tile
     static constexpr int RB = kScanTile * Sh::NP * (int)sizeof(Tin);     // a staged B or C tile
     static constexpr int STAGE = 3 * RX + 2 * RB;
-    static constexpr int Y = kScanWarps * kScanTile * Sh::YP * 4;
+    static constexpr int PARTS = Sh::NL <= 4 ? Sh::NL : 1;               // sums over n still to be joined
+    static constexpr int Y = kScanWarps * kScanHalf * PARTS * Sh::YP * 4;
     static constexpr int MAIN = 2 * STAGE + Y;
     static constexpr int SUMMARY = 2 * STAGE;
 };
@@ -93,10 +96,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
     for (int p = 0; p < PP; ++p) dts[p] = 0ull;
     // a lane finishes CPT channels of every row it is given: the same ones in every tile
     const int oc = warp * Sh::CW + lane % CLN * CPT, orow = lane / CLN;
-    float skip[CPT];
+    f2 skip[PP];
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) skip[c] = !SUM && P.a.Dskip && oc + c < ncols ? P.a.Dskip[c0 + oc + c] : 0.f;
-    float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * kScanTile * Sh::YP;
+    for (int p = 0; p < PP; ++p) {
+        const int c = oc + 2 * p;
+        skip[p] = pack2(!SUM && P.a.Dskip && c < ncols ? P.a.Dskip[c0 + c] : 0.f,
+                        !SUM && P.a.Dskip && c + 1 < ncols ? P.a.Dskip[c0 + c + 1] : 0.f);
+    }
+    float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * kScanHalf * Sm::PARTS * Sh::YP;
 
     int b = 0;
     while (use.next(P, tl)) {
@@ -123,84 +130,91 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
         f2 dt_tile[PP] = {};
         // rows behind the tile's last are zeros: dt = 0 leaves h as it is
 #pragma unroll 1
-        for (int t4 = 0; t4 < kScanTile; t4 += 4) {
-            float acc[4 * CPT];
+        for (int t8 = 0; t8 < kScanTile; t8 += kScanHalf) {
+#pragma unroll 1
+            for (int t4 = t8; t4 < t8 + kScanHalf; t4 += 4) {
+                float acc[4 * CPT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = t4 + k;
-                f2 dt[PP], u[PP], B[4], C[4], y[PP];
-                load_pairs(ds + t * CB + wc, dt);
-                load_pairs(xs + t * CB + wc, u);
-                load_twice(Bs + t * NP + n0, B);
-                if (!SUM) load_twice(Cs + t * NP + n0, C);
+                for (int k = 0; k < 4; ++k) {
+                    const int t = t4 + k;
+                    f2 dt[PP], u[PP], B[4], C[4], y[PP];
+                    load_pairs(ds + t * CB + wc, dt);
+                    load_pairs(xs + t * CB + wc, u);
+                    load_twice(Bs + t * NP + n0, B);
+                    if (!SUM) load_twice(Cs + t * NP + n0, C);
+#pragma unroll
+                    for (int p = 0; p < PP; ++p) {
+                        u[p] = mul2(dt[p], u[p]);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            h[n][p] = fma2(decay2(dt[p], A2[n][p]), h[n][p], mul2(u[p], B[n]));
+                            if (!SUM) y[p] = n == 0 ? mul2(C[n], h[n][p]) : fma2(C[n], h[n][p], y[p]);
+                        }
+                        if (SUM) dt_tile[p] = add2(dt_tile[p], dt[p]);
+                        else if (NL > 4) {
+                            const float2 v = unpack2(y[p]);
+                            acc[k * CPT + 2 * p] = v.x;
+                            acc[k * CPT + 2 * p + 1] = v.y;
+                        }
+                    }
+                    // up to four lanes' sums are joined where the row is finished, more of them here by shuffles
+                    if (!SUM && NL <= 4) store_pairs(ys + ((t - t8) * NL + nl) * Sh::YP + cl * CPT, y);
+                }
+                if (!SUM && NL > 4) {
+                    constexpr int M = 4 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
+                    group_reduce<M, NL>(acc, nl);
+                    if (nl % REP == 0) {
+#pragma unroll
+                        for (int i = 0; i < KEEP; ++i) {
+                            const int v = nl / REP * KEEP + i;
+                            ys[(t4 - t8 + v / CPT) * Sh::YP + cl * CPT + v % CPT] = acc[i];
+                        }
+                    }
+                }
+            }
+            if (SUM) continue;
+            __syncwarp();
+            // skip, gate and output of these rows
+#pragma unroll
+            for (int r0 = 0; r0 < kScanHalf; r0 += NL) {
+                const int r = r0 + orow, t = t8 + r;
+                if ((NL > kScanHalf && r >= kScanHalf) || t >= tl.n || oc >= ncols) continue;
+                f2 y[PP], x2[PP], z2[PP];
+                load_pairs(ys + r * Sm::PARTS * Sh::YP + lane % CLN * CPT, y);
+#pragma unroll
+                for (int q = 1; q < Sm::PARTS; ++q) {
+                    f2 more[PP];
+                    load_pairs(ys + (r * Sm::PARTS + q) * Sh::YP + lane % CLN * CPT, more);
+#pragma unroll
+                    for (int p = 0; p < PP; ++p) y[p] = add2(y[p], more[p]);
+                }
+                load_pairs(xs + t * CB + oc, x2);
+                if (P.a.z) load_pairs(zs + t * CB + oc, z2);
+                float out[CPT];
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
-                    u[p] = mul2(dt[p], u[p]);
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        h[n][p] = fma2(decay2(dt[p], A2[n][p]), h[n][p], mul2(u[p], B[n]));
-                        if (!SUM) y[p] = n == 0 ? mul2(C[n], h[n][p]) : fma2(C[n], h[n][p], y[p]);
+                    y[p] = fma2(skip[p], x2[p], y[p]);
+                    if (P.a.z) {
+                        const float2 z = unpack2(z2[p]);
+                        y[p] = mul2(y[p], mul2(z2[p], pack2(fast_sigmoid(z.x), fast_sigmoid(z.y))));
                     }
-                    if (SUM) {
-                        dt_tile[p] = add2(dt_tile[p], dt[p]);
-                    } else {
-                        const float2 v = unpack2(y[p]);
-                        acc[k * CPT + 2 * p] = v.x;
-                        acc[k * CPT + 2 * p + 1] = v.y;
-                    }
+                    const float2 v = unpack2(y[p]);
+                    out[2 * p] = tl.seq < 0 ? 0.f : v.x;
+                    out[2 * p + 1] = tl.seq < 0 ? 0.f : v.y;
                 }
+                const int64_t o = (int64_t)(tl.t0 + t) * P.a.y_stride + c0 + oc;
+                if (P.a.out_dtype == GDN_BF16)
+                    store_row(static_cast<bf16 *>(P.a.y) + o, out, ncols - oc, P.vec & kVecY);
+                else
+                    store_row(static_cast<float *>(P.a.y) + o, out, ncols - oc, P.vec & kVecY);
             }
-            if (!SUM) {
-                constexpr int M = 4 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
-                group_reduce<M, NL>(acc, nl);
-                if (nl % REP == 0) {
-#pragma unroll
-                    for (int i = 0; i < KEEP; ++i) {
-                        const int v = nl / REP * KEEP + i;
-                        ys[(t4 + v / CPT) * Sh::YP + cl * CPT + v % CPT] = acc[i];
-                    }
-                }
-            }
+            __syncwarp();
         }
         if (SUM) {
 #pragma unroll
             for (int p = 0; p < PP; ++p) dts[p] = add2(dts[p], dt_tile[p]);
-        } else {
-            if (tl.ends && P.a.h_last) store_entries(P.a.h_last + tl.slot * dn, d0, D, n0, N, vst, h);
-            __syncwarp();
-            // skip, gate and output of the tile's rows
-#pragma unroll
-            for (int r0 = 0; r0 < kScanTile; r0 += NL) {
-                const int r = r0 + orow;
-                if (r >= tl.n || oc >= ncols) continue;
-                float y[CPT];
-#pragma unroll
-                for (int p = 0; p < PP; ++p) {
-                    const float2 v = *reinterpret_cast<const float2 *>(ys + r * Sh::YP + lane % CLN * CPT + 2 * p);
-                    y[2 * p] = v.x;
-                    y[2 * p + 1] = v.y;
-                }
-                f2 x2[PP], z2[PP];
-                load_pairs(xs + r * CB + oc, x2);
-                if (P.a.z) load_pairs(zs + r * CB + oc, z2);
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const float2 xv = unpack2(x2[c / 2]);
-                    y[c] = fmaf(skip[c], c & 1 ? xv.y : xv.x, y[c]);
-                    if (P.a.z) {
-                        const float2 zp = unpack2(z2[c / 2]);
-                        const float z = c & 1 ? zp.y : zp.x;
-                        y[c] *= z * fast_sigmoid(z);
-                    }
-                    if (tl.seq < 0) y[c] = 0.f;
-                }
-                const int64_t o = (int64_t)(tl.t0 + r) * P.a.y_stride + c0 + oc;
-                if (P.a.out_dtype == GDN_BF16)
-                    store_row(static_cast<bf16 *>(P.a.y) + o, y, ncols - oc, P.vec & kVecY);
-                else
-                    store_row(static_cast<float *>(P.a.y) + o, y, ncols - oc, P.vec & kVecY);
-            }
-            __syncwarp();
+        } else if (tl.ends && P.a.h_last) {
+            store_entries(P.a.h_last + tl.slot * dn, d0, D, n0, N, vst, h);
         }
         b ^= 1;
     }
@@ -236,14 +250,19 @@ template <typename Tin, int NL, int CPT> static int launch_shape(const ScanLaunc
     return launch_one<Tin, NL, CPT, false>(P, P.G, stream) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
+template <typename Tin, int NL> static int launch_lanes(const ScanLaunch &P, cudaStream_t stream)
+{
+    return P.cpt == 2 ? launch_shape<Tin, NL, 2>(P, stream) : launch_shape<Tin, NL, 4>(P, stream);
+}
+
 template <typename Tin> static int launch_typed(const ScanLaunch &P, cudaStream_t stream)
 {
-    switch (scan_shape(P.a.N).NL) {
-    case 2: return launch_shape<Tin, 2, 4>(P, stream);
-    case 4: return launch_shape<Tin, 4, 4>(P, stream);
-    case 8: return launch_shape<Tin, 8, 4>(P, stream);
-    case 16: return launch_shape<Tin, 16, 4>(P, stream);
-    default: return launch_shape<Tin, 32, 4>(P, stream);
+    switch (scan_lanes(P.a.N)) {
+    case 2: return launch_lanes<Tin, 2>(P, stream);
+    case 4: return launch_lanes<Tin, 4>(P, stream);
+    case 8: return launch_lanes<Tin, 8>(P, stream);
+    case 16: return launch_lanes<Tin, 16>(P, stream);
+    default: return launch_lanes<Tin, 32>(P, stream);
     }
 }
 

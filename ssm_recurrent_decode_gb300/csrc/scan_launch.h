@@ -16,6 +16,7 @@ struct ScanLaunch {
     mamba_scan_args a;
     int L;              // rows per sequence without cu_seqlens
     int C, G;           // rows per chunk, chunks
+    int cpt;            // channels per thread
     int nct;            // channel tiles
     int vec;
     int has_states;     // state indices are checked
@@ -35,19 +36,11 @@ struct ScanLaunch {
     int W;              // workers per channel tile
 };
 
-// lanes along the state, channels per thread and per CTA for a state size
-struct ScanTileShape { int NL, CPT; int channels; };
-inline ScanTileShape scan_shape(int N)
-{
-    const int nl = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32;
-    return {nl, 4, 4 * (32 / nl) * 4};
-}
+// lanes along the state for a state size, and the channels of a CTA of four warps
+inline int scan_lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+inline int scan_channels(int N, int cpt) { return 4 * (32 / scan_lanes(N)) * cpt; }
 
 constexpr int kScanBackChunk = 64;   // token rows per chunk of the backward pass
-
-// Rows per chunk of the forward and the backward call (a function of the sizes alone, so that the
-// workspace can be sized before the call).
-int scan_chunk(int T, int S, int D, int N, bool uniform, bool backward);
 
 // The carry pass over the chunks (forward; with both also the backward one, over e).
 cudaError_t launch_scan_carry(const ScanLaunch &P, bool both, cudaStream_t stream);
