@@ -22,6 +22,10 @@ namespace {
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelVecs = 4;                 // 16-byte loads per thread and chunk, all in flight
+#ifndef KSEL
+#define KSEL 4
+#endif
+constexpr int kSelCtas = KSEL;                 // resident CTAs per SM
 constexpr int kSelCap = 1024;               // candidates kept before they are ranked
 constexpr int kSelMaxSegs = 32;             // segments per row: a lane each in the join
 constexpr unsigned kFullMask = 0xFFFFFFFFu;
@@ -54,34 +58,28 @@ template <typename T> struct Vec16 {
     static constexpr int E = 16 / (int)sizeof(T);
 };
 
-__device__ __forceinline__ void unpack16(uint4 v, float (&x)[4])
+// a 16-byte vector as pairs of fp32
+__device__ __forceinline__ void unpack16(uint4 v, float2 (&x)[2])
 {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
+    x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ void unpack16(uint4 v, float (&x)[8])
+__device__ __forceinline__ void unpack16(uint4 v, float2 (&x)[4])
 {
     const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 // The elements i .. i + E - 1 (i a multiple of E) of a row of V elements; those outside are -inf. In a
 // row that starts `shift` elements behind a 16-byte boundary they lie in two aligned vectors and are
 // shifted out of them: which thread adds up which elements depends on their index alone, so that equal
 // rows give bit-equal sums wherever they lie.
-template <typename T, bool SHIFTED>
-__device__ __forceinline__ void load_vec(const T *row, int64_t i, int V, int shift, float (&x)[Vec16<T>::E])
+template <typename T, bool SHIFTED> __device__ __forceinline__ uint4 load_vec(const T *row, int64_t i, int V, int shift)
 {
     constexpr int E = Vec16<T>::E;
-    if (!SHIFTED && i + E <= V) {
-        unpack16(__ldcs(reinterpret_cast<const uint4 *>(row + i)), x);
-    } else if (SHIFTED && i >= shift && i - shift + 2 * E <= V) {
+    if (!SHIFTED && i + E <= V) return __ldcs(reinterpret_cast<const uint4 *>(row + i));
+    if (SHIFTED && i >= shift && i - shift + 2 * E <= V) {
         const uint4 lo = *reinterpret_cast<const uint4 *>(row + i - shift), hi = *reinterpret_cast<const uint4 *>(row + i - shift + E);
         unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
         const int words = shift * (int)sizeof(T) / 4;
@@ -97,32 +95,72 @@ __device__ __forceinline__ void load_vec(const T *row, int64_t i, int V, int shi
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
         }
-        unpack16(make_uint4(w[0], w[1], w[2], w[3]), x);
-    } else {
-#pragma unroll
-        for (int k = 0; k < E; ++k) x[k] = i + k < V ? to_f32(row[i + k]) : -INFINITY;
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    unsigned w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (sizeof(T) == 4) {
+            w[k] = i + k < V ? *reinterpret_cast<const unsigned *>(row + i + k) : 0xFF800000u;
+        } else {
+            const unsigned short *p = reinterpret_cast<const unsigned short *>(row);
+            const unsigned lo = i + 2 * k < V ? p[i + 2 * k] : 0xFF80u, hi = i + 2 * k + 1 < V ? p[i + 2 * k + 1] : 0xFF80u;
+            w[k] = lo | hi << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// sum of exp(x - m) over n values; an element that is NaN counts nothing, an infinite maximum counts
-// its elements
-template <int NX> __device__ __forceinline__ float exp_sum(const float (&x)[NX], float m)
+// the largest of a vector's elements (NaN only if all are)
+__device__ __forceinline__ float vec_max(const uint4 (&v)[kSelVecs], float)
 {
-    float s = 0.f;
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kSelVecs; ++k)
+        m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v[k].x)), fmaxf(__uint_as_float(v[k].y), __uint_as_float(v[k].z))), __uint_as_float(v[k].w));
+    return m;
+}
+__device__ __forceinline__ float vec_max(const uint4 (&v)[kSelVecs], bf16)
+{
+    __nv_bfloat162 m = __float2bfloat162_rn(-INFINITY);
+#pragma unroll
+    for (int k = 0; k < kSelVecs; ++k) {
+        const unsigned w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
+    }
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+// Sum of exp(x - m) over a thread's elements. An element that is NaN counts nothing; an infinite
+// maximum counts its elements.
+template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[kSelVecs], float m)
+{
+    constexpr int E = Vec16<T>::E;
     if (m == -INFINITY) return 0.f;
-    if (m == INFINITY) {
+    float s0 = 0.f, s1 = 0.f;
+    const bool finite = m < INFINITY;
 #pragma unroll
-        for (int k = 0; k < NX; ++k) s += x[k] == INFINITY ? 1.f : 0.f;
-        return s;
+    for (int k = 0; k < kSelVecs; ++k) {
+        float2 x[E / 2];
+        unpack16(v[k], x);
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+            s0 += __expf(x[j].x - m);
+            s1 += __expf(x[j].y - m);
+        }
     }
+    if (finite && s0 + s1 == s0 + s1) return s0 + s1;
+    s0 = 0.f;
 #pragma unroll
-    for (int k = 0; k < NX; ++k) s += __expf(x[k] - m);
-    if (s != s) {
-        s = 0.f;
+    for (int k = 0; k < kSelVecs; ++k) {
+        float2 x[E / 2];
+        unpack16(v[k], x);
 #pragma unroll
-        for (int k = 0; k < NX; ++k) s += x[k] == x[k] ? __expf(x[k] - m) : 0.f;
+        for (int j = 0; j < E / 2; ++j)
+            for (float y : {x[j].x, x[j].y}) s0 += y == m ? 1.f : y == y && finite ? __expf(y - m) : 0.f;
     }
-    return s;
+    return s0;
 }
 
 // (m, s) of two parts joined
@@ -169,10 +207,10 @@ __device__ __forceinline__ float kth_top(float top, int k, int lane, int warp, f
 }
 
 template <typename T, bool SHIFTED>
-__global__ void __launch_bounds__(kSelThreads) beam_segment_kernel(const __grid_constant__ SelectLaunch P)
+__global__ void __launch_bounds__(kSelThreads, kSelCtas) beam_segment_kernel(const __grid_constant__ SelectLaunch P)
 {
-    constexpr int E = Vec16<T>::E, NX = kSelVecs * E;
-    constexpr int64_t CHUNK = (int64_t)kSelThreads * NX;
+    constexpr int E = Vec16<T>::E;
+    constexpr int64_t CHUNK = (int64_t)kSelThreads * kSelVecs * E;
     __shared__ unsigned long long list[kSelCap], sorted[GDN_BEAM_MAX_SELECT];
     __shared__ float wthr[kSelWarps], wm[kSelWarps], ws[kSelWarps];
     __shared__ unsigned long long wkey[kSelWarps];
@@ -200,20 +238,20 @@ __global__ void __launch_bounds__(kSelThreads) beam_segment_kernel(const __grid_
     bool full = false, overflow = false;
     if (tid == 0) count = 0;
     __syncthreads();
+    uint4 ahead[kSelVecs];
+#pragma unroll
+    for (int v = 0; v < kSelVecs; ++v) ahead[v] = load_vec<T, SHIFTED>(row, first + ((int64_t)v * kSelThreads + tid) * E, V, shift);
     for (int64_t base = first; base < last; base += CHUNK) {
-        float x[NX];
+        uint4 x[kSelVecs];
 #pragma unroll
-        for (int v = 0; v < kSelVecs; ++v) {
-            float y[E];
-            load_vec<T, SHIFTED>(row, base + ((int64_t)v * kSelThreads + tid) * E, V, shift, y);
+        for (int v = 0; v < kSelVecs; ++v) x[v] = ahead[v];
+        if (base + CHUNK < last) {
 #pragma unroll
-            for (int k = 0; k < E; ++k) x[v * E + k] = y[k];
+            for (int v = 0; v < kSelVecs; ++v)
+                ahead[v] = load_vec<T, SHIFTED>(row, base + CHUNK + ((int64_t)v * kSelThreads + tid) * E, V, shift);
         }
-        float top = x[0];
-#pragma unroll
-        for (int k = 1; k < NX; ++k) top = fmaxf(top, x[k]);
-        top = fmaxf(top, -INFINITY);             // all of them NaN
-        join_stats(m, s, top, exp_sum(x, top));
+        const float top = vec_max(x, T());
+        join_stats(m, s, top, exp_sum<T>(x, top));
 
         if (base == first) {
             // a value that at least K elements reach, if there are as many: from every warp its share,
@@ -225,9 +263,11 @@ __global__ void __launch_bounds__(kSelThreads) beam_segment_kernel(const __grid_
 #pragma unroll
             for (int v = 0; v < kSelVecs; ++v) {
                 const int64_t i = base + ((int64_t)v * kSelThreads + tid) * E;
+                float2 e[E / 2];
+                unpack16(x[v], e);
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
-                    const float y = x[v * E + k];
+                    const float y = k & 1 ? e[k / 2].y : e[k / 2].x;
                     if ((full ? y > thr : y >= thr) && y > -INFINITY) {
                         const int at = atomicAdd(&count, 1);
                         if (at < kSelCap) list[at] = make_key(y, (int)(i + k));
@@ -317,17 +357,45 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
     return (unsigned long long)hi << 32 | lo;
 }
 
+// log(x) for a normal x > 0 in fp64, to about 1e-15: x = 2^e f with f in [sqrt(1/2), sqrt(2)), and
+// log f = 2 atanh(q) = 2 (q + q^3/3 + ...) at q = (f - 1) / (f + 1), |q| <= 0.1716 (11 terms)
+__device__ __forceinline__ double log64(double x)
+{
+    long long b = __double_as_longlong(x);
+    int e = (int)(b >> 52) - 1023;
+    double f = __longlong_as_double((b & 0x000FFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
+    if (f > 1.4142135623730951) {
+        f *= 0.5;
+        ++e;
+    }
+    const double q = (f - 1.0) / (f + 1.0), q2 = q * q;
+    // even and odd terms side by side, to halve the chain
+    const double q4 = q2 * q2;
+    double even = 1.0 / 21, odd = 1.0 / 19;
+    even = fma(even, q4, 1.0 / 17);
+    odd = fma(odd, q4, 1.0 / 15);
+    even = fma(even, q4, 1.0 / 13);
+    odd = fma(odd, q4, 1.0 / 11);
+    even = fma(even, q4, 1.0 / 9);
+    odd = fma(odd, q4, 1.0 / 7);
+    even = fma(even, q4, 1.0 / 5);
+    odd = fma(odd, q4, 1.0 / 3);
+    even = fma(even, q4, 1.0);
+    return fma((double)e, 0.69314718055994530942, 2.0 * q * fma(odd, q2, even));
+}
+
 // One CTA per batch entry, a warp per beam.
 __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(const __grid_constant__ SelectLaunch P)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    ordinary_launch_start();
     const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
     const int K = P.a.K, beams = P.a.beams;
     double *score = reinterpret_cast<double *>(smem);                       // [beams, K]
     int *token = reinterpret_cast<int *>(score + beams * K);                // [beams, K]
     const int64_t beam = (int64_t)blockIdx.x * beams + j;
 
+    // The call's inputs may be read before the wait: this kernel's CTAs start when every CTA of the
+    // segment kernel has let them, which each does after its own wait for the kernels before it.
     const float cum = P.a.scores[beam];
     const int64_t r = P.a.rows ? (int64_t)P.a.rows[beam] : beam;
     const bool live = cum > -INFINITY && r >= 0 && r < P.a.num_rows;
@@ -337,22 +405,23 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
         token[j * K + k] = done && k == 0 ? P.a.eos_token : -1;
     }
     __syncwarp();
+    ordinary_launch_start();
     if (live && !done) {
+        // the segments' lists, best first: a lane's two next keys are at hand
+        const bool on = lane < P.segs;
+        const unsigned long long *mine = P.keys + (beam * P.segs + lane) * K;
+        const float2 st = on ? P.stats[beam * P.segs + lane] : make_float2(-INFINITY, 0.f);
+        unsigned long long head = on ? mine[0] : 0, next = on && K > 1 ? mine[1] : 0;
         // the row's maximum, and the logarithm of its sum
-        float2 st = make_float2(-INFINITY, 0.f);
-        if (lane < P.segs) st = P.stats[beam * P.segs + lane];
         float top = st.x;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
         if (top > -INFINITY) {
-            double sum = st.x == -INFINITY ? 0.0 : st.x == top ? (double)st.y : (double)st.y * exp((double)st.x - (double)top);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
-            const double base = (double)cum, norm = log(sum);
-            // the segments' lists, best first: a lane's two next keys are at hand
-            const unsigned long long *mine = P.keys + (beam * P.segs + lane) * K;
-            const bool on = lane < P.segs;
-            unsigned long long head = on ? mine[0] : 0, next = on && K > 1 ? mine[1] : 0;
+            double sum = st.x == -INFINITY ? 0.0 : st.x == top ? (double)st.y : (double)(st.y * __expf(st.x - top));
+            int lanes = 1;
+            while (lanes < P.segs) lanes *= 2;
+            for (int off = lanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
+            const double base = (double)cum, norm = log64(__shfl_sync(kFullMask, sum, 0));
             int at = 2;
             for (int k = 0; k < K; ++k) {
                 const unsigned long long best = warp_max(head);
@@ -375,7 +444,7 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     // the beams' lists: a lane per beam; the lowest lane wins a tie
     int at = 0;
     const bool on = lane < beams;
-    unsigned long long none = ordered64(-INFINITY);
+    const unsigned long long none = ordered64(-INFINITY);
     unsigned long long head = on ? ordered64(score[lane * K]) : none;
     for (int k = 0; k < K; ++k) {
         const unsigned long long best = warp_max(head);
@@ -399,18 +468,24 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     }
 }
 
-// segments per row and chunks per segment: a few CTAs' worth of segments on every SM, each of at
-// least one chunk
+// Segments per row and chunks per segment: the split whose CTAs take the fewest rounds of chunks, with a
+// CTA's own work (threshold, ranking) counted as one and a half chunks.
 void segment_plan(int64_t rows, int vocab, int elem_bytes, int &segs, int &chunks)
 {
-    constexpr int64_t kCtas = 152 * 8;
+    constexpr int64_t kSlots = 152 * kSelCtas;
     const int64_t chunk = (int64_t)kSelThreads * kSelVecs * (16 / elem_bytes);
     const int64_t all = (vocab + chunk - 1) / chunk;
-    int64_t want = (kCtas + rows - 1) / rows;
-    want = want < 1 ? 1 : want > kSelMaxSegs ? kSelMaxSegs : want;
-    if (want > all) want = all;
-    chunks = (int)((all + want - 1) / want);
-    segs = (int)((all + chunks - 1) / chunks);
+    double best = 0;
+    segs = 0;
+    for (int64_t n = 1; n <= kSelMaxSegs && n <= all; ++n) {
+        const int64_t c = (all + n - 1) / n, used = (all + c - 1) / c;
+        const double cost = (double)((rows * used + kSlots - 1) / kSlots) * (c + 1.5);
+        if (segs == 0 || cost < best) {
+            best = cost;
+            segs = (int)used;
+            chunks = (int)c;
+        }
+    }
 }
 
 bool select_sizes_ok(int32_t batch, int32_t beams, int32_t vocab, int32_t K)

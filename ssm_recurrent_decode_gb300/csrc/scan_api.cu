@@ -66,7 +66,7 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
     if (backward) {
         P.C = kScanBackChunk;
     } else {
-        constexpr int64_t kSlots = 4 * kSms;     // resident CTAs
+        const int64_t kSlots = (P.a.N > 32 ? FBW : FB_MAIN) * kSms;     // resident CTAs
         // Chunks of equal length that fill the GPU once, and no shorter than the 32 rows below which a
         // chunk's own costs (its rates, states and launch) outweigh its rows.
         int64_t C = (T * P.nct + kSlots - 1) / kSlots;
@@ -166,7 +166,7 @@ int mamba_selective_scan(const mamba_scan_args *args, gdn_stream_t stream)
     gdn::set_inputs(P);
     P.has_states = args->h0 || args->h_last;
     const size_t os = args->out_dtype == GDN_BF16 ? 2 : 4;
-    if (gdn::aligned(args->y, 4 * os) && args->y_stride % 4 == 0) P.vec |= gdn::kVecY;
+    if (gdn::aligned(args->y, P.cpt * os) && args->y_stride % P.cpt == 0) P.vec |= gdn::kVecY;
     return gdn::launch_scan_forward(P, reinterpret_cast<cudaStream_t>(stream));
 }
 

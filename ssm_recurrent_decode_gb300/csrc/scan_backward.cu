@@ -238,9 +238,12 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
     if (P.a.T > 0) load_rates(P.a.A, d0, D, n0, N, vst, A2);
     // a lane finishes four channels of every row it is given: the same ones in every tile
     const int oc = warp * Sh::CW + lane % CLN * 4, orow = lane / CLN;
-    float skip[4], dD[4] = {};
+    f2 skip[2], dD[2] = {};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) skip[c] = P.a.Dskip && oc + c < T.ncols ? P.a.Dskip[c0 + oc + c] : 0.f;
+    for (int p = 0; p < 2; ++p) {
+        const int c = oc + 2 * p;
+        skip[p] = pack2(P.a.Dskip && c < T.ncols ? P.a.Dskip[c0 + c] : 0.f, P.a.Dskip && c + 1 < T.ncols ? P.a.Dskip[c0 + c + 1] : 0.f);
+    }
 
     // a gradient of the final state goes straight through an empty sequence
     if (P.g.dh0 && (P.a.cu_seqlens || P.L == 0)) {
@@ -446,32 +449,34 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                     const int r = r0 + orow;
                     if (r >= n || oc >= T.ncols) continue;
                     const int sc = r * YP + lane % CLN * 4;
-                    float gx[4], gt[4], gz[4] = {};
-                    f2 x2[2], d2[2], y2[2], z2[2];
+                    f2 x2[2], d2[2], y2[2], z2[2], g2[2], u2[2], w2[2], s2[2], gx[2], gt[2], gz[2];
                     load_pairs(xs + r * CB + oc, x2);
                     load_pairs(ds + r * CB + oc, d2);
+                    load_pairs(gs + sc, g2);
+                    load_pairs(sum_u + sc, u2);
+                    load_pairs(sum_w + sc, w2);
                     if (P.g.dz) {
                         load_pairs(dys + r * CB + oc, y2);
                         load_pairs(zs + r * CB + oc, z2);
+                        load_pairs(sum_y + sc, s2);
                     }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 xp = unpack2(x2[c / 2]), dp = unpack2(d2[c / 2]);
-                        const float x = c & 1 ? xp.y : xp.x, dtv = c & 1 ? dp.y : dp.x, gk = gs[sc + c], u = sum_u[sc + c];
-                        gx[c] = fmaf(u, dtv, skip[c] * gk);
-                        gt[c] = fmaf(u, x, kLn2 * sum_w[sc + c]);      // A2 = A log2(e)
-                        dD[c] = fmaf(gk, x, dD[c]);
+                    for (int p = 0; p < 2; ++p) {
+                        gx[p] = fma2(u2[p], d2[p], mul2(skip[p], g2[p]));
+                        gt[p] = fma2(u2[p], x2[p], mul2(pack2(kLn2, kLn2), w2[p]));      // A2 = A log2(e)
+                        dD[p] = fma2(g2[p], x2[p], dD[p]);
                         if (P.g.dz) {
-                            const float2 yp = unpack2(y2[c / 2]), zp = unpack2(z2[c / 2]);
-                            const float dy = c & 1 ? yp.y : yp.x, z = c & 1 ? zp.y : zp.x, sg = fast_sigmoid(z);
-                            gz[c] = dy * fmaf(skip[c], x, sum_y[sc + c]) * (sg * fmaf(z, 1.f - sg, 1.f));
+                            const float2 z = unpack2(z2[p]);
+                            const float sx = fast_sigmoid(z.x), sy = fast_sigmoid(z.y);
+                            const f2 slope = pack2(sx * fmaf(z.x, 1.f - sx, 1.f), sy * fmaf(z.y, 1.f - sy, 1.f));
+                            gz[p] = mul2(mul2(y2[p], fma2(skip[p], x2[p], s2[p])), slope);
                         }
                     }
                     const int64_t row = t0 + r;
                     const int left = T.ncols - oc, col = c0 + oc;
-                    if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, P.vec & kVecDx);
-                    if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, P.vec & kVecDdt);
-                    if (P.g.dz) store_row(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, gz, left, P.vec & kVecDz);
+                    if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, (P.vec & kVecDx) && left >= 4);
+                    if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, (P.vec & kVecDdt) && left >= 4);
+                    if (P.g.dz) store_row(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, gz, left, (P.vec & kVecDz) && left >= 4);
                 }
                 // this channel tile's share of dB and dC: the warps' sums in order
                 for (int i = tid; i < n * 2 * NP; i += kScanThreads) {
@@ -490,13 +495,16 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
     store_entries(P.part_a + w * dn, d0, D, n0, N, vst, dA);
     // dD: the lanes that share four channels
 #pragma unroll
-    for (int off = CLN; off < 32; off <<= 1)
+    for (int p = 0; p < 2; ++p) {
+        float2 v = unpack2(dD[p]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) dD[c] += __shfl_xor_sync(kScanFull, dD[c], off);
-    if (orow == 0) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (oc + c < T.ncols) P.part_d[(int64_t)w * D + c0 + oc + c] = dD[c];
+        for (int off = CLN; off < 32; off <<= 1) {
+            v.x += __shfl_xor_sync(kScanFull, v.x, off);
+            v.y += __shfl_xor_sync(kScanFull, v.y, off);
+        }
+        const int c = oc + 2 * p;
+        if (orow == 0 && c < T.ncols) P.part_d[(int64_t)w * D + c0 + c] = v.x;
+        if (orow == 0 && c + 1 < T.ncols) P.part_d[(int64_t)w * D + c0 + c + 1] = v.y;
     }
 }
 

@@ -352,22 +352,32 @@ template <int P> __device__ __forceinline__ void load_rates(const float *A, int 
 }
 
 // a thread's consecutive elements of a row-strided output, as one access where the row allows it
-template <typename T>
-__device__ __forceinline__ void store_row(T *p, const float (&v)[4], int left, bool vec)
+__device__ __forceinline__ void store_whole(float *p, const f2 (&v)[1]) { *reinterpret_cast<f2 *>(p) = v[0]; }
+__device__ __forceinline__ void store_whole(float *p, const f2 (&v)[2]) { store_pairs(p, v); }
+__device__ __forceinline__ uint32_t narrow2(f2 v)
 {
-    if (vec && left >= 4) {
-        store4(p, make_float4(v[0], v[1], v[2], v[3]));
+    const float2 f = unpack2(v);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ void store_whole(bf16 *p, const f2 (&v)[1]) { *reinterpret_cast<uint32_t *>(p) = narrow2(v[0]); }
+__device__ __forceinline__ void store_whole(bf16 *p, const f2 (&v)[2])
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(narrow2(v[0]), narrow2(v[1]));
+}
+// whole: the access is aligned and within the row
+template <typename T, int P> __device__ __forceinline__ void store_row(T *p, const f2 (&v)[P], int left, bool whole)
+{
+    if (whole) {
+        store_whole(p, v);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < left) p[j] = from_f32<T>(v[j]);
+        for (int j = 0; j < P; ++j) {
+            const float2 f = unpack2(v[j]);
+            if (2 * j < left) p[2 * j] = from_f32<T>(f.x);
+            if (2 * j + 1 < left) p[2 * j + 1] = from_f32<T>(f.y);
+        }
     }
-}
-template <typename T>
-__device__ __forceinline__ void store_row(T *p, const float (&v)[2], int left, bool)
-{
-    p[0] = from_f32<T>(v[0]);
-    if (left > 1) p[1] = from_f32<T>(v[1]);
 }
 
 }  // namespace gdn

@@ -6,15 +6,14 @@
 
 namespace gdn {
 
-constexpr int kScanHalf = 8;        // rows between two stores of outputs
-
 // Shared memory, in bytes.
 template <typename Tin, class Sh> struct ScanSmem {
     static constexpr int RX = kScanTile * Sh::CB * (int)sizeof(Tin);     // a staged x, dt or z tile
     static constexpr int RB = kScanTile * Sh::NP * (int)sizeof(Tin);     // a staged B or C tile
     static constexpr int STAGE = 3 * RX + 2 * RB;
+    static constexpr int HALF = 8;                                       // rows between two stores of outputs
     static constexpr int PARTS = Sh::NL <= 4 ? Sh::NL : 1;               // sums over n still to be joined
-    static constexpr int Y = kScanWarps * kScanHalf * PARTS * Sh::YP * 4;
+    static constexpr int Y = kScanWarps * HALF * PARTS * Sh::YP * 4;
     static constexpr int MAIN = 2 * STAGE + Y;
     static constexpr int SUMMARY = 2 * STAGE;
 };
@@ -23,7 +22,7 @@ template <typename Tin, class Sh> struct ScanSmem {
 // of the sequence that goes on behind the chunk); else the outputs. Tiles of 16 rows are staged one
 // ahead by asynchronous copies; a warp's channels are its own, so only the staging needs barriers.
 template <typename Tin, int NL, int CPT, bool SUM>
-__global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
+__global__ void __launch_bounds__(kScanThreads, NL >= 16 ? FBW : FB_MAIN) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
 {
     using Sh = ScanShape<NL, CPT>;
     using Sm = ScanSmem<Tin, Sh>;
@@ -96,6 +95,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
     for (int p = 0; p < PP; ++p) dts[p] = 0ull;
     // a lane finishes CPT channels of every row it is given: the same ones in every tile
     const int oc = warp * Sh::CW + lane % CLN * CPT, orow = lane / CLN;
+    const bool whole = (P.vec & kVecY) && oc + CPT <= ncols;
     f2 skip[PP];
 #pragma unroll
     for (int p = 0; p < PP; ++p) {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
         skip[p] = pack2(!SUM && P.a.Dskip && c < ncols ? P.a.Dskip[c0 + c] : 0.f,
                         !SUM && P.a.Dskip && c + 1 < ncols ? P.a.Dskip[c0 + c + 1] : 0.f);
     }
-    float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * kScanHalf * Sm::PARTS * Sh::YP;
+    float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * Sm::HALF * Sm::PARTS * Sh::YP;
 
     int b = 0;
     while (use.next(P, tl)) {
@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
         f2 dt_tile[PP] = {};
         // rows behind the tile's last are zeros: dt = 0 leaves h as it is
 #pragma unroll 1
-        for (int t8 = 0; t8 < kScanTile; t8 += kScanHalf) {
+        for (int t8 = 0; t8 < kScanTile; t8 += Sm::HALF) {
 #pragma unroll 1
-            for (int t4 = t8; t4 < t8 + kScanHalf; t4 += 4) {
+            for (int t4 = t8; t4 < t8 + Sm::HALF; t4 += 4) {
                 float acc[4 * CPT];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
             __syncwarp();
             // skip, gate and output of these rows
 #pragma unroll
-            for (int r0 = 0; r0 < kScanHalf; r0 += NL) {
+            for (int r0 = 0; r0 < Sm::HALF; r0 += NL) {
                 const int r = r0 + orow, t = t8 + r;
-                if ((NL > kScanHalf && r >= kScanHalf) || t >= tl.n || oc >= ncols) continue;
+                if ((NL > Sm::HALF && r >= Sm::HALF) || t >= tl.n || oc >= ncols) continue;
                 f2 y[PP], x2[PP], z2[PP];
                 load_pairs(ys + r * Sm::PARTS * Sh::YP + lane % CLN * CPT, y);
 #pragma unroll
@@ -190,7 +190,6 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
                 }
                 load_pairs(xs + t * CB + oc, x2);
                 if (P.a.z) load_pairs(zs + t * CB + oc, z2);
-                float out[CPT];
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
                     y[p] = fma2(skip[p], x2[p], y[p]);
@@ -198,15 +197,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_forward_kernel(const __g
                         const float2 z = unpack2(z2[p]);
                         y[p] = mul2(y[p], mul2(z2[p], pack2(fast_sigmoid(z.x), fast_sigmoid(z.y))));
                     }
-                    const float2 v = unpack2(y[p]);
-                    out[2 * p] = tl.seq < 0 ? 0.f : v.x;
-                    out[2 * p + 1] = tl.seq < 0 ? 0.f : v.y;
+                    if (tl.seq < 0) y[p] = 0ull;
                 }
                 const int64_t o = (int64_t)(tl.t0 + t) * P.a.y_stride + c0 + oc;
                 if (P.a.out_dtype == GDN_BF16)
-                    store_row(static_cast<bf16 *>(P.a.y) + o, out, ncols - oc, P.vec & kVecY);
+                    store_row(static_cast<bf16 *>(P.a.y) + o, y, ncols - oc, whole);
                 else
-                    store_row(static_cast<float *>(P.a.y) + o, out, ncols - oc, P.vec & kVecY);
+                    store_row(static_cast<float *>(P.a.y) + o, y, ncols - oc, whole);
             }
             __syncwarp();
         }

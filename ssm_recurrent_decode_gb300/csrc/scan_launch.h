@@ -5,6 +5,15 @@
 #include <cuda_runtime.h>
 
 #include "mamba_scan.h"
+#ifndef FB_MAIN
+#define FB_MAIN 4
+#endif
+#ifndef FB_SUM
+#define FB_SUM 4
+#endif
+#ifndef FBW
+#define FBW 3
+#endif
 
 namespace gdn {
 
