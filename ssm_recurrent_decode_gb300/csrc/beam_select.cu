@@ -14,6 +14,7 @@
 #include "gdn_beam.h"
 #include "gdn_chain.cuh"
 #include "gdn_common.cuh"
+#include "scan_common.cuh"
 
 namespace gdn {
 
@@ -132,35 +133,50 @@ __device__ __forceinline__ float vec_max(const uint4 (&v)[kSelVecs], bf16)
     return fmaxf(__low2float(m), __high2float(m));
 }
 
-// Sum of exp(x - m) over a thread's elements. An element that is NaN counts nothing; an infinite
-// maximum counts its elements.
+__device__ __forceinline__ float exp_fast(float d)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.4426950408889634f));
+    return r;
+}
+
+// Sum of exp(x - m) over a thread's elements, on pairs (the difference first, in its own rounding: it is
+// exact near the maximum). An element that is NaN counts nothing; an infinite maximum counts its elements.
 template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[kSelVecs], float m)
 {
     constexpr int E = Vec16<T>::E;
     if (m == -INFINITY) return 0.f;
-    float s0 = 0.f, s1 = 0.f;
-    const bool finite = m < INFINITY;
+    f2 total = 0ull;
+    const f2 minus = pack2(-m, -m), log2e = pack2(1.4426950408889634f, 1.4426950408889634f);
 #pragma unroll
     for (int k = 0; k < kSelVecs; ++k) {
         float2 x[E / 2];
         unpack16(v[k], x);
 #pragma unroll
         for (int j = 0; j < E / 2; ++j) {
-            s0 += __expf(x[j].x - m);
-            s1 += __expf(x[j].y - m);
+            const float2 d = unpack2(mul2(add2(pack2(x[j].x, x[j].y), minus), log2e));
+            total = add2(total, pack2(ex2_approx(d.x), ex2_approx(d.y)));
         }
     }
-    if (finite && s0 + s1 == s0 + s1) return s0 + s1;
-    s0 = 0.f;
+    const float2 both = unpack2(total);
+    const bool finite = m < INFINITY;
+    float s = both.x + both.y;
+    if (finite && s == s) return s;
+    s = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < kSelVecs * E; ++k) {
+        float y = 0.f;
 #pragma unroll
-    for (int k = 0; k < kSelVecs; ++k) {
-        float2 x[E / 2];
-        unpack16(v[k], x);
+        for (int q = 0; q < kSelVecs; ++q) {       // no dynamic index into registers
+            float2 x[E / 2];
+            unpack16(v[q], x);
 #pragma unroll
-        for (int j = 0; j < E / 2; ++j)
-            for (float y : {x[j].x, x[j].y}) s0 += y == m ? 1.f : y == y && finite ? __expf(y - m) : 0.f;
+            for (int j = 0; j < E; ++j)
+                if (q * E + j == k) y = j & 1 ? x[j / 2].y : x[j / 2].x;
+        }
+        s += y == m ? 1.f : y == y && finite ? exp_fast(y - m) : 0.f;
     }
-    return s0;
+    return s;
 }
 
 // (m, s) of two parts joined
@@ -168,7 +184,7 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float m2, float s
 {
     const float top = fmaxf(m, m2);
     if (top == -INFINITY) return;
-    s = (m == top ? s : s * __expf(m - top)) + (m2 == top ? s2 : s2 * __expf(m2 - top));
+    s = (m == top ? s : s * exp_fast(m - top)) + (m2 == top ? s2 : s2 * exp_fast(m2 - top));
     m = top;
 }
 
@@ -387,11 +403,16 @@ __device__ __forceinline__ double log64(double x)
 // One CTA per batch entry, a warp per beam.
 __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(const __grid_constant__ SelectLaunch P)
 {
+    // fp64 runs at two lanes a clock, so each fp64 step is taken once for all beams (or candidates) side
+    // by side, not in every beam's warp
     extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ double row_sum[GDN_BEAM_MAX_BEAMS];
+    __shared__ float row_top[GDN_BEAM_MAX_BEAMS];
     const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
     const int K = P.a.K, beams = P.a.beams;
     double *score = reinterpret_cast<double *>(smem);                       // [beams, K]
-    int *token = reinterpret_cast<int *>(score + beams * K);                // [beams, K]
+    float *logit = reinterpret_cast<float *>(score + beams * K);            // [beams, K]
+    int *token = reinterpret_cast<int *>(logit + beams * K);                // [beams, K]
     const int64_t beam = (int64_t)blockIdx.x * beams + j;
 
     // The call's inputs may be read before the wait: this kernel's CTAs start when every CTA of the
@@ -401,8 +422,12 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     const bool live = cum > -INFINITY && r >= 0 && r < P.a.num_rows;
     const bool done = P.a.finished && P.a.finished[beam] && cum > -INFINITY;
     for (int k = lane; k < K; k += 32) {
-        score[j * K + k] = done && k == 0 ? (double)cum : -INFINITY;
+        logit[j * K + k] = done && k == 0 ? 0.f : -INFINITY;
         token[j * K + k] = done && k == 0 ? P.a.eos_token : -1;
+    }
+    if (lane == 0) {
+        row_sum[j] = 1.0;            // an ended beam: score + 0 - log 1
+        row_top[j] = 0.f;
     }
     __syncwarp();
     ordinary_launch_start();
@@ -412,16 +437,19 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
         const unsigned long long *mine = P.keys + (beam * P.segs + lane) * K;
         const float2 st = on ? P.stats[beam * P.segs + lane] : make_float2(-INFINITY, 0.f);
         unsigned long long head = on ? mine[0] : 0, next = on && K > 1 ? mine[1] : 0;
-        // the row's maximum, and the logarithm of its sum
+        // the row's maximum and sum
         float top = st.x;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
+        int lanes = 1;
+        while (lanes < P.segs) lanes *= 2;
+        for (int off = lanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
+        top = __shfl_sync(kFullMask, top, 0);
         if (top > -INFINITY) {
-            double sum = st.x == -INFINITY ? 0.0 : st.x == top ? (double)st.y : (double)(st.y * __expf(st.x - top));
-            int lanes = 1;
-            while (lanes < P.segs) lanes *= 2;
+            double sum = st.x == -INFINITY ? 0.0 : st.x == top ? (double)st.y : (double)(st.y * exp_fast(st.x - top));
             for (int off = lanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
-            const double base = (double)cum, norm = log64(__shfl_sync(kFullMask, sum, 0));
+            if (lane == 0) {
+                row_sum[j] = sum;
+                row_top[j] = top;
+            }
             int at = 2;
             for (int k = 0; k < K; ++k) {
                 const unsigned long long best = warp_max(head);
@@ -432,12 +460,20 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
                     ++at;
                 }
                 if (lane == 0) {
-                    const float x = unordered((unsigned)(best >> 32));
-                    score[j * K + k] = base + ((x == top ? 0.0 : (double)x - (double)top) - norm);
+                    logit[j * K + k] = unordered((unsigned)(best >> 32));
                     token[j * K + k] = (int)(0xFFFFFFFFu - (unsigned)best);
                 }
             }
         }
+    }
+    __syncthreads();
+    if (j == 0 && lane < beams) row_sum[lane] = log64(row_sum[lane]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < beams * K; i += 32 * beams) {
+        const int q = i / K;
+        const float x = logit[i], top = row_top[q];
+        const double base = (double)P.a.scores[(int64_t)blockIdx.x * beams + q];
+        score[i] = x == -INFINITY ? -INFINITY : base + ((x == top ? 0.0 : (double)x - (double)top) - row_sum[q]);
     }
     __syncthreads();
     if (j != 0) return;
@@ -545,7 +581,7 @@ int gdn_beam_select(const gdn_beam_select_args *a, gdn_stream_t stream)
     const auto kern = es == 2 ? (shifted ? beam_segment_kernel<bf16, true> : beam_segment_kernel<bf16, false>)
                               : (shifted ? beam_segment_kernel<float, true> : beam_segment_kernel<float, false>);
     if (launch_ordinary(kern, grid, dim3(kSelThreads), 0, s, P) != cudaSuccess) return GDN_ERR_LAUNCH;
-    const size_t smem = (size_t)a->beams * a->K * 12;
+    const size_t smem = (size_t)a->beams * a->K * 16;
     return launch_ordinary(beam_join_kernel, dim3((unsigned)a->batch), dim3(32u * a->beams), smem, s, P) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_LAUNCH;
