@@ -1,13 +1,12 @@
 // beam_select.cu -- one beam-search selection (gdn_beam_select).
 //
 // Launch 1 reads the logits once: a CTA takes a segment of one beam's row, keeps the running maximum
-// and sum of exponentials, and the segment's K best logits. Candidates are found by a threshold:
-// after the first chunk of the segment, the smallest over the eight warps of the warp's
-// ceil(K / 8)-th largest per-lane maximum is a value that at least K elements reach, and only a few
-// more do; after that the K-th best so far, which hardly any element passes. Only those elements are
-// ranked. Launch 2, one CTA per batch entry, joins the segments of each row (a warp per beam), then
-// the beams.
-// Bound by reading the logits: 5 instructions per element stay below the memory time.
+// and sum of exponentials, and the segment's K best logits. Only elements that reach a threshold
+// become candidates. In the segment's first chunk it is the smallest over the eight warps of the warp's
+// ceil(K / 8)-th largest per-lane maximum: at least K elements reach it, and only a few more do. After
+// that chunk it is the K-th best found there, and the warps go on without barriers, each appending what
+// passes to a list of its own (a full list is cut to its K best). All lists are ranked at the end.
+// Launch 2, one CTA per batch entry, joins the segments of each row (a warp per beam), then the beams.
 #include <cmath>
 #include <cstdint>
 
@@ -23,18 +22,17 @@ namespace {
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelVecs = 4;                 // 16-byte loads per thread and chunk, all in flight
-#ifndef KSEL
-#define KSEL 4
-#endif
-constexpr int kSelCtas = KSEL;                 // resident CTAs per SM
-constexpr int kSelCap = 1024;               // candidates kept before they are ranked
+constexpr int kSelCtas = 3;                 // resident CTAs per SM
+constexpr int kSelCap = 128;                // candidates of a warp
 constexpr int kSelMaxSegs = 32;             // segments per row: a lane each in the join
 constexpr unsigned kFullMask = 0xFFFFFFFFu;
+constexpr float kLowest = -3.402823466e38f;  // every finite logit reaches it
 
 struct SelectLaunch {
     gdn_beam_select_args a;
     int segs;             // segments per row
     int chunks;           // chunks per segment
+    int staged;           // the join copies the segments' keys to shared memory
     unsigned long long *keys;   // [batch * beams, segs, K] best first, 0: none
     float2 *stats;              // [batch * beams, segs] maximum, sum of exp(logit - maximum)
 };
@@ -76,14 +74,14 @@ __device__ __forceinline__ void unpack16(uint4 v, float2 (&x)[4])
 // row that starts `shift` elements behind a 16-byte boundary they lie in two aligned vectors and are
 // shifted out of them: which thread adds up which elements depends on their index alone, so that equal
 // rows give bit-equal sums wherever they lie.
-template <typename T, bool SHIFTED> __device__ __forceinline__ uint4 load_vec(const T *row, int64_t i, int V, int shift)
+template <typename T, bool SHIFTED> __device__ __forceinline__ uint4 load_vec(const T *row, unsigned i, unsigned V, unsigned shift)
 {
-    constexpr int E = Vec16<T>::E;
+    constexpr unsigned E = Vec16<T>::E;
     if (!SHIFTED && i + E <= V) return __ldcs(reinterpret_cast<const uint4 *>(row + i));
     if (SHIFTED && i >= shift && i - shift + 2 * E <= V) {
         const uint4 lo = *reinterpret_cast<const uint4 *>(row + i - shift), hi = *reinterpret_cast<const uint4 *>(row + i - shift + E);
         unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const int words = shift * (int)sizeof(T) / 4;
+        const unsigned words = shift * (unsigned)sizeof(T) / 4;
         if (words & 2) {
 #pragma unroll
             for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
@@ -112,25 +110,18 @@ template <typename T, bool SHIFTED> __device__ __forceinline__ uint4 load_vec(co
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// the largest of a vector's elements (NaN only if all are)
-__device__ __forceinline__ float vec_max(const uint4 (&v)[kSelVecs], float)
+// the largest of a vector's elements; NaN counts as -inf
+__device__ __forceinline__ float vec_max(uint4 v, float)
 {
-    float m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kSelVecs; ++k)
-        m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v[k].x)), fmaxf(__uint_as_float(v[k].y), __uint_as_float(v[k].z))), __uint_as_float(v[k].w));
-    return m;
+    return fmaxf(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))), -INFINITY);
 }
-__device__ __forceinline__ float vec_max(const uint4 (&v)[kSelVecs], bf16)
+__device__ __forceinline__ float vec_max(uint4 v, bf16)
 {
-    __nv_bfloat162 m = __float2bfloat162_rn(-INFINITY);
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&w[0]);
 #pragma unroll
-    for (int k = 0; k < kSelVecs; ++k) {
-        const unsigned w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-    }
-    return fmaxf(__low2float(m), __high2float(m));
+    for (int j = 1; j < 4; ++j) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
 }
 
 __device__ __forceinline__ float exp_fast(float d)
@@ -140,12 +131,11 @@ __device__ __forceinline__ float exp_fast(float d)
     return r;
 }
 
-// Sum of exp(x - m) over a thread's elements, on pairs (the difference first, in its own rounding: it is
-// exact near the maximum). An element that is NaN counts nothing; an infinite maximum counts its elements.
+// Sum of exp(x - m) over a thread's elements for a finite m, on pairs (the difference first, in its own
+// rounding: it is exact near the maximum). NaN where an element is.
 template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[kSelVecs], float m)
 {
     constexpr int E = Vec16<T>::E;
-    if (m == -INFINITY) return 0.f;
     f2 total = 0ull;
     const f2 minus = pack2(-m, -m), log2e = pack2(1.4426950408889634f, 1.4426950408889634f);
 #pragma unroll
@@ -159,22 +149,19 @@ template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[
         }
     }
     const float2 both = unpack2(total);
-    const bool finite = m < INFINITY;
-    float s = both.x + both.y;
-    if (finite && s == s) return s;
-    s = 0.f;
-#pragma unroll 1
-    for (int k = 0; k < kSelVecs * E; ++k) {
-        float y = 0.f;
-#pragma unroll
-        for (int q = 0; q < kSelVecs; ++q) {       // no dynamic index into registers
-            float2 x[E / 2];
-            unpack16(v[q], x);
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (q * E + j == k) y = j & 1 ? x[j / 2].y : x[j / 2].x;
-        }
-        s += y == m ? 1.f : y == y && finite ? exp_fast(y - m) : 0.f;
+    return both.x + both.y;
+}
+
+// The same for any m, element by element from memory: NaN counts nothing, an infinite maximum counts its
+// elements. Rare, and kept out of the loop's code.
+template <typename T> __device__ __noinline__ float exp_sum_careful(const T *row, unsigned base, unsigned V, float m)
+{
+    constexpr unsigned E = Vec16<T>::E;
+    float s = 0.f;
+    for (unsigned k = 0; k < kSelVecs * E; ++k) {
+        const unsigned i = base + (k / E * kSelThreads + threadIdx.x) * E + k % E;
+        const float y = i < V ? to_f32(row[i]) : -INFINITY;
+        s += y == m ? 1.f : y == y && m < INFINITY ? exp_fast(y - m) : 0.f;
     }
     return s;
 }
@@ -188,22 +175,40 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float m2, float s
     m = top;
 }
 
-// Ranks list[0 .. n) (all different) and leaves its best min(n, K) in order at its front. Contains
-// barriers; every thread calls it. `sorted` holds K keys.
-__device__ __forceinline__ void rank_list(unsigned long long *list, int n, int K, unsigned long long *sorted, int tid)
+// How many of n keys (all different) are larger than k.
+__device__ __forceinline__ int rank_of(unsigned long long k, const unsigned long long *keys, int n)
 {
-    for (int i = tid; i < n; i += kSelThreads) {
-        const unsigned long long k = list[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += list[j] > k;
-        if (rank < K) sorted[rank] = k;
-    }
-    __syncthreads();
-    for (int i = tid; i < min(n, K); i += kSelThreads) list[i] = sorted[i];
-    __syncthreads();
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += keys[j] > k;
+    return rank;
 }
 
-// Every warp's k-th largest of its lanes' values (-inf where it has fewer): the largest or the smallest
+// A warp cuts its list of n candidates to the K best, in order; returns how many are left.
+__device__ __noinline__ int cut_list(unsigned long long *list, int n, int K, int lane)
+{
+    unsigned long long k[kSelCap / 32];
+    int rank[kSelCap / 32];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kSelCap / 32; ++i) {
+        k[i] = i * 32 + lane < n ? list[i * 32 + lane] : 0;
+        rank[i] = k[i] ? 0 : K;
+    }
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long o = list[j];
+#pragma unroll
+        for (int i = 0; i < kSelCap / 32; ++i) rank[i] += o > k[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kSelCap / 32; ++i)
+        if (rank[i] < K) list[rank[i]] = k[i];
+    __syncwarp();
+    return min(n, K);
+}
+
+// Every warp's k-th largest of its lanes' values (the lowest finite value where it has fewer): the largest or the smallest
 // of them over the warps. Contains barriers.
 __device__ __forceinline__ float kth_top(float top, int k, int lane, int warp, float *wthr, bool largest)
 {
@@ -214,7 +219,7 @@ __device__ __forceinline__ float kth_top(float top, int k, int lane, int warp, f
         if (lane == __ffs(at) - 1) mine = 0;
     }
     __syncthreads();
-    if (lane == 0) wthr[warp] = best ? unordered(best) : -INFINITY;
+    if (lane == 0) wthr[warp] = best ? unordered(best) : kLowest;
     __syncthreads();
     float t = wthr[0];
 #pragma unroll
@@ -225,124 +230,150 @@ __device__ __forceinline__ float kth_top(float top, int k, int lane, int warp, f
 template <typename T, bool SHIFTED>
 __global__ void __launch_bounds__(kSelThreads, kSelCtas) beam_segment_kernel(const __grid_constant__ SelectLaunch P)
 {
-    constexpr int E = Vec16<T>::E;
-    constexpr int64_t CHUNK = (int64_t)kSelThreads * kSelVecs * E;
-    __shared__ unsigned long long list[kSelCap], sorted[GDN_BEAM_MAX_SELECT];
+    constexpr unsigned E = Vec16<T>::E, CHUNK = kSelThreads * kSelVecs * E;
+    __shared__ unsigned long long lists[kSelWarps][kSelCap];
+    __shared__ unsigned long long all[kSelWarps * kSelCap];
     __shared__ float wthr[kSelWarps], wm[kSelWarps], ws[kSelWarps];
-    __shared__ unsigned long long wkey[kSelWarps];
-    __shared__ int count;
+    __shared__ int wcount[kSelWarps];
+    __shared__ float kth;
     ordinary_launch_start();
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int beam = (int)(blockIdx.x / (unsigned)P.segs), seg = (int)(blockIdx.x % (unsigned)P.segs);
-    const int V = P.a.vocab, K = P.a.K;
+    const unsigned V = (unsigned)P.a.vocab;
+    const int K = P.a.K;
     unsigned long long *out = P.keys + ((int64_t)beam * P.segs + seg) * K;
     const int64_t r = P.a.rows ? (int64_t)P.a.rows[beam] : beam;
+    const float cum = P.a.scores[beam];
+    const bool ended = P.a.finished && P.a.finished[beam];
     if (r < 0 || r >= P.a.num_rows) {
         if (tid == 0 && seg == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
         return;                                   // the join does not look at this beam
     }
-    if (!(P.a.scores[beam] > -INFINITY) || (P.a.finished && P.a.finished[beam])) return;
+    if (!(cum > -INFINITY) || ended) return;
 
     const T *row = static_cast<const T *>(P.a.logits) + r * P.a.row_stride;
-    const int shift = SHIFTED ? (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)) : 0;
-    const int64_t first = (int64_t)seg * P.chunks * CHUNK;
-    const int64_t last = min((int64_t)V, first + P.chunks * CHUNK);     // the segment: elements first .. last - 1
+    const unsigned shift = SHIFTED ? (unsigned)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)) : 0;
+    // the segment: elements first .. last - 1 (below 2^32: vocab fits 31 bits)
+    const unsigned first = (unsigned)seg * P.chunks * CHUNK, last = min(V, first + P.chunks * CHUNK);
 
     float m = -INFINITY, s = 0.f;
-    float thr = -INFINITY;       // candidates are above it (full) or reach it (not yet K found)
-    bool full = false, overflow = false;
-    if (tid == 0) count = 0;
-    __syncthreads();
+    float thr = kLowest;         // candidates reach it (strict: are above it); -inf and NaN never do
+    bool strict = false;
+    unsigned long long *list = lists[warp];
+    int n = 0;                   // candidates in this warp's list
     uint4 ahead[kSelVecs];
 #pragma unroll
-    for (int v = 0; v < kSelVecs; ++v) ahead[v] = load_vec<T, SHIFTED>(row, first + ((int64_t)v * kSelThreads + tid) * E, V, shift);
-    for (int64_t base = first; base < last; base += CHUNK) {
+    for (int v = 0; v < kSelVecs; ++v) ahead[v] = load_vec<T, SHIFTED>(row, first + (v * kSelThreads + tid) * E, V, shift);
+    for (unsigned base = first; base < last; base += CHUNK) {
         uint4 x[kSelVecs];
+        float vtop[kSelVecs], top = m;
 #pragma unroll
-        for (int v = 0; v < kSelVecs; ++v) x[v] = ahead[v];
+        for (int v = 0; v < kSelVecs; ++v) {
+            x[v] = ahead[v];
+            vtop[v] = vec_max(x[v], T());
+            top = fmaxf(top, vtop[v]);
+        }
         if (base + CHUNK < last) {
 #pragma unroll
             for (int v = 0; v < kSelVecs; ++v)
-                ahead[v] = load_vec<T, SHIFTED>(row, base + CHUNK + ((int64_t)v * kSelThreads + tid) * E, V, shift);
+                ahead[v] = load_vec<T, SHIFTED>(row, base + CHUNK + (v * kSelThreads + tid) * E, V, shift);
         }
-        const float top = vec_max(x, T());
-        join_stats(m, s, top, exp_sum<T>(x, top));
-
+        if (top > -INFINITY) {
+            float more = exp_sum<T>(x, top);
+            if (!(top < INFINITY && more == more)) more = exp_sum_careful(row, base, V, top);
+            s = more + (m == top ? s : s * exp_fast(m - top));
+            m = top;
+        }
         if (base == first) {
             // a value that at least K elements reach, if there are as many: from every warp its share,
             // or, where warps have too few values, K from one of them
             thr = kth_top(top, (K + kSelWarps - 1) / kSelWarps, lane, warp, wthr, false);
-            if (thr == -INFINITY && K <= 32) thr = kth_top(top, K, lane, warp, wthr, true);
+            if (thr == kLowest && K <= 32) thr = kth_top(top, K, lane, warp, wthr, true);
         }
-        if (full ? top > thr : top >= thr) {
 #pragma unroll
-            for (int v = 0; v < kSelVecs; ++v) {
-                const int64_t i = base + ((int64_t)v * kSelThreads + tid) * E;
-                float2 e[E / 2];
-                unpack16(x[v], e);
+        for (int v = 0; v < kSelVecs; ++v) {
+            if (!__any_sync(kFullMask, strict ? vtop[v] > thr : vtop[v] >= thr)) continue;
+            unsigned bits = 0;       // which of the vector's elements pass
+            float2 e[E / 2];
+            unpack16(x[v], e);
 #pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    const float y = k & 1 ? e[k / 2].y : e[k / 2].x;
-                    if ((full ? y > thr : y >= thr) && y > -INFINITY) {
-                        const int at = atomicAdd(&count, 1);
-                        if (at < kSelCap) list[at] = make_key(y, (int)(i + k));
+            for (int k = 0; k < E; ++k) {
+                const float y = k & 1 ? e[k / 2].y : e[k / 2].x;
+                if (strict ? y > thr : y >= thr) bits |= 1u << k;
+            }
+            const unsigned i = base + (v * kSelThreads + tid) * E;
+            unsigned lanes;
+            while ((lanes = __ballot_sync(kFullMask, bits != 0)) != 0) {
+                if (n + 32 > kSelCap) {
+                    n = cut_list(list, n, K, lane);
+                    const float own = unordered((unsigned)(list[K - 1] >> 32));     // more than K were there
+                    if (own > thr) {
+                        thr = own;
+                        strict = false;          // an equal one in this chunk may have a lower token
                     }
                 }
+                if (bits) {
+                    const int at = __ffs(bits) - 1;
+                    bits &= bits - 1;
+                    float y = e[0].x;
+#pragma unroll
+                    for (int k = 1; k < E; ++k)
+                        if (at == k) y = k & 1 ? e[k / 2].y : e[k / 2].x;
+                    list[n + __popc(lanes & ((1u << lane) - 1))] = make_key(y, (int)(i + at));
+                }
+                n += __popc(lanes);
             }
         }
-        __syncthreads();
-        const int n = count;
-        __syncthreads();             // nobody adds to the next chunk's count before all have read this one
-        if (n > kSelCap) {
-            overflow = true;
-            break;
-        }
-        if (n >= K && n > (full ? K : 0) && base + CHUNK < last) {
-            rank_list(list, n, K, sorted, tid);
-            if (tid == 0) count = K;
-            thr = unordered((unsigned)(list[K - 1] >> 32));
-            full = true;
+        if (base + CHUNK >= last) break;
+        if (base == first) {
+            // the K-th best so far: later elements that only equal it have higher tokens
+            if (n > K) n = cut_list(list, n, K, lane);
+            if (lane == 0) wcount[warp] = n;
+            if (tid == 0) kth = kLowest;
             __syncthreads();
+            int total = 0, before = 0;
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w) {
+                before += w < warp ? wcount[w] : 0;
+                total += wcount[w];
+            }
+            for (int j = lane; j < n; j += 32) all[before + j] = list[j];
+            __syncthreads();
+            for (int j = tid; j < total; j += kSelThreads)
+                if (rank_of(all[j], all, total) == K - 1) kth = unordered((unsigned)(all[j] >> 32));
+            __syncthreads();
+            if (total >= K) {
+                thr = kth;
+                strict = true;
+            }
+        } else if (n >= 2 * K + 16) {
+            n = cut_list(list, n, K, lane);
+            const float own = unordered((unsigned)(list[K - 1] >> 32));
+            if (own >= thr) {
+                thr = own;
+                strict = true;
+            }
         }
     }
-    if (overflow) {
-        // Many equal values, or an adversarial order: exactly, one candidate at a time.
-        m = -INFINITY;
-        s = 0.f;
-        unsigned long long before = ~0ull;
-        for (int k = 0; k < K; ++k) {
-            unsigned long long best = 0;
-            for (int64_t i = first + tid; i < last; i += kSelThreads) {
-                const float y = to_f32(row[i]);
-                if (!(y > -INFINITY)) continue;
-                const unsigned long long key = make_key(y, (int)i);
-                if (key < before && key > best) best = key;
-                if (k == 0) join_stats(m, s, y, 1.f);
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                const unsigned long long o = __shfl_xor_sync(kFullMask, best, off);
-                best = o > best ? o : best;
-            }
-            __syncthreads();
-            if (lane == 0) wkey[warp] = best;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kSelWarps; ++w) best = wkey[w] > best ? wkey[w] : best;
-            if (tid == 0) out[k] = best;
-            before = best;                        // 0 once there are none left
-        }
-    } else {
-        const int n = count;
+    {
+        if (n > K) n = cut_list(list, n, K, lane);
+        __syncthreads();             // wcount and all may still be read
+        if (lane == 0) wcount[warp] = n;
         __syncthreads();
-        for (int i = tid; i < n; i += kSelThreads) {
-            const unsigned long long k = list[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += list[j] > k;
-            if (rank < K) out[rank] = k;
+        int total = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) {
+            before += w < warp ? wcount[w] : 0;
+            total += wcount[w];
         }
-        for (int i = n + tid; i < K; i += kSelThreads) out[i] = 0;
+        for (int j = lane; j < n; j += 32) all[before + j] = list[j];
+        __syncthreads();
+        for (int j = tid; j < total; j += kSelThreads) {
+            const int rank = rank_of(all[j], all, total);
+            if (rank < K) out[rank] = all[j];
+        }
+        for (int j = total + tid; j < K; j += kSelThreads) out[j] = 0;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
@@ -373,31 +404,22 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
     return (unsigned long long)hi << 32 | lo;
 }
 
-// log(x) for a normal x > 0 in fp64, to about 1e-15: x = 2^e f with f in [sqrt(1/2), sqrt(2)), and
-// log f = 2 atanh(q) = 2 (q + q^3/3 + ...) at q = (f - 1) / (f + 1), |q| <= 0.1716 (11 terms)
+// log(x) for a normal x > 0 in fp64, to about 1e-9: x = 2^e f with f in [sqrt(1/2), sqrt(2)), and
+// log f = 2 atanh(q) = 2 (q + q^3/3 + ... + q^9/9) at q = (f - 1) / (f + 1), |q| <= 0.1716 (the next term
+// is below 7e-10). The division is a fp32 reciprocal with one Newton step.
 __device__ __forceinline__ double log64(double x)
 {
-    long long b = __double_as_longlong(x);
+    const long long b = __double_as_longlong(x);
     int e = (int)(b >> 52) - 1023;
     double f = __longlong_as_double((b & 0x000FFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
     if (f > 1.4142135623730951) {
         f *= 0.5;
         ++e;
     }
-    const double q = (f - 1.0) / (f + 1.0), q2 = q * q;
-    // even and odd terms side by side, to halve the chain
-    const double q4 = q2 * q2;
-    double even = 1.0 / 21, odd = 1.0 / 19;
-    even = fma(even, q4, 1.0 / 17);
-    odd = fma(odd, q4, 1.0 / 15);
-    even = fma(even, q4, 1.0 / 13);
-    odd = fma(odd, q4, 1.0 / 11);
-    even = fma(even, q4, 1.0 / 9);
-    odd = fma(odd, q4, 1.0 / 7);
-    even = fma(even, q4, 1.0 / 5);
-    odd = fma(odd, q4, 1.0 / 3);
-    even = fma(even, q4, 1.0);
-    return fma((double)e, 0.69314718055994530942, 2.0 * q * fma(odd, q2, even));
+    const double den = f + 1.0, r0 = (double)(1.0f / (float)den);
+    const double r = fma(r0, fma(-den, r0, 1.0), r0), q = (f - 1.0) * r, q2 = q * q;
+    const double p = fma(fma(fma(fma(1.0 / 9, q2, 1.0 / 7), q2, 1.0 / 5), q2, 1.0 / 3), q2, 1.0);
+    return fma((double)e, 0.69314718055994530942, 2.0 * q * p);
 }
 
 // One CTA per batch entry, a warp per beam.
@@ -407,12 +429,13 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     // by side, not in every beam's warp
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ double row_sum[GDN_BEAM_MAX_BEAMS];
-    __shared__ float row_top[GDN_BEAM_MAX_BEAMS];
+    __shared__ float row_top[GDN_BEAM_MAX_BEAMS], row_cum[GDN_BEAM_MAX_BEAMS];
     const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
     const int K = P.a.K, beams = P.a.beams;
     double *score = reinterpret_cast<double *>(smem);                       // [beams, K]
     float *logit = reinterpret_cast<float *>(score + beams * K);            // [beams, K]
     int *token = reinterpret_cast<int *>(logit + beams * K);                // [beams, K]
+    unsigned long long *keys = reinterpret_cast<unsigned long long *>(token + beams * K);   // [beams, segs, K] where they fit
     const int64_t beam = (int64_t)blockIdx.x * beams + j;
 
     // The call's inputs may be read before the wait: this kernel's CTAs start when every CTA of the
@@ -428,6 +451,7 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     if (lane == 0) {
         row_sum[j] = 1.0;            // an ended beam: score + 0 - log 1
         row_top[j] = 0.f;
+        row_cum[j] = cum;
     }
     __syncwarp();
     ordinary_launch_start();
@@ -435,6 +459,12 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
         // the segments' lists, best first: a lane's two next keys are at hand
         const bool on = lane < P.segs;
         const unsigned long long *mine = P.keys + (beam * P.segs + lane) * K;
+        if (P.staged) {
+            unsigned long long *mem = keys + j * P.segs * K;
+            for (int i = lane; i < P.segs * K; i += 32) mem[i] = P.keys[beam * P.segs * K + i];
+            __syncwarp();
+            mine = mem + lane * K;
+        }
         const float2 st = on ? P.stats[beam * P.segs + lane] : make_float2(-INFINITY, 0.f);
         unsigned long long head = on ? mine[0] : 0, next = on && K > 1 ? mine[1] : 0;
         // the row's maximum and sum
@@ -450,18 +480,30 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
                 row_sum[j] = sum;
                 row_top[j] = top;
             }
-            int at = 2;
-            for (int k = 0; k < K; ++k) {
-                const unsigned long long best = warp_max(head);
-                if (best == 0) break;
-                if (head == best) {
-                    head = next;
-                    next = on && at < K ? mine[at] : 0;
-                    ++at;
+            if (P.staged && P.segs * K <= 128) {
+                // few keys: each is ranked against all
+                for (int i = lane; i < P.segs * K; i += 32) {
+                    const unsigned long long key = keys[j * P.segs * K + i];
+                    const int rank = rank_of(key, keys + j * P.segs * K, P.segs * K);
+                    if (key != 0 && rank < K) {
+                        logit[j * K + rank] = unordered((unsigned)(key >> 32));
+                        token[j * K + rank] = (int)(0xFFFFFFFFu - (unsigned)key);
+                    }
                 }
-                if (lane == 0) {
-                    logit[j * K + k] = unordered((unsigned)(best >> 32));
-                    token[j * K + k] = (int)(0xFFFFFFFFu - (unsigned)best);
+            } else {
+                int at = 2;
+                for (int k = 0; k < K; ++k) {
+                    const unsigned long long best = warp_max(head);
+                    if (best == 0) break;
+                    if (head == best) {
+                        head = next;
+                        next = on && at < K ? mine[at] : 0;
+                        ++at;
+                    }
+                    if (lane == 0) {
+                        logit[j * K + k] = unordered((unsigned)(best >> 32));
+                        token[j * K + k] = (int)(0xFFFFFFFFu - (unsigned)best);
+                    }
                 }
             }
         }
@@ -469,37 +511,65 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     __syncthreads();
     if (j == 0 && lane < beams) row_sum[lane] = log64(row_sum[lane]);
     __syncthreads();
+    unsigned long long *order = reinterpret_cast<unsigned long long *>(score);      // the scores, as integers in their order
+    const unsigned long long none = ordered64(-INFINITY);
     for (int i = threadIdx.x; i < beams * K; i += 32 * beams) {
         const int q = i / K;
         const float x = logit[i], top = row_top[q];
-        const double base = (double)P.a.scores[(int64_t)blockIdx.x * beams + q];
-        score[i] = x == -INFINITY ? -INFINITY : base + ((x == top ? 0.0 : (double)x - (double)top) - row_sum[q]);
+        const double v = (double)row_cum[q] + ((x == top ? 0.0 : (double)x - (double)top) - row_sum[q]);
+        logit[i] = (float)v;
+        order[i] = x == -INFINITY ? none : ordered64(v);
     }
     __syncthreads();
+    const int64_t out = (int64_t)blockIdx.x * K;
+    const auto put = [&](int k, int i) {
+        const int t = token[i];
+        P.a.out_scores[out + k] = logit[i];
+        P.a.out_parents[out + k] = i / K;
+        P.a.out_tokens[out + k] = t;
+        if (P.a.out_finished) P.a.out_finished[out + k] = t == P.a.eos_token;
+    };
+    const auto put_none = [&](int k) {
+        P.a.out_scores[out + k] = -INFINITY;
+        P.a.out_parents[out + k] = -1;
+        P.a.out_tokens[out + k] = -1;
+        if (P.a.out_finished) P.a.out_finished[out + k] = 0;
+    };
+    if (beams * K <= 256) {
+        // few candidates: each is ranked against all, equal ones by beam
+        int live_here = 0;
+        for (int i = threadIdx.x; i < beams * K; i += 32 * beams) {
+            const unsigned long long v = order[i];
+            int rank = 0;
+#pragma unroll 4
+            for (int o = 0; o < beams * K; ++o) rank += order[o] > v || (order[o] == v && o < i);
+            if (v > none) {
+                ++live_here;
+                if (rank < K) put(rank, i);
+            }
+        }
+        __shared__ int found;
+        if (threadIdx.x == 0) found = 0;
+        __syncthreads();
+        if (live_here) atomicAdd(&found, live_here);
+        __syncthreads();
+        for (int k = found + threadIdx.x; k < K; k += 32 * beams) put_none(k);
+        return;
+    }
     if (j != 0) return;
     // the beams' lists: a lane per beam; the lowest lane wins a tie
     int at = 0;
     const bool on = lane < beams;
-    const unsigned long long none = ordered64(-INFINITY);
-    unsigned long long head = on ? ordered64(score[lane * K]) : none;
+    unsigned long long head = on ? order[lane * K] : none;
     for (int k = 0; k < K; ++k) {
         const unsigned long long best = warp_max(head);
-        const bool any = best > none;
         const int who = __ffs(__ballot_sync(kFullMask, on && head == best)) - 1;
-        const int64_t o = (int64_t)blockIdx.x * K + k;
-        if (any && lane == who) {
-            const int t = token[lane * K + at];
-            P.a.out_scores[o] = (float)score[lane * K + at];
-            P.a.out_parents[o] = lane;
-            P.a.out_tokens[o] = t;
-            if (P.a.out_finished) P.a.out_finished[o] = t == P.a.eos_token;
+        if (best > none && lane == who) {
+            put(k, lane * K + at);
             ++at;
-            head = at < K ? ordered64(score[lane * K + at]) : none;
-        } else if (!any && lane == 0) {
-            P.a.out_scores[o] = -INFINITY;
-            P.a.out_parents[o] = -1;
-            P.a.out_tokens[o] = -1;
-            if (P.a.out_finished) P.a.out_finished[o] = 0;
+            head = at < K ? order[lane * K + at] : none;
+        } else if (best <= none && lane == 0) {
+            put_none(k);
         }
     }
 }
@@ -581,7 +651,10 @@ int gdn_beam_select(const gdn_beam_select_args *a, gdn_stream_t stream)
     const auto kern = es == 2 ? (shifted ? beam_segment_kernel<bf16, true> : beam_segment_kernel<bf16, false>)
                               : (shifted ? beam_segment_kernel<float, true> : beam_segment_kernel<float, false>);
     if (launch_ordinary(kern, grid, dim3(kSelThreads), 0, s, P) != cudaSuccess) return GDN_ERR_LAUNCH;
-    const size_t smem = (size_t)a->beams * a->K * 16;
+    size_t smem = (size_t)a->beams * a->K * 16;
+    const size_t keys = (size_t)a->beams * P.segs * a->K * 8;
+    P.staged = smem + keys <= 40 * 1024;
+    if (P.staged) smem += keys;
     return launch_ordinary(beam_join_kernel, dim3((unsigned)a->batch), dim3(32u * a->beams), smem, s, P) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_LAUNCH;
