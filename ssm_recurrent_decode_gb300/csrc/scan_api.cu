@@ -64,9 +64,12 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
     P.cpt = 4;
     P.nct = tiles(4);
     if (backward) {
-        P.C = kScanBackChunk;
+        // Chunks of 64 rows (what the states kept per CTA allow), shorter ones where those would leave SMs
+        // without work.
+        const int64_t C = (T * P.nct + kScanBackCtas * kSms - 1) / (kScanBackCtas * kSms);
+        P.C = (int)(C >= kScanBackChunk ? kScanBackChunk : C <= 16 ? 16 : (C + 7) / 8 * 8);
     } else {
-        const int64_t kSlots = (P.a.N > 32 ? FBW : FB_MAIN) * kSms;     // resident CTAs
+        const int64_t kSlots = (int64_t)scan_ctas(scan_lanes(P.a.N)) * kSms;     // resident CTAs
         // Chunks of equal length that fill the GPU once, and no shorter than the 32 rows below which a
         // chunk's own costs (its rates, states and launch) outweigh its rows.
         int64_t C = (T * P.nct + kSlots - 1) / kSlots;
@@ -83,7 +86,7 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
     P.W = 1;
     if (backward) {
         // two CTAs per SM (what their registers allow), each walking over chunks
-        const int64_t want = (int64_t)2 * kSms / P.nct > 0 ? (int64_t)2 * kSms / P.nct : 1;
+        const int64_t fit = (int64_t)kScanBackCtas * kSms / P.nct, want = fit > 0 ? fit : 1;
         P.W = (int)(want < P.G ? want : P.G);
     }
 }

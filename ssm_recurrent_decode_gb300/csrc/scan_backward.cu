@@ -12,6 +12,7 @@
 
 namespace gdn {
 
+constexpr int kBackCpt = 4;         // channels per thread
 constexpr int kBackTile = 8;        // token rows per tile: their states and decays fit a thread's registers
 constexpr int kBackTiles = kScanBackChunk / kBackTile;
 
@@ -22,7 +23,7 @@ template <typename Tin, class Sh> struct BackSmem {
     static constexpr int STAGE = 4 * RX + 2 * RB;
     static constexpr int SUMS = kScanWarps * R * Sh::YP * 4;              // a value per row and channel
     static constexpr int PART = kScanWarps * R * 2 * Sh::NP * 4;          // dB and dC per warp
-    static constexpr int STATES = kBackTiles * 4 * kScanThreads * 16;
+    static constexpr int STATES = (kBackTiles - 2) * 4 * kScanThreads * 8 * Sh::P;   // not before the first and the last tile
     static constexpr int SUMMARY = 2 * STAGE + SUMS;
     static constexpr int MAIN = 2 * STAGE + 4 * SUMS + PART + STATES;
 };
@@ -68,35 +69,35 @@ template <typename Tin, class Sh> struct BackTile {
     // g of this warp's channels into gs [R][YP]; the warp alone reads it
     __device__ __forceinline__ void gate(int b, float *gs, int lane, int warp)
     {
-        constexpr int CLN = Sh::CLN, NL = Sh::NL;
-        const int c = lane % CLN * 4;
+        constexpr int CLN = Sh::CLN, NL = Sh::NL, PP = Sh::P;
+        const int c = lane % CLN * Sh::CPT;
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += NL) {
             const int r = r0 + lane / CLN;
             if (NL > R && r >= R) break;
-            f2 g[2], z[2];
+            f2 g[PP], z[PP];
             load_pairs(raw(b, 3) + r * CB + warp * Sh::CW + c, g);
             if (P.a.z) {
                 load_pairs(raw(b, 2) + r * CB + warp * Sh::CW + c, z);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
+                for (int p = 0; p < PP; ++p) {
                     const float2 v = unpack2(z[p]);
                     g[p] = mul2(g[p], pack2(v.x * fast_sigmoid(v.x), v.y * fast_sigmoid(v.y)));
                 }
             }
-            *reinterpret_cast<ulonglong2 *>(gs + r * Sh::YP + c) = make_ulonglong2(g[0], g[1]);
+            store_pairs(gs + r * Sh::YP + c, g);
         }
     }
 };
 
 // (1) The summaries of chunk g: for the sequence that goes on behind the chunk its end state from
 // zero, for the sequence that began before it what its rows send back. Usually one and the same.
-template <typename Tin, int NL>
+template <typename Tin, int NL, int CPT>
 __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(const __grid_constant__ ScanLaunch P)
 {
-    using Sh = ScanShape<NL, 4>;
+    using Sh = ScanShape<NL, CPT>;
     using Sm = BackSmem<Tin, Sh>;
-    constexpr int R = kBackTile, NP = Sh::NP, CB = Sh::CB;
+    constexpr int R = kBackTile, NP = Sh::NP, CB = Sh::CB, PP = Sh::P;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[kScanWarps];
     ordinary_launch_start();
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
     const int nl = lane % NL, cl = lane / NL;
     const int ct = (int)(blockIdx.x % (unsigned)P.nct), g = (int)(blockIdx.x / (unsigned)P.nct);
     const int D = P.a.D, N = P.a.N, c0 = ct * CB;
-    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * 4, d0 = c0 + wc;
+    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * CPT, d0 = c0 + wc;
     const int64_t dn = (int64_t)D * N;
     const bool vst = (P.vec & kVecState) != 0;
     const int row0 = g * P.C, row1 = (int)min((int64_t)P.a.T, (int64_t)row0 + P.C);
@@ -133,14 +134,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
     if (pos < row1) T.stage(0, pos, clip(pos), true);
     cp_async_commit();
 
-    f2 A2[4][2], h[4][2], prod[4][2], e[4][2], dt_head[2] = {}, dt_tail[2] = {};
+    f2 A2[4][PP], h[4][PP], prod[4][PP], e[4][PP], dt_head[PP] = {}, dt_tail[PP] = {};
     load_rates(P.a.A, d0, D, n0, N, vst, A2);
     zero_entries(h);
     zero_entries(e);
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) prod[n][p] = pack2(1.f, 1.f);
+        for (int p = 0; p < PP; ++p) prod[n][p] = pack2(1.f, 1.f);
 
     while (pos < row1) {
         const bool head = pos < head_end, tail = pos >= tail_begin;
@@ -152,17 +153,17 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
         T.gate(b, gs, lane, warp);
         __syncwarp();
         const Tin *xs = T.raw(b, 0), *ds = T.raw(b, 1), *Bs = T.raw_bc(b, 0), *Cs = T.raw_bc(b, 1);
-        f2 dts[2] = {};
+        f2 dts[PP] = {};
 #pragma unroll 2
         for (int t = 0; t < R; ++t) {
-            f2 dt[2], u[2], gv[2], B[4], C[4];
+            f2 dt[PP], u[PP], gv[PP], B[4], C[4];
             load_pairs(ds + t * CB + wc, dt);
             load_pairs(xs + t * CB + wc, u);
-            load_pairs(gs + t * Sh::YP + cl * 4, gv);
+            load_pairs(gs + t * Sh::YP + cl * CPT, gv);
             load_twice(Bs + t * NP + n0, B);
             load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < PP; ++p) {
                 dts[p] = add2(dts[p], dt[p]);
                 u[p] = mul2(u[p], dt[p]);
 #pragma unroll
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
         }
         if (!tail) zero_entries(h);          // the sequence that goes on behind the chunk has not begun
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < PP; ++p) {
             if (head) dt_head[p] = add2(dt_head[p], dts[p]);
             if (tail) dt_tail[p] = add2(dt_tail[p], dts[p]);
         }
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
     }
     if (behind) store_entries(P.hin + g * dn, d0, D, n0, N, vst, h);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < PP; ++p) {
         const float2 ht = unpack2(dt_head[p]), tt = unpack2(dt_tail[p]);
         const int d = d0 + 2 * p;
         const int64_t o = (int64_t)g * D + d;
@@ -207,12 +208,12 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
 // every tile in shared memory, then tile by tile backwards: the tile's states again, now kept in
 // registers, and the recurrence of dh through them (the decays a third time: one instruction pair
 // each, where keeping them would take another 128 registers).
-template <typename Tin, int NL>
-__global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid_constant__ ScanLaunch P)
+template <typename Tin, int NL, int CPT>
+__global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(const __grid_constant__ ScanLaunch P)
 {
-    using Sh = ScanShape<NL, 4>;
+    using Sh = ScanShape<NL, CPT>;
     using Sm = BackSmem<Tin, Sh>;
-    constexpr int R = kBackTile, NP = Sh::NP, CB = Sh::CB, CLN = Sh::CLN, YP = Sh::YP;
+    constexpr int R = kBackTile, NP = Sh::NP, CB = Sh::CB, CLN = Sh::CLN, YP = Sh::YP, PP = Sh::P;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[kScanWarps];
     ordinary_launch_start();
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
     const int nl = lane % NL, cl = lane / NL;
     const int ct = (int)(blockIdx.x % (unsigned)P.nct), w = (int)(blockIdx.x / (unsigned)P.nct);
     const int D = P.a.D, N = P.a.N, c0 = ct * CB;
-    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * 4, d0 = c0 + wc;
+    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * CPT, d0 = c0 + wc;
     const int64_t dn = (int64_t)D * N;
     const bool vst = (P.vec & kVecState) != 0;
 
@@ -230,17 +231,17 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
     float *gs = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * R * YP;
     float *sum_y = gs + Sm::SUMS / 4, *sum_u = sum_y + Sm::SUMS / 4, *sum_w = sum_u + Sm::SUMS / 4;
     float *part = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + 4 * Sm::SUMS);
-    ulonglong2 *states = reinterpret_cast<ulonglong2 *>(smem + Sm::MAIN - Sm::STATES);
+    float *states = reinterpret_cast<float *>(smem + Sm::MAIN - Sm::STATES);
 
-    f2 A2[4][2], dA[4][2];
+    f2 A2[4][PP], dA[4][PP];
     zero_entries(A2);
     zero_entries(dA);
     if (P.a.T > 0) load_rates(P.a.A, d0, D, n0, N, vst, A2);
-    // a lane finishes four channels of every row it is given: the same ones in every tile
-    const int oc = warp * Sh::CW + lane % CLN * 4, orow = lane / CLN;
-    f2 skip[2], dD[2] = {};
+    // a lane finishes CPT channels of every row it is given: the same ones in every tile
+    const int oc = warp * Sh::CW + lane % CLN * CPT, orow = lane / CLN;
+    f2 skip[PP], dD[PP] = {};
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < PP; ++p) {
         const int c = oc + 2 * p;
         skip[p] = pack2(P.a.Dskip && c < T.ncols ? P.a.Dskip[c0 + c] : 0.f, P.a.Dskip && c + 1 < T.ncols ? P.a.Dskip[c0 + c + 1] : 0.f);
     }
@@ -294,11 +295,12 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
             stage_job(first_job, 0);
             cp_async_commit();
 
-            f2 h[4][2], e[4][2];
+            f2 h[4][PP], e[4][PP];
             zero_entries(h);
             zero_entries(e);
+            const float *hf = nullptr;      // where the rows' first state is
             if (live) {
-                const float *hf = starts ? (P.a.h0 ? P.a.h0 + slot * dn : nullptr) : P.hin ? P.hin + g * dn : nullptr;
+                hf = starts ? (P.a.h0 ? P.a.h0 + slot * dn : nullptr) : P.hin ? P.hin + g * dn : nullptr;
                 const float *ef = ends ? (P.g.dh_last ? P.g.dh_last + slot * dn : nullptr) : P.ein ? P.ein + g * dn : nullptr;
                 if (hf) load_entries(hf, d0, D, n0, N, vst, h);
                 if (ef) load_entries(ef, d0, D, n0, N, vst, e);
@@ -316,16 +318,18 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                 const Tin *Bs = T.raw_bc(b, 0), *Cs = T.raw_bc(b, 1);
 
                 if (!back) {
+                    if (tile > 0) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) states[(tile * 4 + q) * kScanThreads + tid] = make_ulonglong2(h[q][0], h[q][1]);
+                        for (int q = 0; q < 4; ++q) store_pairs(states + (((tile - 1) * 4 + q) * kScanThreads + tid) * CPT, h[q]);
+                    }
 #pragma unroll 2
                     for (int t = 0; t < R; ++t) {
-                        f2 dt[2], u[2], B[4];
+                        f2 dt[PP], u[PP], B[4];
                         load_pairs(ds + t * CB + wc, dt);
                         load_pairs(xs + t * CB + wc, u);
                         load_twice(Bs + t * NP + n0, B);
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
+                        for (int p = 0; p < PP; ++p) {
                             u[p] = mul2(u[p], dt[p]);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) h[k][p] = fma2(decay2(dt[p], A2[k][p]), h[k][p], mul2(u[p], B[k]));
@@ -336,31 +340,35 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
 
                 T.gate(b, gs, lane, warp);
                 // the tile's states, hp[t] before row t
-                f2 hp[R + 1][4][2];
+                f2 hp[R + 1][4][PP];
+                if (tile == nt - 1 || !live) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (tile == nt - 1 || !live) {
-                        hp[0][q][0] = h[q][0];
-                        hp[0][q][1] = h[q][1];
-                    } else {
-                        const ulonglong2 v = states[(tile * 4 + q) * kScanThreads + tid];
-                        hp[0][q][0] = v.x;
-                        hp[0][q][1] = v.y;
+                    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                        for (int p = 0; p < PP; ++p) hp[0][q][p] = h[q][p];
+                    }
+                } else if (tile == 0) {
+                    zero_entries(hp[0]);
+                    if (hf) load_entries(hf, d0, D, n0, N, vst, hp[0]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        load_pairs(states + (((tile - 1) * 4 + q) * kScanThreads + tid) * CPT, hp[0][q]);
                     }
                 }
 #pragma unroll
                 for (int t4 = 0; t4 < R; t4 += 4) {
-                    float acc[16];
+                    float acc[4 * CPT];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int t = t4 + k;
-                        f2 dt[2], u[2], B[4], C[4], y[2];
+                        f2 dt[PP], u[PP], B[4], C[4], y[PP];
                         load_pairs(ds + t * CB + wc, dt);
                         load_pairs(xs + t * CB + wc, u);
                         load_twice(Bs + t * NP + n0, B);
                         load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
+                        for (int p = 0; p < PP; ++p) {
                             u[p] = mul2(u[p], dt[p]);
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
@@ -368,18 +376,18 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                                 y[p] = q == 0 ? mul2(C[q], hp[t + 1][q][p]) : fma2(C[q], hp[t + 1][q][p], y[p]);
                             }
                             const float2 v = unpack2(y[p]);
-                            acc[k * 4 + 2 * p] = v.x;
-                            acc[k * 4 + 2 * p + 1] = v.y;
+                            acc[k * CPT + 2 * p] = v.x;
+                            acc[k * CPT + 2 * p + 1] = v.y;
                         }
                     }
                     if (P.g.dz) {
-                        constexpr int KEEP = 16 >= NL ? 16 / NL : 1, REP = 16 >= NL ? 1 : NL / 16;
-                        group_reduce<16, NL>(acc, nl);
+                        constexpr int M = 4 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
+                        group_reduce<M, NL>(acc, nl);
                         if (nl % REP == 0) {
 #pragma unroll
                             for (int i = 0; i < KEEP; ++i) {
                                 const int v = nl / REP * KEEP + i;
-                                sum_y[(t4 + v / 4) * YP + cl * 4 + v % 4] = acc[i];
+                                sum_y[(t4 + v / CPT) * YP + cl * CPT + v % CPT] = acc[i];
                             }
                         }
                     }
@@ -388,14 +396,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                 // backwards
 #pragma unroll
                 for (int t = R - 1; t >= 0; --t) {
-                    f2 dt[2], u[2], gv[2], B[4], C[4], db[4], dc[4], us[2], ws[2];
+                    f2 dt[PP], u[PP], gv[PP], B[4], C[4], db[4], dc[4], us[PP], ws[PP];
                     load_pairs(ds + t * CB + wc, dt);
                     load_pairs(xs + t * CB + wc, u);
-                    load_pairs(gs + t * YP + cl * 4, gv);
+                    load_pairs(gs + t * YP + cl * CPT, gv);
                     load_twice(Bs + t * NP + n0, B);
                     load_twice(Cs + t * NP + n0, C);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
+                    for (int p = 0; p < PP; ++p) {
                         u[p] = mul2(u[p], dt[p]);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -410,15 +418,22 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                         }
                     }
                     {
-                        const float2 u0 = unpack2(us[0]), u1 = unpack2(us[1]), w0 = unpack2(ws[0]), w1 = unpack2(ws[1]);
-                        float v[8] = {u0.x, u0.y, u1.x, u1.y, w0.x, w0.y, w1.x, w1.y};
-                        constexpr int KEEP = 8 >= NL ? 8 / NL : 1, REP = 8 >= NL ? 1 : NL / 8;
-                        group_reduce<8, NL>(v, nl);
+                        constexpr int M = 2 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
+                        float v[M];
+#pragma unroll
+                        for (int p = 0; p < PP; ++p) {
+                            const float2 uv = unpack2(us[p]), wv = unpack2(ws[p]);
+                            v[2 * p] = uv.x;
+                            v[2 * p + 1] = uv.y;
+                            v[CPT + 2 * p] = wv.x;
+                            v[CPT + 2 * p + 1] = wv.y;
+                        }
+                        group_reduce<M, NL>(v, nl);
                         if (nl % REP == 0) {
 #pragma unroll
                             for (int i = 0; i < KEEP; ++i) {
-                                const int k = nl / REP * KEEP + i;      // 0 .. 3: sum of B dh, 4 .. 7: of A w
-                                (k < 4 ? sum_u : sum_w)[t * YP + cl * 4 + k % 4] = v[i];
+                                const int k = nl / REP * KEEP + i;      // the first half: sums of B dh, the second: of A w
+                                (k < CPT ? sum_u : sum_w)[t * YP + cl * CPT + k % CPT] = v[i];
                             }
                         }
                     }
@@ -448,8 +463,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                 for (int r0 = 0; r0 < R; r0 += NL) {
                     const int r = r0 + orow;
                     if (r >= n || oc >= T.ncols) continue;
-                    const int sc = r * YP + lane % CLN * 4;
-                    f2 x2[2], d2[2], y2[2], z2[2], g2[2], u2[2], w2[2], s2[2], gx[2], gt[2], gz[2];
+                    const int sc = r * YP + lane % CLN * CPT;
+                    f2 x2[PP], d2[PP], y2[PP], z2[PP], g2[PP], u2[PP], w2[PP], s2[PP], gx[PP], gt[PP], gz[PP];
                     load_pairs(xs + r * CB + oc, x2);
                     load_pairs(ds + r * CB + oc, d2);
                     load_pairs(gs + sc, g2);
@@ -461,7 +476,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                         load_pairs(sum_y + sc, s2);
                     }
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
+                    for (int p = 0; p < PP; ++p) {
                         gx[p] = fma2(u2[p], d2[p], mul2(skip[p], g2[p]));
                         gt[p] = fma2(u2[p], x2[p], mul2(pack2(kLn2, kLn2), w2[p]));      // A2 = A log2(e)
                         dD[p] = fma2(g2[p], x2[p], dD[p]);
@@ -474,9 +489,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
                     }
                     const int64_t row = t0 + r;
                     const int left = T.ncols - oc, col = c0 + oc;
-                    if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, (P.vec & kVecDx) && left >= 4);
-                    if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, (P.vec & kVecDdt) && left >= 4);
-                    if (P.g.dz) store_row(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, gz, left, (P.vec & kVecDz) && left >= 4);
+                    if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, (P.vec & kVecDx) && left >= CPT);
+                    if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, (P.vec & kVecDdt) && left >= CPT);
+                    if (P.g.dz) store_row(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, gz, left, (P.vec & kVecDz) && left >= CPT);
                 }
                 // this channel tile's share of dB and dC: the warps' sums in order
                 for (int i = tid; i < n * 2 * NP; i += kScanThreads) {
@@ -493,9 +508,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_back_kernel(const __grid
     }
 
     store_entries(P.part_a + w * dn, d0, D, n0, N, vst, dA);
-    // dD: the lanes that share four channels
+    // dD: the lanes that share channels
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < PP; ++p) {
         float2 v = unpack2(dD[p]);
 #pragma unroll
         for (int off = CLN; off < 32; off <<= 1) {
@@ -541,22 +556,22 @@ template <typename Tin> __global__ void __launch_bounds__(256) scan_back_sum_ker
 
 template <typename Kern> static cudaError_t launch_sized(Kern kern, int64_t ctas, int bytes, const ScanLaunch &P, cudaStream_t stream)
 {
-    if (bytes > 48 * 1024) {
+    if (bytes > 40 * 1024) {      // the kernels have a little static shared memory too
         const cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (rc != cudaSuccess) return rc;
     }
     return launch_ordinary(kern, dim3((unsigned)ctas), dim3(kScanThreads), bytes, stream, P);
 }
 
-template <typename Tin, int NL> static int launch_shape(const ScanLaunch &P, cudaStream_t stream)
+template <typename Tin, int NL, int CPT> static int launch_shape(const ScanLaunch &P, cudaStream_t stream)
 {
-    using Sm = BackSmem<Tin, ScanShape<NL, 4>>;
+    using Sm = BackSmem<Tin, ScanShape<NL, CPT>>;
     if (P.hin) {
-        if (launch_sized(scan_back_summary_kernel<Tin, NL>, (int64_t)P.G * P.nct, Sm::SUMMARY, P, stream) != cudaSuccess)
+        if (launch_sized(scan_back_summary_kernel<Tin, NL, CPT>, (int64_t)P.G * P.nct, Sm::SUMMARY, P, stream) != cudaSuccess)
             return GDN_ERR_LAUNCH;
         if (launch_scan_carry(P, true, stream) != cudaSuccess) return GDN_ERR_LAUNCH;
     }
-    if (launch_sized(scan_back_kernel<Tin, NL>, (int64_t)P.W * P.nct, Sm::MAIN, P, stream) != cudaSuccess) return GDN_ERR_LAUNCH;
+    if (launch_sized(scan_back_kernel<Tin, NL, CPT>, (int64_t)P.W * P.nct, Sm::MAIN, P, stream) != cudaSuccess) return GDN_ERR_LAUNCH;
     const int64_t outs = (int64_t)P.a.T * 2 * P.a.N + (int64_t)P.a.D * P.a.N + P.a.D;
     return launch_ordinary(scan_back_sum_kernel<Tin>, dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, stream, P) == cudaSuccess
                ? GDN_OK
@@ -566,11 +581,11 @@ template <typename Tin, int NL> static int launch_shape(const ScanLaunch &P, cud
 template <typename Tin> static int launch_typed(const ScanLaunch &P, cudaStream_t stream)
 {
     switch (scan_lanes(P.a.N)) {
-    case 2: return launch_shape<Tin, 2>(P, stream);
-    case 4: return launch_shape<Tin, 4>(P, stream);
-    case 8: return launch_shape<Tin, 8>(P, stream);
-    case 16: return launch_shape<Tin, 16>(P, stream);
-    default: return launch_shape<Tin, 32>(P, stream);
+    case 2: return launch_shape<Tin, 2, kBackCpt>(P, stream);
+    case 4: return launch_shape<Tin, 4, kBackCpt>(P, stream);
+    case 8: return launch_shape<Tin, 8, kBackCpt>(P, stream);
+    case 16: return launch_shape<Tin, 16, kBackCpt>(P, stream);
+    default: return launch_shape<Tin, 32, kBackCpt>(P, stream);
     }
 }
 

@@ -6,9 +6,9 @@ namespace gdn {
 
 constexpr int kCarryThreads = 64;      // small CTAs: the loads in flight are spread over the SMs
 
-// One thread per state entry walks the chunks in order (blockIdx.y = 0) or backwards (1). Two loads
-// per chunk do not depend on the carry, so U chunks' values are in flight at a time; the traffic is
-// 12 bytes per entry and chunk.
+// One thread per state entry walks the chunks in order (blockIdx.y = 0) or backwards (1). The loads of a
+// chunk do not depend on the carry: those of the next U chunks are in flight while U chunks are worked
+// on. The traffic is 12 bytes per entry and chunk.
 __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const __grid_constant__ ScanLaunch P)
 {
     ordinary_launch_start();
@@ -22,30 +22,36 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const __grid_
     const float *sums = back ? P.sumdt_head : P.sumdt;
     const float *boundary = back ? P.g.dh_last : P.a.h0;
     float carry = 0.f;
-    constexpr int U = 16;
-    for (int k0 = 0; k0 < P.G; k0 += U) {
-        float loc[U], sum[U];
-        int seq[U], edge[U];
+    constexpr int U = 8;
+    // chunk of position k in this direction; nothing goes on behind the last (before the first)
+    const auto chunk = [&](int k) { return back ? P.G - 1 - k : k; };
+    float loc[U], sum[U];
+    int seq[U], edge[U];
+    const auto fetch = [&](int k0, float (&lo)[U], float (&su)[U], int (&sq)[U], int (&ed)[U]) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const bool on = k0 + k < P.G - 1;       // nothing goes on behind the last chunk (before the first)
-            const int g = back ? P.G - 1 - (k0 + k) : k0 + k;
-            const int4 info = on ? P.info[g] : make_int4(-1, 0, -1, 0);
-            seq[k] = back ? info.z : info.x;
-            edge[k] = back ? info.w : info.y;
-            loc[k] = seq[k] >= 0 ? val[g * dn + i] : 0.f;
-            sum[k] = seq[k] >= 0 ? sums[(int64_t)g * P.a.D + d] : 0.f;
+            const bool on = k0 + k < P.G - 1;
+            const int g = chunk(on ? k0 + k : 0);
+            const int4 info = P.info[g];
+            lo[k] = on ? val[g * dn + i] : 0.f;
+            su[k] = on ? sums[(int64_t)g * P.a.D + d] : 0.f;
+            sq[k] = on ? (back ? info.z : info.x) : -1;
+            ed[k] = back ? info.w : info.y;
         }
+    };
+    fetch(0, loc, sum, seq, edge);
+    for (int k0 = 0; k0 < P.G; k0 += U) {
+        float loc2[U], sum2[U], decay[U];
+        int seq2[U], edge2[U];
+        if (k0 + U < P.G) fetch(k0 + U, loc2, sum2, seq2, edge2);      // while this batch is worked on
+#pragma unroll
+        for (int k = 0; k < U; ++k) decay[k] = expf(A * sum[k]);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (k0 + k >= P.G) break;
-            const int g = back ? P.G - 1 - (k0 + k) : k0 + k;
+            const int g = chunk(k0 + k);
             val[g * dn + i] = carry;
-            if (seq[k] < 0) {
-                carry = 0.f;
-                continue;
-            }
-            if (edge[k]) {                          // the sequence begins (backwards: ends) in this chunk
+            if (seq[k] >= 0 && edge[k]) {           // the sequence begins (backwards: ends) in this chunk
                 carry = 0.f;
                 if (boundary) {
                     const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[seq[k]] : seq[k];
@@ -53,8 +59,16 @@ __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const __grid_
                 }
                 if (!back && P.init) P.init[g * dn + i] = carry;
             }
-            // no product with the decay where nothing is carried: 0 x inf is not 0
-            carry = carry == 0.f ? loc[k] : fmaf(expf(A * sum[k]), carry, loc[k]);
+            // where nothing goes on there is no carry, and where it is zero no product: 0 x inf is not 0
+            const float next = carry == 0.f ? loc[k] : fmaf(decay[k], carry, loc[k]);
+            carry = seq[k] >= 0 ? next : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            loc[k] = loc2[k];
+            sum[k] = sum2[k];
+            seq[k] = seq2[k];
+            edge[k] = edge2[k];
         }
     }
 }

@@ -22,7 +22,7 @@ template <typename Tin, class Sh> struct ScanSmem {
 // of the sequence that goes on behind the chunk); else the outputs. Tiles of 16 rows are staged one
 // ahead by asynchronous copies; a warp's channels are its own, so only the staging needs barriers.
 template <typename Tin, int NL, int CPT, bool SUM>
-__global__ void __launch_bounds__(kScanThreads, NL >= 16 ? FBW : FB_MAIN) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
+__global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
 {
     using Sh = ScanShape<NL, CPT>;
     using Sm = ScanSmem<Tin, Sh>;
@@ -231,7 +231,7 @@ static cudaError_t launch_one(const ScanLaunch &P, int chunks, cudaStream_t stre
 {
     constexpr int bytes = SUM ? ScanSmem<Tin, ScanShape<NL, CPT>>::SUMMARY : ScanSmem<Tin, ScanShape<NL, CPT>>::MAIN;
     auto kern = scan_forward_kernel<Tin, NL, CPT, SUM>;
-    if (bytes > 48 * 1024) {
+    if (bytes > 40 * 1024) {      // the kernels have a little static shared memory too
         const cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (rc != cudaSuccess) return rc;
     }

@@ -5,15 +5,6 @@
 #include <cuda_runtime.h>
 
 #include "mamba_scan.h"
-#ifndef FB_MAIN
-#define FB_MAIN 4
-#endif
-#ifndef FB_SUM
-#define FB_SUM 4
-#endif
-#ifndef FBW
-#define FBW 3
-#endif
 
 namespace gdn {
 
@@ -49,7 +40,13 @@ struct ScanLaunch {
 inline int scan_lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
 inline int scan_channels(int N, int cpt) { return 4 * (32 / scan_lanes(N)) * cpt; }
 
-constexpr int kScanBackChunk = 64;   // token rows per chunk of the backward pass
+constexpr int kScanBackChunk = 64;   // most token rows per chunk of the backward pass
+constexpr int kScanBackCtas = 2;     // its resident CTAs per SM
+
+// Resident CTAs per SM of the forward kernel. Wide states (N above 32) ran faster with more registers a
+// thread than with a fourth CTA (N = 128, 4 x 1024 rows, fp32: 266 against 342 us), narrow ones did not
+// care (N = 16, 32768 rows: 401 against 404), and six CTAs of 80 registers were slower for both (437, 432).
+constexpr int scan_ctas(int lanes) { return lanes >= 16 ? 3 : 4; }
 
 // The carry pass over the chunks (forward; with both also the backward one, over e).
 cudaError_t launch_scan_carry(const ScanLaunch &P, bool both, cudaStream_t stream);
