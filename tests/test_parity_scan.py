@@ -376,3 +376,9 @@ def test_backward_a_bad_state_index_zeroes_its_sequence_only():
     sc.check("dx", g["dx"][:30].cpu().numpy(), parts[0][0]["dx"], parts[0][1]["dx"], u)
     sc.check("dx", g["dx"][100:].cpu().numpy(), parts[1][0]["dx"], parts[1][1]["dx"], u)
     sc.check("dA", g["dA"].cpu().numpy(), parts[0][0]["dA"] + parts[1][0]["dA"], parts[0][1]["dA"] + parts[1][1]["dA"], u, terms=120)
+
+
+def test_long_chunks():
+    """Sizes whose chunks hold many tiles: several hundred rows forward, 64 backward, sequences across them."""
+    _forward([2500, 0, 3400, 100], 2000, 16, "bf16", seed=31)
+    _backward([500, 1, 700, 0, 99], 2000, 16, "bf16", seed=32)
