@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kReThreads) beam_reorder_kernel(const __grid_c
         const ReorderPool &q = P.pool[lo];
         const int64_t off = (int64_t)(piece - q.pieces_before) * kRePiece;
         const int64_t n = min(kRePiece, q.bytes - off);
+        if (!GDN_IN(P.err_flags, off, q.bytes) || !GDN_IN(P.err_flags, n - 1, kRePiece)) continue;
         const unsigned char *src = q.base + c.x * q.stride + off;
         unsigned char *dst = q.base + c.y * q.stride + off;
         switch (q.width) {

@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
     const int64_t out = (int64_t)blockIdx.x * K;
     const auto put = [&](int k, int i) {
         const int t = token[i];
+        if (!GDN_IN(P.a.err_flags, t, P.a.vocab) || !GDN_IN(P.a.err_flags, k, K)) return;
         P.a.out_scores[out + k] = logit[i];
         P.a.out_parents[out + k] = i / K;
         P.a.out_tokens[out + k] = t;

@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                         }
                     }
                     const int64_t row = t0 + r;
+                    if (!GDN_IN(P.a.err_flags, row, P.a.T)) continue;
                     const int left = T.ncols - oc, col = c0 + oc;
                     if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, (P.vec & kVecDx) && left >= CPT);
                     if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, (P.vec & kVecDdt) && left >= CPT);
@@ -500,10 +501,11 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                     float v = 0.f;
 #pragma unroll
                     for (int q = 0; q < kScanWarps; ++q) v += part[((q * R + r) * 2 + k) * NP + nn];
-                    P.part_bc[((int64_t)ct * P.a.T + t0 + r) * 2 * N + k * N + nn] = v;
+                    const int64_t o = ((int64_t)ct * P.a.T + t0 + r) * 2 * N + k * N + nn;
+                    if (GDN_IN(P.a.err_flags, o, (int64_t)P.nct * P.a.T * 2 * N)) P.part_bc[o] = v;
                 }
             }
-            if (starts && live && P.g.dh0) store_entries(P.g.dh0 + slot * dn, d0, D, n0, N, vst, e);
+            if (starts && live && P.g.dh0 && GDN_IN(P.a.err_flags, slot, P.a.num_states)) store_entries(P.g.dh0 + slot * dn, d0, D, n0, N, vst, e);
         }
     }
 

@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
                     }
                     if (tl.seq < 0) y[p] = 0ull;
                 }
+                if (!GDN_IN(P.a.err_flags, (int64_t)tl.t0 + t, P.a.T)) continue;
                 const int64_t o = (int64_t)(tl.t0 + t) * P.a.y_stride + c0 + oc;
                 if (P.a.out_dtype == GDN_BF16)
                     store_row(static_cast<bf16 *>(P.a.y) + o, y, ncols - oc, whole);
@@ -210,12 +211,12 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
         if (SUM) {
 #pragma unroll
             for (int p = 0; p < PP; ++p) dts[p] = add2(dts[p], dt_tile[p]);
-        } else if (tl.ends && P.a.h_last) {
+        } else if (tl.ends && P.a.h_last && GDN_IN(P.a.err_flags, tl.slot, P.a.num_states)) {
             store_entries(P.a.h_last + tl.slot * dn, d0, D, n0, N, vst, h);
         }
         b ^= 1;
     }
-    if (SUM) {
+    if (SUM && GDN_IN(P.a.err_flags, g, P.G)) {
         store_entries(P.hin + g * dn, d0, D, n0, N, vst, h);
 #pragma unroll
         for (int p = 0; p < PP; ++p) {
