@@ -111,18 +111,21 @@ int check(const mamba_scan_args &a, bool backward, bool states)
     return GDN_OK;
 }
 
-int row_bit(const void *p, int64_t stride, size_t es, int bit)
+int row_mode(const void *p, int64_t stride, size_t es)
 {
-    return p && aligned(p, 16) && (stride * (int64_t)es) % 16 == 0 ? bit : 0;
+    const auto on = [&](int64_t bytes) { return aligned(p, (size_t)bytes) && stride * (int64_t)es % bytes == 0; };
+    return on(16) ? kRows16 : on(4) ? kRows4 : kRowsAny;
 }
 
 void set_inputs(ScanLaunch &P)
 {
     const mamba_scan_args &a = P.a;
     const size_t es = a.in_dtype == GDN_BF16 ? 2 : 4;
-    P.vec = row_bit(a.x, a.x_stride, es, kVecX) | row_bit(a.dt, a.dt_stride, es, kVecDt) |
-            row_bit(a.z, a.z_stride, es, kVecZ) | row_bit(a.Bm, a.B_stride, es, kVecB) |
-            row_bit(a.Cm, a.C_stride, es, kVecC);
+    P.mode_x = row_mode(a.x, a.x_stride, es);
+    P.mode_dt = row_mode(a.dt, a.dt_stride, es);
+    P.mode_z = row_mode(a.z, a.z_stride, es);
+    P.mode_b = row_mode(a.Bm, a.B_stride, es);
+    P.mode_c = row_mode(a.Cm, a.C_stride, es);
     if (a.N % 4 == 0 && aligned(a.A, 16) && aligned(a.h0, 16) && aligned(a.h_last, 16)) P.vec |= kVecState;
 }
 
@@ -205,7 +208,7 @@ int mamba_selective_scan_backward(const mamba_scan_grad_args *args, gdn_stream_t
     gdn::set_inputs(P);
     if (!gdn::aligned(q.dh_last, 16) || !gdn::aligned(q.dh0, 16)) P.vec &= ~gdn::kVecState;
     P.has_states = states;
-    P.vec |= gdn::row_bit(q.dy, q.dy_stride, es, gdn::kVecDy);
+    P.mode_dy = gdn::row_mode(q.dy, q.dy_stride, es);
     const auto out_bit = [&](const void *p, int64_t stride, int bit) {
         if (p && gdn::aligned(p, 4 * es) && stride % 4 == 0) P.vec |= bit;
     };

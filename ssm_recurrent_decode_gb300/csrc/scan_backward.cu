@@ -48,22 +48,19 @@ template <typename Tin, class Sh> struct BackTile {
     {
         return reinterpret_cast<Tin *>(smem + b * Sm::STAGE + 4 * Sm::RX + k * Sm::RB);
     }
-    __device__ __forceinline__ void rows(Tin *dst, const void *src, int64_t stride, int64_t t0, int n, int bit)
-    {
-        stage_rows<Tin, CB, R>(dst, static_cast<const Tin *>(src) + t0 * stride + c0, stride, n, ncols, P.vec & bit, tid);
-    }
     // rows t0 .. t0 + n - 1 into buffer b; grads: also what only the gradients need
     __device__ __forceinline__ void stage(int b, int t0, int n, bool grads)
     {
-        rows(raw(b, 0), P.a.x, P.a.x_stride, t0, n, kVecX);
-        rows(raw(b, 1), P.a.dt, P.a.dt_stride, t0, n, kVecDt);
-        stage_rows<Tin, NP, R>(raw_bc(b, 0), static_cast<const Tin *>(P.a.Bm) + (int64_t)t0 * P.a.B_stride, P.a.B_stride, n,
-                               P.a.N, P.vec & kVecB, tid);
+        const auto rows = [&](const void *base, int64_t stride, int col, int width, int mode) {
+            return TileSource<Tin>{static_cast<const Tin *>(base), stride, t0, P.a.T, col, width, mode};
+        };
+        stage_rows<Tin, CB, R>(raw(b, 0), rows(P.a.x, P.a.x_stride, c0, P.a.D, P.mode_x), n, tid);
+        stage_rows<Tin, CB, R>(raw(b, 1), rows(P.a.dt, P.a.dt_stride, c0, P.a.D, P.mode_dt), n, tid);
+        stage_rows<Tin, NP, R>(raw_bc(b, 0), rows(P.a.Bm, P.a.B_stride, 0, P.a.N, P.mode_b), n, tid);
         if (grads) {
-            if (P.a.z) rows(raw(b, 2), P.a.z, P.a.z_stride, t0, n, kVecZ);
-            rows(raw(b, 3), P.g.dy, P.g.dy_stride, t0, n, kVecDy);
-            stage_rows<Tin, NP, R>(raw_bc(b, 1), static_cast<const Tin *>(P.a.Cm) + (int64_t)t0 * P.a.C_stride, P.a.C_stride,
-                                   n, P.a.N, P.vec & kVecC, tid);
+            if (P.a.z) stage_rows<Tin, CB, R>(raw(b, 2), rows(P.a.z, P.a.z_stride, c0, P.a.D, P.mode_z), n, tid);
+            stage_rows<Tin, CB, R>(raw(b, 3), rows(P.g.dy, P.g.dy_stride, c0, P.a.D, P.mode_dy), n, tid);
+            stage_rows<Tin, NP, R>(raw_bc(b, 1), rows(P.a.Cm, P.a.C_stride, 0, P.a.N, P.mode_c), n, tid);
         }
     }
     // g of this warp's channels into gs [R][YP]; the warp alone reads it

@@ -142,15 +142,102 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// rows >= n and columns >= ncols are filled with zeros. `src` is the first element of the tile;
-// vec: src and every row are 16-byte aligned (asynchronous 16-byte copies), else element by element.
-template <typename T, int W, int R = kScanTile>
-__device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t stride, int n, int ncols, bool vec, int tid)
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, int bytes)
 {
-    if (vec) {
-        constexpr int VE = 16 / (int)sizeof(T);
-        static_assert(W % VE == 0, "a staged row is whole 16-byte vectors");
-        constexpr int VPR = W / VE;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// Where a staged tile lies in its tensor: rows t0 .. of T, columns c0 .. of `width`.
+template <typename T> struct TileSource {
+    const T *base;
+    int64_t stride;
+    int t0, rows, c0, width;
+    int mode;            // kRows16, kRows4 or kRowsAny
+};
+
+// eight bf16 elements from p on, which may lie across 16-byte boundaries: shifted out of two aligned vectors
+__device__ __forceinline__ uint4 load_across(const bf16 *p)
+{
+    const int shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / 2);
+    const uint4 lo = *reinterpret_cast<const uint4 *>(p - shift), hi = *reinterpret_cast<const uint4 *>(p - shift + 8);
+    unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (shift & 4) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    }
+    if (shift & 2) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    }
+    if (shift & 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// bf16 rows of any alignment, through registers. A vector is read whole where both aligned vectors lie in the
+// tensor: in its row, or between rows that it has.
+template <int W, int R, typename T>
+__device__ __forceinline__ void stage_across(T *, const T *, const TileSource<T> &, int, int, int)
+{
+}
+template <int W, int R>
+__device__ __forceinline__ void stage_across(bf16 *dst, const bf16 *src, const TileSource<bf16> &s, int n, int ncols, int tid)
+{
+    constexpr int VPR = W / 8;
+#pragma unroll 2
+    for (int i = tid; i < R * VPR; i += kScanThreads) {
+        const int r = i / VPR, v = i % VPR, c = s.c0 + v * 8, left = ncols - v * 8;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (r < n && left > 0) {
+            const bf16 *p = src + r * s.stride + v * 8;
+            const int row = s.t0 + r;
+            if (left >= 8 && (c >= 7 || row > 0) && (c + 16 <= s.width || row + 1 < s.rows)) {
+                q = load_across(p);
+            } else {
+                const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+                unsigned w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = (2 * k < left ? u[2 * k] : 0u) | (2 * k + 1 < left ? (unsigned)u[2 * k + 1] << 16 : 0u);
+                q = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + r * W + v * 8) = q;
+    }
+}
+
+template <typename T, int W, int R> __device__ __noinline__ void stage_unaligned(T *dst, TileSource<T> s, int n, int tid)
+{
+    const T *src = s.base + (int64_t)s.t0 * s.stride + s.c0;
+    const int ncols = min(W, s.width - s.c0);
+    if (sizeof(T) == 4 || s.mode == kRows4) {
+        constexpr int E = 4 / (int)sizeof(T), PR = W / E;
+#pragma unroll 4
+        for (int i = tid; i < R * PR; i += kScanThreads) {
+            const int r = i / PR, v = i % PR;
+            int left = r < n ? (ncols - v * E) * (int)sizeof(T) : 0;
+            left = left < 0 ? 0 : left > 4 ? 4 : left;
+            cp_async4(dst + r * W + v * E, left ? src + r * s.stride + v * E : src, left);
+        }
+    } else {
+        stage_across<W, R>(dst, src, s, n, ncols, tid);
+    }
+}
+
+// Rows >= n and columns >= the tensor's width are filled with zeros. Aligned rows are copied asynchronously
+// in 16 bytes, rows on 4-byte boundaries in 4; bf16 rows that begin between those (odd strides) go through
+// registers in 16 bytes (4 x 2000 rows, N = 16, bf16: 777 channels 106 us against 84 for 776; gradients 341
+// against 261).
+template <typename T, int W, int R = kScanTile>
+__device__ __forceinline__ void stage_rows(T *dst, const TileSource<T> &s, int n, int tid)
+{
+    constexpr int VE = 16 / (int)sizeof(T), VPR = W / VE;
+    static_assert(W % VE == 0, "a staged row is whole 16-byte vectors");
+    const T *src = s.base + (int64_t)s.t0 * s.stride + s.c0;
+    const int ncols = min(W, s.width - s.c0);
+    if (s.mode == kRows16) {
 #pragma unroll
         for (int k = 0; k < (R * VPR + kScanThreads - 1) / kScanThreads; ++k) {
             const int i = k * kScanThreads + tid;
@@ -158,15 +245,11 @@ __device__ __forceinline__ void stage_rows(T *dst, const T *src, int64_t stride,
             if (R * VPR % kScanThreads == 0 || r < R) {
                 int left = r < n ? (ncols - v * VE) * (int)sizeof(T) : 0;
                 left = left < 0 ? 0 : left > 16 ? 16 : left;
-                cp_async16(dst + r * W + v * VE, left ? src + r * stride + v * VE : src, left);
+                cp_async16(dst + r * W + v * VE, left ? src + r * s.stride + v * VE : src, left);
             }
         }
     } else {
-#pragma unroll 4
-        for (int i = tid; i < R * W; i += kScanThreads) {
-            const int r = i / W, c = i % W;
-            dst[i] = r < n && c < ncols ? src[r * stride + c] : from_f32<T>(0.f);
-        }
+        stage_unaligned<T, W, R>(dst, s, n, tid);
     }
 }
 

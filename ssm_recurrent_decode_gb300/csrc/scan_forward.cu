@@ -73,14 +73,15 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
         Tin *xs = reinterpret_cast<Tin *>(smem + b * Sm::STAGE);
         Tin *ds = xs + kScanTile * CB, *zs = ds + kScanTile * CB;
         Tin *Bs = zs + kScanTile * CB, *Cs = Bs + kScanTile * NP;
-        const int64_t r = t.t0;
-        stage_rows<Tin, CB>(xs, static_cast<const Tin *>(P.a.x) + r * P.a.x_stride + c0, P.a.x_stride, t.n, ncols, P.vec & kVecX, tid);
-        stage_rows<Tin, CB>(ds, static_cast<const Tin *>(P.a.dt) + r * P.a.dt_stride + c0, P.a.dt_stride, t.n, ncols, P.vec & kVecDt, tid);
-        stage_rows<Tin, NP>(Bs, static_cast<const Tin *>(P.a.Bm) + r * P.a.B_stride, P.a.B_stride, t.n, N, P.vec & kVecB, tid);
+        const auto rows = [&](const void *base, int64_t stride, int col, int width, int mode) {
+            return TileSource<Tin>{static_cast<const Tin *>(base), stride, t.t0, P.a.T, col, width, mode};
+        };
+        stage_rows<Tin, CB>(xs, rows(P.a.x, P.a.x_stride, c0, D, P.mode_x), t.n, tid);
+        stage_rows<Tin, CB>(ds, rows(P.a.dt, P.a.dt_stride, c0, D, P.mode_dt), t.n, tid);
+        stage_rows<Tin, NP>(Bs, rows(P.a.Bm, P.a.B_stride, 0, N, P.mode_b), t.n, tid);
         if (!SUM) {
-            if (P.a.z)
-                stage_rows<Tin, CB>(zs, static_cast<const Tin *>(P.a.z) + r * P.a.z_stride + c0, P.a.z_stride, t.n, ncols, P.vec & kVecZ, tid);
-            stage_rows<Tin, NP>(Cs, static_cast<const Tin *>(P.a.Cm) + r * P.a.C_stride, P.a.C_stride, t.n, N, P.vec & kVecC, tid);
+            if (P.a.z) stage_rows<Tin, CB>(zs, rows(P.a.z, P.a.z_stride, c0, D, P.mode_z), t.n, tid);
+            stage_rows<Tin, NP>(Cs, rows(P.a.Cm, P.a.C_stride, 0, N, P.mode_c), t.n, tid);
         }
     };
     ScanTile tl, nxt;

@@ -8,9 +8,10 @@
 
 namespace gdn {
 
-// 16-byte copies allowed for a row-strided tensor (bits of ScanLaunch::vec)
-enum { kVecX = 1, kVecDt = 2, kVecZ = 4, kVecB = 8, kVecC = 16, kVecDy = 32, kVecY = 64, kVecState = 128,
-       kVecDx = 256, kVecDdt = 512, kVecDz = 1024 };
+// how the rows of an input tensor may be copied
+enum { kRowsAny = 0, kRows4 = 1, kRows16 = 2 };
+// whole-vector access to outputs and states (bits of ScanLaunch::vec)
+enum { kVecY = 1, kVecState = 2, kVecDx = 4, kVecDdt = 8, kVecDz = 16 };
 
 struct ScanLaunch {
     mamba_scan_args a;
@@ -19,6 +20,7 @@ struct ScanLaunch {
     int cpt;            // channels per thread
     int nct;            // channel tiles
     int vec;
+    int mode_x, mode_dt, mode_z, mode_b, mode_c, mode_dy;
     int has_states;     // state indices are checked
     // workspace
     int4 *info;         // [G] x: sequence that goes on behind the chunk (-1: none), y: it begins inside,
