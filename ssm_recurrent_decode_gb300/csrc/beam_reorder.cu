@@ -52,7 +52,8 @@ template <typename W> __device__ __forceinline__ void copy_piece(unsigned char *
 
 __global__ void __launch_bounds__(kReThreads) beam_reorder_kernel(const __grid_constant__ ReorderLaunch P)
 {
-    __shared__ int par[kReMaxBeams];        // parent, or -1
+    __shared__ short par[kReMaxBeams];      // parent, or -1
+    __shared__ int slot_of[kReMaxBeams];
     __shared__ unsigned char first[kReMaxBeams], kept[kReMaxBeams];
     __shared__ int2 copies[kReMaxBeams];    // source slot, destination slot
     __shared__ int wcount[kReThreads / 32];
@@ -62,7 +63,8 @@ __global__ void __launch_bounds__(kReThreads) beam_reorder_kernel(const __grid_c
 
     for (int i = tid; i < R; i += kReThreads) {
         const int p = P.parents[i];
-        par[i] = p >= 0 && p < beams ? p : -1;
+        par[i] = p >= 0 && p < beams ? (short)p : (short)-1;
+        slot_of[i] = P.slots[i];
         kept[i] = 0;
     }
     __syncthreads();
@@ -83,16 +85,16 @@ __global__ void __launch_bounds__(kReThreads) beam_reorder_kernel(const __grid_c
             const int b0 = i - i % beams, p = par[i];
             int slot;
             if (first[i]) {
-                slot = P.slots[b0 + p];
+                slot = slot_of[b0 + p];
             } else {
                 int rank = 0;               // how many before this one need a free slot
                 for (int j = b0; j < i; ++j) rank += !first[j];
                 int j = b0;
                 for (;; ++j)
                     if (!kept[j] && rank-- == 0) break;      // as many are free as are needed
-                slot = P.slots[j];
+                slot = slot_of[j];
                 if (p >= 0) {
-                    c = make_int2(P.slots[b0 + p], slot);
+                    c = make_int2(slot_of[b0 + p], slot);
                     copy = c.x >= 0 && c.x < P.num_slots && c.y >= 0 && c.y < P.num_slots;
                     if (!copy && blockIdx.x == 0) raise_flag(P.err_flags, GDN_DEVERR_BAD_INDEX);
                 }
