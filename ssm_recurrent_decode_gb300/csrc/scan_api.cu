@@ -34,8 +34,9 @@ size_t carve(ScanLaunch &P, bool uniform, bool backward, unsigned char *base)
 {
     Carver w{base};
     const size_t dn = (size_t)P.a.D * P.a.N;
-    // one sequence per chunk, or all rows in one chunk: no state crosses a chunk border
-    const bool carried = P.G > 1 && !(uniform && P.C == P.L);
+    // one sequence per chunk, or all rows in one chunk: no state crosses a chunk border; in a cluster it
+    // crosses through shared memory
+    const bool carried = P.G > 1 && !P.cluster && !(uniform && P.C == P.L);
     if (carried) {
         P.info = w.take<int4>(P.G);
         P.sumdt = w.take<float>((size_t)P.G * P.a.D);
@@ -79,8 +80,13 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
             P.cpt = 2;                           // too few rows for that: more threads for each
             P.nct = tiles(2);
         }
-        // One pass over whole sequences where they are about as long as the chunks would be.
-        if (uniform && P.L > 0 && P.L <= 4 * P.C) P.C = P.L;
+        if (T > 32 && T <= 8 * 32 && !(uniform && P.L <= 32)) {
+            // a few chunks: a cluster of at most eight CTAs per channel tile, in one launch
+            P.C = T <= 8 * 16 ? 16 : 32;
+            P.cluster = 1;
+        } else if (uniform && P.L > 0 && P.L <= 4 * P.C) {
+            P.C = P.L;                           // about as long as the chunks would be: one pass over whole sequences
+        }
     }
     P.G = T > 0 ? (int)((T + P.C - 1) / P.C) : 1;   // without rows: one chunk of empty sequences
     P.W = 1;

@@ -2,6 +2,7 @@
 //
 // Source: "Triton decode kernel + MBU analysis", "Kernel design" (the per-token arithmetic) and
 // "Prefill path" (a scan over the prompt).
+#include "gdn_cluster.cuh"
 #include "scan_common.cuh"
 
 namespace gdn {
@@ -18,56 +19,57 @@ template <typename Tin, class Sh> struct ScanSmem {
     static constexpr int SUMMARY = 2 * STAGE;
 };
 
-// One CTA: rows g C .. of channel tile ct. SUM: the summary pass (end state from zero and sum of dt
-// of the sequence that goes on behind the chunk); else the outputs. Tiles of 16 rows are staged one
-// ahead by asynchronous copies; a warp's channels are its own, so only the staging needs barriers.
-template <typename Tin, int NL, int CPT, bool SUM>
-__global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
-{
-    using Sh = ScanShape<NL, CPT>;
-    using Sm = ScanSmem<Tin, Sh>;
-    constexpr int CB = Sh::CB, NP = Sh::NP, PP = Sh::P, CLN = Sh::CLN;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int scratch[kScanWarps];
-    ordinary_launch_start();
+// A thread's place: its CTA's chunk and channel tile, its lanes, its first state entry and channel.
+template <class Sh> struct ScanPlace {
+    int tid, lane, warp, nl, cl, ct, g, c0, ncols, n0, wc, d0, row0, row1;
+    __device__ __forceinline__ ScanPlace(const ScanLaunch &P, int g_, int ct_)
+    {
+        tid = threadIdx.x;
+        lane = tid & 31;
+        warp = tid >> 5;
+        nl = lane % Sh::NL;
+        cl = lane / Sh::NL;
+        g = g_;
+        ct = ct_;
+        c0 = ct * Sh::CB;
+        ncols = min(Sh::CB, P.a.D - c0);
+        n0 = 4 * nl;
+        wc = warp * Sh::CW + cl * Sh::CPT;
+        d0 = c0 + wc;
+        row0 = (int)min((int64_t)g * P.C, (int64_t)P.a.T);
+        row1 = (int)min((int64_t)(g + 1) * P.C, (int64_t)P.a.T);
+    }
+};
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nl = lane % NL, cl = lane / NL;
-    const int ct = (int)(blockIdx.x % (unsigned)P.nct), g = (int)(blockIdx.x / (unsigned)P.nct);
-    const int D = P.a.D, N = P.a.N;
-    const int c0 = ct * CB, ncols = min(CB, D - c0);
-    const int n0 = 4 * nl, wc = warp * Sh::CW + cl * CPT, d0 = c0 + wc;      // this thread's first entry and channel
+// What a summary is taken of: the rows from `first` on of the sequence that goes on behind the chunk.
+struct ScanTail {
+    int seq, first;
+    bool goes_on, begins;       // begins: in this chunk
+};
+template <class Sh> __device__ __forceinline__ ScanTail scan_tail(const ScanLaunch &P, const ScanPlace<Sh> &at, int *scratch)
+{
+    ScanTail t;
+    t.seq = find_seq(P, at.row1 - 1, scratch, at.tid);
+    t.goes_on = t.seq >= 0 && t.seq < P.a.S && seq_bound(P, t.seq + 1) > at.row1;
+    t.begins = t.goes_on && seq_bound(P, t.seq) >= at.row0;
+    t.first = t.goes_on ? max(seq_bound(P, t.seq), at.row0) : at.row1;
+    return t;
+}
+
+// Walks the rows of `load` tile by tile. SUM: only the states (h ends as the last row's) and the sum of dt; else
+// the outputs too. start(tile, h) sets h where a sequence begins or the chunk does. Tiles of 16 rows are
+// staged one ahead by asynchronous copies; a warp's channels are its own, so only the staging needs barriers.
+template <typename Tin, class Sh, bool SUM, typename Start>
+__device__ __forceinline__ void scan_pass(const ScanLaunch &P, unsigned char *smem, const ScanPlace<Sh> &at, ScanIter load,
+                                          const f2 (&A2)[4][Sh::P], f2 (&h)[4][Sh::P], f2 (&dts)[Sh::P], Start start)
+{
+    using Sm = ScanSmem<Tin, Sh>;
+    constexpr int NL = Sh::NL, CPT = Sh::CPT, CB = Sh::CB, NP = Sh::NP, PP = Sh::P, CLN = Sh::CLN;
+    const int tid = at.tid, lane = at.lane, warp = at.warp, nl = at.nl, cl = at.cl, c0 = at.c0, ncols = at.ncols, n0 = at.n0,
+              wc = at.wc, D = P.a.D, N = P.a.N;
     const int64_t dn = (int64_t)D * N;
     const bool vst = (P.vec & kVecState) != 0;
-    const int row0 = (int)min((int64_t)g * P.C, (int64_t)P.a.T), row1 = (int)min((int64_t)(g + 1) * P.C, (int64_t)P.a.T);
-
-    ScanIter load, use;
-    if (SUM) {
-        // only the rows of the sequence that goes on behind the chunk
-        const int s = find_seq(P, row1 - 1, scratch, tid);
-        const bool goes_on = s >= 0 && s < P.a.S && seq_bound(P, s + 1) > row1;
-        const int first = goes_on ? max(seq_bound(P, s), row0) : row1;
-        if (tid == 0 && ct == 0)
-            P.info[g] = make_int4(goes_on ? s : -1, goes_on && seq_bound(P, s) >= row0, 0, 0);
-        if (!goes_on) return;
-        load.init(first, row1, s);
-    } else {
-        load.init(row0, row1, find_seq(P, row0, scratch, tid));
-        // empty sequences pass their state on (each handled by one chunk's CTAs)
-        if (P.a.h_last && P.a.h_last != P.a.h0 && (P.a.cu_seqlens || P.L == 0)) {
-            for (int s = g; s < P.a.S; s += P.G) {
-                if (seq_bound(P, s) != seq_bound(P, s + 1)) continue;
-                const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[s] : s;
-                if (slot < 0 || slot >= P.a.num_states) {
-                    if (tid == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
-                    continue;
-                }
-                for (int i = tid; i < ncols * N; i += kScanThreads)
-                    P.a.h_last[slot * dn + (int64_t)c0 * N + i] = P.a.h0 ? P.a.h0[slot * dn + (int64_t)c0 * N + i] : 0.f;
-            }
-        }
-    }
-    use = load;
+    ScanIter use = load;
 
     auto stage_tile = [&](const ScanTile &t, int b) {
         Tin *xs = reinterpret_cast<Tin *>(smem + b * Sm::STAGE);
@@ -88,10 +90,6 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
     if (load.next(P, nxt)) stage_tile(nxt, 0);
     cp_async_commit();
 
-    f2 A2[4][PP], h[4][PP], dts[PP];
-    zero_entries(A2);
-    zero_entries(h);
-    if (row0 < row1) load_rates(P.a.A, d0, D, n0, N, vst, A2);
 #pragma unroll
     for (int p = 0; p < PP; ++p) dts[p] = 0ull;
     // a lane finishes CPT channels of every row it is given: the same ones in every tile
@@ -117,15 +115,8 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
         const Tin *ds = xs + kScanTile * CB, *zs = ds + kScanTile * CB;
         const Tin *Bs = zs + kScanTile * CB, *Cs = Bs + kScanTile * NP;
         if (tl.fresh) {
-            const float *from = nullptr;
-            if (!SUM && tl.seq >= 0)
-                // (a sequence that goes on behind the chunk: in place, a later chunk's CTA may already have
-                // written its row of h_last, so its initial state comes from the carry pass's copy)
-                from = !tl.starts ? (P.hin ? P.hin + g * dn : nullptr)
-                       : !P.a.h0  ? nullptr
-                       : P.hin && g < P.G - 1 && P.info[g].x == tl.seq ? P.init + g * dn : P.a.h0 + tl.slot * dn;
             zero_entries(h);
-            if (from) load_entries(from, d0, D, n0, N, vst, h);
+            if (tl.seq >= 0) start(tl, h);
         }
 
         f2 dt_tile[PP] = {};
@@ -213,19 +204,201 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
 #pragma unroll
             for (int p = 0; p < PP; ++p) dts[p] = add2(dts[p], dt_tile[p]);
         } else if (tl.ends && P.a.h_last && GDN_IN(P.a.err_flags, tl.slot, P.a.num_states)) {
-            store_entries(P.a.h_last + tl.slot * dn, d0, D, n0, N, vst, h);
+            store_entries(P.a.h_last + tl.slot * dn, at.d0, D, n0, N, vst, h);
         }
         b ^= 1;
     }
+}
+
+// An empty sequence passes its state on: each is handled by one chunk's CTAs.
+template <class Sh> __device__ __forceinline__ void pass_empty_on(const ScanLaunch &P, const ScanPlace<Sh> &at)
+{
+    if (!P.a.h_last || P.a.h_last == P.a.h0 || (!P.a.cu_seqlens && P.L != 0)) return;
+    const int64_t dn = (int64_t)P.a.D * P.a.N;
+    for (int s = at.g; s < P.a.S; s += P.G) {
+        if (seq_bound(P, s) != seq_bound(P, s + 1)) continue;
+        const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[s] : s;
+        if (slot < 0 || slot >= P.a.num_states) {
+            if (at.tid == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
+            continue;
+        }
+        for (int i = at.tid; i < at.ncols * P.a.N; i += kScanThreads) {
+            const int64_t o = slot * dn + (int64_t)at.c0 * P.a.N + i;
+            P.a.h_last[o] = P.a.h0 ? P.a.h0[o] : 0.f;
+        }
+    }
+}
+
+// One CTA: the rows of chunk g, channel tile ct. SUM: the summary pass (end state from zero and sum of dt
+// of the sequence that goes on behind the chunk); else the outputs.
+template <typename Tin, int NL, int CPT, bool SUM>
+__global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kernel(const __grid_constant__ ScanLaunch P)
+{
+    using Sh = ScanShape<NL, CPT>;
+    constexpr int PP = Sh::P;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int scratch[kScanWarps];
+    ordinary_launch_start();
+
+    const ScanPlace<Sh> at(P, (int)(blockIdx.x / (unsigned)P.nct), (int)(blockIdx.x % (unsigned)P.nct));
+    const int D = P.a.D, N = P.a.N, g = at.g;
+    const int64_t dn = (int64_t)D * N;
+    const bool vst = (P.vec & kVecState) != 0;
+    ScanIter rows;
+    if (SUM) {
+        const ScanTail t = scan_tail(P, at, scratch);
+        if (at.tid == 0 && at.ct == 0) P.info[g] = make_int4(t.goes_on ? t.seq : -1, t.begins, 0, 0);
+        if (!t.goes_on) return;
+        rows.init(t.first, at.row1, t.seq);
+    } else {
+        rows.init(at.row0, at.row1, find_seq(P, at.row0, scratch, at.tid));
+        pass_empty_on(P, at);
+    }
+    f2 A2[4][PP], h[4][PP], dts[PP];
+    zero_entries(A2);
+    if (at.row0 < at.row1) load_rates(P.a.A, at.d0, D, at.n0, N, vst, A2);
+    zero_entries(h);
+    scan_pass<Tin, Sh, SUM>(P, smem, at, rows, A2, h, dts, [&](const ScanTile &tl, f2 (&v)[4][PP]) {
+        if (SUM) return;             // from zero
+        // (a sequence that goes on behind the chunk: in place, a later chunk's CTA may already have
+        // written its row of h_last, so its initial state comes from the carry pass's copy)
+        const float *from = !tl.starts ? (P.hin ? P.hin + g * dn : nullptr)
+                            : !P.a.h0  ? nullptr
+                            : P.hin && g < P.G - 1 && P.info[g].x == tl.seq ? P.init + g * dn : P.a.h0 + tl.slot * dn;
+        if (from) load_entries(from, at.d0, D, at.n0, N, vst, v);
+    });
     if (SUM && GDN_IN(P.a.err_flags, g, P.G)) {
-        store_entries(P.hin + g * dn, d0, D, n0, N, vst, h);
+        store_entries(P.hin + g * dn, at.d0, D, at.n0, N, vst, h);
 #pragma unroll
         for (int p = 0; p < PP; ++p) {
             const float2 v = unpack2(dts[p]);
-            if (nl == 0 && d0 + 2 * p < D) P.sumdt[(int64_t)g * D + d0 + 2 * p] = v.x;
-            if (nl == 0 && d0 + 2 * p + 1 < D) P.sumdt[(int64_t)g * D + d0 + 2 * p + 1] = v.y;
+            const int d = at.d0 + 2 * p;
+            if (at.nl == 0 && d < D) P.sumdt[(int64_t)g * D + d] = v.x;
+            if (at.nl == 0 && d + 1 < D) P.sumdt[(int64_t)g * D + d + 1] = v.y;
         }
     }
+}
+
+// A short call in one launch: its up to eight chunks are the CTAs of a thread-block cluster (per channel
+// tile). Each takes its summary, reads those before it from the other CTAs' shared memory, folds them into
+// the state it starts from, and takes its outputs. (One prompt of 128 tokens, D = 1536, N = 16: PROMPT_TIME us; in
+// one pass without chunks 17.0, in three launches 20.)
+template <typename Tin, int NL, int CPT>
+__global__ void __launch_bounds__(kScanThreads) scan_cluster_kernel(const __grid_constant__ ScanLaunch P)
+{
+    using Sh = ScanShape<NL, CPT>;
+    constexpr int PP = Sh::P, KEYS = 8 * PP;         // a thread's state entries
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int scratch[kScanWarps];
+    __shared__ int info[2];                          // goes on, begins here
+    __shared__ float first_state[KEYS][kScanThreads];   // initial state of the sequence that goes on
+    __shared__ float end_state[KEYS][kScanThreads], sum_dt[2 * PP][kScanThreads];
+    ordinary_launch_start();
+
+    // the cluster's CTAs are consecutive: rank g of channel tile ct
+    const ScanPlace<Sh> at(P, (int)(blockIdx.x % (unsigned)P.G), (int)(blockIdx.x / (unsigned)P.G));
+    const int D = P.a.D, N = P.a.N, tid = at.tid;
+    const int64_t dn = (int64_t)D * N;
+    const bool vst = (P.vec & kVecState) != 0;
+    f2 A2[4][PP], h[4][PP], dts[PP];
+    load_rates(P.a.A, at.d0, D, at.n0, N, vst, A2);
+
+    const ScanTail tail = scan_tail(P, at, scratch);
+    const bool goes_on = tail.goes_on && at.g + 1 < P.G;
+    ScanIter rows;
+    if (goes_on) {
+        rows.init(tail.first, at.row1, tail.seq);
+        zero_entries(h);
+        scan_pass<Tin, Sh, true>(P, smem, at, rows, A2, h, dts, [](const ScanTile &, f2 (&)[4][PP]) {});
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                const float2 v = unpack2(h[n][p]);
+                end_state[2 * (n * PP + p)][tid] = v.x;
+                end_state[2 * (n * PP + p) + 1][tid] = v.y;
+            }
+#pragma unroll
+        for (int p = 0; p < PP; ++p) {
+            const float2 v = unpack2(dts[p]);
+            sum_dt[2 * p][tid] = v.x;
+            sum_dt[2 * p + 1][tid] = v.y;
+        }
+        // read before any CTA of the cluster writes a final state: h_last may be h0
+        f2 v[4][PP];
+        zero_entries(v);
+        if (tail.begins && P.a.h0) {
+            const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[tail.seq] : tail.seq;
+            if (slot >= 0 && slot < P.a.num_states) load_entries(P.a.h0 + slot * dn, at.d0, D, at.n0, N, vst, v);
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                const float2 q = unpack2(v[n][p]);
+                first_state[2 * (n * PP + p)][tid] = q.x;
+                first_state[2 * (n * PP + p) + 1][tid] = q.y;
+            }
+    }
+    if (tid == 0) {
+        info[0] = goes_on;
+        info[1] = tail.begins;
+    }
+    cluster_sync_all();
+
+    // the state this chunk starts from: the summaries of the chunks before it, from the one on in which
+    // its first row's sequence begins
+    f2 carry[4][PP];
+    zero_entries(carry);
+    int from = at.g;
+    while (from > 0 && cluster_ld_s32(cluster_map(smem_u32(&info[0]), from - 1)) &&
+           (from == at.g || !cluster_ld_s32(cluster_map(smem_u32(&info[1]), from))))
+        --from;
+    for (int r = from; r < at.g; ++r) {
+        const bool begins = cluster_ld_s32(cluster_map(smem_u32(&info[1]), r)) != 0;
+        f2 dt[PP];
+#pragma unroll
+        for (int p = 0; p < PP; ++p)
+            dt[p] = pack2(cluster_ld_f32(cluster_map(smem_u32(&sum_dt[2 * p][tid]), r)),
+                          cluster_ld_f32(cluster_map(smem_u32(&sum_dt[2 * p + 1][tid]), r)));
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                const int k = 2 * (n * PP + p);
+                float2 c = unpack2(carry[n][p]);
+                if (begins) {
+                    c.x = cluster_ld_f32(cluster_map(smem_u32(&first_state[k][tid]), r));
+                    c.y = cluster_ld_f32(cluster_map(smem_u32(&first_state[k + 1][tid]), r));
+                }
+                const float2 a = unpack2(decay2(dt[p], A2[n][p]));
+                const float lx = cluster_ld_f32(cluster_map(smem_u32(&end_state[k][tid]), r)),
+                            ly = cluster_ld_f32(cluster_map(smem_u32(&end_state[k + 1][tid]), r));
+                // no product with the decay where nothing is carried: 0 x inf is not 0
+                carry[n][p] = pack2(c.x == 0.f ? lx : fmaf(a.x, c.x, lx), c.y == 0.f ? ly : fmaf(a.y, c.y, ly));
+            }
+    }
+    cluster_sync_all();              // every CTA has read what it needs of the others
+
+    rows.init(at.row0, at.row1, find_seq(P, at.row0, scratch, tid));
+    pass_empty_on(P, at);
+    zero_entries(h);
+    scan_pass<Tin, Sh, false>(P, smem, at, rows, A2, h, dts, [&](const ScanTile &tl, f2 (&v)[4][PP]) {
+        if (!tl.starts) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int p = 0; p < PP; ++p) v[n][p] = carry[n][p];
+        } else if (goes_on && tl.seq == tail.seq) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+                    v[n][p] = pack2(first_state[2 * (n * PP + p)][tid], first_state[2 * (n * PP + p) + 1][tid]);
+        } else if (P.a.h0) {
+            load_entries(P.a.h0 + tl.slot * dn, at.d0, D, at.n0, N, vst, v);
+        }
+    });
 }
 
 template <typename Tin, int NL, int CPT, bool SUM>
@@ -240,8 +413,30 @@ static cudaError_t launch_one(const ScanLaunch &P, int chunks, cudaStream_t stre
     return launch_ordinary(kern, dim3((unsigned)((int64_t)chunks * P.nct)), dim3(kScanThreads), bytes, stream, P);
 }
 
+template <typename Tin, int NL, int CPT> static cudaError_t launch_cluster(const ScanLaunch &P, cudaStream_t stream)
+{
+    constexpr int bytes = ScanSmem<Tin, ScanShape<NL, CPT>>::MAIN;
+    auto kern = scan_cluster_kernel<Tin, NL, CPT>;
+    const cudaError_t rc = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (rc != cudaSuccess) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    set_programmatic(attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)P.G;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(P.G * P.nct));
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, P);
+}
+
 template <typename Tin, int NL, int CPT> static int launch_shape(const ScanLaunch &P, cudaStream_t stream)
 {
+    if (P.cluster) return launch_cluster<Tin, NL, CPT>(P, stream) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
     if (P.hin) {
         if (launch_one<Tin, NL, CPT, true>(P, P.G - 1, stream) != cudaSuccess) return GDN_ERR_LAUNCH;
         if (launch_scan_carry(P, false, stream) != cudaSuccess) return GDN_ERR_LAUNCH;

@@ -19,6 +19,7 @@ struct ScanLaunch {
     int C, G;           // rows per chunk, chunks
     int cpt;            // channels per thread
     int nct;            // channel tiles
+    int cluster;        // a short forward call: its G chunks are a thread-block cluster, in one launch
     int vec;
     int mode_x, mode_dt, mode_z, mode_b, mode_c, mode_dy;
     int has_states;     // state indices are checked

@@ -382,3 +382,18 @@ def test_long_chunks():
     """Sizes whose chunks hold many tiles: several hundred rows forward, 64 backward, sequences across them."""
     _forward([2500, 0, 3400, 100], 2000, 16, "bf16", seed=31)
     _backward([500, 1, 700, 0, 99], 2000, 16, "bf16", seed=32)
+
+
+@pytest.mark.parametrize("N", [3, 16, 24, 50, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_state_sizes_across_chunks(N, dtype):
+    """Calls too long for one cluster of chunks: a summary, a carry and an output launch."""
+    _forward([5, 0, 270, 1, 64], 37, N, dtype, seed=N, out=dtype)
+
+
+@pytest.mark.parametrize("T", [33, 100, 128, 129, 255, 256, 257])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_short_calls(T, in_place):
+    """Calls of a few chunks: one sequence, and one that ends and one that begins inside."""
+    _forward([T], 72, 16, "f32", seed=T, in_place=in_place)
+    _forward([T // 3, T - T // 3 - 5, 5], 72, 16, "f32", seed=T, in_place=in_place)
