@@ -35,6 +35,21 @@ __device__ __forceinline__ float cluster_ld_f32(uint32_t caddr)
     return v;
 }
 
+__device__ __forceinline__ float4 cluster_ld_f32x4(uint32_t caddr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(caddr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_st_s32x2(uint32_t caddr, int x, int y)
+{
+    asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(caddr), "r"(x), "r"(y) : "memory");
+}
+
 __device__ __forceinline__ int cluster_ld_s32(uint32_t caddr)
 {
     int v;

@@ -281,18 +281,19 @@ __global__ void __launch_bounds__(kScanThreads, scan_ctas(NL)) scan_forward_kern
 
 // A short call in one launch: its up to eight chunks are the CTAs of a thread-block cluster (per channel
 // tile). Each takes its summary, reads those before it from the other CTAs' shared memory, folds them into
-// the state it starts from, and takes its outputs. (One prompt of 128 tokens, D = 1536, N = 16: PROMPT_TIME us; in
+// the state it starts from, and takes its outputs. (One prompt of 128 tokens, D = 1536, N = 16: 12.2 us; in
 // one pass without chunks 17.0, in three launches 20.)
 template <typename Tin, int NL, int CPT>
 __global__ void __launch_bounds__(kScanThreads) scan_cluster_kernel(const __grid_constant__ ScanLaunch P)
 {
     using Sh = ScanShape<NL, CPT>;
-    constexpr int PP = Sh::P, KEYS = 8 * PP;         // a thread's state entries
+    constexpr int PP = Sh::P;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int scratch[kScanWarps];
-    __shared__ int info[2];                          // goes on, begins here
-    __shared__ float first_state[KEYS][kScanThreads];   // initial state of the sequence that goes on
-    __shared__ float end_state[KEYS][kScanThreads], sum_dt[2 * PP][kScanThreads];
+    __shared__ int2 info[8];                         // per rank: goes on, begins there
+    // a thread's entries n = 0 .. 3 of each channel: the initial state of the sequence that goes on, its end
+    // state from zero, and its channels' sums of dt
+    __shared__ float4 first_state[2 * PP][kScanThreads], end_state[2 * PP][kScanThreads], sum_dt[kScanThreads];
     ordinary_launch_start();
 
     // the cluster's CTAs are consecutive: rank g of channel tile ct
@@ -303,27 +304,35 @@ __global__ void __launch_bounds__(kScanThreads) scan_cluster_kernel(const __grid
     f2 A2[4][PP], h[4][PP], dts[PP];
     load_rates(P.a.A, at.d0, D, at.n0, N, vst, A2);
 
+    const auto put = [&](float4 (&to)[2 * PP][kScanThreads], const f2 (&v)[4][PP]) {
+#pragma unroll
+        for (int p = 0; p < PP; ++p) {
+            const float2 a = unpack2(v[0][p]), b = unpack2(v[1][p]), c = unpack2(v[2][p]), d = unpack2(v[3][p]);
+            to[2 * p][tid] = make_float4(a.x, b.x, c.x, d.x);
+            to[2 * p + 1][tid] = make_float4(a.y, b.y, c.y, d.y);
+        }
+    };
+    const auto get = [&](const float4 (&from)[2 * PP][kScanThreads], f2 (&v)[4][PP]) {
+#pragma unroll
+        for (int p = 0; p < PP; ++p) {
+            const float4 x = from[2 * p][tid], y = from[2 * p + 1][tid];
+            v[0][p] = pack2(x.x, y.x);
+            v[1][p] = pack2(x.y, y.y);
+            v[2][p] = pack2(x.z, y.z);
+            v[3][p] = pack2(x.w, y.w);
+        }
+    };
     const ScanTail tail = scan_tail(P, at, scratch);
     const bool goes_on = tail.goes_on && at.g + 1 < P.G;
+    cluster_sync_all();              // the others' shared memory exists
     ScanIter rows;
     if (goes_on) {
         rows.init(tail.first, at.row1, tail.seq);
         zero_entries(h);
         scan_pass<Tin, Sh, true>(P, smem, at, rows, A2, h, dts, [](const ScanTile &, f2 (&)[4][PP]) {});
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int p = 0; p < PP; ++p) {
-                const float2 v = unpack2(h[n][p]);
-                end_state[2 * (n * PP + p)][tid] = v.x;
-                end_state[2 * (n * PP + p) + 1][tid] = v.y;
-            }
-#pragma unroll
-        for (int p = 0; p < PP; ++p) {
-            const float2 v = unpack2(dts[p]);
-            sum_dt[2 * p][tid] = v.x;
-            sum_dt[2 * p + 1][tid] = v.y;
-        }
+        put(end_state, h);
+        const float2 s0 = unpack2(dts[0]), s1 = unpack2(dts[PP - 1]);
+        sum_dt[tid] = make_float4(s0.x, s0.y, s1.x, s1.y);
         // read before any CTA of the cluster writes a final state: h_last may be h0
         f2 v[4][PP];
         zero_entries(v);
@@ -331,19 +340,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_cluster_kernel(const __grid
             const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[tail.seq] : tail.seq;
             if (slot >= 0 && slot < P.a.num_states) load_entries(P.a.h0 + slot * dn, at.d0, D, at.n0, N, vst, v);
         }
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int p = 0; p < PP; ++p) {
-                const float2 q = unpack2(v[n][p]);
-                first_state[2 * (n * PP + p)][tid] = q.x;
-                first_state[2 * (n * PP + p) + 1][tid] = q.y;
-            }
+        put(first_state, v);
     }
-    if (tid == 0) {
-        info[0] = goes_on;
-        info[1] = tail.begins;
-    }
+    // everyone's flags to everyone, so that none has to be fetched below
+    if (tid < P.G) cluster_st_s32x2(cluster_map(smem_u32(&info[at.g]), tid), goes_on, tail.begins);
     cluster_sync_all();
 
     // the state this chunk starts from: the summaries of the chunks before it, from the one on in which
@@ -351,32 +351,53 @@ __global__ void __launch_bounds__(kScanThreads) scan_cluster_kernel(const __grid
     f2 carry[4][PP];
     zero_entries(carry);
     int from = at.g;
-    while (from > 0 && cluster_ld_s32(cluster_map(smem_u32(&info[0]), from - 1)) &&
-           (from == at.g || !cluster_ld_s32(cluster_map(smem_u32(&info[1]), from))))
-        --from;
-    for (int r = from; r < at.g; ++r) {
-        const bool begins = cluster_ld_s32(cluster_map(smem_u32(&info[1]), r)) != 0;
-        f2 dt[PP];
+    while (from > 0 && info[from - 1].x && (from == at.g || !info[from].y)) --from;
+    struct Summary {
+        float4 end[2 * PP], dt;
+    };
+    const auto fetch = [&](int r) {
+        Summary q;
+        q.dt = cluster_ld_f32x4(cluster_map(smem_u32(&sum_dt[tid]), r));
 #pragma unroll
-        for (int p = 0; p < PP; ++p)
-            dt[p] = pack2(cluster_ld_f32(cluster_map(smem_u32(&sum_dt[2 * p][tid]), r)),
-                          cluster_ld_f32(cluster_map(smem_u32(&sum_dt[2 * p + 1][tid]), r)));
+        for (int c = 0; c < 2 * PP; ++c) q.end[c] = cluster_ld_f32x4(cluster_map(smem_u32(&end_state[c][tid]), r));
+        return q;
+    };
+    if (from < at.g) {
+        if (info[from].y) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int p = 0; p < PP; ++p) {
-                const int k = 2 * (n * PP + p);
-                float2 c = unpack2(carry[n][p]);
-                if (begins) {
-                    c.x = cluster_ld_f32(cluster_map(smem_u32(&first_state[k][tid]), r));
-                    c.y = cluster_ld_f32(cluster_map(smem_u32(&first_state[k + 1][tid]), r));
-                }
-                const float2 a = unpack2(decay2(dt[p], A2[n][p]));
-                const float lx = cluster_ld_f32(cluster_map(smem_u32(&end_state[k][tid]), r)),
-                            ly = cluster_ld_f32(cluster_map(smem_u32(&end_state[k + 1][tid]), r));
-                // no product with the decay where nothing is carried: 0 x inf is not 0
-                carry[n][p] = pack2(c.x == 0.f ? lx : fmaf(a.x, c.x, lx), c.y == 0.f ? ly : fmaf(a.y, c.y, ly));
+            for (int c = 0; c < 2 * PP; c += 2) {
+                const float4 x = cluster_ld_f32x4(cluster_map(smem_u32(&first_state[c][tid]), from)),
+                             y = cluster_ld_f32x4(cluster_map(smem_u32(&first_state[c + 1][tid]), from));
+                carry[0][c / 2] = pack2(x.x, y.x);
+                carry[1][c / 2] = pack2(x.y, y.y);
+                carry[2][c / 2] = pack2(x.z, y.z);
+                carry[3][c / 2] = pack2(x.w, y.w);
             }
+        }
+        // a remote load takes most of a microsecond: as many ranks' as the registers hold are under way together
+        constexpr int BATCH = PP == 1 ? 7 : 4;
+        for (int r0 = from; r0 < at.g; r0 += BATCH) {
+            Summary q[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (r0 + i < at.g) q[i] = fetch(r0 + i);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if (r0 + i >= at.g) break;
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    const f2 dt = p == 0 ? pack2(q[i].dt.x, q[i].dt.y) : pack2(q[i].dt.z, q[i].dt.w);
+                    const float4 ex = q[i].end[2 * p], ey = q[i].end[2 * p + 1];
+                    const float lx[4] = {ex.x, ex.y, ex.z, ex.w}, ly[4] = {ey.x, ey.y, ey.z, ey.w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 c = unpack2(carry[n][p]), a = unpack2(decay2(dt, A2[n][p]));
+                        // no product with the decay where nothing is carried: 0 x inf is not 0
+                        carry[n][p] = pack2(c.x == 0.f ? lx[n] : fmaf(a.x, c.x, lx[n]), c.y == 0.f ? ly[n] : fmaf(a.y, c.y, ly[n]));
+                    }
+                }
+            }
+        }
     }
     cluster_sync_all();              // every CTA has read what it needs of the others
 
@@ -390,11 +411,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_cluster_kernel(const __grid
 #pragma unroll
                 for (int p = 0; p < PP; ++p) v[n][p] = carry[n][p];
         } else if (goes_on && tl.seq == tail.seq) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int p = 0; p < PP; ++p)
-                    v[n][p] = pack2(first_state[2 * (n * PP + p)][tid], first_state[2 * (n * PP + p) + 1][tid]);
+            get(first_state, v);
         } else if (P.a.h0) {
             load_entries(P.a.h0 + tl.slot * dn, at.d0, D, at.n0, N, vst, v);
         }
