@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
         __syncwarp();
         const Tin *xs = T.raw(b, 0), *ds = T.raw(b, 1), *Bs = T.raw_bc(b, 0), *Cs = T.raw_bc(b, 1);
         f2 dts[PP] = {};
-#pragma unroll 2
+#pragma unroll
         for (int t = 0; t < R; ++t) {
             f2 dt[PP], u[PP], gv[PP], B[4], C[4];
             load_pairs(ds + t * CB + wc, dt);
