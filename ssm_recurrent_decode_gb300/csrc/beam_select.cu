@@ -422,105 +422,119 @@ __device__ __forceinline__ double log64(double x)
     return fma((double)e, 0.69314718055994530942, 2.0 * q * p);
 }
 
-// One CTA per batch entry, a warp per beam.
-__global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(const __grid_constant__ SelectLaunch P)
+// The best K of one row's segments by rounds: a lane per segment holds its list's two next keys. For rows
+// with more keys than are ranked against each other (or fit shared memory).
+__device__ __noinline__ void join_row(const unsigned long long *keys, int segs, int K, int lane, float *logit, int *token)
 {
-    // fp64 runs at two lanes a clock, so each fp64 step is taken once for all beams (or candidates) side
-    // by side, not in every beam's warp
+    const bool on = lane < segs;
+    const unsigned long long *mine = keys + lane * K;
+    unsigned long long head = on ? mine[0] : 0, next = on && K > 1 ? mine[1] : 0;
+    int at = 2;
+    for (int k = 0; k < K; ++k) {
+        const unsigned long long best = warp_max(head);
+        if (best == 0) break;
+        if (head == best) {
+            head = next;
+            next = on && at < K ? mine[at] : 0;
+            ++at;
+        }
+        if (lane == 0) {
+            logit[k] = unordered((unsigned)(best >> 32));
+            token[k] = (int)(0xFFFFFFFFu - (unsigned)best);
+        }
+    }
+}
+
+// One CTA per batch entry. fp64 runs at two lanes a clock, so each fp64 step is taken once for all beams (or
+// candidates) side by side. Few keys are ranked each against all, which beats rounds of warp-wide maxima
+// (each some 120 cycles) up to the counts below.
+constexpr int kJoinThreads = 256;
+constexpr int kRankKeys = 128;             // keys of a row
+constexpr int kRankCandidates = 256;       // of a batch entry
+
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ SelectLaunch P)
+{
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ double row_sum[GDN_BEAM_MAX_BEAMS];
     __shared__ float row_top[GDN_BEAM_MAX_BEAMS], row_cum[GDN_BEAM_MAX_BEAMS];
-    const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
-    const int K = P.a.K, beams = P.a.beams;
-    double *score = reinterpret_cast<double *>(smem);                       // [beams, K]
-    float *logit = reinterpret_cast<float *>(score + beams * K);            // [beams, K]
-    int *token = reinterpret_cast<int *>(logit + beams * K);                // [beams, K]
-    unsigned long long *keys = reinterpret_cast<unsigned long long *>(token + beams * K);   // [beams, segs, K] where they fit
-    const int64_t beam = (int64_t)blockIdx.x * beams + j;
+    __shared__ int row_state[GDN_BEAM_MAX_BEAMS];        // 0: no beam, 1: ended, 2: has a row
+    constexpr int kWarps = kJoinThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = P.a.K, beams = P.a.beams, n = beams * K, per_row = P.segs * K;
+    unsigned long long *order = reinterpret_cast<unsigned long long *>(smem);               // [beams, K] the scores, as integers
+    float *logit = reinterpret_cast<float *>(order + n);                                    // [beams, K]
+    int *token = reinterpret_cast<int *>(logit + n);                                        // [beams, K]
+    unsigned long long *keys = reinterpret_cast<unsigned long long *>(token + n);           // [beams, segs, K] where they fit
+    const int64_t beam0 = (int64_t)blockIdx.x * beams;
 
     // The call's inputs may be read before the wait: this kernel's CTAs start when every CTA of the
     // segment kernel has let them, which each does after its own wait for the kernels before it.
-    const float cum = P.a.scores[beam];
-    const int64_t r = P.a.rows ? (int64_t)P.a.rows[beam] : beam;
-    const bool live = cum > -INFINITY && r >= 0 && r < P.a.num_rows;
-    const bool done = P.a.finished && P.a.finished[beam] && cum > -INFINITY;
-    for (int k = lane; k < K; k += 32) {
-        logit[j * K + k] = done && k == 0 ? 0.f : -INFINITY;
-        token[j * K + k] = done && k == 0 ? P.a.eos_token : -1;
+    if (tid < beams) {
+        const float cum = P.a.scores[beam0 + tid];
+        const int64_t r = P.a.rows ? (int64_t)P.a.rows[beam0 + tid] : beam0 + tid;
+        const bool ended = P.a.finished && P.a.finished[beam0 + tid];
+        row_state[tid] = !(cum > -INFINITY) ? 0 : ended ? 1 : r >= 0 && r < P.a.num_rows ? 2 : 0;
+        row_cum[tid] = cum;
+        row_sum[tid] = 1.0;              // an ended beam: score + 0 - log 1
+        row_top[tid] = 0.f;
     }
-    if (lane == 0) {
-        row_sum[j] = 1.0;            // an ended beam: score + 0 - log 1
-        row_top[j] = 0.f;
-        row_cum[j] = cum;
+    __syncthreads();
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const bool itself = row_state[i / K] == 1 && i % K == 0;
+        logit[i] = itself ? 0.f : -INFINITY;
+        token[i] = itself ? P.a.eos_token : -1;
     }
-    __syncwarp();
     ordinary_launch_start();
-    if (live && !done) {
-        // the segments' lists, best first: a lane's two next keys are at hand
-        const bool on = lane < P.segs;
-        const unsigned long long *mine = P.keys + (beam * P.segs + lane) * K;
-        if (P.staged) {
-            unsigned long long *mem = keys + j * P.segs * K;
-            for (int i = lane; i < P.segs * K; i += 32) mem[i] = P.keys[beam * P.segs * K + i];
-            __syncwarp();
-            mine = mem + lane * K;
-        }
-        const float2 st = on ? P.stats[beam * P.segs + lane] : make_float2(-INFINITY, 0.f);
-        unsigned long long head = on ? mine[0] : 0, next = on && K > 1 ? mine[1] : 0;
+
+    if (P.staged) {
+        for (int i = tid; i < beams * per_row; i += kJoinThreads) keys[i] = P.keys[beam0 * per_row + i];
+    }
+    for (int j = warp; j < beams; j += kWarps) {
+        if (row_state[j] != 2) continue;
         // the row's maximum and sum
+        const float2 st = lane < P.segs ? P.stats[(beam0 + j) * P.segs + lane] : make_float2(-INFINITY, 0.f);
         float top = st.x;
         int lanes = 1;
         while (lanes < P.segs) lanes *= 2;
         for (int off = lanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
         top = __shfl_sync(kFullMask, top, 0);
-        if (top > -INFINITY) {
-            double sum = st.x == -INFINITY ? 0.0 : st.x == top ? (double)st.y : (double)(st.y * exp_fast(st.x - top));
-            for (int off = lanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
-            if (lane == 0) {
-                row_sum[j] = sum;
-                row_top[j] = top;
-            }
-            if (P.staged && P.segs * K <= 128) {
-                // few keys: each is ranked against all
-                for (int i = lane; i < P.segs * K; i += 32) {
-                    const unsigned long long key = keys[j * P.segs * K + i];
-                    const int rank = rank_of(key, keys + j * P.segs * K, P.segs * K);
-                    if (key != 0 && rank < K) {
-                        logit[j * K + rank] = unordered((unsigned)(key >> 32));
-                        token[j * K + rank] = (int)(0xFFFFFFFFu - (unsigned)key);
-                    }
-                }
-            } else {
-                int at = 2;
-                for (int k = 0; k < K; ++k) {
-                    const unsigned long long best = warp_max(head);
-                    if (best == 0) break;
-                    if (head == best) {
-                        head = next;
-                        next = on && at < K ? mine[at] : 0;
-                        ++at;
-                    }
-                    if (lane == 0) {
-                        logit[j * K + k] = unordered((unsigned)(best >> 32));
-                        token[j * K + k] = (int)(0xFFFFFFFFu - (unsigned)best);
-                    }
-                }
-            }
+        if (top == -INFINITY) continue;
+        double sum = st.x == -INFINITY ? 0.0 : st.x == top ? (double)st.y : (double)(st.y * exp_fast(st.x - top));
+        for (int off = lanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
+        if (lane == 0) {
+            row_sum[j] = sum;
+            row_top[j] = top;
         }
     }
+    __syncthreads();                     // the keys and sums are there, and the lists are cleared
+    if (warp == kWarps - 1 && lane < beams) row_sum[lane] = log64(row_sum[lane]);
+    if (P.staged && per_row <= kRankKeys) {
+        for (int i = tid; i < beams * per_row; i += kJoinThreads) {
+            const int j = i / per_row;
+            if (row_state[j] != 2) continue;
+            const unsigned long long key = keys[i];
+            const int rank = rank_of(key, keys + j * per_row, per_row);
+            if (key != 0 && rank < K) {
+                logit[j * K + rank] = unordered((unsigned)(key >> 32));
+                token[j * K + rank] = (int)(0xFFFFFFFFu - (unsigned)key);
+            }
+        }
+    } else {
+        for (int j = warp; j < beams; j += kWarps)
+            if (row_state[j] == 2)
+                join_row(P.staged ? keys + j * per_row : P.keys + (beam0 + j) * per_row, P.segs, K, lane, logit + j * K, token + j * K);
+    }
     __syncthreads();
-    if (j == 0 && lane < beams) row_sum[lane] = log64(row_sum[lane]);
-    __syncthreads();
-    unsigned long long *order = reinterpret_cast<unsigned long long *>(score);      // the scores, as integers in their order
     const unsigned long long none = ordered64(-INFINITY);
-    for (int i = threadIdx.x; i < beams * K; i += 32 * beams) {
-        const int q = i / K;
-        const float x = logit[i], top = row_top[q];
-        const double v = (double)row_cum[q] + ((x == top ? 0.0 : (double)x - (double)top) - row_sum[q]);
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const int j = i / K;
+        const float x = logit[i], top = row_top[j];
+        const double v = (double)row_cum[j] + ((x == top ? 0.0 : (double)x - (double)top) - row_sum[j]);
         logit[i] = (float)v;
         order[i] = x == -INFINITY ? none : ordered64(v);
     }
     __syncthreads();
+
     const int64_t out = (int64_t)blockIdx.x * K;
     const auto put = [&](int k, int i) {
         const int t = token[i];
@@ -536,28 +550,23 @@ __global__ void __launch_bounds__(32 * GDN_BEAM_MAX_BEAMS) beam_join_kernel(cons
         P.a.out_tokens[out + k] = -1;
         if (P.a.out_finished) P.a.out_finished[out + k] = 0;
     };
-    if (beams * K <= 256) {
-        // few candidates: each is ranked against all, equal ones by beam
-        int live_here = 0;
-        for (int i = threadIdx.x; i < beams * K; i += 32 * beams) {
-            const unsigned long long v = order[i];
-            int rank = 0;
+    if (n <= kRankCandidates) {
+        // a candidate a thread; equal ones by beam (a row's own are in order already)
+        int rank = K;
+        bool any = false;
+        if (tid < n) {
+            const unsigned long long v = order[tid];
+            any = v > none;
+            rank = 0;
 #pragma unroll 4
-            for (int o = 0; o < beams * K; ++o) rank += order[o] > v || (order[o] == v && o < i);
-            if (v > none) {
-                ++live_here;
-                if (rank < K) put(rank, i);
-            }
+            for (int o = 0; o < n; ++o) rank += order[o] > v || (order[o] == v && o < tid);
+            if (any && rank < K) put(rank, tid);
         }
-        __shared__ int found;
-        if (threadIdx.x == 0) found = 0;
-        __syncthreads();
-        if (live_here) atomicAdd(&found, live_here);
-        __syncthreads();
-        for (int k = found + threadIdx.x; k < K; k += 32 * beams) put_none(k);
+        const int count = __syncthreads_count(any);
+        for (int k = count + tid; k < K; k += kJoinThreads) put_none(k);
         return;
     }
-    if (j != 0) return;
+    if (warp != 0) return;
     // the beams' lists: a lane per beam; the lowest lane wins a tie
     int at = 0;
     const bool on = lane < beams;
@@ -656,7 +665,7 @@ int gdn_beam_select(const gdn_beam_select_args *a, gdn_stream_t stream)
     const size_t keys = (size_t)a->beams * P.segs * a->K * 8;
     P.staged = smem + keys <= 40 * 1024;
     if (P.staged) smem += keys;
-    return launch_ordinary(beam_join_kernel, dim3((unsigned)a->batch), dim3(32u * a->beams), smem, s, P) == cudaSuccess
+    return launch_ordinary(beam_join_kernel, dim3((unsigned)a->batch), dim3(kJoinThreads), smem, s, P) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_LAUNCH;
 }
