@@ -131,25 +131,28 @@ __device__ __forceinline__ float exp_fast(float d)
     return r;
 }
 
-// Sum of exp(x - m) over a thread's elements for a finite m, on pairs (the difference first, in its own
-// rounding: it is exact near the maximum). NaN where an element is.
+// Sum of exp(x - m) over a thread's elements for a finite m, on pairs: 2^(x L - c) with L = log2(e) in fp32
+// and c = m L rounded. The product is exact inside the multiply-add, so each exponent is (x - m) L plus the
+// rounding error of c, the same for all: it is taken out of the sum. NaN where an element is.
 template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[kSelVecs], float m)
 {
     constexpr int E = Vec16<T>::E;
+    constexpr float L = 1.4426950408889634f;
     f2 total = 0ull;
-    const f2 minus = pack2(-m, -m), log2e = pack2(1.4426950408889634f, 1.4426950408889634f);
+    const float c = m * L;
+    const f2 minus = pack2(-c, -c), log2e = pack2(L, L);
 #pragma unroll
     for (int k = 0; k < kSelVecs; ++k) {
         float2 x[E / 2];
         unpack16(v[k], x);
 #pragma unroll
         for (int j = 0; j < E / 2; ++j) {
-            const float2 d = unpack2(mul2(add2(pack2(x[j].x, x[j].y), minus), log2e));
+            const float2 d = unpack2(fma2(pack2(x[j].x, x[j].y), log2e, minus));
             total = add2(total, pack2(ex2_approx(d.x), ex2_approx(d.y)));
         }
     }
     const float2 both = unpack2(total);
-    return both.x + both.y;
+    return (both.x + both.y) * ex2_approx(-fmaf(m, L, -c));
 }
 
 // The same for any m, element by element from memory: NaN counts nothing, an infinite maximum counts its
