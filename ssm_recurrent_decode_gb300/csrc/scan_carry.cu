@@ -5,71 +5,85 @@
 namespace gdn {
 
 constexpr int kCarryThreads = 64;      // small CTAs: the loads in flight are spread over the SMs
+constexpr int kCarryU = 16;            // chunks whose loads are in flight while as many are worked on
 
-// One thread per state entry walks the chunks in order (blockIdx.y = 0) or backwards (1). The loads of a
-// chunk do not depend on the carry: those of the next U chunks are in flight while U chunks are worked
-// on. The traffic is 12 bytes per entry and chunk.
+// One thread per state entry walks the chunks in order (blockIdx.y = 0) or backwards (1). The traffic is 12
+// bytes per entry and chunk, the loads do not depend on the carry; what counted was instructions: 73 per
+// entry and chunk with every chunk's borders looked at by every thread (57 us for 256 chunks of 24576 entries
+// in both directions), some 15 where a batch of chunks has none (30 us).
 __global__ void __launch_bounds__(kCarryThreads) scan_carry_kernel(const __grid_constant__ ScanLaunch P)
 {
     ordinary_launch_start();
+    const int lane = threadIdx.x & 31;
     const int64_t dn = (int64_t)P.a.D * P.a.N;
-    const int64_t i = (int64_t)blockIdx.x * kCarryThreads + threadIdx.x;
-    if (i >= dn) return;
+    const int64_t at = (int64_t)blockIdx.x * kCarryThreads + threadIdx.x;
+    const bool live = at < dn;
+    const int64_t i = live ? at : dn - 1;
     const bool back = blockIdx.y != 0;
     const int d = (int)(i / P.a.N);
-    const float A = finite_rate(P.a.A[i]);
-    float *val = back ? P.ein : P.hin;
-    const float *sums = back ? P.sumdt_head : P.sumdt;
+    const float A2 = finite_rate(P.a.A[i] * kLog2e);
     const float *boundary = back ? P.g.dh_last : P.a.h0;
-    float carry = 0.f;
-    constexpr int U = 8;
-    // chunk of position k in this direction; nothing goes on behind the last (before the first)
-    const auto chunk = [&](int k) { return back ? P.G - 1 - k : k; };
-    float loc[U], sum[U];
-    int seq[U], edge[U];
-    const auto fetch = [&](int k0, float (&lo)[U], float (&su)[U], int (&sq)[U], int (&ed)[U]) {
+    // position k of this direction is chunk k, or G - 1 - k
+    const int64_t vstep = back ? -dn : dn, sstep = back ? -(int64_t)P.a.D : P.a.D;
+    float *val = (back ? P.ein + (P.G - 1) * dn : P.hin) + i;
+    const float *sums = (back ? P.sumdt_head + (int64_t)(P.G - 1) * P.a.D : P.sumdt) + d;
+    const int last = P.G - 1;             // nothing goes on behind the last position
+
+    float loc[kCarryU], sum[kCarryU], loc2[kCarryU], sum2[kCarryU];
+    int4 info = make_int4(-1, 0, -1, 0), info2;          // of position k0 + lane
+    const auto fetch = [&](int k0, float (&lo)[kCarryU], float (&su)[kCarryU], int4 &in) {
+        const int mine = min(k0 + (lane & (kCarryU - 1)), last);
+        in = P.info[back ? P.G - 1 - mine : mine];
+        const float *v = val + k0 * vstep, *s = sums + k0 * sstep;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const bool on = k0 + k < P.G - 1;
-            const int g = chunk(on ? k0 + k : 0);
-            const int4 info = P.info[g];
-            lo[k] = on ? val[g * dn + i] : 0.f;
-            su[k] = on ? sums[(int64_t)g * P.a.D + d] : 0.f;
-            sq[k] = on ? (back ? info.z : info.x) : -1;
-            ed[k] = back ? info.w : info.y;
+        for (int k = 0; k < kCarryU; ++k) {
+            lo[k] = k0 + k < last ? *v : 0.f;
+            su[k] = k0 + k < last ? *s : 0.f;
+            v += vstep;
+            s += sstep;
         }
     };
-    fetch(0, loc, sum, seq, edge);
-    for (int k0 = 0; k0 < P.G; k0 += U) {
-        float loc2[U], sum2[U], decay[U];
-        int seq2[U], edge2[U];
-        if (k0 + U < P.G) fetch(k0 + U, loc2, sum2, seq2, edge2);      // while this batch is worked on
+    float carry = 0.f;
+    fetch(0, loc, sum, info);
+    for (int k0 = 0; k0 < P.G; k0 += kCarryU) {
+        const bool more = k0 + kCarryU < P.G;
+        if (more) fetch(k0 + kCarryU, loc2, sum2, info2);
+        // (the last position's own record is not looked at: forward, no summary wrote it)
+        const bool inner = k0 + (lane & (kCarryU - 1)) < last;
+        const int seq = !inner ? -1 : back ? info.z : info.x, edge = back ? info.w : info.y;
+        const bool plain = k0 + kCarryU <= last && __all_sync(kScanFull, seq >= 0 && !edge);
+        float *v = val + k0 * vstep;
+        if (plain) {
+            // no product with the decay where nothing is carried: 0 x inf is not 0
 #pragma unroll
-        for (int k = 0; k < U; ++k) decay[k] = expf(A * sum[k]);
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (k0 + k >= P.G) break;
-            const int g = chunk(k0 + k);
-            val[g * dn + i] = carry;
-            if (seq[k] >= 0 && edge[k]) {           // the sequence begins (backwards: ends) in this chunk
-                carry = 0.f;
-                if (boundary) {
-                    const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[seq[k]] : seq[k];
-                    if (slot >= 0 && slot < P.a.num_states) carry = boundary[slot * dn + i];
-                }
-                if (!back && P.init) P.init[g * dn + i] = carry;
+            for (int k = 0; k < kCarryU; ++k) {
+                if (live) *v = carry;
+                v += vstep;
+                carry = carry == 0.f ? loc[k] : fmaf(ex2_approx(fmaf(A2, sum[k], kDecayBias)), carry, loc[k]);
             }
-            // where nothing goes on there is no carry, and where it is zero no product: 0 x inf is not 0
-            const float next = carry == 0.f ? loc[k] : fmaf(decay[k], carry, loc[k]);
-            carry = seq[k] >= 0 ? next : 0.f;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kCarryU; ++k) {
+                const int sq = __shfl_sync(kScanFull, seq, k), ed = __shfl_sync(kScanFull, edge, k);
+                if (k0 + k >= P.G) break;
+                if (live) *v = carry;
+                v += vstep;
+                if (sq >= 0 && ed) {      // the sequence begins (backwards: ends) in this chunk
+                    carry = 0.f;
+                    const int64_t slot = P.a.state_indices ? (int64_t)P.a.state_indices[sq] : sq;
+                    if (boundary && slot >= 0 && slot < P.a.num_states) carry = boundary[slot * dn + i];
+                    if (!back && P.init && live) P.init[(int64_t)(k0 + k) * dn + i] = carry;
+                }
+                const float next = carry == 0.f ? loc[k] : fmaf(ex2_approx(fmaf(A2, sum[k], kDecayBias)), carry, loc[k]);
+                carry = sq >= 0 ? next : 0.f;
+            }
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < kCarryU; ++k) {
             loc[k] = loc2[k];
             sum[k] = sum2[k];
-            seq[k] = seq2[k];
-            edge[k] = edge2[k];
         }
+        info = info2;
     }
 }
 

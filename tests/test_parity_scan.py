@@ -397,3 +397,27 @@ def test_short_calls(T, in_place):
     """Calls of a few chunks: one sequence, and one that ends and one that begins inside."""
     _forward([T], 72, 16, "f32", seed=T, in_place=in_place)
     _forward([T // 3, T - T // 3 - 5, 5], 72, 16, "f32", seed=T, in_place=in_place)
+
+
+@pytest.mark.parametrize("fill", [0x00, 0x01, 0x7F])
+def test_what_the_workspace_held_does_not_matter(fill):
+    """Several chunks with states in a pool: outputs bit-equal whatever the workspace's bytes were."""
+    lengths, D, N = [5, 0, 400, 1, 64], 72, 16
+    c = sc.make(lengths, D, N, "bf16", 50)
+    d = _dev(c, "bf16")
+    h0, rows = _pool(c["h0"], 5, D, N, 50)
+    out = []
+    for byte in (fill, 0xFF):
+        y, last = torch.zeros(470, D, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(h0)
+        ws = _workspace(lengths, D, N, False)
+        assert ws is not None
+        gdn.mamba_selective_scan(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], y, Dskip=d["Dskip"], z=d["z"], cu_seqlens=_cu(lengths),
+                                 state_indices=rows, h0=h0, h_last=last, workspace=ws.fill_(byte))
+        dx, dA, dh0 = torch.zeros_like(d["x"]), torch.zeros(D, N, device="cuda"), torch.zeros_like(h0)
+        gdn.mamba_selective_scan_backward(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["dy"], Dskip=d["Dskip"], z=d["z"],
+                                          cu_seqlens=_cu(lengths), state_indices=rows, h0=h0, dh_last=h0, dx=dx, dA=dA, dh0=dh0,
+                                          workspace=_workspace(lengths, D, N, False, True).fill_(byte))
+        torch.cuda.synchronize()
+        out.append((y, last, dx, dA, dh0))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
