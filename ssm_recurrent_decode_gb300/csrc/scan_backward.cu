@@ -77,10 +77,7 @@ template <typename Tin, class Sh> struct BackTile {
             if (P.a.z) {
                 load_pairs(raw(b, 2) + r * CB + warp * Sh::CW + c, z);
 #pragma unroll
-                for (int p = 0; p < PP; ++p) {
-                    const float2 v = unpack2(z[p]);
-                    g[p] = mul2(g[p], pack2(v.x * fast_sigmoid(v.x), v.y * fast_sigmoid(v.y)));
-                }
+                for (int p = 0; p < PP; ++p) g[p] = mul2(g[p], mul2(z[p], sigmoid2(z[p])));
             }
             store_pairs(gs + r * Sh::YP + c, g);
         }
@@ -478,9 +475,9 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                         gt[p] = fma2(u2[p], x2[p], mul2(pack2(kLn2, kLn2), w2[p]));      // A2 = A log2(e)
                         dD[p] = fma2(g2[p], x2[p], dD[p]);
                         if (P.g.dz) {
-                            const float2 z = unpack2(z2[p]);
-                            const float sx = fast_sigmoid(z.x), sy = fast_sigmoid(z.y);
-                            const f2 slope = pack2(sx * fmaf(z.x, 1.f - sx, 1.f), sy * fmaf(z.y, 1.f - sy, 1.f));
+                            // silu'(z) = s (1 + z (1 - s)) at s = sigmoid(z)
+                            const f2 sg = sigmoid2(z2[p]), one = pack2(1.f, 1.f);
+                            const f2 slope = mul2(sg, fma2(z2[p], fma2(sg, pack2(-1.f, -1.f), one), one));
                             gz[p] = mul2(mul2(y2[p], fma2(skip[p], x2[p], s2[p])), slope);
                         }
                     }

@@ -99,12 +99,16 @@ __device__ __forceinline__ f2 decay2(f2 dtdt, f2 A2)
     return pack2(ex2_approx(y.x), ex2_approx(y.y));
 }
 
-// sigmoid on the fast reciprocal and exponential (relative error of a few 2^-23; exactly 0 where exp(-z) overflows)
-__device__ __forceinline__ float fast_sigmoid(float z)
+// sigmoid of a pair on the fast reciprocal and exponential (relative error of a few 2^-23; exactly 0 where
+// exp(-z) overflows)
+__device__ __forceinline__ f2 sigmoid2(f2 z)
 {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * z)));
-    return r;
+    const float2 t = unpack2(mul2(z, pack2(-kLog2e, -kLog2e)));
+    const float2 d = unpack2(add2(pack2(ex2_approx(t.x), ex2_approx(t.y)), pack2(1.f, 1.f)));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    return pack2(r.x, r.y);
 }
 
 // Sums v[0 .. M) over the NL lanes of a group, M values at once: each halving of the lanes halves

@@ -185,10 +185,7 @@ __device__ __forceinline__ void scan_pass(const ScanLaunch &P, unsigned char *sm
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
                     y[p] = fma2(skip[p], x2[p], y[p]);
-                    if (P.a.z) {
-                        const float2 z = unpack2(z2[p]);
-                        y[p] = mul2(y[p], mul2(z2[p], pack2(fast_sigmoid(z.x), fast_sigmoid(z.y))));
-                    }
+                    if (P.a.z) y[p] = mul2(y[p], mul2(z2[p], sigmoid2(z2[p])));
                     if (tl.seq < 0) y[p] = 0ull;
                 }
                 if (!GDN_IN(P.a.err_flags, (int64_t)tl.t0 + t, P.a.T)) continue;
