@@ -21,7 +21,8 @@
  *
  * Sequences are packed end to end: token rows 0 .. T-1. With cu_seqlens sequence s owns rows
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 (it may be empty: its final state is then its initial one);
- * without, T rows are S sequences of T / S tokens each.
+ * without, T rows are S sequences of T / S tokens each. Two sequences of a call may not name the same
+ * state row (the result is then undefined).
  */
 #ifndef MAMBA_SCAN_H
 #define MAMBA_SCAN_H

@@ -65,6 +65,11 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
     P.cpt = 4;
     P.nct = tiles(4);
     if (backward) {
+        // (two channels a thread for N <= 8, whose tiles of four would leave room for one CTA per SM)
+        if (scan_lanes(P.a.N) == 2) {
+            P.cpt = 2;
+            P.nct = tiles(2);
+        }
         // Chunks of 64 rows (what the states kept per CTA allow), shorter ones where those would leave SMs
         // without work.
         const int64_t C = (T * P.nct + kScanBackCtas * kSms - 1) / (kScanBackCtas * kSms);

@@ -12,7 +12,6 @@
 
 namespace gdn {
 
-constexpr int kBackCpt = 4;         // channels per thread
 constexpr int kBackTile = 8;        // token rows per tile: their states and decays fit a thread's registers
 constexpr int kBackTiles = kScanBackChunk / kBackTile;
 
@@ -22,11 +21,31 @@ template <typename Tin, class Sh> struct BackSmem {
     static constexpr int RB = R * Sh::NP * (int)sizeof(Tin);              // a staged B or C tile
     static constexpr int STAGE = 4 * RX + 2 * RB;
     static constexpr int SUMS = kScanWarps * R * Sh::YP * 4;              // a value per row and channel
+    // Sums over the state's lanes: up to four lanes' are joined through shared memory where the rows are finished,
+    // four rows at a time (bf16: the room is there beside two CTAs' stages), others by shuffles (8 x 2048 rows,
+    // N = 16, bf16: 760 us joined, 778 by shuffles).
+    static constexpr bool JOINED = Sh::NL <= 4 && sizeof(Tin) == 2;
+    static constexpr int LANES = JOINED ? Sh::NL : 1, HALF = JOINED ? 4 : R;       // HALF rows are finished at a time
+    static constexpr int JOIN = kScanWarps * HALF * LANES * Sh::YP * 4;
+    static constexpr int JOIN_Y = JOINED ? JOIN : SUMS;       // the shuffled sums of C h are taken with the states, all rows'
     static constexpr int PART = kScanWarps * R * 2 * Sh::NP * 4;          // dB and dC per warp
     static constexpr int STATES = (kBackTiles - 2) * 4 * kScanThreads * 8 * Sh::P;   // not before the first and the last tile
     static constexpr int SUMMARY = 2 * STAGE + SUMS;
-    static constexpr int MAIN = 2 * STAGE + 4 * SUMS + PART + STATES;
+    static constexpr int MAIN = 2 * STAGE + SUMS + JOIN_Y + 2 * JOIN + PART + STATES;
 };
+
+// the sum of LANES vectors of pairs, one row pitch apart
+template <int LANES, int PITCH, int P> __device__ __forceinline__ void join_lanes(const float *from, f2 (&v)[P])
+{
+    load_pairs(from, v);
+#pragma unroll
+    for (int q = 1; q < LANES; ++q) {
+        f2 more[P];
+        load_pairs(from + q * PITCH, more);
+#pragma unroll
+        for (int p = 0; p < P; ++p) v[p] = add2(v[p], more[p]);
+    }
+}
 
 // Staging that the summary and the gradient kernel share, and g = dy silu(z) of a tile.
 template <typename Tin, class Sh> struct BackTile {
@@ -221,10 +240,12 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
     const bool vst = (P.vec & kVecState) != 0;
 
     BackTile<Tin, Sh> T(P, smem, tid, c0);
-    // per warp [R][YP]: g, and sums over n of C h, B dh and A w
+    // per warp: g [R][YP], and of HALF rows the sums over n of C h, B dh and A w
     float *gs = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * R * YP;
-    float *sum_y = gs + Sm::SUMS / 4, *sum_u = sum_y + Sm::SUMS / 4, *sum_w = sum_u + Sm::SUMS / 4;
-    float *part = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + 4 * Sm::SUMS);
+    float *sum_y = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::SUMS) + warp * (Sm::JOIN_Y / 4 / kScanWarps);
+    float *sum_u = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::SUMS + Sm::JOIN_Y) + warp * (Sm::JOIN / 4 / kScanWarps),
+          *sum_w = sum_u + Sm::JOIN / 4;
+    float *part = reinterpret_cast<float *>(smem + 2 * Sm::STAGE + Sm::SUMS + Sm::JOIN_Y + 2 * Sm::JOIN);
     float *states = reinterpret_cast<float *>(smem + Sm::MAIN - Sm::STATES);
 
     f2 A2[4][PP], dA[4][PP];
@@ -360,21 +381,23 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                         load_pairs(ds + t * CB + wc, dt);
                         load_pairs(xs + t * CB + wc, u);
                         load_twice(Bs + t * NP + n0, B);
-                        load_twice(Cs + t * NP + n0, C);
+                        if (!Sm::JOINED) load_twice(Cs + t * NP + n0, C);
 #pragma unroll
                         for (int p = 0; p < PP; ++p) {
                             u[p] = mul2(u[p], dt[p]);
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 hp[t + 1][q][p] = fma2(decay2(dt[p], A2[q][p]), hp[t][q][p], mul2(u[p], B[q]));
-                                y[p] = q == 0 ? mul2(C[q], hp[t + 1][q][p]) : fma2(C[q], hp[t + 1][q][p], y[p]);
+                                if (!Sm::JOINED) y[p] = q == 0 ? mul2(C[q], hp[t + 1][q][p]) : fma2(C[q], hp[t + 1][q][p], y[p]);
                             }
-                            const float2 v = unpack2(y[p]);
-                            acc[k * CPT + 2 * p] = v.x;
-                            acc[k * CPT + 2 * p + 1] = v.y;
+                            if (!Sm::JOINED) {
+                                const float2 v = unpack2(y[p]);
+                                acc[k * CPT + 2 * p] = v.x;
+                                acc[k * CPT + 2 * p + 1] = v.y;
+                            }
                         }
                     }
-                    if (P.g.dz) {
+                    if (!Sm::JOINED && P.g.dz) {
                         constexpr int M = 4 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
                         group_reduce<M, NL>(acc, nl);
                         if (nl % REP == 0) {
@@ -387,10 +410,12 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                     }
                 }
                 __syncwarp();
-                // backwards
+                // backwards, HALF rows at a time
 #pragma unroll
-                for (int t = R - 1; t >= 0; --t) {
-                    f2 dt[PP], u[PP], gv[PP], B[4], C[4], db[4], dc[4], us[PP], ws[PP];
+                for (int half = R - Sm::HALF; half >= 0; half -= Sm::HALF) {
+#pragma unroll
+                for (int t = half + Sm::HALF - 1; t >= half; --t) {
+                    f2 dt[PP], u[PP], gv[PP], B[4], C[4], db[4], dc[4], us[PP], ws[PP], ys[PP];
                     load_pairs(ds + t * CB + wc, dt);
                     load_pairs(xs + t * CB + wc, u);
                     load_pairs(gs + t * YP + cl * CPT, gv);
@@ -405,13 +430,19 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                             dc[q] = p == 0 ? mul2(gv[p], hp[t + 1][q][p]) : fma2(gv[p], hp[t + 1][q][p], dc[q]);
                             db[q] = p == 0 ? mul2(u[p], dh) : fma2(u[p], dh, db[q]);
                             us[p] = q == 0 ? mul2(B[q], dh) : fma2(B[q], dh, us[p]);
+                            if (Sm::JOINED) ys[p] = q == 0 ? mul2(C[q], hp[t + 1][q][p]) : fma2(C[q], hp[t + 1][q][p], ys[p]);
                             e[q][p] = mul2(decay2(dt[p], A2[q][p]), dh);
                             const f2 wv = mul2(e[q][p], hp[t][q][p]);
                             ws[p] = q == 0 ? mul2(wv, A2[q][p]) : fma2(wv, A2[q][p], ws[p]);
                             dA[q][p] = fma2(wv, dt[p], dA[q][p]);
                         }
                     }
-                    {
+                    if (Sm::JOINED) {
+                        const int o = ((t - half) * NL + nl) * YP + cl * CPT;
+                        store_pairs(sum_y + o, ys);
+                        store_pairs(sum_u + o, us);
+                        store_pairs(sum_w + o, ws);
+                    } else {
                         constexpr int M = 2 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
                         float v[M];
 #pragma unroll
@@ -427,7 +458,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
 #pragma unroll
                             for (int i = 0; i < KEEP; ++i) {
                                 const int k = nl / REP * KEEP + i;      // the first half: sums of B dh, the second: of A w
-                                (k < CPT ? sum_u : sum_w)[t * YP + cl * CPT + k % CPT] = v[i];
+                                (k < CPT ? sum_u : sum_w)[(t - half) * YP + cl * CPT + k % CPT] = v[i];
                             }
                         }
                     }
@@ -450,24 +481,23 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                         }
                     }
                 }
-                __syncthreads();
-
-                // this warp's per-channel gradients of the tile's rows
+                __syncwarp();
+                // this warp's per-channel gradients of these rows
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += NL) {
-                    const int r = r0 + orow;
-                    if (r >= n || oc >= T.ncols) continue;
-                    const int sc = r * YP + lane % CLN * CPT;
+                for (int r0 = 0; r0 < Sm::HALF; r0 += NL) {
+                    const int r = half + r0 + orow;
+                    if ((NL > Sm::HALF && orow >= Sm::HALF) || r >= n || oc >= T.ncols) continue;
+                    const int sc = (r - half) * Sm::LANES * YP + lane % CLN * CPT;
                     f2 x2[PP], d2[PP], y2[PP], z2[PP], g2[PP], u2[PP], w2[PP], s2[PP], gx[PP], gt[PP], gz[PP];
                     load_pairs(xs + r * CB + oc, x2);
                     load_pairs(ds + r * CB + oc, d2);
-                    load_pairs(gs + sc, g2);
-                    load_pairs(sum_u + sc, u2);
-                    load_pairs(sum_w + sc, w2);
+                    load_pairs(gs + r * YP + lane % CLN * CPT, g2);
+                    join_lanes<Sm::LANES, YP>(sum_u + sc, u2);
+                    join_lanes<Sm::LANES, YP>(sum_w + sc, w2);
                     if (P.g.dz) {
                         load_pairs(dys + r * CB + oc, y2);
                         load_pairs(zs + r * CB + oc, z2);
-                        load_pairs(sum_y + sc, s2);
+                        join_lanes<Sm::LANES, YP>(sum_y + (Sm::JOINED ? sc : r * YP + lane % CLN * CPT), s2);
                     }
 #pragma unroll
                     for (int p = 0; p < PP; ++p) {
@@ -488,6 +518,9 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                     if (P.g.ddt) store_row(static_cast<Tin *>(P.g.ddt) + row * P.g.ddt_stride + col, gt, left, (P.vec & kVecDdt) && left >= CPT);
                     if (P.g.dz) store_row(static_cast<Tin *>(P.g.dz) + row * P.g.dz_stride + col, gz, left, (P.vec & kVecDz) && left >= CPT);
                 }
+                __syncwarp();
+                }
+                __syncthreads();
                 // this channel tile's share of dB and dC: the warps' sums in order
                 for (int i = tid; i < n * 2 * NP; i += kScanThreads) {
                     const int r = i / (2 * NP), k = i / NP % 2, nn = i % NP;
@@ -577,11 +610,11 @@ template <typename Tin, int NL, int CPT> static int launch_shape(const ScanLaunc
 template <typename Tin> static int launch_typed(const ScanLaunch &P, cudaStream_t stream)
 {
     switch (scan_lanes(P.a.N)) {
-    case 2: return launch_shape<Tin, 2, kBackCpt>(P, stream);
-    case 4: return launch_shape<Tin, 4, kBackCpt>(P, stream);
-    case 8: return launch_shape<Tin, 8, kBackCpt>(P, stream);
-    case 16: return launch_shape<Tin, 16, kBackCpt>(P, stream);
-    default: return launch_shape<Tin, 32, kBackCpt>(P, stream);
+    case 2: return launch_shape<Tin, 2, 2>(P, stream);
+    case 4: return launch_shape<Tin, 4, 4>(P, stream);
+    case 8: return launch_shape<Tin, 8, 4>(P, stream);
+    case 16: return launch_shape<Tin, 16, 4>(P, stream);
+    default: return launch_shape<Tin, 32, 4>(P, stream);
     }
 }
 

@@ -8,7 +8,7 @@
 // States cross chunk borders through a summary pass (the state each chunk would end with from zero,
 // and the sum of its dt: its decay is exp(A sum dt), one exp per entry and chunk) and a carry pass
 // over the chunks. The summary costs a second exp per state entry, so it is skipped where the
-// sequences alone fill the GPU (mamba_scan_plan).
+// sequences alone fill the GPU (plan in scan_api.cu).
 #pragma once
 
 #include <cmath>

@@ -421,3 +421,34 @@ def test_what_the_workspace_held_does_not_matter(fill):
         out.append((y, last, dx, dA, dh0))
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,S", [(60, 2), (300, 3), (30, 1)])
+def test_rows_of_no_sequence_are_zero_and_flagged(T, S):
+    """cu_seqlens that begin behind row 0 and end before row T - 1: the other rows' outputs and gradients are zeros."""
+    D, N, first = 40, 16, 7
+    lengths = [(T - 20) // S] * S
+    end = first + sum(lengths)
+    c = sc.make([T], D, N, "f32", 60, states=False)
+    d = _dev(c, "f32")
+    cu = torch.tensor(first + np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    y = torch.full((T, D), 5.0, device="cuda")
+    ws = gdn.mamba_scan_workspace(T, D, N, sequences=S, uniform=False)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.mamba_selective_scan(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], y, Dskip=d["Dskip"], z=d["z"], cu_seqlens=cu,
+                             workspace=ws, err_flags=err)
+    assert int(err.item()) == gdn.GDN_DEVERR_BAD_INDEX
+    g = {"dx": torch.full((T, D), 5.0, device="cuda"), "dCm": torch.full((T, N), 5.0, device="cuda"), "dA": torch.empty(D, N, device="cuda")}
+    err.zero_()
+    gdn.mamba_selective_scan_backward(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["dy"], Dskip=d["Dskip"], z=d["z"], cu_seqlens=cu,
+                                      workspace=gdn.mamba_scan_workspace(T, D, N, sequences=S, uniform=False, backward=True),
+                                      err_flags=err, **g)
+    assert int(err.item()) == gdn.GDN_DEVERR_BAD_INDEX
+    inner = {**c, **{k: c[k][first:end] for k in ("x", "dt", "Bm", "Cm", "z", "dy")}, "lengths": lengths}
+    (ref, mag), (gref, gmag), u = sc.forward(inner), sc.backward(inner), sc.unit(inner)
+    sc.check("y", y[first:end].cpu().numpy(), ref["y"], mag["y"], u)
+    sc.check("dx", g["dx"][first:end].cpu().numpy(), gref["dx"], gmag["dx"], 2 * u)
+    sc.check("dCm", g["dCm"][first:end].cpu().numpy(), gref["dCm"], gmag["dCm"], 2 * u, terms=D)
+    sc.check("dA", g["dA"].cpu().numpy(), gref["dA"], gmag["dA"], 2 * u, terms=T)
+    for t in (y, g["dx"], g["dCm"]):
+        assert torch.all(t[:first] == 0) and torch.all(t[end:] == 0)
