@@ -14,7 +14,8 @@ template <typename Tin, class Sh> struct ScanSmem {
     static constexpr int STAGE = 3 * RX + 2 * RB;
     static constexpr int HALF = 8;                                       // rows between two stores of outputs
     static constexpr int PARTS = Sh::NL <= 4 ? Sh::NL : 1;               // sums over n still to be joined
-    static constexpr int Y = kScanWarps * HALF * PARTS * Sh::YP * 4;
+    static constexpr int JOIN = Sh::NL > 4 ? HALF * 32 * Sh::CPT * 4 : 0;   // a warp's sums before eight lanes' are joined
+    static constexpr int Y = kScanWarps * (HALF * PARTS * Sh::YP * 4 + JOIN);
     static constexpr int MAIN = 2 * STAGE + Y;
     static constexpr int SUMMARY = 2 * STAGE;
 };
@@ -103,6 +104,7 @@ __device__ __forceinline__ void scan_pass(const ScanLaunch &P, unsigned char *sm
                         !SUM && P.a.Dskip && c + 1 < ncols ? P.a.Dskip[c0 + c + 1] : 0.f);
     }
     float *ys = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + warp * Sm::HALF * Sm::PARTS * Sh::YP;
+    float *before = reinterpret_cast<float *>(smem + 2 * Sm::STAGE) + kScanWarps * Sm::HALF * Sm::PARTS * Sh::YP + warp * (Sm::JOIN / 4);
 
     int b = 0;
     while (use.next(P, tl)) {
@@ -125,7 +127,6 @@ __device__ __forceinline__ void scan_pass(const ScanLaunch &P, unsigned char *sm
         for (int t8 = 0; t8 < kScanTile; t8 += Sm::HALF) {
 #pragma unroll
             for (int t4 = t8; t4 < t8 + Sm::HALF; t4 += 4) {       // eight rows' work to schedule among (401 -> 379 us)
-                float acc[4 * CPT];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int t = t4 + k;
@@ -143,26 +144,34 @@ __device__ __forceinline__ void scan_pass(const ScanLaunch &P, unsigned char *sm
                             if (!SUM) y[p] = n == 0 ? mul2(C[n], h[n][p]) : fma2(C[n], h[n][p], y[p]);
                         }
                         if (SUM) dt_tile[p] = add2(dt_tile[p], dt[p]);
-                        else if (NL > 4) {
-                            const float2 v = unpack2(y[p]);
-                            acc[k * CPT + 2 * p] = v.x;
-                            acc[k * CPT + 2 * p + 1] = v.y;
-                        }
                     }
-                    // up to four lanes' sums are joined where the row is finished, more of them here by shuffles
+                    // up to four lanes' sums are joined where the row is finished, more of them eight by eight below
                     if (!SUM && NL <= 4) store_pairs(ys + ((t - t8) * NL + nl) * Sh::YP + cl * CPT, y);
+                    if (!SUM && NL > 4) store_pairs(before + ((t - t8) * 32 + lane) * CPT, y);
                 }
-                if (!SUM && NL > 4) {
-                    constexpr int M = 4 * CPT, KEEP = M >= NL ? M / NL : 1, REP = M >= NL ? 1 : NL / M;
-                    group_reduce<M, NL>(acc, nl);
-                    if (nl % REP == 0) {
+            }
+            if (!SUM && NL > 4) {
+                // the eight rows' 256 sums, eight to a lane (each lane begins at another, for the banks): those of one
+                // row and channel lane lie in NL / 8 lanes
+                __syncwarp();
+                f2 y[PP];
+                load_pairs(before + (lane * 8 + (lane & 7)) * CPT, y);
 #pragma unroll
-                        for (int i = 0; i < KEEP; ++i) {
-                            const int v = nl / REP * KEEP + i;
-                            ys[(t4 - t8 + v / CPT) * Sh::YP + cl * CPT + v % CPT] = acc[i];
-                        }
-                    }
+                for (int i = 1; i < 8; ++i) {
+                    f2 more[PP];
+                    load_pairs(before + (lane * 8 + ((lane + i) & 7)) * CPT, more);
+#pragma unroll
+                    for (int p = 0; p < PP; ++p) y[p] = add2(y[p], more[p]);
                 }
+#pragma unroll
+                for (int off = 1; off < NL / 8; off <<= 1)
+#pragma unroll
+                    for (int p = 0; p < PP; ++p) {
+                        const float2 v = unpack2(y[p]);
+                        y[p] = add2(y[p], pack2(__shfl_xor_sync(kScanFull, v.x, off), __shfl_xor_sync(kScanFull, v.y, off)));
+                    }
+                constexpr int SHARE = NL >= 8 ? NL / 8 : 1;
+                if (lane % SHARE == 0) store_pairs(ys + lane / 4 * Sh::YP + lane % 4 * 8 / NL * CPT, y);
             }
             if (SUM) continue;
             __syncwarp();
