@@ -47,8 +47,9 @@ constexpr int kScanBackChunk = 64;   // most token rows per chunk of the backwar
 constexpr int kScanBackCtas = 2;     // its resident CTAs per SM
 
 // Resident CTAs per SM of the forward kernel. Wide states (N above 32) ran faster with more registers a
-// thread than with a fourth CTA (N = 128, 4 x 1024 rows, fp32: 266 against 342 us), narrow ones did not
-// care (N = 16, 32768 rows: 401 against 404), and six CTAs of 80 registers were slower for both (437, 432).
+// thread than with a fourth CTA (N = 128, 4 x 1024 rows, fp32: 245 against 323 us), narrow ones a little slower
+// (N = 16, 32768 rows: 382 against 379; 24 ragged prompts of 8000: 131 against 123 to 129), and six CTAs of 80
+// registers were slower for both.
 constexpr int scan_ctas(int lanes) { return lanes >= 16 ? 3 : 4; }
 
 // The carry pass over the chunks (forward; with both also the backward one, over e).
