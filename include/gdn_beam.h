@@ -82,7 +82,7 @@ typedef struct gdn_beam_reorder_args {
     const int32_t *slots;       /* [batch, beams]: each beam's slot, all different */
     const int32_t *parents;     /* [batch, beams]: the beam that each new beam continues; outside
                                    [0, beams): the new beam continues none, and only gets a slot */
-    int32_t *new_slots;         /* [batch, beams]: each new beam's slot; may not overlap slots */
+    int32_t *new_slots;         /* [batch, beams]: each new beam's slot; may not overlap slots or parents */
     int32_t *err_flags;         /* optional device word: GDN_DEVERR_BAD_INDEX for a copy from or to a
                                    slot outside [0, num_slots); the copy is skipped */
 } gdn_beam_reorder_args;
@@ -95,8 +95,8 @@ typedef struct gdn_beam_reorder_args {
  * written. The next decode step reads its slots from new_slots (cache_indices of
  * gdn_decode_step_indexed). One launch for up to 2048 beams. A chained decode call may not directly
  * follow this one on the stream (it writes states: the first layer's call has to be an ordinary one).
- * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_ALIGN, GDN_ERR_ARG (new_slots is slots) or
- * GDN_ERR_LAUNCH.
+ * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_ALIGN, GDN_ERR_ARG (new_slots overlaps slots or
+ * parents) or GDN_ERR_LAUNCH.
  */
 int gdn_beam_reorder(const gdn_beam_reorder_args *args, gdn_stream_t stream);
 

@@ -138,6 +138,12 @@ __global__ void __launch_bounds__(kReThreads) beam_reorder_kernel(const __grid_c
     }
 }
 
+bool overlap(const void *p, size_t pn, const void *q, size_t qn)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + qn && b < a + pn;
+}
+
 }  // namespace
 
 }  // namespace gdn
@@ -150,7 +156,9 @@ extern "C" int gdn_beam_reorder(const gdn_beam_reorder_args *a, gdn_stream_t str
         a->num_pools > GDN_BEAM_MAX_POOLS)
         return GDN_ERR_SHAPE;
     if ((a->num_pools > 0 && !a->pools) || (a->batch > 0 && (!a->slots || !a->parents || !a->new_slots))) return GDN_ERR_NULL;
-    if (a->batch > 0 && a->new_slots == a->slots) return GDN_ERR_ARG;
+    // every CTA reads both tables, and the first writes new_slots while others may still be reading
+    const size_t table = (size_t)a->batch * a->beams * sizeof(int32_t);
+    if (overlap(a->new_slots, table, a->slots, table) || overlap(a->new_slots, table, a->parents, table)) return GDN_ERR_ARG;
     for (const void *p : {(const void *)a->slots, (const void *)a->parents, (const void *)a->new_slots})
         if (reinterpret_cast<uintptr_t>(p) % 4) return GDN_ERR_ALIGN;
     ReorderLaunch P;
