@@ -615,6 +615,26 @@ bool select_sizes_ok(int32_t batch, int32_t beams, int32_t vocab, int32_t K)
 
 size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
+bool overlap(const void *p, size_t pn, const void *q, size_t qn)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + qn && b < a + pn;
+}
+
+// Whether an output lies over memory that the join still reads: its CTAs run in no order, and each reads its entry's
+// part of the tables before it writes its own results. So only a table of the very same layout may be an output.
+bool outputs_overlap(const gdn_beam_select_args &a, size_t workspace)
+{
+    const size_t in = (size_t)a.batch * a.beams, out = (size_t)a.batch * a.K;
+    const struct { const void *p; size_t es; } tables[] = {{a.rows, 4}, {a.scores, 4}, {a.finished, 1}},
+                                               outputs[] = {{a.out_scores, 4}, {a.out_parents, 4}, {a.out_tokens, 4}, {a.out_finished, 1}};
+    for (const auto &o : outputs) {
+        if (overlap(o.p, out * o.es, a.workspace, workspace)) return true;
+        for (const auto &t : tables)
+            if (overlap(o.p, out * o.es, t.p, in * t.es) && !(o.p == t.p && o.es == t.es && a.K == a.beams)) return true;
+    }
+    return false;
+}
 
 }  // namespace
 
@@ -647,11 +667,13 @@ int gdn_beam_select(const gdn_beam_select_args *a, gdn_stream_t stream)
     if (!a->logits || !a->scores || !a->out_scores || !a->out_parents || !a->out_tokens || !a->workspace) return GDN_ERR_NULL;
     if (a->row_stride < a->vocab || a->num_rows < 1 || (!a->rows && a->num_rows < (int64_t)a->batch * a->beams))
         return GDN_ERR_SHAPE;
-    if (a->workspace_bytes < gdn_beam_select_workspace_bytes(a->batch, a->beams, a->vocab, a->K)) return GDN_ERR_SHAPE;
+    const size_t need = gdn_beam_select_workspace_bytes(a->batch, a->beams, a->vocab, a->K);
+    if (a->workspace_bytes < need) return GDN_ERR_SHAPE;
     const int es = a->logits_dtype == GDN_BF16 ? 2 : 4;
     if (!aligned_to(a->logits, es) || !aligned_to(a->rows, 4) || !aligned_to(a->scores, 4) || !aligned_to(a->out_scores, 4) ||
         !aligned_to(a->out_parents, 4) || !aligned_to(a->out_tokens, 4) || !aligned_to(a->workspace, 16))
         return GDN_ERR_ALIGN;
+    if (outputs_overlap(*a, need)) return GDN_ERR_ARG;
     SelectLaunch P;
     P.a = *a;
     const int64_t rows = (int64_t)a->batch * a->beams;
