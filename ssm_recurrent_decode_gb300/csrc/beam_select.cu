@@ -133,7 +133,9 @@ __device__ __forceinline__ float exp_fast(float d)
 
 // Sum of exp(x - m) over a thread's elements for a finite m, on pairs: 2^(x L - c) with L = log2(e) in fp32
 // and c = m L rounded. The product is exact inside the multiply-add, so each exponent is (x - m) L plus the
-// rounding error of c, the same for all: it is taken out of the sum. NaN where an element is.
+// rounding error r = m L - c, the same for all: 2^-r takes it out of the sum. NaN where an element is, and where
+// |r| is so large (|m| above 1.5e9) that 2^r, a sum of up to 32 of them or 2^-r could leave the normal numbers:
+// up to 96 they stay within 2^-96 .. 2^101.
 template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[kSelVecs], float m)
 {
     constexpr int E = Vec16<T>::E;
@@ -152,7 +154,8 @@ template <typename T> __device__ __forceinline__ float exp_sum(const uint4 (&v)[
         }
     }
     const float2 both = unpack2(total);
-    return (both.x + both.y) * ex2_approx(-fmaf(m, L, -c));
+    const float r = fmaf(m, L, -c);
+    return fabsf(r) <= 96.f ? (both.x + both.y) * ex2_approx(-r) : NAN;
 }
 
 // The same for any m, element by element from memory: NaN counts nothing, an infinite maximum counts its
