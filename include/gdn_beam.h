@@ -47,7 +47,8 @@ typedef struct gdn_beam_select_args {
     void *workspace;            /* gdn_beam_select_workspace_bytes bytes, 16-byte aligned */
     size_t workspace_bytes;
     int32_t *err_flags;         /* optional device word: GDN_DEVERR_BAD_INDEX for a row outside
-                                   [0, num_rows); that beam then has no candidates */
+                                   [0, num_rows) of a beam whose logits are read (one that lives and has
+                                   not ended); that beam then has no candidates */
 } gdn_beam_select_args;
 
 /* Workspace bytes for these sizes; 0 for sizes that the call refuses. */

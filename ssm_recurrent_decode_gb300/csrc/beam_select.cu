@@ -252,11 +252,11 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas) beam_segment_kernel(con
     const int64_t r = P.a.rows ? (int64_t)P.a.rows[beam] : beam;
     const float cum = P.a.scores[beam];
     const bool ended = P.a.finished && P.a.finished[beam];
+    if (!(cum > -INFINITY) || ended) return;      // its row is not read, whatever it is
     if (r < 0 || r >= P.a.num_rows) {
         if (tid == 0 && seg == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
         return;                                   // the join does not look at this beam
     }
-    if (!(cum > -INFINITY) || ended) return;
 
     const T *row = static_cast<const T *>(P.a.logits) + r * P.a.row_stride;
     const unsigned shift = SHIFTED ? (unsigned)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)) : 0;
