@@ -67,19 +67,19 @@ template <typename Tin, class Sh> struct BackTile {
     {
         return reinterpret_cast<Tin *>(smem + b * Sm::STAGE + 4 * Sm::RX + k * Sm::RB);
     }
-    // rows t0 .. t0 + n - 1 into buffer b; grads: also what only the gradients need
-    __device__ __forceinline__ void stage(int b, int t0, int n, bool grads)
+    // rows t0 .. t0 + n - 1 into buffer b (LAST: as the tile's last rows); grads: also what only the gradients need
+    template <bool LAST> __device__ __forceinline__ void stage(int b, int t0, int n, bool grads)
     {
         const auto rows = [&](const void *base, int64_t stride, int col, int width, int mode) {
             return TileSource<Tin>{static_cast<const Tin *>(base), stride, t0, P.a.T, col, width, mode};
         };
-        stage_rows<Tin, CB, R>(raw(b, 0), rows(P.a.x, P.a.x_stride, c0, P.a.D, P.mode_x), n, tid);
-        stage_rows<Tin, CB, R>(raw(b, 1), rows(P.a.dt, P.a.dt_stride, c0, P.a.D, P.mode_dt), n, tid);
-        stage_rows<Tin, NP, R>(raw_bc(b, 0), rows(P.a.Bm, P.a.B_stride, 0, P.a.N, P.mode_b), n, tid);
+        stage_rows<Tin, CB, R, LAST>(raw(b, 0), rows(P.a.x, P.a.x_stride, c0, P.a.D, P.mode_x), n, tid);
+        stage_rows<Tin, CB, R, LAST>(raw(b, 1), rows(P.a.dt, P.a.dt_stride, c0, P.a.D, P.mode_dt), n, tid);
+        stage_rows<Tin, NP, R, LAST>(raw_bc(b, 0), rows(P.a.Bm, P.a.B_stride, 0, P.a.N, P.mode_b), n, tid);
         if (grads) {
-            if (P.a.z) stage_rows<Tin, CB, R>(raw(b, 2), rows(P.a.z, P.a.z_stride, c0, P.a.D, P.mode_z), n, tid);
-            stage_rows<Tin, CB, R>(raw(b, 3), rows(P.g.dy, P.g.dy_stride, c0, P.a.D, P.mode_dy), n, tid);
-            stage_rows<Tin, NP, R>(raw_bc(b, 1), rows(P.a.Cm, P.a.C_stride, 0, P.a.N, P.mode_c), n, tid);
+            if (P.a.z) stage_rows<Tin, CB, R, LAST>(raw(b, 2), rows(P.a.z, P.a.z_stride, c0, P.a.D, P.mode_z), n, tid);
+            stage_rows<Tin, CB, R, LAST>(raw(b, 3), rows(P.g.dy, P.g.dy_stride, c0, P.a.D, P.mode_dy), n, tid);
+            stage_rows<Tin, NP, R, LAST>(raw_bc(b, 1), rows(P.a.Cm, P.a.C_stride, 0, P.a.N, P.mode_c), n, tid);
         }
     }
     // g of this warp's channels into gs [R][YP]; the warp alone reads it
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
     };
     auto first_at = [&](int pos) { return pos >= head_end && pos < tail_begin ? tail_begin : pos; };   // skips what is neither
     int pos = first_at(row0), b = 0;
-    if (pos < row1) T.stage(0, pos, clip(pos), true);
+    if (pos < row1) T.template stage<false>(0, pos, clip(pos), true);
     cp_async_commit();
 
     f2 A2[4][PP], h[4][PP], prod[4][PP], e[4][PP], dt_head[PP] = {}, dt_tail[PP] = {};
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_back_summary_kernel(cons
         const int next = first_at(pos + clip(pos));
         cp_async_wait<0>();
         __syncthreads();
-        if (next < row1) T.stage(b ^ 1, next, clip(next), true);
+        if (next < row1) T.template stage<false>(b ^ 1, next, clip(next), true);
         cp_async_commit();
         T.gate(b, gs, lane, warp);
         __syncwarp();
@@ -301,9 +301,12 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
 
             // jobs 0 .. nt - 2: tiles 0 .. nt - 2 forward; jobs nt - 1 .. 2 nt - 2: tiles nt - 1 .. 0 backward
             auto tile_of = [&](int j) { return j < nt - 1 ? j : 2 * nt - 2 - j; };
+            // A tile of fewer than R rows has them at its end, behind rows of zeros. Such a row passes h and e on and adds
+            // (e h) 0 to dA: before the first row that is no number only where that row's own share of dA is none.
+            // Behind the last row it would also be where the state there, which dA does not see, is infinite or NaN.
             auto stage_job = [&](int j, int buf) {
                 const int t0 = ra + tile_of(j) * R;
-                T.stage(buf, t0, live ? min(R, rb - t0) : 0, j >= nt - 1);      // of no sequence: zeros
+                T.template stage<true>(buf, t0, live ? min(R, rb - t0) : 0, j >= nt - 1);      // of no sequence: zeros
             };
             const int first_job = live ? 0 : nt - 1;
             __syncthreads();                 // the buffers of the rows before are free
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
             int b = 0;
             for (int j = first_job; j < 2 * nt - 1; ++j, b ^= 1) {
                 const bool back = j >= nt - 1;
-                const int tile = tile_of(j), t0 = ra + tile * R, n = min(R, rb - t0);
+                const int tile = tile_of(j), t0 = ra + tile * R, n = min(R, rb - t0), lead = R - n;
                 cp_async_wait<0>();
                 __syncthreads();
                 if (j + 1 < 2 * nt - 1) stage_job(j + 1, b ^ 1);
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
 #pragma unroll
                 for (int r0 = 0; r0 < Sm::HALF; r0 += NL) {
                     const int r = half + r0 + orow;
-                    if ((NL > Sm::HALF && orow >= Sm::HALF) || r >= n || oc >= T.ncols) continue;
+                    if ((NL > Sm::HALF && orow >= Sm::HALF) || r < lead || oc >= T.ncols) continue;
                     const int sc = (r - half) * Sm::LANES * YP + lane % CLN * CPT;
                     f2 x2[PP], d2[PP], y2[PP], z2[PP], g2[PP], u2[PP], w2[PP], s2[PP], gx[PP], gt[PP], gz[PP];
                     load_pairs(xs + r * CB + oc, x2);
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                             gz[p] = mul2(mul2(y2[p], fma2(skip[p], x2[p], s2[p])), slope);
                         }
                     }
-                    const int64_t row = t0 + r;
+                    const int64_t row = t0 + r - lead;
                     if (!GDN_IN(P.a.err_flags, row, P.a.T)) continue;
                     const int left = T.ncols - oc, col = c0 + oc;
                     if (P.g.dx) store_row(static_cast<Tin *>(P.g.dx) + row * P.g.dx_stride + col, gx, left, (P.vec & kVecDx) && left >= CPT);
@@ -527,7 +530,7 @@ __global__ void __launch_bounds__(kScanThreads, kScanBackCtas) scan_back_kernel(
                     if (nn >= N) continue;
                     float v = 0.f;
 #pragma unroll
-                    for (int q = 0; q < kScanWarps; ++q) v += part[((q * R + r) * 2 + k) * NP + nn];
+                    for (int q = 0; q < kScanWarps; ++q) v += part[((q * R + lead + r) * 2 + k) * NP + nn];
                     const int64_t o = ((int64_t)ct * P.a.T + t0 + r) * 2 * N + k * N + nn;
                     if (GDN_IN(P.a.err_flags, o, (int64_t)P.nct * P.a.T * 2 * N)) P.part_bc[o] = v;
                 }

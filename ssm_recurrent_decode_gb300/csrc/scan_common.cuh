@@ -184,21 +184,23 @@ __device__ __forceinline__ uint4 load_across(const bf16 *p)
 
 // bf16 rows of any alignment, through registers. A vector is read whole where both aligned vectors lie in the
 // tensor: in its row, or between rows that it has.
-template <int W, int R, typename T>
+template <int W, int R, bool LAST, typename T>
 __device__ __forceinline__ void stage_across(T *, const T *, const TileSource<T> &, int, int, int)
 {
 }
-template <int W, int R>
+template <int W, int R, bool LAST>
 __device__ __forceinline__ void stage_across(bf16 *dst, const bf16 *src, const TileSource<bf16> &s, int n, int ncols, int tid)
 {
     constexpr int VPR = W / 8;
+    const int lead = LAST ? R - n : 0;
+    const bf16 *at = src - lead * s.stride;       // where row 0 of the tile would be
 #pragma unroll 2
     for (int i = tid; i < R * VPR; i += kScanThreads) {
         const int r = i / VPR, v = i % VPR, c = s.c0 + v * 8, left = ncols - v * 8;
         uint4 q = make_uint4(0, 0, 0, 0);
-        if (r < n && left > 0) {
-            const bf16 *p = src + r * s.stride + v * 8;
-            const int row = s.t0 + r;
+        if ((LAST ? r >= lead : r < n) && left > 0) {
+            const bf16 *p = at + r * s.stride + v * 8;
+            const int row = s.t0 + r - lead;
             if (left >= 8 && (c >= 7 || row > 0) && (c + 16 <= s.width || row + 1 < s.rows)) {
                 q = load_across(p);
             } else {
@@ -214,29 +216,32 @@ __device__ __forceinline__ void stage_across(bf16 *dst, const bf16 *src, const T
     }
 }
 
-template <typename T, int W, int R> __device__ __noinline__ void stage_unaligned(T *dst, TileSource<T> s, int n, int tid)
+template <typename T, int W, int R, bool LAST> __device__ __noinline__ void stage_unaligned(T *dst, TileSource<T> s, int n, int tid)
 {
     const T *src = s.base + (int64_t)s.t0 * s.stride + s.c0;
     const int ncols = min(W, s.width - s.c0);
     if (sizeof(T) == 4 || s.mode == kRows4) {
         constexpr int E = 4 / (int)sizeof(T), PR = W / E;
+        const int lead = LAST ? R - n : 0;
+        const T *at = src - lead * s.stride;
 #pragma unroll 4
         for (int i = tid; i < R * PR; i += kScanThreads) {
             const int r = i / PR, v = i % PR;
-            int left = r < n ? (ncols - v * E) * (int)sizeof(T) : 0;
+            int left = (LAST ? r >= lead : r < n) ? (ncols - v * E) * (int)sizeof(T) : 0;
             left = left < 0 ? 0 : left > 4 ? 4 : left;
-            cp_async4(dst + r * W + v * E, left ? src + r * s.stride + v * E : src, left);
+            cp_async4(dst + r * W + v * E, left ? at + r * s.stride + v * E : src, left);
         }
     } else {
-        stage_across<W, R>(dst, src, s, n, ncols, tid);
+        stage_across<W, R, LAST>(dst, src, s, n, ncols, tid);
     }
 }
 
-// Rows >= n and columns >= the tensor's width are filled with zeros. Aligned rows are copied asynchronously
+// The n rows from t0 on become the tile's first ones or, with LAST, its last ones; its other rows and columns >= the
+// tensor's width are filled with zeros. Aligned rows are copied asynchronously
 // in 16 bytes, rows on 4-byte boundaries in 4; bf16 rows that begin between those (odd strides) go through
 // registers in 16 bytes (4 x 2000 rows, N = 16, bf16: 777 channels 106 us against 84 for 776; gradients 341
 // against 261).
-template <typename T, int W, int R = kScanTile>
+template <typename T, int W, int R = kScanTile, bool LAST = false>
 __device__ __forceinline__ void stage_rows(T *dst, const TileSource<T> &s, int n, int tid)
 {
     constexpr int VE = 16 / (int)sizeof(T), VPR = W / VE;
@@ -244,18 +249,20 @@ __device__ __forceinline__ void stage_rows(T *dst, const TileSource<T> &s, int n
     const T *src = s.base + (int64_t)s.t0 * s.stride + s.c0;
     const int ncols = min(W, s.width - s.c0);
     if (s.mode == kRows16) {
+        const int lead = LAST ? R - n : 0;
+        const T *at = src - lead * s.stride;
 #pragma unroll
         for (int k = 0; k < (R * VPR + kScanThreads - 1) / kScanThreads; ++k) {
             const int i = k * kScanThreads + tid;
             const int r = i / VPR, v = i % VPR;
             if (R * VPR % kScanThreads == 0 || r < R) {
-                int left = r < n ? (ncols - v * VE) * (int)sizeof(T) : 0;
+                int left = (LAST ? r >= lead : r < n) ? (ncols - v * VE) * (int)sizeof(T) : 0;
                 left = left < 0 ? 0 : left > 16 ? 16 : left;
-                cp_async16(dst + r * W + v * VE, left ? src + r * s.stride + v * VE : src, left);
+                cp_async16(dst + r * W + v * VE, left ? at + r * s.stride + v * VE : src, left);
             }
         }
     } else {
-        stage_unaligned<T, W, R>(dst, s, n, tid);
+        stage_unaligned<T, W, R, LAST>(dst, s, n, tid);
     }
 }
 
