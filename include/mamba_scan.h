@@ -92,7 +92,8 @@ typedef struct mamba_scan_grad_args {
     float *dA;                    /* [D, N] dense */
     float *dDskip;                /* [D]; only with Dskip */
     float *dh0;                   /* [num_states, D, N]; rows that no sequence names are left as they are;
-                                     may not overlap dh_last */
+                                     may not overlap dh_last. Without h0 too: the gradient at a start
+                                     from zero */
 } mamba_scan_grad_args;
 
 /* Bytes of workspace that a call with these sizes needs; uniform: non-zero when cu_seqlens is NULL.
@@ -109,8 +110,8 @@ size_t mamba_scan_workspace_bytes(int32_t T, int32_t S, int32_t D, int32_t N, in
 int mamba_selective_scan(const mamba_scan_args *args, gdn_stream_t stream);
 
 /* mamba_selective_scan_backward -- its gradients; the same status codes, and GDN_ERR_ARG for dz without
- * z, dDskip without Dskip or dh0 without h0. Recomputes the states from the inputs: nothing of the
- * forward call has to be kept. */
+ * z or dDskip without Dskip. Recomputes the states from the inputs: nothing of the forward call has to
+ * be kept. */
 int mamba_selective_scan_backward(const mamba_scan_grad_args *args, gdn_stream_t stream);
 
 #ifdef __cplusplus

@@ -765,7 +765,7 @@ def mamba_selective_scan_backward(x, dt, A, Bm, Cm, dy, *, Dskip=None, z=None, s
                                   stream=None, prepare=False):
     """Gradients of mamba_selective_scan (declared in include/mamba_scan.h). dy: [T, D], dh_last: [num_states, D, N]
     fp32 or None (zero). Each gradient buffer given is written: dx, ddt, dz like x; dBm, dCm like Bm (all in the dtype
-    of x), dA [D, N], dDskip [D] and dh0 [num_states, D, N] fp32."""
+    of x), dA [D, N], dDskip [D] and dh0 [num_states, D, N] fp32 (also without h0: at a start from zero)."""
     torch = _torch()
     m, T, D, N = _scan_args(x, dt, A, Bm, Cm, Dskip=Dskip, z=z, sequences=sequences, cu_seqlens=cu_seqlens,
                             state_indices=state_indices, h0=h0, other_states=(dh_last, dh0), workspace=workspace,
