@@ -59,8 +59,9 @@ typedef struct mamba_scan_args {
     const int32_t *state_indices; /* [S]: row of each sequence in h0, h_last, dh_last and dh0, or NULL: row s */
     int32_t num_states;           /* rows of those buffers */
     const float *h0;              /* [num_states, D, N] or NULL: start from zero */
-    float *h_last;                /* [num_states, D, N] or NULL; may be h0 itself (in place). Rows that no
-                                     sequence names are left as they are */
+    float *h_last;                /* [num_states, D, N] or NULL; may be h0 itself (in place); where it
+                                     overlaps h0 otherwise, no row written may be a row that another sequence
+                                     reads. Rows that no sequence names are left as they are */
     void *y;                      /* [T, D] out_dtype, row stride y_stride */
     int64_t y_stride;
     void *workspace;              /* mamba_scan_workspace_bytes bytes, 16-byte aligned (NULL when that is 0) */
@@ -105,13 +106,14 @@ size_t mamba_scan_workspace_bytes(int32_t T, int32_t S, int32_t D, int32_t N, in
  * where one is needed), GDN_ERR_SHAPE (negative sizes, N outside 1..128, T not a multiple of S without
  * cu_seqlens, a row stride below the row, a workspace that is too small), GDN_ERR_DTYPE, GDN_ERR_ALIGN
  * (a pointer not aligned to its element, or the workspace not to 16 bytes) or GDN_ERR_LAUNCH. Any row
- * stride is accepted; rows that are 16-byte aligned (pointer and stride) are copied faster.
+ * stride is accepted; rows that are 16-byte aligned (pointer and stride) are copied faster. Other outputs
+ * than h_last may not overlap the inputs, one another or the workspace (not checked).
  */
 int mamba_selective_scan(const mamba_scan_args *args, gdn_stream_t stream);
 
 /* mamba_selective_scan_backward -- its gradients; the same status codes, and GDN_ERR_ARG for dz without
- * z or dDskip without Dskip. Recomputes the states from the inputs: nothing of the forward call has to
- * be kept. */
+ * z, dDskip without Dskip or dh0 over dh_last. Recomputes the states from the inputs: nothing of the
+ * forward call has to be kept. */
 int mamba_selective_scan_backward(const mamba_scan_grad_args *args, gdn_stream_t stream);
 
 #ifdef __cplusplus

@@ -12,6 +12,11 @@ constexpr size_t kWsAlign = 256;
 
 size_t round_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
+bool overlap(const void *p, const void *q, size_t bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + bytes && b < a + bytes;
+}
 bool sizes_ok(int T, int S, int D, int N, bool uniform)
 {
     return T >= 0 && S >= 1 && D >= 1 && N >= 1 && N <= kMaxState && (!uniform || T % S == 0);
@@ -197,6 +202,8 @@ int mamba_selective_scan_backward(const mamba_scan_grad_args *args, gdn_stream_t
     if ((q.dz && !q.s.z) || (q.dDskip && !q.s.Dskip)) return GDN_ERR_ARG;
     if (q.s.T > 0 && !q.dy) return GDN_ERR_NULL;
     const int64_t D = q.s.D, N = q.s.N;
+    // a sequence's first chunk may be done before its last one has read dh_last
+    if (gdn::overlap(q.dh0, q.dh_last, (size_t)q.s.num_states * D * N * sizeof(float))) return GDN_ERR_ARG;
     if (q.dy_stride < D || (q.dx && q.dx_stride < D) || (q.ddt && q.ddt_stride < D) || (q.dz && q.dz_stride < D) ||
         (q.dBm && q.dB_stride < N) || (q.dCm && q.dC_stride < N))
         return GDN_ERR_SHAPE;
