@@ -62,8 +62,9 @@ size_t gdn_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t voc
  * (+inf logits share their row's whole probability.) One pass over the logits in two launches; the
  * sums run in fp32 over short ranges and in fp64 over those, and scores are compared in fp64 and
  * rounded once. The result does not depend on timing.
- * The outputs may not overlap one another, the workspace, rows, scores or finished, except that with
- * K = beams an output may be one of those three itself (in place; the type's size being the same).
+ * The outputs may not overlap one another or the workspace, nor, with more than one batch entry, rows,
+ * scores or finished, except that with K = beams an output may be one of those three itself (in place;
+ * the type's size being the same).
  * Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN, GDN_ERR_ARG (eos_token
  * outside the vocabulary where it is used, or an output over the workspace or an input as above) or
  * GDN_ERR_LAUNCH.

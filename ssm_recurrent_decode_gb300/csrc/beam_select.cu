@@ -625,7 +625,8 @@ bool overlap(const void *p, size_t pn, const void *q, size_t qn)
 }
 
 // Whether an output lies over memory that the join still reads: its CTAs run in no order, and each reads its entry's
-// part of the tables before it writes its own results. So only a table of the very same layout may be an output.
+// part of the tables before it writes its own results. So with several entries only a table of the very same layout
+// may be an output.
 bool outputs_overlap(const gdn_beam_select_args &a, size_t workspace)
 {
     const size_t in = (size_t)a.batch * a.beams, out = (size_t)a.batch * a.K;
@@ -634,7 +635,7 @@ bool outputs_overlap(const gdn_beam_select_args &a, size_t workspace)
     for (const auto &o : outputs) {
         if (overlap(o.p, out * o.es, a.workspace, workspace)) return true;
         for (const auto &t : tables)
-            if (overlap(o.p, out * o.es, t.p, in * t.es) && !(o.p == t.p && o.es == t.es && a.K == a.beams)) return true;
+            if (a.batch > 1 && overlap(o.p, out * o.es, t.p, in * t.es) && !(o.p == t.p && o.es == t.es && a.K == a.beams)) return true;
     }
     return false;
 }

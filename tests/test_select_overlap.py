@@ -78,3 +78,23 @@ def test_in_place(batch, beams):
     torch.cuda.synchronize()
     for a, b in zip(apart, place):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("beams,K", [(1, 4), (4, 2), (3, 9)])
+def test_one_entry_in_place(beams, K):
+    """A single entry's results may lie over its tables whatever the sizes: all is read before any is written."""
+    V = 4000
+    x = beam._logits(beams, V, "bf16", 42)
+    scores = torch.from_numpy(beam._scores(1, beams, 42)).cuda()
+    ws = gdn.beam_select_workspace(1, beams, V, K)
+    new = lambda t: torch.full((1, K), 7, dtype=t, device="cuda")
+    apart = [new(torch.float32), new(torch.int32), new(torch.int32)]
+    gdn.gdn_beam_select(x, scores, *apart, workspace=ws)
+    both = torch.zeros(max(beams, K), device="cuda")
+    both[:beams] = scores[0]
+    place = [both[:K].view(1, K), new(torch.int32), new(torch.int32)]
+    gdn.gdn_beam_select(x, both[:beams].view(1, beams), *place, workspace=ws)
+    torch.cuda.synchronize()
+    for a, b in zip(apart, place):
+        assert torch.equal(a, b)
