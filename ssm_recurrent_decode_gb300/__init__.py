@@ -800,7 +800,8 @@ def beam_select_workspace(batch, beams, vocab, K, device=None):
 def _table(t, name, shape, dtype):
     if t is None:
         return None
-    if tuple(t.shape) != shape and t.numel() != shape[0] * shape[1]:
+    # (a flat table is taken; two axes of other sizes are another table, a transposed one say)
+    if tuple(t.shape) != shape and (t.dim() == 2 or t.numel() != shape[0] * shape[1]):
         raise ValueError(f"{name} must be {list(shape)}")
     return _ptr(_dense(t, name), name, dtype)
 
