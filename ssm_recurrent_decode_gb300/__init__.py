@@ -800,8 +800,9 @@ def beam_select_workspace(batch, beams, vocab, K, device=None):
 def _table(t, name, shape, dtype):
     if t is None:
         return None
-    # (a flat table is taken; two axes of other sizes are another table, a transposed one say)
-    if tuple(t.shape) != shape and (t.dim() == 2 or t.numel() != shape[0] * shape[1]):
+    # (a flat table, or a row or column, is taken; two axes of other sizes are another table, a transposed one say)
+    n = shape[0] * shape[1]
+    if tuple(t.shape) != shape and (t.numel() != n or (t.dim() == 2 and max(t.shape) != n)):
         raise ValueError(f"{name} must be {list(shape)}")
     return _ptr(_dense(t, name), name, dtype)
 

@@ -1,4 +1,4 @@
-"""The binding takes the beam search's tables as [batch, beams] or [batch, K], or flat, and refuses two axes of other
+"""The binding takes the beam search's tables as [batch, beams] or [batch, K], or flat (or a row or column), and refuses two axes of other
 sizes: a transposed table has as many entries, but other ones in each place."""
 import pytest
 import torch
@@ -38,3 +38,4 @@ def test_flat_tables_are_taken(monkeypatch):
     gdn.gdn_beam_select(torch.zeros(B * N, V), torch.zeros(B, N), torch.zeros(B, K), _i(B * K), _i(B * K), rows=_i(B * N),
                         finished=torch.zeros(B * N, dtype=torch.bool), eos_token=0, prepare=True)
     gdn.gdn_beam_reorder([], _i(B, N), _i(B * N), _i(B * N), prepare=True)
+    gdn.gdn_beam_reorder([], _i(B, N), _i(B * N, 1), _i(1, B * N), prepare=True)
