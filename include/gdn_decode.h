@@ -264,10 +264,11 @@ const char *gdn_strerror(int status);
 /* ABI checks for bindings: sizeof of the args structs (which: 0 step, 1 ring, 2 fused, 3 the
  * decode projection's gdn_gemv_args of gdn_gemv.h, 4 gdn_front_args of gdn_front.h, 5
  * mamba_decode_args of mamba_decode.h, 6 mamba_scan_args and 7 mamba_scan_grad_args of mamba_scan.h, 8
- * gdn_beam_select_args and 10 gdn_beam_reorder_args of gdn_beam.h; 0 for any other). */
+ * gdn_beam_select_args, 10 gdn_beam_reorder_args and 11 gdn_beam_pool of gdn_beam.h; 0 for any other, 9
+ * among them). */
 size_t gdn_abi_struct_size(int which);
 
-/* Library ABI version (incremented on any change of the args structs; currently 7). */
+/* Library ABI version (incremented on any change of the args structs; currently 8). */
 int gdn_abi_version(void);
 
 #ifdef __cplusplus

@@ -207,9 +207,9 @@ def _load(path: str):
     L.gdn_strerror.restype = ctypes.c_char_p
     L.gdn_abi_struct_size.argtypes = [ctypes.c_int]
     L.gdn_abi_struct_size.restype = ctypes.c_size_t
-    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10)]
+    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10, 11)]
     want = [ctypes.sizeof(c) for c in (GdnStepArgs, GdnRingArgs, GdnFusedArgs, GemvArgs, GdnFrontArgs, MambaArgs,
-                                       MambaScanArgs, MambaScanGradArgs, BeamSelectArgs, BeamReorderArgs)]
+                                       MambaScanArgs, MambaScanGradArgs, BeamSelectArgs, BeamReorderArgs, BeamPool)]
     if sizes != want or L.gdn_abi_version() != ABI_VERSION:
         raise RuntimeError(f"libgdn_decode.so ABI mismatch: struct sizes {sizes} vs {want}")
     return L

@@ -283,6 +283,7 @@ size_t gdn_abi_struct_size(int which)
     case 7: return sizeof(mamba_scan_grad_args);
     case 8: return sizeof(gdn_beam_select_args);
     case 10: return sizeof(gdn_beam_reorder_args);
+    case 11: return sizeof(gdn_beam_pool);
     default: return 0;
     }
 }
