@@ -80,8 +80,8 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
         const int64_t C = (T * P.nct + kScanBackCtas * kSms - 1) / (kScanBackCtas * kSms);
         P.C = (int)(C >= kScanBackChunk ? kScanBackChunk : C <= 16 ? 16 : (C + 7) / 8 * 8);
     } else {
-        const int64_t kSlots = (int64_t)scan_ctas(scan_lanes(P.a.N)) * kSms;     // resident CTAs
-        // Chunks of equal length that fill the GPU once, and no shorter than the 32 rows below which a
+        const int64_t kSlots = (int64_t)scan_ctas(scan_lanes(P.a.N)) * kSms;     // resident CTAs, by registers
+        // Chunks of equal length that fill those slots once, and no shorter than the 32 rows below which a
         // chunk's own costs (its rates, states and launch) outweigh its rows.
         int64_t C = (T * P.nct + kSlots - 1) / kSlots;
         C = (C + 15) / 16 * 16;
@@ -91,11 +91,17 @@ void plan(ScanLaunch &P, bool uniform, bool backward)
             P.nct = tiles(2);
         }
         if (T > 32 && T <= 8 * 32 && !(uniform && P.L <= 32)) {
-            // a few chunks: a cluster of at most eight CTAs per channel tile, in one launch
+            // a few chunks: a cluster of at most eight CTAs per channel tile, in one launch. Against three launches
+            // (D = 1536, N = 16, bf16): 64 rows 9.7 and 14.2 us, 128 rows 12.8 and 14.8, 256 rows 15.9 and 17.5. A
+            // cluster's CTA has up to 196 registers a thread, so many channel tiles take several rounds and lose:
+            // 128 rows, D = 4096, N = 16: 28.7 and 19.3; 256 rows, D = 1536, N = 128: 57 and 39, in fp32 65 and 39.
             P.C = T <= 8 * 16 ? 16 : 32;
             P.cluster = 1;
         } else if (uniform && P.L > 0 && P.L <= 4 * P.C) {
-            P.C = P.L;                           // about as long as the chunks would be: one pass over whole sequences
+            // About as long as the chunks would be: one pass over whole sequences. Against the same rows in chunks
+            // (by cu_seqlens; bf16): 60 x 128, D = 64, N = 16: 17.0 and 37.3 us; 8 x 128, D = 1536: 22.8 and 31.2;
+            // 16 x 512: 108 and 116; 64 x 256: 136 and 184; N = 128, 4 x 256: 68 and 108, 4 x 1024: 256 and 398.
+            P.C = P.L;
         }
     }
     P.G = T > 0 ? (int)((T + P.C - 1) / P.C) : 1;   // without rows: one chunk of empty sequences

@@ -46,7 +46,10 @@ inline int scan_channels(int N, int cpt) { return 4 * (32 / scan_lanes(N)) * cpt
 constexpr int kScanBackChunk = 64;   // most token rows per chunk of the backward pass
 constexpr int kScanBackCtas = 2;     // its resident CTAs per SM
 
-// Resident CTAs per SM of the forward kernel. Wide states (N above 32) ran faster with more registers a
+// Resident CTAs per SM of the forward kernel by its registers, which chunks are counted out for. Shared memory
+// allows as many for states above 16 and for 9 to 16 entries in bf16 at four channels a thread; fewer for 9 to 16 in fp32
+// (73 KB a CTA: 3) and up to 8 (67 KB in bf16: 3; 116 KB in fp32: 1), whose chunks then take a second round or more:
+// 32768 rows, D = 1536: N = 4, 8 and 16 in bf16 272, 258 and 379 us, in fp32 379, 380 and 401. Wide states (N above 32) ran faster with more registers a
 // thread than with a fourth CTA (N = 128, 4 x 1024 rows, fp32: 245 against 323 us), narrow ones a little slower
 // (N = 16, 32768 rows: 382 against 379; 24 ragged prompts of 8000: 131 against 123 to 129), and six CTAs of 80
 // registers were slower for both.
