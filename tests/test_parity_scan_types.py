@@ -50,3 +50,32 @@ def test_guard_bands_forward(lengths, D, N, dtype):
 @pytest.mark.parametrize("lengths,D,N,dtype", CASES)
 def test_guard_bands_backward(lengths, D, N, dtype):
     canaries.test_scan_backward(lengths, D, N, dtype)
+
+
+def test_gradients_on_another_stream_and_in_a_graph():
+    lengths, D, N = [70, 0, 90], 64, 24
+    c = scan.sc.make(lengths, D, N, "bf16", 14)
+    d = scan._dev(c, "bf16")
+    h0, dhl = torch.from_numpy(c["h0"]).cuda(), torch.from_numpy(c["dh_last"]).cuda()
+    ws, cu = scan._workspace(lengths, D, N, False, True), scan._cu(lengths)
+    bf = lambda w: torch.zeros(160, w, dtype=torch.bfloat16, device="cuda")
+    new = lambda: {"dx": bf(D), "ddt": bf(D), "dz": bf(D), "dBm": bf(N), "dCm": bf(N), "dA": torch.zeros(D, N, device="cuda"),
+                   "dDskip": torch.zeros(D, device="cuda"), "dh0": torch.zeros_like(h0)}
+
+    def call(g, stream=None):
+        scan.gdn.mamba_selective_scan_backward(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["dy"], Dskip=d["Dskip"], z=d["z"],
+                                               cu_seqlens=cu, h0=h0, dh_last=dhl, workspace=ws, stream=stream, **g)
+    plain, other, captured = new(), new(), new()
+    call(plain)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    call(other, stream=s)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(captured)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k in plain:
+        assert torch.equal(other[k], plain[k]) and torch.equal(captured[k], plain[k]), k
