@@ -16,6 +16,10 @@ Entry points (same names as the C ABI):
   mamba_selective_scan_backward  its gradients
   gdn_beam_select          the best K of beams x vocabulary by cumulative log-probability
   gdn_beam_reorder         the chosen beams' states, moved within their slot pools
+  gdn_linear_attention     linear attention with a decay for each head over whole sequences (prompts)
+  gdn_linear_attention_backward  its gradients
+  gdn_linear_attention_step  its single-token step over a pool of states
+  gdn_rotary               rotary positions of q and k
 plus ``fused_recurrent_gated_delta_rule_packed_decode``, the packed call with the keyword names
 of "Microbenchmark: buffered output-only GDN decode (ReplaySSM Part A)" (_bench_cfg, run_packed).
 """
@@ -36,6 +40,9 @@ __all__ = [
     "mamba_scan_workspace",
     "BeamSelectArgs", "BeamPool", "BeamReorderArgs", "gdn_beam_select", "beam_select_workspace",
     "gdn_beam_reorder",
+    "LinearArgs", "LinearGradArgs", "LinearStepArgs", "RotaryArgs", "gdn_linear_attention",
+    "gdn_linear_attention_backward", "gdn_linear_attention_step", "linear_attention_workspace", "gdn_rotary",
+    "rotary_frequencies",
     "GemvArgs", "gdn_gemv_bf16", "gemv_workspace",
     "GDN_F32", "GDN_BF16", "GDN_DEVERR_BAD_INDEX", "GDN_DEVERR_BAD_WRITE_POS", "GDN_DEVERR_TIMEOUT",
     "GDN_DEVERR_RANGE", "debug_lib", "using_debug_build",
@@ -49,7 +56,7 @@ GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1
 GDN_DEVERR_BAD_INDEX, GDN_DEVERR_BAD_WRITE_POS, GDN_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 GDN_DEVERR_RANGE = 0x8
 GDN_KERNEL = {"auto": 0, "tile": 1, "pipe": 2, "stage": 3}
-ABI_VERSION = 8
+ABI_VERSION = 9
 
 # every function the header declares
 EXPORTS = ("gdn_decode_step", "gdn_decode_step_indexed", "gdn_decode_buffered", "gdn_decode_fused",
@@ -58,7 +65,9 @@ EXPORTS = ("gdn_decode_step", "gdn_decode_step_indexed", "gdn_decode_buffered", 
            "gdn_gemv_workspace_bytes", "gdn_gemv_bf16_noalloc", "gdn_decode_front",
            "gdn_front_proj_width", "gdn_gemv_set_wait_limit", "gdn_decode_step_indexed_chained",
            "mamba_selective_scan", "mamba_selective_scan_backward", "mamba_scan_workspace_bytes",
-           "gdn_beam_select", "gdn_beam_select_workspace_bytes", "gdn_beam_reorder")
+           "gdn_beam_select", "gdn_beam_select_workspace_bytes", "gdn_beam_reorder",
+           "gdn_linear_attention", "gdn_linear_attention_backward", "gdn_linear_attention_step",
+           "gdn_linear_workspace_bytes", "gdn_rotary")
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -143,6 +152,46 @@ class BeamReorderArgs(ctypes.Structure):
                 ("err_flags", _vp)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("S", _i32), ("H", _i32), ("HV", _i32), ("K", _i32), ("V", _i32),
+                ("in_dtype", _i32), ("out_dtype", _i32),
+                ("q", _vp), ("q_stride", _i64), ("q_head_stride", _i64),
+                ("k", _vp), ("k_stride", _i64), ("k_head_stride", _i64),
+                ("v", _vp), ("v_stride", _i64), ("v_head_stride", _i64),
+                ("g", _vp), ("g_stride", _i64), ("scale", _f32), ("cu_seqlens", _vp), ("state_indices", _vp),
+                ("num_states", _i32), ("initial_state", _vp), ("final_state", _vp),
+                ("o", _vp), ("o_stride", _i64), ("o_head_stride", _i64),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("err_flags", _vp)]
+
+
+class LinearGradArgs(ctypes.Structure):
+    _fields_ = [("s", LinearArgs), ("d_o", _vp), ("do_stride", _i64), ("do_head_stride", _i64), ("d_final_state", _vp),
+                ("dq", _vp), ("dq_stride", _i64), ("dq_head_stride", _i64),
+                ("dk", _vp), ("dk_stride", _i64), ("dk_head_stride", _i64),
+                ("dv", _vp), ("dv_stride", _i64), ("dv_head_stride", _i64),
+                ("dg", _vp), ("dg_stride", _i64), ("d_initial_state", _vp)]
+
+
+class LinearStepArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("H", _i32), ("HV", _i32), ("K", _i32), ("V", _i32), ("num_slots", _i32),
+                ("in_dtype", _i32), ("out_dtype", _i32), ("state_dtype", _i32),
+                ("q", _vp), ("q_stride", _i64), ("q_head_stride", _i64),
+                ("k", _vp), ("k_stride", _i64), ("k_head_stride", _i64),
+                ("v", _vp), ("v_stride", _i64), ("v_head_stride", _i64),
+                ("g", _vp), ("g_stride", _i64), ("scale", _f32), ("rotary_dim", _i32), ("interleaved", _i32),
+                ("positions", _vp), ("frequencies", _vp), ("magnitude", _f32), ("state", _vp), ("out", _vp),
+                ("err_flags", _vp)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("HK", _i32), ("D", _i32), ("rotary_dim", _i32), ("interleaved", _i32),
+                ("inverse", _i32), ("dtype", _i32), ("magnitude", _f32), ("positions", _vp), ("frequencies", _vp),
+                ("q", _vp), ("q_stride", _i64), ("q_head_stride", _i64),
+                ("q_out", _vp), ("q_out_stride", _i64), ("q_out_head_stride", _i64),
+                ("k", _vp), ("k_stride", _i64), ("k_head_stride", _i64),
+                ("k_out", _vp), ("k_out_stride", _i64), ("k_out_head_stride", _i64)]
+
+
 class GdnError(RuntimeError):
     """A non-zero status from the library (the message is gdn_strerror's)."""
 
@@ -184,6 +233,16 @@ def _load(path: str):
     L.gdn_beam_select_workspace_bytes.restype = ctypes.c_size_t
     L.gdn_beam_reorder.argtypes = [ctypes.POINTER(BeamReorderArgs), _vp]
     L.gdn_beam_reorder.restype = ctypes.c_int
+    L.gdn_linear_attention.argtypes = [ctypes.POINTER(LinearArgs), _vp]
+    L.gdn_linear_attention.restype = ctypes.c_int
+    L.gdn_linear_attention_backward.argtypes = [ctypes.POINTER(LinearGradArgs), _vp]
+    L.gdn_linear_attention_backward.restype = ctypes.c_int
+    L.gdn_linear_attention_step.argtypes = [ctypes.POINTER(LinearStepArgs), _vp, _i32, _vp]
+    L.gdn_linear_attention_step.restype = ctypes.c_int
+    L.gdn_linear_workspace_bytes.argtypes = [_i32] * 9
+    L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_rotary.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
+    L.gdn_rotary.restype = ctypes.c_int
     L.gdn_selftest_bounded_wait.argtypes = [_vp, _i64, _i32, _vp]
     L.gdn_decode_front.argtypes = [ctypes.POINTER(GdnFrontArgs), _vp]
     L.gdn_decode_front.restype = ctypes.c_int
@@ -207,9 +266,10 @@ def _load(path: str):
     L.gdn_strerror.restype = ctypes.c_char_p
     L.gdn_abi_struct_size.argtypes = [ctypes.c_int]
     L.gdn_abi_struct_size.restype = ctypes.c_size_t
-    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10, 11)]
+    sizes = [L.gdn_abi_struct_size(i) for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10, 11, 12, 13, 14, 15)]
     want = [ctypes.sizeof(c) for c in (GdnStepArgs, GdnRingArgs, GdnFusedArgs, GemvArgs, GdnFrontArgs, MambaArgs,
-                                       MambaScanArgs, MambaScanGradArgs, BeamSelectArgs, BeamReorderArgs, BeamPool)]
+                                       MambaScanArgs, MambaScanGradArgs, BeamSelectArgs, BeamReorderArgs, BeamPool,
+                                       LinearArgs, LinearGradArgs, LinearStepArgs, RotaryArgs)]
     if sizes != want or L.gdn_abi_version() != ABI_VERSION:
         raise RuntimeError(f"libgdn_decode.so ABI mismatch: struct sizes {sizes} vs {want}")
     return L
@@ -871,6 +931,254 @@ def gdn_beam_reorder(pools, slots, parents, new_slots, *, err_flags=None, stream
     a.err_flags = _ptr(err_flags, "err_flags", torch.int32)
     keep = (a, table, pools, slots, parents, new_slots, err_flags)
     return _run_or_prepare("gdn_beam_reorder", (ctypes.byref(a),), keep, stream, prepare, new_slots)
+
+
+def _head_rows(t, name: str, rows=None, heads=None, dim=None, dtype=None):
+    """A [rows, heads, dim] tensor (or [S, L, heads, dim], whose sequences follow one another at the row stride) of any
+    row and head strides: pointer, row stride, head stride, and its sizes."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name}: expected [rows, heads, dim] or [S, L, heads, dim]")
+    n, h, d = t.numel() // max(1, t.shape[-1] * t.shape[-2]), t.shape[-2], t.shape[-1]
+    if 0 in t.shape[:-2]:
+        n = 0
+    for have, want, what in ((n, rows, "rows"), (h, heads, "heads"), (d, dim, "channels")):
+        if want is not None and have != want:
+            raise ValueError(f"{name}: expected {want} {what}, got {have}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if d > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: heads need unit inner stride")
+    head = t.stride(-2) if h > 1 else d
+    if t.dim() == 4 and n > 0:
+        S, L = t.shape[0], t.shape[1]
+        row = t.stride(1) if L > 1 else t.stride(0)
+        if S > 1 and L > 1 and t.stride(0) != L * row:
+            raise ValueError(f"{name}: sequences must follow one another at the row stride")
+    else:
+        row = t.stride(0) if t.dim() == 3 else h * d
+    if n <= 1:
+        row = h * d
+    return _ptr(t, name), row, head, (n, h, d)
+
+
+def _put_rows(a, field, t, name, stride=None, **kw):
+    """Sets a struct's pointer, row stride and head stride of a tensor of head rows; returns its sizes."""
+    stride = stride or field
+    p, row, head, sizes = _head_rows(t, name, **kw)
+    setattr(a, field, p)
+    setattr(a, stride + "_stride", row)
+    setattr(a, stride + "_head_stride", head)
+    return sizes
+
+
+def _log_decays(g, rows, heads):
+    """g [HV], or [rows, HV] (or [S, L, HV]) fp32: pointer and row stride (0: one decay a head)."""
+    torch = _torch()
+    if g.dim() == 1:
+        if g.shape[0] != heads or g.stride(0) != 1 and heads > 1:
+            raise ValueError(f"g: expected {heads} dense entries")
+        return _ptr(g, "g", torch.float32), 0
+    p, stride = _token_rows(g, "g", rows, heads, torch.float32)
+    if rows > 1 and stride == 0:
+        raise ValueError("g: rows of one decay a head are given as a tensor [HV]")
+    return p, stride if rows > 1 else max(stride, heads)
+
+
+def linear_attention_workspace(T, H, HV, K, V, *, sequences=1, uniform=True, backward=False, dtype=None, device=None):
+    """A workspace tensor for gdn_linear_attention (or its backward pass) over T token rows of `sequences` sequences,
+    of equal lengths (uniform) or given by cu_seqlens, with inputs of `dtype` (default bfloat16); None when the call
+    needs none. Calls that may run at the same time need one each."""
+    torch = _torch()
+    code = GDN_F32 if dtype == torch.float32 else GDN_BF16
+    nbytes = lib().gdn_linear_workspace_bytes(int(T), int(sequences), int(H), int(HV), int(K), int(V), code, int(uniform),
+                                              int(backward))
+    if nbytes == 0:
+        return None
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def _linear_args(q, k, v, g, *, scale, sequences, cu_seqlens, state_indices, states, workspace, err_flags):
+    torch = _torch()
+    a = LinearArgs()
+    a.in_dtype = _dtype_code(q)
+    a.T, a.H, a.K = _put_rows(a, "q", q, "q")
+    _put_rows(a, "k", k, "k", rows=a.T, heads=a.H, dim=a.K, dtype=q.dtype)
+    _, a.HV, a.V = _put_rows(a, "v", v, "v", rows=a.T, dtype=q.dtype)
+    a.g, a.g_stride = _log_decays(g, a.T, a.HV)
+    a.scale = 0.0 if scale is None else float(scale)
+    if cu_seqlens is not None:
+        if sequences is not None:
+            raise ValueError("give cu_seqlens or sequences, not both")
+        a.S = cu_seqlens.numel() - 1
+        a.cu_seqlens = _ptr(_dense(cu_seqlens, "cu_seqlens"), "cu_seqlens", torch.int32)
+    else:
+        a.S = sequences if sequences is not None else (q.shape[0] if q.dim() == 4 else 1)
+    if state_indices is not None:
+        if state_indices.numel() != a.S:
+            raise ValueError(f"state_indices must have {a.S} entries")
+        a.state_indices = _ptr(_dense(state_indices, "state_indices"), "state_indices", torch.int32)
+    states = [t for t in states if t is not None]
+    for t in states:
+        if t.dim() != 4 or t.shape != states[0].shape or tuple(t.shape[1:]) != (a.HV, a.V, a.K):
+            raise ValueError(f"state buffers must be [num_states, {a.HV}, {a.V}, {a.K}], all with the same num_states")
+        _ptr(_dense(t, "a state buffer"), "a state buffer", torch.float32)
+    a.num_states = states[0].shape[0] if states else 0
+    if workspace is not None:
+        a.workspace = _ptr(_dense(workspace, "workspace"), "workspace")
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    a.err_flags = _ptr(err_flags, "err_flags", torch.int32)
+    return a
+
+
+def gdn_linear_attention(q, k, v, g, o, *, scale=None, sequences=None, cu_seqlens=None, state_indices=None,
+                         initial_state=None, final_state=None, workspace=None, err_flags=None, stream=None, prepare=False):
+    """Linear attention with a decay for each head over whole sequences (declared in include/gdn_linear.h):
+    S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t. q, k: [T, H, K] and v, o: [T, HV, V] (or [S, L, ..]) of any
+    row and head strides, fp32 or bf16 (o of its own dtype); g: log decays fp32, [T, HV] or one per head [HV]. The T
+    rows are `sequences` equal sequences (default: q's first axis of four, else one), or those of cu_seqlens (int32
+    [S + 1] on the device; rows outside them are left as they are). initial_state and final_state: [num_states, HV, V, K]
+    fp32 at row state_indices[s] (int32; default s) of sequence s; final_state may be initial_state. workspace: see
+    linear_attention_workspace."""
+    a = _linear_args(q, k, v, g, scale=scale, sequences=sequences, cu_seqlens=cu_seqlens, state_indices=state_indices,
+                     states=(initial_state, final_state), workspace=workspace, err_flags=err_flags)
+    a.out_dtype = _dtype_code(o)
+    _put_rows(a, "o", o, "o", rows=a.T, heads=a.HV, dim=a.V)
+    a.initial_state = None if initial_state is None else initial_state.data_ptr()
+    a.final_state = None if final_state is None else final_state.data_ptr()
+    keep = (a, q, k, v, g, o, cu_seqlens, state_indices, initial_state, final_state, workspace, err_flags)
+    return _run_or_prepare("gdn_linear_attention", (ctypes.byref(a),), keep, stream, prepare, o)
+
+
+def gdn_linear_attention_backward(q, k, v, g, do, *, scale=None, sequences=None, cu_seqlens=None, state_indices=None,
+                                  initial_state=None, d_final_state=None, dq=None, dk=None, dv=None, dg=None,
+                                  d_initial_state=None, workspace=None, err_flags=None, stream=None, prepare=False):
+    """Gradients of gdn_linear_attention (declared in include/gdn_linear.h). do: like v; d_final_state: [num_states, HV,
+    V, K] fp32 or None (zero). Each gradient buffer given is written: dq, dk like q, dv like v (in q's dtype, any row
+    and head strides), dg fp32 like g, d_initial_state [num_states, HV, V, K] fp32 (also without initial_state: at a
+    start from zero; not over initial_state or d_final_state)."""
+    torch = _torch()
+    s = _linear_args(q, k, v, g, scale=scale, sequences=sequences, cu_seqlens=cu_seqlens, state_indices=state_indices,
+                     states=(initial_state, d_final_state, d_initial_state), workspace=workspace, err_flags=err_flags)
+    s.initial_state = None if initial_state is None else initial_state.data_ptr()
+    a = LinearGradArgs()
+    a.s = s
+    _put_rows(a, "d_o", do, "do", "do", rows=s.T, heads=s.HV, dim=s.V, dtype=q.dtype)
+    for t, name, heads, dim in ((dq, "dq", s.H, s.K), (dk, "dk", s.H, s.K), (dv, "dv", s.HV, s.V)):
+        if t is not None:
+            _put_rows(a, name, t, name, rows=s.T, heads=heads, dim=dim, dtype=q.dtype)
+    if dg is not None:
+        if (dg.dim() == 1) != (g.dim() == 1):
+            raise ValueError("dg must have the shape of g")
+        a.dg, a.dg_stride = _log_decays(dg, s.T, s.HV)
+    a.d_final_state = None if d_final_state is None else d_final_state.data_ptr()
+    a.d_initial_state = None if d_initial_state is None else d_initial_state.data_ptr()
+    keep = (a, q, k, v, g, do, cu_seqlens, state_indices, initial_state, d_final_state, dq, dk, dv, dg, d_initial_state,
+            workspace, err_flags)
+    return _run_or_prepare("gdn_linear_attention_backward", (ctypes.byref(a),), keep, stream, prepare, None)
+
+
+def _rotary_table(frequencies):
+    if frequencies.dim() != 1 or frequencies.numel() < 1:
+        raise ValueError("frequencies must be [rotary_dim / 2]")
+    return _ptr(_dense(frequencies, "frequencies"), "frequencies", _torch().float64), 2 * frequencies.numel()
+
+
+def gdn_linear_attention_step(q, k, v, g, state, out, cache_indices=None, *, pad_slot_id=-1, scale=None, positions=None,
+                              frequencies=None, interleaved=False, magnitude=1.0, err_flags=None, stream=None,
+                              prepare=False):
+    """One token of linear attention for each request row (declared in include/gdn_linear.h). q, k: [B, H, K] and v: [B,
+    HV, V] of any row and head strides; g: log decays fp32, [B, HV] or [HV]; state: [num_slots, HV, V, K] fp32 or bf16,
+    updated in place; out: [B, HV, V] dense. Row b is on slot cache_indices[b] (int32; default b); rows whose index is
+    pad_slot_id are skipped (out zeroed). With frequencies (see gdn_rotary) q and k are turned to positions [B] first."""
+    torch = _torch()
+    a = LinearStepArgs()
+    a.in_dtype, a.out_dtype, a.state_dtype = _dtype_code(q), _dtype_code(out), _dtype_code(state)
+    a.B, a.H, a.K = _put_rows(a, "q", q, "q")
+    _put_rows(a, "k", k, "k", rows=a.B, heads=a.H, dim=a.K, dtype=q.dtype)
+    _, a.HV, a.V = _put_rows(a, "v", v, "v", rows=a.B, dtype=q.dtype)
+    a.g, a.g_stride = _log_decays(g, a.B, a.HV)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (a.HV, a.V, a.K):
+        raise ValueError(f"state must be [num_slots, {a.HV}, {a.V}, {a.K}]")
+    a.num_slots, a.state = state.shape[0], _ptr(_dense(state, "state"), "state")
+    if out.numel() != a.B * a.HV * a.V:
+        raise ValueError(f"out must hold {a.B * a.HV * a.V} elements")
+    a.out = _ptr(_dense(out, "out"), "out")
+    a.scale = 0.0 if scale is None else float(scale)
+    if (positions is None) != (frequencies is None):
+        raise ValueError("positions and frequencies go together")
+    if frequencies is not None:
+        a.frequencies, a.rotary_dim = _rotary_table(frequencies)
+        if positions.numel() != a.B:
+            raise ValueError(f"positions must have {a.B} entries")
+        a.positions = _ptr(_dense(positions, "positions"), "positions", torch.int32)
+        a.interleaved, a.magnitude = int(bool(interleaved)), float(magnitude)
+    a.err_flags = _ptr(err_flags, "err_flags", torch.int32)
+    idx = None
+    if cache_indices is not None:
+        if cache_indices.numel() != a.B:
+            raise ValueError(f"cache_indices must have {a.B} entries")
+        idx = _ptr(_dense(cache_indices, "cache_indices"), "cache_indices", torch.int32)
+    keep = (a, q, k, v, g, state, out, cache_indices, positions, frequencies, err_flags)
+    return _run_or_prepare("gdn_linear_attention_step", (ctypes.byref(a), ctypes.c_void_p(idx), ctypes.c_int32(int(pad_slot_id))),
+                           keep, stream, prepare, out)
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_length=None, keep_turns=32.0,
+                       scale_turns=1.0, device=None):
+    """fp64 frequencies [rotary_dim / 2] (radians a position) base^(-2i / rotary_dim) for gdn_rotary, scaled for contexts
+    `factor` times as long as the trained one: None (as they are); "linear" (all divided by factor); "base" (a larger base, so
+    that the slowest is divided by factor and the fastest kept); "parts" (what turns more than keep_turns times in
+    original_length positions is kept, what turns less than scale_turns divided by factor, linearly between)."""
+    torch = _torch()
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    if not factor > 0:
+        raise ValueError("factor must be positive")
+    if scaling == "base" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original_length is None:
+            raise ValueError("scaling in parts needs original_length")
+        turns = original_length * f / (2 * torch.pi)
+        keep = ((turns - scale_turns) / (keep_turns - scale_turns)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device or "cuda")
+
+
+def gdn_rotary(q, k, positions, frequencies, *, q_out=None, k_out=None, interleaved=False, inverse=False, magnitude=1.0,
+               stream=None, prepare=False):
+    """Rotary positions of q [T, H, D] and k [T, HK, D] (or None), fp32 or bf16 of any row and head strides (declared in
+    include/gdn_rotary.h): the first 2 * len(frequencies) channels of every head are turned by positions[t] *
+    frequencies[i] (int32 [T]; fp64, see rotary_frequencies) and multiplied by magnitude, as pairs (i, i + half) or
+    (2i, 2i + 1) when interleaved. Without q_out and k_out in place. inverse=True turns back: the gradients of q and
+    k from those of the outputs. Returns (q_out, k_out)."""
+    torch = _torch()
+    a = RotaryArgs()
+    a.dtype = _dtype_code(q)
+    a.T, a.H, a.D = _put_rows(a, "q", q, "q")
+    q_out = q if q_out is None else q_out
+    _put_rows(a, "q_out", q_out, "q_out", rows=a.T, heads=a.H, dim=a.D, dtype=q.dtype)
+    if k is not None:
+        _, a.HK, _ = _put_rows(a, "k", k, "k", rows=a.T, dim=a.D, dtype=q.dtype)
+        k_out = k if k_out is None else k_out
+        _put_rows(a, "k_out", k_out, "k_out", rows=a.T, heads=a.HK, dim=a.D, dtype=q.dtype)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if positions.numel() != a.T:
+        raise ValueError(f"positions must have {a.T} entries")
+    a.positions = _ptr(_dense(positions, "positions"), "positions", torch.int32)
+    a.frequencies, a.rotary_dim = _rotary_table(frequencies)
+    a.interleaved, a.inverse = int(bool(interleaved)), int(bool(inverse))
+    a.magnitude = float(magnitude)
+    if a.magnitude == 0.0:
+        raise ValueError("magnitude must not be 0")
+    keep = (a, q, k, q_out, k_out, positions, frequencies)
+    return _run_or_prepare("gdn_rotary", (ctypes.byref(a),), keep, stream, prepare, (q_out, k_out))
 
 
 def gdn_selftest_bounded_wait(err_flags, limit_cycles, arrive, stream=None):

@@ -9,12 +9,14 @@
 #include "gdn_front.h"
 #include "gdn_gemv.h"
 #include "gdn_launch.h"
+#include "gdn_linear.h"
+#include "gdn_rotary.h"
 #include "mamba_decode.h"
 #include "mamba_scan.h"
 
 namespace {
 
-constexpr int kAbiVersion = 8;
+constexpr int kAbiVersion = 9;
 
 bool k_supported(int K) { return K == 16 || K == 32 || K == 64 || K == 128; }
 bool dtype_ok(int d) { return d == GDN_F32 || d == GDN_BF16; }
@@ -284,6 +286,10 @@ size_t gdn_abi_struct_size(int which)
     case 8: return sizeof(gdn_beam_select_args);
     case 10: return sizeof(gdn_beam_reorder_args);
     case 11: return sizeof(gdn_beam_pool);
+    case 12: return sizeof(gdn_linear_args);
+    case 13: return sizeof(gdn_linear_grad_args);
+    case 14: return sizeof(gdn_linear_step_args);
+    case 15: return sizeof(gdn_rotary_args);
     default: return 0;
     }
 }

@@ -1,0 +1,281 @@
+// linear_api.cu -- host checks, workspace layout and dispatch of linear attention.
+#include <cmath>
+#include <cstring>
+
+#include "linear_launch.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kSms = 152;              // GB300
+constexpr size_t kWsAlign = 256;
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool overlap(const void *p, const void *q, size_t bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + bytes && b < a + bytes;
+}
+
+bool sizes_ok(const gdn_linear_args &a, bool uniform)
+{
+    return a.T >= 0 && a.S >= 1 && a.H >= 1 && a.HV >= 1 && a.HV <= 65535 && a.HV % a.H == 0 && a.V >= 1 && a.V <= 128 &&
+           (a.K == 16 || a.K == 32 || a.K == 64 || a.K == 128) && (!uniform || a.T % a.S == 0);
+}
+
+// what the backward pass keeps besides the states between segments
+struct BackwardSpace {
+    float *part;                       // [T, HV, K] dq, then dk of every value head
+    float *qdq, *kdk;                  // [T, HV]
+    float *end_dot;                    // [S, HV, parts]
+    float *dg_part;
+};
+
+struct Carver {
+    unsigned char *base;
+    size_t used = 0;
+    float *take(size_t count)
+    {
+        float *p = base ? reinterpret_cast<float *>(base + used) : nullptr;
+        used += (count * sizeof(float) + kWsAlign - 1) / kWsAlign * kWsAlign;
+        return p;
+    }
+};
+
+int z_parts(int dz) { return (dz + kLinearZ - 1) / kLinearZ; }
+
+// Splits the sequences into segments, by the call's sizes alone.
+void plan(LinearLaunch &P, bool uniform, bool backward)
+{
+    const gdn_linear_args &a = P.a;
+    P.Ls = uniform ? a.T / a.S : 0;
+    const int64_t ctas = (int64_t)a.HV * z_parts(backward ? (a.K < a.V ? a.K : a.V) : a.V);
+    int64_t seg = ((int64_t)a.T * ctas + 4 * kSms - 1) / (4 * kSms);
+    seg = (seg + 15) / 16 * 16;
+    if (seg < 48) seg = 48;
+    const int64_t longest = uniform ? P.Ls : a.T;
+    if (seg >= longest) seg = longest > 0 ? longest : 1;
+    P.seg = (int)seg;
+    P.carried = longest > seg;
+    P.items = (int)(uniform ? (int64_t)a.S * (P.Ls > 0 ? (P.Ls + seg - 1) / seg : 1) : a.S + a.T / seg);
+}
+
+size_t carve(LinearLaunch &P, BackwardSpace *B, unsigned char *base)
+{
+    Carver w{base};
+    const gdn_linear_args &a = P.a;
+    if (P.carried) {
+        P.local = w.take((size_t)P.items * a.HV * a.K * a.V);
+        P.total = w.take((size_t)P.items * a.HV);
+    }
+    if (B) {
+        const size_t th = (size_t)a.T * a.HV;
+        B->part = w.take(th * a.K);
+        B->qdq = w.take(th);
+        B->kdk = w.take(th);
+        B->end_dot = w.take((size_t)a.S * a.HV * z_parts(a.K));
+        B->dg_part = w.take(linear_dg_part_floats(a.S, a.HV));
+    }
+    return w.used;
+}
+
+int check_rows(const void *p, int64_t stride, int64_t head, size_t es)
+{
+    if (stride < 0 || head < 0) return GDN_ERR_SHAPE;
+    return aligned(p, es) ? GDN_OK : GDN_ERR_ALIGN;
+}
+
+// rows [T, heads, n] of an output: no two of them on the same memory
+int check_output(const void *p, int64_t stride, int64_t head, int T, int heads, int n, size_t es)
+{
+    const int rc = check_rows(p, stride, head, es);
+    if (rc != GDN_OK) return rc;
+    const bool by_token = (T <= 1 || stride >= (heads > 1 ? (heads - 1) * head : 0) + n) && (heads == 1 || head >= n);
+    const bool by_head = (heads == 1 || head >= (int64_t)(T - 1) * stride + n) && (T <= 1 || stride >= n);
+    return by_token || by_head ? GDN_OK : GDN_ERR_SHAPE;
+}
+
+int check(const gdn_linear_args &a, bool states)
+{
+    if (!sizes_ok(a, !a.cu_seqlens)) return GDN_ERR_SHAPE;
+    if (a.in_dtype != GDN_F32 && a.in_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (states && (a.num_states < 1 || (!a.state_indices && a.num_states < a.S))) return GDN_ERR_SHAPE;
+    if (a.T > 0 && (!a.q || !a.k || !a.v || !a.g)) return GDN_ERR_NULL;
+    const size_t es = a.in_dtype == GDN_BF16 ? 2 : 4;
+    for (int rc : {check_rows(a.q, a.q_stride, a.q_head_stride, es), check_rows(a.k, a.k_stride, a.k_head_stride, es),
+                   check_rows(a.v, a.v_stride, a.v_head_stride, es), check_rows(a.g, a.g_stride, 0, 4)})
+        if (rc != GDN_OK) return rc;
+    if (!aligned(a.cu_seqlens, 4) || !aligned(a.state_indices, 4) || !aligned(a.initial_state, 16) || !aligned(a.final_state, 16))
+        return GDN_ERR_ALIGN;
+    return GDN_OK;
+}
+
+int check_workspace(const gdn_linear_args &a, size_t need)
+{
+    if (need == 0) return GDN_OK;
+    if (!a.workspace) return GDN_ERR_NULL;
+    if (a.workspace_bytes < need) return GDN_ERR_SHAPE;
+    return aligned(a.workspace, 16) ? GDN_OK : GDN_ERR_ALIGN;
+}
+
+// the sweep (x, y, z) = (q, k, v); the others exchange roles
+LinearSweep forward_sweep(const LinearLaunch &P)
+{
+    const gdn_linear_args &a = P.a;
+    LinearSweep p = {};
+    const int G = a.HV / a.H;
+    p.x = a.q, p.x_stride = a.q_stride, p.x_head = a.q_head_stride, p.x_group = G;
+    p.y = a.k, p.y_stride = a.k_stride, p.y_head = a.k_head_stride, p.y_group = G;
+    p.z = a.v, p.z_stride = a.v_stride, p.z_head = a.v_head_stride, p.z_group = 1;
+    p.DY = a.K, p.DZ = a.V;
+    p.x_scale = P.scale, p.z_scale = 1.f;
+    p.sy = 1, p.sz = a.K;
+    return p;
+}
+
+int run(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream) { return launch_linear_recurrent(P, p, true, stream); }
+
+// the states between the segments
+int run_states(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream)
+{
+    if (!P.carried) return GDN_OK;
+    const int rc = launch_linear_recurrent(P, p, false, stream);
+    return rc != GDN_OK ? rc : launch_linear_carry(P, p, stream);
+}
+
+LinearLaunch make(const gdn_linear_args &a, bool backward, bool states)
+{
+    LinearLaunch P;
+    std::memset(&P, 0, sizeof(P));
+    P.a = a;
+    P.scale = a.scale != 0.f ? a.scale : 1.0f / std::sqrt((float)a.K);
+    P.states = states;
+    plan(P, !a.cu_seqlens, backward);
+    return P;
+}
+
+}  // namespace
+
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_linear_workspace_bytes(int32_t T, int32_t S, int32_t H, int32_t HV, int32_t K, int32_t V, int32_t in_dtype,
+                                  int32_t uniform, int32_t backward)
+{
+    gdn::LinearLaunch P;
+    std::memset(&P, 0, sizeof(P));
+    P.a.T = T, P.a.S = S, P.a.H = H, P.a.HV = HV, P.a.K = K, P.a.V = V, P.a.in_dtype = in_dtype;
+    if (!gdn::sizes_ok(P.a, uniform != 0)) return 0;
+    gdn::plan(P, uniform != 0, backward != 0);
+    gdn::BackwardSpace B;
+    return gdn::carve(P, backward ? &B : nullptr, nullptr);
+}
+
+int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream)
+{
+    if (!args) return GDN_ERR_NULL;
+    const gdn_linear_args &a = *args;
+    const bool states = a.initial_state || a.final_state;
+    int rc = gdn::check(a, states);
+    if (rc != GDN_OK) return rc;
+    if (a.out_dtype != GDN_F32 && a.out_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (a.T > 0 && !a.o) return GDN_ERR_NULL;
+    rc = gdn::check_output(a.o, a.o_stride, a.o_head_stride, a.T, a.HV, a.V, a.out_dtype == GDN_BF16 ? 2 : 4);
+    if (rc != GDN_OK || (a.T == 0 && !a.final_state)) return rc;
+    gdn::LinearLaunch P = gdn::make(a, false, states);
+    rc = gdn::check_workspace(a, gdn::carve(P, nullptr, nullptr));
+    if (rc != GDN_OK) return rc;
+    gdn::carve(P, nullptr, static_cast<unsigned char *>(a.workspace));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    gdn::LinearSweep p = gdn::forward_sweep(P);
+    p.start = a.initial_state;
+    p.end = a.final_state;
+    p.out = a.o, p.out_stride = a.o_stride, p.out_head = a.o_head_stride, p.out_f32 = a.out_dtype == GDN_F32;
+    rc = gdn::run_states(P, p, s);
+    return rc != GDN_OK ? rc : gdn::run(P, p, s);
+}
+
+int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t stream)
+{
+    if (!args) return GDN_ERR_NULL;
+    const gdn_linear_grad_args &q = *args;
+    const gdn_linear_args &a = q.s;
+    const bool states = a.initial_state || q.d_final_state || q.d_initial_state;
+    gdn_linear_args in = a;
+    in.final_state = nullptr;
+    int rc = gdn::check(in, states);
+    if (rc != GDN_OK) return rc;
+    if (a.T > 0 && !q.d_o) return GDN_ERR_NULL;
+    const size_t es = a.in_dtype == GDN_BF16 ? 2 : 4, pool = states ? (size_t)a.num_states * a.HV * a.K * a.V * 4 : 0;
+    for (int r : {gdn::check_rows(q.d_o, q.do_stride, q.do_head_stride, es),
+                  q.dq ? gdn::check_output(q.dq, q.dq_stride, q.dq_head_stride, a.T, a.H, a.K, es) : (int)GDN_OK,
+                  q.dk ? gdn::check_output(q.dk, q.dk_stride, q.dk_head_stride, a.T, a.H, a.K, es) : (int)GDN_OK,
+                  q.dv ? gdn::check_output(q.dv, q.dv_stride, q.dv_head_stride, a.T, a.HV, a.V, es) : (int)GDN_OK,
+                  q.dg && a.g_stride ? gdn::check_output(q.dg, q.dg_stride, a.HV, a.T, 1, a.HV, 4) : (int)GDN_OK})
+        if (r != GDN_OK) return r;
+    if (!gdn::aligned(q.dg, 4) || !gdn::aligned(q.d_final_state, 16) || !gdn::aligned(q.d_initial_state, 16)) return GDN_ERR_ALIGN;
+    if (gdn::overlap(q.d_initial_state, q.d_final_state, pool) || gdn::overlap(q.d_initial_state, a.initial_state, pool)) return GDN_ERR_ARG;
+    gdn::LinearLaunch P = gdn::make(in, true, states);
+    gdn::BackwardSpace B;
+    rc = gdn::check_workspace(a, gdn::carve(P, &B, nullptr));
+    if (rc != GDN_OK) return rc;
+    gdn::carve(P, &B, static_cast<unsigned char *>(a.workspace));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int G = a.HV / a.H;
+
+    // forward: dq from the states
+    if (q.dq || q.dg) {
+        gdn::LinearSweep p = gdn::forward_sweep(P);
+        p.start = a.initial_state;
+        rc = gdn::run_states(P, p, s);
+        if (rc != GDN_OK) return rc;
+        p.x = q.d_o, p.x_stride = q.do_stride, p.x_head = q.do_head_stride, p.x_group = 1;
+        p.y = a.v, p.y_stride = a.v_stride, p.y_head = a.v_head_stride, p.y_group = 1;
+        p.z = a.k, p.z_stride = a.k_stride, p.z_head = a.k_head_stride, p.z_group = G;
+        p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
+        p.out = B.part, p.out_stride = (int64_t)a.HV * a.K, p.out_head = a.K, p.out_f32 = 1;
+        if (q.dg && q.d_final_state) p.with_end = q.d_final_state, p.end_dot = B.end_dot;
+        rc = gdn::run(P, p, s);
+        if (rc != GDN_OK) return rc;
+        const gdn::LinearFold f = {B.part, q.dq, q.dq_stride, q.dq_head_stride, a.q, a.q_stride, a.q_head_stride, q.dg ? B.qdq : nullptr};
+        rc = gdn::launch_linear_fold(P, f, s);
+        if (rc != GDN_OK) return rc;
+    }
+    // backward: dv and dk from the states' gradients
+    if (q.dk || q.dv || q.dg || q.d_initial_state) {
+        gdn::LinearSweep p = gdn::forward_sweep(P);
+        p.reverse = 1;
+        p.start = q.d_final_state;
+        p.x = a.k, p.x_stride = a.k_stride, p.x_head = a.k_head_stride;
+        p.y = a.q, p.y_stride = a.q_stride, p.y_head = a.q_head_stride;
+        p.z = q.d_o, p.z_stride = q.do_stride, p.z_head = q.do_head_stride;
+        p.x_scale = 1.f, p.z_scale = P.scale;
+        rc = gdn::run_states(P, p, s);
+        if (rc != GDN_OK) return rc;
+        if (q.dv || q.d_initial_state) {
+            p.end = q.d_initial_state;
+            p.out = q.dv, p.out_stride = q.dv_stride, p.out_head = q.dv_head_stride, p.out_f32 = a.in_dtype == GDN_F32;
+            rc = gdn::run(P, p, s);
+            if (rc != GDN_OK) return rc;
+            p.end = nullptr;
+        }
+        if (q.dk || q.dg) {
+            p.x = a.v, p.x_stride = a.v_stride, p.x_head = a.v_head_stride, p.x_group = 1;
+            p.y = q.d_o, p.y_stride = q.do_stride, p.y_head = q.do_head_stride, p.y_group = 1;
+            p.z = a.q, p.z_stride = a.q_stride, p.z_head = a.q_head_stride, p.z_group = G;
+            p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
+            p.out = B.part, p.out_stride = (int64_t)a.HV * a.K, p.out_head = a.K, p.out_f32 = 1;
+            rc = gdn::run(P, p, s);
+            if (rc != GDN_OK) return rc;
+            const gdn::LinearFold f = {B.part, q.dk, q.dk_stride, q.dk_head_stride, a.k, a.k_stride, a.k_head_stride, q.dg ? B.kdk : nullptr};
+            rc = gdn::launch_linear_fold(P, f, s);
+            if (rc != GDN_OK) return rc;
+        }
+    }
+    if (!q.dg) return GDN_OK;
+    return gdn::launch_linear_dg(P, B.qdq, B.kdk, q.d_final_state ? B.end_dot : nullptr, gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,150 @@
+// linear_common.cuh -- segments and decays of linear attention (internal to libgdn_decode.so).
+#pragma once
+
+#include "gdn_common.cuh"
+#include "linear_launch.h"
+
+namespace gdn {
+
+// A segment of a sequence: rows [begin, begin + n) of the packed tokens.
+struct LinearItem {
+    int seq;            // -1: none
+    int begin, n;
+    int seq_begin, seq_end;
+    int state;          // row in the state buffers; -1: a bad index (no states, outputs zeroed)
+    int index;          // of the segment in the sequence
+};
+
+// rows of sequence s; a sequence whose borders leave 0 .. T or decrease has none (bad)
+__device__ __forceinline__ void linear_rows(const LinearLaunch &P, int s, int &b, int &e, bool &bad)
+{
+    if (P.a.cu_seqlens) {
+        b = P.a.cu_seqlens[s];
+        e = P.a.cu_seqlens[s + 1];
+        bad = b < 0 || e > P.a.T || e < b;
+        if (bad) b = e = 0;
+    } else {
+        b = s * P.Ls;
+        e = b + P.Ls;
+        bad = false;
+    }
+}
+
+__device__ __forceinline__ int linear_segments(const LinearLaunch &P, int rows)
+{
+    return rows <= P.seg ? 1 : (rows + P.seg - 1) / P.seg;
+}
+
+// The first segment of sequence s, and the sequence's rows; all 32 lanes of a warp call it.
+__device__ __forceinline__ int linear_first_item(const LinearLaunch &P, int s)
+{
+    if (!P.a.cu_seqlens) return s * linear_segments(P, P.Ls);
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int s0 = lane; s0 < s; s0 += 32) {
+        int b, e;
+        bool bad;
+        linear_rows(P, s0, b, e, bad);
+        before += linear_segments(P, e - b);
+    }
+    return __reduce_add_sync(0xFFFFFFFFu, before);
+}
+
+// The segment that item i stands for; all 32 lanes of a warp call it and get the same answer. With cu_seqlens the
+// sequences' segments are counted 32 sequences at a time.
+__device__ __forceinline__ LinearItem linear_item(const LinearLaunch &P, int i, bool report)
+{
+    LinearItem it;
+    it.seq = -1;
+    it.begin = it.n = it.seq_begin = it.seq_end = it.state = it.index = 0;
+    const int lane = threadIdx.x & 31;
+    if (!P.a.cu_seqlens) {
+        const int per = linear_segments(P, P.Ls);
+        const int s = i / per;
+        if (s >= P.a.S) return it;
+        it.seq = s;
+        it.index = i - s * per;
+        it.seq_begin = s * P.Ls;
+        it.seq_end = it.seq_begin + P.Ls;
+    } else {
+        int before = 0;
+        for (int s0 = 0; s0 < P.a.S; s0 += 32) {
+            const int s = s0 + lane;
+            int b = 0, e = 0, m = 0;
+            bool bad = false;
+            if (s < P.a.S) {
+                linear_rows(P, s, b, e, bad);
+                m = linear_segments(P, e - b);
+            }
+            int sum = m;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const bool mine = s < P.a.S && i >= before + sum - m && i < before + sum;
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
+            if (who) {
+                const int src = __ffs(who) - 1;
+                it.seq = s0 + src;
+                it.index = i - (before + __shfl_sync(0xFFFFFFFFu, sum - m, src));
+                it.seq_begin = __shfl_sync(0xFFFFFFFFu, b, src);
+                it.seq_end = __shfl_sync(0xFFFFFFFFu, e, src);
+                const int wrong = __shfl_sync(0xFFFFFFFFu, (int)bad, src);
+                if (wrong) {
+                    if (report && lane == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
+                    it.seq = -1;
+                    return it;
+                }
+                break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (it.seq < 0) return it;
+    }
+    it.begin = it.seq_begin + it.index * P.seg;
+    it.n = min(P.seg, it.seq_end - it.begin);
+    it.state = it.seq;
+    if (P.states) {
+        if (P.a.state_indices) it.state = P.a.state_indices[it.seq];
+        if (it.state < 0 || it.state >= P.a.num_states) {
+            if (report && lane == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
+            it.state = -1;
+        }
+    }
+    return it;
+}
+
+// ---- decays ------------------------------------------------------------------------------------
+// Log decays are summed in 64 bits as powers of two and turned into factors whole: a product of a thousand rounded
+// factors near one would be off by a thousand times their common rounding error.
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr double kLog2e = 1.4426950408889634;
+
+__device__ __forceinline__ double linear_log2(float g)
+{
+    return (g < -200.f ? -200.0 : (double)g) * kLog2e;     // (a NaN stays one)
+}
+
+// 2^a to fp32 accuracy for any a
+__device__ __forceinline__ float exp2_wide(double a)
+{
+    if (a < -160.0) return 0.f;
+    const double n = rint(a < 200.0 ? a : 200.0);
+    return ldexpf(exp2f((float)(a - n)), (int)n);
+}
+
+// decay that a sweep applies before it takes token t (in its own direction)
+__device__ __forceinline__ double linear_decay(const LinearLaunch &P, int hv, int t, int seq_end, int reverse)
+{
+    const int at = reverse ? t + 1 : t;
+    return at < seq_end ? linear_log2(P.a.g[at * P.a.g_stride + hv]) : 0.0;
+}
+
+// debug build: element (t, head, c) of a tensor with T rows lies inside it
+__device__ __forceinline__ bool linear_in(const LinearLaunch &P, int t, int head, int heads)
+{
+    return GDN_IN(P.a.err_flags, t, P.a.T) && GDN_IN(P.a.err_flags, head, heads);
+}
+
+}  // namespace gdn
