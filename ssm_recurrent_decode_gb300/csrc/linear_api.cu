@@ -45,20 +45,34 @@ struct Carver {
 
 int z_parts(int dz) { return (dz + kLinearZ - 1) / kLinearZ; }
 
+void set_segments(LinearLaunch &P, bool uniform, int64_t seg)
+{
+    const int64_t longest = uniform ? P.Ls : P.a.T;
+    if (seg >= longest) seg = longest > 0 ? longest : 1;
+    P.seg = (int)seg;
+    P.carried = longest > seg;
+    P.items = (int)(uniform ? (int64_t)P.a.S * (P.Ls > 0 ? (P.Ls + seg - 1) / seg : 1) : P.a.S + P.a.T / seg);
+}
+
 // Splits the sequences into segments, by the call's sizes alone.
 void plan(LinearLaunch &P, bool uniform, bool backward)
 {
     const gdn_linear_args &a = P.a;
     P.Ls = uniform ? a.T / a.S : 0;
+    P.tc = a.in_dtype == GDN_BF16;
+    if (P.tc) {
+        // one CTA an SM; whole chunks
+        int64_t seg = ((int64_t)a.T * a.HV + 2 * kSms - 1) / (2 * kSms);
+        seg = (seg + kLinearChunk - 1) / kLinearChunk * kLinearChunk;
+        if (seg < 2 * kLinearChunk) seg = 2 * kLinearChunk;
+        set_segments(P, uniform, seg);
+        return;
+    }
     const int64_t ctas = (int64_t)a.HV * z_parts(backward ? (a.K < a.V ? a.K : a.V) : a.V);
     int64_t seg = ((int64_t)a.T * ctas + 4 * kSms - 1) / (4 * kSms);
     seg = (seg + 15) / 16 * 16;
     if (seg < 48) seg = 48;
-    const int64_t longest = uniform ? P.Ls : a.T;
-    if (seg >= longest) seg = longest > 0 ? longest : 1;
-    P.seg = (int)seg;
-    P.carried = longest > seg;
-    P.items = (int)(uniform ? (int64_t)a.S * (P.Ls > 0 ? (P.Ls + seg - 1) / seg : 1) : a.S + a.T / seg);
+    set_segments(P, uniform, seg);
 }
 
 size_t carve(LinearLaunch &P, BackwardSpace *B, unsigned char *base)
@@ -134,13 +148,35 @@ LinearSweep forward_sweep(const LinearLaunch &P)
     return p;
 }
 
-int run(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream) { return launch_linear_recurrent(P, p, true, stream); }
+int run(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream) 
+{
+    return P.tc ? launch_linear_chunk(P, p, true, stream) : launch_linear_recurrent(P, p, true, stream);
+}
+
+struct Rows {
+    const void *p;
+    int64_t stride, head;
+};
+
+// A sweep whose outputs are summed over the value heads that share a q/k head: dq or dk, and each value head's product
+// with q or k.
+int run_heads(const LinearLaunch &P, LinearSweep p, float *part, Rows out, Rows with, float *dot, cudaStream_t stream)
+{
+    const gdn_linear_args &a = P.a;
+    const bool direct = P.tc && a.HV == a.H;           // one value head a head: nothing to sum
+    if (P.tc && dot) p.dot = dot, p.dot_with = with.p, p.dot_stride = with.stride, p.dot_head = with.head, p.dot_group = a.HV / a.H;
+    if (direct) p.out = const_cast<void *>(out.p), p.out_stride = out.stride, p.out_head = out.head, p.out_f32 = 0;
+    else p.out = part, p.out_stride = (int64_t)a.HV * a.K, p.out_head = a.K, p.out_f32 = 1;
+    const int rc = run(P, p, stream);
+    if (rc != GDN_OK || direct || (P.tc && !out.p)) return rc;
+    return launch_linear_fold(P, {part, const_cast<void *>(out.p), out.stride, out.head, with.p, with.stride, with.head, P.tc ? nullptr : dot}, stream);
+}
 
 // the states between the segments
 int run_states(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream)
 {
     if (!P.carried) return GDN_OK;
-    const int rc = launch_linear_recurrent(P, p, false, stream);
+    const int rc = P.tc ? launch_linear_chunk(P, p, false, stream) : launch_linear_recurrent(P, p, false, stream);
     return rc != GDN_OK ? rc : launch_linear_carry(P, p, stream);
 }
 
@@ -235,12 +271,8 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
         p.y = a.v, p.y_stride = a.v_stride, p.y_head = a.v_head_stride, p.y_group = 1;
         p.z = a.k, p.z_stride = a.k_stride, p.z_head = a.k_head_stride, p.z_group = G;
         p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
-        p.out = B.part, p.out_stride = (int64_t)a.HV * a.K, p.out_head = a.K, p.out_f32 = 1;
         if (q.dg && q.d_final_state) p.with_end = q.d_final_state, p.end_dot = B.end_dot;
-        rc = gdn::run(P, p, s);
-        if (rc != GDN_OK) return rc;
-        const gdn::LinearFold f = {B.part, q.dq, q.dq_stride, q.dq_head_stride, a.q, a.q_stride, a.q_head_stride, q.dg ? B.qdq : nullptr};
-        rc = gdn::launch_linear_fold(P, f, s);
+        rc = gdn::run_heads(P, p, B.part, {q.dq, q.dq_stride, q.dq_head_stride}, {a.q, a.q_stride, a.q_head_stride}, q.dg ? B.qdq : nullptr, s);
         if (rc != GDN_OK) return rc;
     }
     // backward: dv and dk from the states' gradients
@@ -266,16 +298,12 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
             p.y = q.d_o, p.y_stride = q.do_stride, p.y_head = q.do_head_stride, p.y_group = 1;
             p.z = a.q, p.z_stride = a.q_stride, p.z_head = a.q_head_stride, p.z_group = G;
             p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
-            p.out = B.part, p.out_stride = (int64_t)a.HV * a.K, p.out_head = a.K, p.out_f32 = 1;
-            rc = gdn::run(P, p, s);
-            if (rc != GDN_OK) return rc;
-            const gdn::LinearFold f = {B.part, q.dk, q.dk_stride, q.dk_head_stride, a.k, a.k_stride, a.k_head_stride, q.dg ? B.kdk : nullptr};
-            rc = gdn::launch_linear_fold(P, f, s);
+            rc = gdn::run_heads(P, p, B.part, {q.dk, q.dk_stride, q.dk_head_stride}, {a.k, a.k_stride, a.k_head_stride}, q.dg ? B.kdk : nullptr, s);
             if (rc != GDN_OK) return rc;
         }
     }
     if (!q.dg) return GDN_OK;
-    return gdn::launch_linear_dg(P, B.qdq, B.kdk, q.d_final_state ? B.end_dot : nullptr, gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
+    return gdn::launch_linear_dg(P, B.qdq, B.kdk, q.d_final_state ? B.end_dot : nullptr, P.tc ? 1 : gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
 }
 
 }  // extern "C"

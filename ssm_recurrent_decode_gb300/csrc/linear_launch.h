@@ -27,6 +27,11 @@ struct LinearSweep {
     float *end;                        // [num_states, HV, V, K] states to end with, or null
     const float *with_end;             // [num_states, HV, V, K] or null: its product with the end state goes to
     float *end_dot;                    // [S, HV, parts of z]
+    // of the tensor-core kernel:
+    float *dot;                        // [T, HV] or null: sum_z out_t[z] dot_with_t[z], before rounding
+    const void *dot_with;
+    int64_t dot_stride, dot_head;
+    int dot_group;
 };
 
 struct LinearLaunch {
@@ -37,6 +42,7 @@ struct LinearLaunch {
     int items;          // most segments (of all sequences) there can be; every sequence has at least one
     int carried;        // a sequence may have several segments
     int states;         // state indices are checked
+    int tc;             // the tensor-core kernel
     // workspace
     float *local;       // [items, HV, V, K] the state that a segment ends with from zero; then the one it starts with
     float *total;       // [items, HV] log2 of the segment's decay
@@ -47,6 +53,10 @@ constexpr int kLinearZ = 64;           // columns of z per CTA of the fp32 kerne
 
 // The sweep on the CUDA cores in fp32 (any type, size, stride); outputs: p.x given. Without: local and total.
 int launch_linear_recurrent(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);
+// The same for bf16 inputs on the tensor cores, and whether a call takes it.
+int launch_linear_chunk(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);
+constexpr int kLinearChunk = 128;      // its tokens per chunk
+
 // Between the two: local from end states to start states.
 int launch_linear_carry(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream);
 
