@@ -30,6 +30,7 @@ struct BackwardSpace {
     float *qdq, *kdk;                  // [T, HV]
     float *end_dot;                    // [S, HV, parts]
     float *dg_part;
+    float *chunk_states, *chunk_dot;   // of the tensor-core kernel
 };
 
 struct Carver {
@@ -88,8 +89,15 @@ size_t carve(LinearLaunch &P, BackwardSpace *B, unsigned char *base)
         B->part = w.take(th * a.K);
         B->qdq = w.take(th);
         B->kdk = w.take(th);
-        B->end_dot = w.take((size_t)a.S * a.HV * z_parts(a.K));
-        B->dg_part = w.take(linear_dg_part_floats(a.S, a.HV));
+        if (P.tc) {
+            const size_t chunks = ((size_t)a.T / kLinearChunk + a.S) * a.HV;
+            B->chunk_states = w.take(chunks * kLinearChunk * (a.K <= 64 ? 64 : 128));
+            B->chunk_dot = w.take(chunks * 8);
+            B->dg_part = w.take(chunks * 8);
+        } else {
+            B->end_dot = w.take((size_t)a.S * a.HV * z_parts(a.K));
+            B->dg_part = w.take(linear_dg_part_floats(a.S, a.HV));
+        }
     }
     return w.used;
 }
@@ -228,7 +236,7 @@ int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream)
     gdn::LinearSweep p = gdn::forward_sweep(P);
     p.start = a.initial_state;
     p.end = a.final_state;
-    p.out = a.o, p.out_stride = a.o_stride, p.out_head = a.o_head_stride, p.out_f32 = a.out_dtype == GDN_F32;
+    p.out = a.o, p.out_stride = a.o_stride, p.out_head = a.o_head_stride, p.out_f32 = p.exact = a.out_dtype == GDN_F32;
     rc = gdn::run_states(P, p, s);
     return rc != GDN_OK ? rc : gdn::run(P, p, s);
 }
@@ -271,7 +279,8 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
         p.y = a.v, p.y_stride = a.v_stride, p.y_head = a.v_head_stride, p.y_group = 1;
         p.z = a.k, p.z_stride = a.k_stride, p.z_head = a.k_head_stride, p.z_group = G;
         p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
-        if (q.dg && q.d_final_state) p.with_end = q.d_final_state, p.end_dot = B.end_dot;
+        if (q.dg && P.tc) p.chunk_states = B.chunk_states;
+        if (q.dg && !P.tc && q.d_final_state) p.with_end = q.d_final_state, p.end_dot = B.end_dot;
         rc = gdn::run_heads(P, p, B.part, {q.dq, q.dq_stride, q.dq_head_stride}, {a.q, a.q_stride, a.q_head_stride}, q.dg ? B.qdq : nullptr, s);
         if (rc != GDN_OK) return rc;
     }
@@ -298,12 +307,14 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
             p.y = q.d_o, p.y_stride = q.do_stride, p.y_head = q.do_head_stride, p.y_group = 1;
             p.z = a.q, p.z_stride = a.q_stride, p.z_head = a.q_head_stride, p.z_group = G;
             p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
+            if (q.dg && P.tc) p.chunk_states = B.chunk_states, p.chunk_dot = B.chunk_dot;
             rc = gdn::run_heads(P, p, B.part, {q.dk, q.dk_stride, q.dk_head_stride}, {a.k, a.k_stride, a.k_head_stride}, q.dg ? B.kdk : nullptr, s);
             if (rc != GDN_OK) return rc;
         }
     }
     if (!q.dg) return GDN_OK;
-    return gdn::launch_linear_dg(P, B.qdq, B.kdk, q.d_final_state ? B.end_dot : nullptr, P.tc ? 1 : gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
+    if (P.tc) return gdn::launch_linear_dg_chunks(P, B.qdq, B.kdk, B.chunk_dot, q.dg, q.dg_stride, B.dg_part, s);
+    return gdn::launch_linear_dg(P, B.qdq, B.kdk, q.d_final_state ? B.end_dot : nullptr, gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
 }
 
 }  // extern "C"

@@ -156,6 +156,70 @@ __global__ void __launch_bounds__(256) linear_dg_fixed_kernel(const float *part,
     }
 }
 
+// Of the tensor-core kernel: no sum is longer than a chunk. A CTA per chunk and 32 heads, eight ranges of 16 rows.
+__global__ void __launch_bounds__(256) linear_dg_chunk_kernel(const __grid_constant__ LinearLaunch P, const float *qdq, const float *kdk,
+                                                           const float *chunk_dot, float *dg, int64_t dg_stride, float *part)
+{
+    const int i = threadIdx.x & 31, range = threadIdx.x >> 5, hv = blockIdx.z * 32 + i, HV = P.a.HV;
+    __shared__ float sums[8][32];
+    const LinearItem it = linear_item(P, blockIdx.x, false);
+    const int at = it.begin + blockIdx.y * kLinearChunk, rows = min(kLinearChunk, it.begin + it.n - at);
+    if (it.seq < 0 || rows <= 0) return;
+    const bool mine = hv < HV && it.state >= 0;
+    const int first = 16 * range, last = min(rows, first + 16);
+    const size_t chunk = (size_t)(at / kLinearChunk + it.seq) * HV + hv;
+    float d[16], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const size_t t = (size_t)(at + first + k) * HV + hv;
+        d[k] = mine && first + k < last ? qdq[t] - kdk[t] : 0.f;
+    }
+#pragma unroll
+    for (int k = 15; k >= 0; --k) sum += d[k];
+    sums[range][i] = sum;
+    __syncthreads();
+    if (hv >= HV) return;
+    float run = 0.f, total = 0.f;
+    if (mine)
+        for (int k = 0; k < 8; ++k) run += chunk_dot[chunk * 8 + k];
+    for (int r = 7; r > range; --r) run += sums[r][i];
+    const bool fixed = P.a.g_stride == 0;
+#pragma unroll
+    for (int k = 15; k >= 0; --k) {
+        run += d[k];
+        if (first + k >= last) continue;
+        if (fixed) total += run;
+        else dg[(int64_t)(at + first + k) * dg_stride + hv] = run;
+    }
+    if (fixed) {
+        __syncwarp();
+        part[chunk * 8 + range] = total;
+    }
+}
+
+// dg of one decay a head: every chunk's parts, in order
+__global__ void __launch_bounds__(256) linear_dg_chunk_fixed_kernel(const __grid_constant__ LinearLaunch P, const float *part, float *dg)
+{
+    const int hv = blockIdx.x;
+    __shared__ double sums[8];
+    double sum = 0.0;
+    for (int s = 0; s < P.a.S; ++s) {
+        int b, e;
+        bool bad;
+        linear_rows(P, s, b, e, bad);
+        for (int k = threadIdx.x; k < (e - b + kLinearChunk - 1) / kLinearChunk * 8; k += 256)
+            sum += part[((size_t)((b + (k >> 3) * kLinearChunk) / kLinearChunk + s) * P.a.HV + hv) * 8 + (k & 7)];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) sum += sums[w];
+        dg[hv] = (float)sum;
+    }
+}
+
 int status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
 
 }  // namespace
@@ -183,6 +247,15 @@ int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, 
     const dim3 grid((unsigned)P.a.S, (unsigned)((P.a.HV + kDgHeads - 1) / kDgHeads));
     linear_dg_kernel<<<grid, kDgHeads * kDgRanges, 0, stream>>>(P, qdq, kdk, end_dot, parts, dg, dg_stride, part);
     if (P.a.g_stride == 0) linear_dg_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(part, P.a.S * kDgRanges, P.a.HV, dg);
+    return status();
+}
+
+int launch_linear_dg_chunks(const LinearLaunch &P, const float *qdq, const float *kdk, const float *chunk_dot, float *dg,
+                            int64_t dg_stride, float *part, cudaStream_t stream)
+{
+    const dim3 grid((unsigned)P.items, (unsigned)((P.seg + kLinearChunk - 1) / kLinearChunk), (unsigned)((P.a.HV + 31) / 32));
+    linear_dg_chunk_kernel<<<grid, 256, 0, stream>>>(P, qdq, kdk, chunk_dot, dg, dg_stride, part);
+    if (P.a.g_stride == 0) linear_dg_chunk_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(P, part, dg);
     return status();
 }
 

@@ -14,19 +14,22 @@
 // once a chunk. Two terms keep 16 bits of what leads to a token's bf16 output; the update's three keep all 24.
 //
 // One CTA owns a segment of a sequence and a value head. Warps 0-3: P, inter's decays and the outputs (a thread a row
-// r); warps 4-7 and 8-11: Y and the state; 12: issues the MMAs; 13: decays, and z's non-finite values; 14, 15:
-// copies x, y and z (cp.async of 16 bytes, whose zero fill ends a sequence inside a tile) into a ring of 32 KB tiles.
+// r); warps 4-7 and 8-11: Y and the state; 12: issues the MMAs; 13: decays, and z's non-finite values; 14:
+// copies x, y and z by TMA into a ring of 32 KB tiles (with 15, by plain loads, what is not aligned to 16 bytes). A tile may end
+// in another sequence's rows: their y's weigh nothing, their scores are not looked at, their outputs are not written.
 //
 // A product with a zero of P would carry a later token's NaN to earlier ones; warp 13 looks z's tile over (one
 // multiply-add a pair), and in the rare tile that has a non-finite value sets it to zero, notes the column's first
 // such row, and the outputs and the state get their NaN from there.
 //
 // Every wait is bounded; a wait that gives up raises GDN_DEVERR_TIMEOUT and ends the CTA, its MMAs and copies done.
+#include <cstring>
 #include <mutex>
 
 #include "gdn_chain.cuh"
 #include "linear_common.cuh"
 #include "tc_ops.cuh"
+#include "tma_map.h"
 
 namespace gdn {
 
@@ -40,96 +43,119 @@ constexpr int kLoaders = 64;
 constexpr long long kWaitLimit = 1LL << 31;           // SM clock cycles, about one second
 
 // columns of tensor memory
-constexpr uint32_t kScores = 0, kOut = 128, kUpdate = 256, kY = 384;
+constexpr uint32_t kScores = 0, kOut = 128, kUpdate = 256, kY = 384, kY2 = 0;    // (kY2: without outputs)
 
-template <int NS> struct Smem {
-    static constexpr int kSlots = NS == 3 ? 4 : 5;    // NS: bf16 terms of the state
+constexpr int kSlots = 4;                             // tiles of x, y and z in shared memory
+
+// what warp 13 says of a chunk's rows; G: sum of the log decays up to and with the row in the sweep's order, as a
+// power of two, hi + lo with hi in steps of 1/256 (differences of hi are exact, lo is small)
+struct Decays {
+    float nhi[kRows], nlo[kRows];                     // -hi, -lo
+    float col[kRows];                                 // e^{(G at the end of the row's 32) - G}
+    float weight[kRows];                              // e^{(G at the chunk's end) - G}; 0 for rows behind the sequence
+};
+
+template <int NS> struct Smem {                       // NS: bf16 terms of the state
     static constexpr uint32_t kStates = kSlots * kTile;
-    static constexpr uint32_t kDecays = kStates + NS * kTile;         // float2 [2][128]: G = x + y in powers of two
-    static constexpr uint32_t kBad = kDecays + 2 * kRows * 8;         // uint8 [2][128]: first non-finite row of a column of z
+    static constexpr uint32_t kDecays = kStates + NS * kTile;
+    static constexpr uint32_t kBad = kDecays + sizeof(Decays);        // uint8 [2][128]: first non-finite row of a column of z
     static constexpr uint32_t kBars = kBad + 2 * kRows;
     static constexpr uint32_t kBytes = kBars + 512;
     static_assert(kBytes <= 232448, "more than an SM's shared memory");
 };
 
+struct ChunkMaps {
+    CUtensorMap x, y, z;
+};
+
 struct Bars {
-    uint64_t full[5], empty[5];
-    uint64_t decays[2], decays_free[2], z_ok[2];
-    uint64_t scores, p_ready, inter, out, out_read, y_ready, y_free, update, state_ready, done;
+    uint64_t full[kSlots], empty[kSlots];             // tiles
+    uint64_t decays, decays_free;
+    uint64_t z_raw[2], z_ok[2], bad_read[2];          // z's tile may be used for the update; for the outputs; first_bad was read
+    uint64_t y_ready[2], y_free[2];                   // the halves of Y
+    uint64_t scores, p_ready, inter, out, out_read, update, state_ready, done;
     LinearItem item;
     uint32_t tmem;
     int abort_flag, zero, bad[2];
-    float sums[8];
+    long long limit;
+    int32_t *err;
 };
 static_assert(sizeof(Bars) <= 512, "");
 
-// Copies one tile: rows of a tensor in the sweep's order, zeros behind n rows and behind dim columns up to 64 * blocks.
+// A tile by plain loads, for rows that TMA cannot copy (not 16-byte aligned): zeros behind n rows and dim columns.
 template <int BLOCKS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t stride, int64_t first, int dir, int n, int dim,
-                                          bool wide, int tid)
+__device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t stride, int n, int dim, int tid)
 {
     constexpr int CH = 8 * BLOCKS;                    // 16-byte chunks of a row
-#pragma unroll 8
-    for (int i = 0; i < kRows * CH / kLoaders; ++i) {
-        const int e = tid + i * kLoaders, r = e / CH, c = e % CH;
+#pragma unroll 2
+    for (int e = tid; e < kRows * CH; e += kLoaders) {
+        const int r = e / CH, c = e % CH;
         const uint32_t to = dst + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        const bool row = r < n;
-        const bf16 *from = src + (first + (int64_t)dir * (row ? r : 0)) * stride;
-        if (wide) {
-            const bool in = row && c * 8 < dim;
-            cp_async16(to, in ? from + c * 8 : from, in);
-        } else {
-            uint32_t w[4];
+        const uint16_t *from = reinterpret_cast<const uint16_t *>(src + (int64_t)(r < n ? r : 0) * stride);
+        uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = c * 8 + 2 * j;
-                const uint32_t lo = row && k < dim ? reinterpret_cast<const uint16_t *>(from)[k] : 0;
-                const uint32_t hi = row && k + 1 < dim ? reinterpret_cast<const uint16_t *>(from)[k + 1] : 0;
-                w[j] = lo | hi << 16;
-            }
-            st_shared16(to, w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) {
+            const int k = c * 8 + 2 * j;
+            const uint32_t lo = r < n && k < dim ? from[k] : 0, hi = r < n && k + 1 < dim ? from[k + 1] : 0;
+            w[j] = lo | hi << 16;
         }
+        st_shared16(to, w[0], w[1], w[2], w[3]);
     }
 }
 
-// two values as N bf16 terms each: word i holds term i of both
-template <int N> __device__ __forceinline__ void split(float a, float b, uint32_t (&w)[N])
+// Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. The clock is read once
+// in a while only, since the warps that wait share their scheduler with those that work, and the code is kept out of the
+// loops for the sake of the instruction caches.
+__device__ __noinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        w[i] = pack_bf16(a, b);
-        if (i + 1 < N) {
-            a -= low_bf16(w[i]);
-            b -= high_bf16(w[i]);
+    bool done = mbar_try_wait(bar, parity & 1u);
+    for (long long t0 = 0; !done;) {
+#pragma unroll 1
+        for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(bar, parity & 1u);
+        if (done) break;
+        const long long t = clock64();
+        if (!t0) t0 = t;
+        if (*(volatile int *)&B->abort_flag) break;
+        if (t - t0 > B->limit) {
+            *(volatile int *)&B->abort_flag = 1;
+            raise_flag(B->err, GDN_DEVERR_TIMEOUT);
+            break;
         }
     }
+    return __all_sync(kAll, done);
 }
 
-// YB, ZB: blocks of 64 columns of x and y, of z. OUT: outputs (else the state a segment ends with from zero).
+// YB, ZB: blocks of 64 columns of x and y, of z. NS: bf16 terms of the state. OUT: outputs (else the state a segment ends with from zero).
 template <int YB, int ZB, int NS, bool OUT>
 __global__ void __launch_bounds__(kThreadsChunk, 1)
-    linear_chunk_kernel(const __grid_constant__ LinearLaunch P, const __grid_constant__ LinearSweep p, const int wide)
+    linear_chunk_kernel(const __grid_constant__ LinearLaunch P, const __grid_constant__ LinearSweep p,
+                        const __grid_constant__ ChunkMaps maps, const int wide)
 {
     using M = Smem<NS>;
-    constexpr int kSlots = M::kSlots;
     constexpr int YP = 64 * YB, ZP = 64 * ZB;
+    constexpr int NP = NS == 1 ? 1 : 2;               // terms of P
     constexpr int TILES = OUT ? 3 : 2;                // x, y, z (x only with outputs)
     constexpr int YI = OUT ? 1 : 0, ZI = OUT ? 2 : 1;
     extern __shared__ __align__(1024) unsigned char sm[];
     Bars &B = *reinterpret_cast<Bars *>(sm + M::kBars);
     const uint32_t sbase = smem_u32(sm);
-    float2(*decays)[kRows] = reinterpret_cast<float2(*)[kRows]>(sm + M::kDecays);
+    Decays &decays = *reinterpret_cast<Decays *>(sm + M::kDecays);
     uint8_t(*first_bad)[kRows] = reinterpret_cast<uint8_t(*)[kRows]>(sm + M::kBad);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hv = blockIdx.y;
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&B.decays[i], 32), mbar_init(&B.decays_free[i], OUT ? 384 : 256), mbar_init(&B.z_ok[i], 32);
-        mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.y_free, 1), mbar_init(&B.update, 1);
-        mbar_init(&B.p_ready, 128), mbar_init(&B.out_read, 128), mbar_init(&B.y_ready, 256), mbar_init(&B.state_ready, 256);
-        mbar_init(&B.done, 1);
+        for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 4);
+        mbar_init(&B.decays, 32), mbar_init(&B.decays_free, OUT ? 384 : 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.z_raw[i], 32), mbar_init(&B.z_ok[i], 32), mbar_init(&B.bad_read[i], 128);
+            mbar_init(&B.y_ready[i], 256), mbar_init(&B.y_free[i], 1);
+        }
+        mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.update, 1), mbar_init(&B.done, 1);
+        mbar_init(&B.p_ready, 128), mbar_init(&B.out_read, 128), mbar_init(&B.state_ready, 256);
         B.abort_flag = B.zero = B.bad[0] = B.bad[1] = 0;
+        B.limit = P.wait_limit > 0 ? P.wait_limit : kWaitLimit;
+        B.err = P.a.err_flags;
         fence_barrier_init();
     }
     if (warp == 13) {
@@ -141,6 +167,15 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     if (it.seq < 0 || (sbase & 1023u)) return;
     const bool whole = it.seq_end - it.seq_begin <= P.seg;
     if (!OUT && (whole || it.state < 0)) return;
+    const int n = it.n, chunks = (n + kRows - 1) / kRows;
+    if (it.state < 0) {                               // a bad state index: zeros
+        for (int e = tid; p.out && e < n * p.DZ; e += kThreadsChunk) {
+            const int64_t at = (int64_t)(it.begin + e / p.DZ) * p.out_stride + (int64_t)hv * p.out_head + e % p.DZ;
+            if (p.out_f32) static_cast<float *>(p.out)[at] = 0.f;
+            else static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(0.f);
+        }
+        return;
+    }
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&B.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -149,67 +184,63 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     __syncthreads();
     tcl_fence_after();
     const uint32_t tmem = B.tmem;
-    const int n = it.n, chunks = (n + kRows - 1) / kRows;
-    const int64_t first = p.reverse ? it.begin + n - 1 : it.begin;
-    const int dir = p.reverse ? -1 : 1;
-    const bool skip = it.state < 0;
-    const long long limit = P.wait_limit > 0 ? P.wait_limit : kWaitLimit;
-    volatile int *abort_flag = &B.abort_flag;
     bool ok = true;
-    const auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait_warp(bar, parity & 1u, abort_flag, limit)) {
-            ok = false;
-            *abort_flag = 1;
-            if (lane == 0) raise_flag(P.a.err_flags, GDN_DEVERR_TIMEOUT);
-        }
-        return ok;
-    };
-    const size_t state_at = ((size_t)(skip ? 0 : it.state) * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &B); };
+    const size_t state_at = ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     const size_t item_at = ((size_t)blockIdx.x * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
 
     if (warp >= 14) {
         // ---------------------------------------------------------------- copies
         const int t = tid - 14 * 32;
-        const bf16 *src[3] = {static_cast<const bf16 *>(OUT ? p.x : p.y) + (int64_t)(hv / (OUT ? p.x_group : p.y_group)) * (OUT ? p.x_head : p.y_head),
-                              static_cast<const bf16 *>(OUT ? p.y : p.z) + (int64_t)(hv / (OUT ? p.y_group : p.z_group)) * (OUT ? p.y_head : p.z_head),
-                              static_cast<const bf16 *>(p.z) + (int64_t)(hv / p.z_group) * p.z_head};
-        const int64_t stride[3] = {OUT ? p.x_stride : p.y_stride, OUT ? p.y_stride : p.z_stride, p.z_stride};
-        int filled = 0;
+        const int hx = OUT ? hv / p.x_group : 0, hy = hv / p.y_group, hz = hv / p.z_group;
+        int issued = 0;
         for (int i = 0; i < chunks && ok; ++i) {
-            const int64_t at = first + (int64_t)dir * i * kRows;
-            const int rows = min(kRows, n - i * kRows);
-#pragma unroll
+            const int at = it.begin + kRows * (p.reverse ? chunks - 1 - i : i);
+#pragma unroll 1
             for (int k = 0; k < TILES; ++k) {
                 const int m = i * TILES + k, slot = m % kSlots;
+                const int which = k + 3 - TILES;      // 0: x, 1: y, 2: z
+                const bool tma = wide >> which & 1;
+                if (tma && warp != 14) continue;
                 if (m >= kSlots && !wait(&B.empty[slot], m / kSlots - 1)) break;
                 const uint32_t dst = sbase + slot * kTile;
-                if (k == ZI) load_tile<ZB>(dst, src[k], stride[k], at, dir, rows, p.DZ, wide & 4, t);
-                else load_tile<YB>(dst, src[k], stride[k], at, dir, rows, p.DY, wide & (OUT && k == 0 ? 1 : 2), t);
-                cp_async_commit();
-                if (m > 0) {                          // the tile before has landed: hand it on
-                    cp_async_wait<1>();
+                if (tma) {
+                    if (lane == 0) {
+                        const CUtensorMap *map = which == 0 ? &maps.x : which == 1 ? &maps.y : &maps.z;
+                        const int head = which == 0 ? hx : which == 1 ? hy : hz, blocks = which == 2 ? ZB : YB;
+                        mbar_arrive_expect_tx(&B.full[slot], blocks * kBlock);
+                        mbar_arrive_n(&B.full[slot], kLoaders - 1);
+                        for (int c = 0; c < blocks; ++c) tma_rows(dst + c * kBlock, map, 64 * c, head, at, &B.full[slot]);
+                    }
+                    __syncwarp();
+                } else {
+                    const int rows = min(kRows, it.begin + n - at);
+                    if (which == 2)
+                        load_tile<ZB>(dst, static_cast<const bf16 *>(p.z) + hz * p.z_head + at * p.z_stride, p.z_stride, rows, p.DZ, t);
+                    else if (which == 1)
+                        load_tile<YB>(dst, static_cast<const bf16 *>(p.y) + hy * p.y_head + at * p.y_stride, p.y_stride, rows, p.DY, t);
+                    else
+                        load_tile<YB>(dst, static_cast<const bf16 *>(p.x) + hx * p.x_head + at * p.x_stride, p.x_stride, rows, p.DY, t);
                     fence_proxy_async();
-                    mbar_arrive(&B.full[(m - 1) % kSlots]);
+                    mbar_arrive(&B.full[slot]);
                 }
-                filled = m + 1;
+                issued = m + 1;
             }
         }
-        cp_async_wait<0>();
-        if (ok && filled) {
-            fence_proxy_async();
-            mbar_arrive(&B.full[(filled - 1) % kSlots]);
-        }
+        if (!ok && warp == 14)                        // copies in flight land before the CTA ends
+            for (int m = max(0, issued - kSlots); m < issued; ++m)
+                if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
     } else if (warp == 13) {
         // ---------------------------------------------------------------- decays; z's non-finite values
         double all = 0.0;
         for (int i = 0; i < chunks; ++i) {
-            const int b = i & 1;
-            if (i >= 2 && !wait(&B.decays_free[b], (i >> 1) - 1)) break;
+            const int b = i & 1, c = p.reverse ? chunks - 1 - i : i, at = it.begin + c * kRows, rows = min(kRows, n - c * kRows);
+            // lane l takes the rows 4 l .. 4 l + 3 in the sweep's order
             double s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = i * kRows + lane * 4 + j;
-                const double d = r < n ? linear_decay(P, hv, (int)first + dir * r, it.seq_end, p.reverse) : 0.0;
+                const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
+                const double d = r < rows ? linear_decay(P, hv, at + r, it.seq_end, p.reverse) : 0.0;
                 s[j] = j ? s[j - 1] + d : d;
             }
             double sum = s[3];
@@ -218,40 +249,67 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const double v = __shfl_up_sync(kAll, sum, o);
                 if (lane >= o) sum += v;
             }
-            const double before = lane ? __shfl_up_sync(kAll, sum, 1) : (__shfl_up_sync(kAll, sum, 1), 0.0);
+            double before = __shfl_up_sync(kAll, sum, 1);
+            if (lane == 0) before = 0.0;
+            all += __shfl_sync(kAll, sum, 31);
+            float hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // 1/256 steps and the rest: differences of the first are exact, of the second small
-                const double G = before + s[j], hi = rint(G * 256.0) * (1.0 / 256.0);
-                decays[b][lane * 4 + j] = make_float2((float)hi, (float)(G - hi));
+                const double G = before + s[j], h = rint(G * 256.0) * (1.0 / 256.0);
+                hi[j] = (float)h;
+                lo[j] = (float)(G - h);
             }
-            all += __shfl_sync(kAll, sum, 31);
-            mbar_arrive(&B.decays[b]);
+            const float hi32 = __shfl_sync(kAll, hi[3], lane | 7), lo32 = __shfl_sync(kAll, lo[3], lane | 7);
+            const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
+            if (i > 0 && !wait(&B.decays_free, i - 1)) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
+                decays.nhi[r] = -hi[j];
+                decays.nlo[r] = -lo[j];
+                decays.col[r] = ex2(hi32 - hi[j]) * ex2(lo32 - lo[j]);
+                decays.weight[r] = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
+            }
+            mbar_arrive(&B.decays);
             const int m = i * TILES + ZI, slot = m % kSlots;
             if (!wait(&B.full[slot], m / kSlots)) break;
-            const uint4 *z = reinterpret_cast<const uint4 *>(sm + slot * kTile);
-            __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
-            const __nv_bfloat162 none = acc;
-#pragma unroll 8
+            uint4 *z = reinterpret_cast<uint4 *>(sm + slot * kTile);
+            const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
+            __nv_bfloat162 acc[4] = {none, none, none, none};
+#pragma unroll 4
             for (int e = lane; e < ZB * (int)kBlock / 16; e += 32) {
                 const uint4 v = z[e];
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), none, acc);
+                for (int j = 0; j < 4; ++j) acc[j] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), none, acc[j]);
             }
-            const bool bad = __any_sync(kAll, __hisnan(acc.x) || __hisnan(acc.y));
+            acc[0] = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+            const bool bad = __any_sync(kAll, __hisnan(acc[0].x) || __hisnan(acc[0].y));
+            if (bad && rows < kRows) {
+                // rows behind the sequence (or before it, none) are another's: zero
+                for (int e = lane; e < ZB * kRows * 8; e += 32)
+                    if ((e >> 3) % kRows >= rows) z[e] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+            }
+            __syncwarp();
+            mbar_arrive(&B.z_raw[b]);
+            if (!OUT) continue;
+            if (i >= 2 && !wait(&B.bad_read[b], (i >> 1) - 1)) break;
             if (bad) {
-                uint16_t *e = reinterpret_cast<uint16_t *>(sm + slot * kTile);
-                for (int c = lane; c < ZP; c += 32) {
+                // the update has its NaN; the outputs' product takes zeros, and the column's first row is noted
+                if (!wait(&B.update, i)) break;
+                uint16_t *e = reinterpret_cast<uint16_t *>(z);
+                for (int k = lane; k < ZP; k += 32) {
                     int from = 255;
-                    for (int r = 0; r < kRows; ++r) {
-                        uint16_t &v = e[(c >> 6) * (kBlock / 2) + r * 64 + ((((c & 63) >> 3) ^ (r & 7)) << 3) + (c & 7)];
+                    for (int j = 0; j < rows; ++j) {
+                        const int r = p.reverse ? rows - 1 - j : j;
+                        uint16_t &v = e[(k >> 6) * (kBlock / 2) + r * 64 + ((((k & 63) >> 3) ^ (r & 7)) << 3) + (k & 7)];
                         if ((v & 0x7F80) == 0x7F80) {
                             if (from == 255) from = r;
                             v = 0;
                         }
                     }
-                    first_bad[b][c] = (uint8_t)from;
+                    first_bad[b][k] = (uint8_t)from;
                 }
                 fence_proxy_async();
             }
@@ -263,17 +321,20 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     } else if (warp == 12) {
         // ---------------------------------------------------------------- MMAs
         constexpr uint32_t id_scores = tc_idesc(128, 128, false), id_z = tc_idesc(128, ZP, true);
+        const uint64_t state = tc_desc(sbase + M::kStates, YP * 128);
         for (int i = 0; i < chunks; ++i) {
             const int mx = i * TILES, my = mx + YI, mz = mx + ZI;
-            const uint32_t tx = sbase + (mx % kSlots) * kTile, ty = sbase + (my % kSlots) * kTile, tz = sbase + (mz % kSlots) * kTile;
+            const uint64_t tx = tc_desc(sbase + (mx % kSlots) * kTile, 16), ty = tc_desc(sbase + (my % kSlots) * kTile, 16);
+            const uint64_t tz = tc_desc(sbase + (mz % kSlots) * kTile, kBlock);
+            // (descriptors step in units of 16 bytes)
             if constexpr (OUT) {
                 if (!wait(&B.full[mx % kSlots], mx / kSlots) || !wait(&B.full[my % kSlots], my / kSlots)) break;
                 tcl_fence_after();
                 if (lane == 0) {
 #pragma unroll
                     for (int k = 0; k < YP / 16; ++k) {
-                        const uint32_t o = (k >> 2) * kBlock + (k & 3) * 32;
-                        tcl_mma_ss(tmem + kScores, tc_desc(tx + o, 16), tc_desc(ty + o, 16), id_scores, k > 0);
+                        const uint32_t o = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                        tcl_mma_ss(tmem + kScores, tx + o, ty + o, id_scores, k > 0);
                     }
                     tcl_commit(&B.scores);
                 }
@@ -284,52 +345,51 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll
                     for (int t = 0; t < NS; ++t)
 #pragma unroll
-                        for (int k = 0; k < YP / 16; ++k) {
-                            const uint32_t a = tx + (k >> 2) * kBlock + (k & 3) * 32, s = sbase + M::kStates + t * kTile + k * 2048;
-                            tcl_mma_ss(tmem + kOut, tc_desc(a, 16), tc_desc(s, YP * 128), id_z, t + k > 0);
-                        }
+                        for (int k = 0; k < YP / 16; ++k)
+                            tcl_mma_ss(tmem + kOut, tx + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), state + ((t * kTile + k * 2048) >> 4), id_z,
+                                       t + k > 0);
                     tcl_commit(&B.inter);
                 }
                 __syncwarp();
             }
-            if (!wait(&B.z_ok[i & 1], i >> 1)) break;
+            if (!wait(&B.z_raw[i & 1], i >> 1)) break;
             bool go = true;
+#pragma unroll 1
             for (int h = 0; h < 2 && go; ++h) {
-                go = wait(&B.y_ready, 2 * i + h);
+                go = wait(&B.y_ready[h], i);
                 if (!go) break;
                 tcl_fence_after();
                 if (lane == 0) {
+                    const uint32_t y = tmem + (!OUT && h ? kY2 : kY);
+                    const uint64_t z = tz + h * (8192 >> 4);
 #pragma unroll
                     for (int t = 0; t < 3; ++t)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t a = tmem + kY + (k >> 1) * 48 + t * 16 + (k & 1) * 8;
-                            tcl_mma_ts(tmem + kUpdate, a, tc_desc(tz + (4 * h + k) * 2048, kBlock), id_z, h + t + k > 0);
-                        }
-                    tcl_commit(&B.y_free);
+                        for (int k = 0; k < 4; ++k)
+                            tcl_mma_ts(tmem + kUpdate, y + k * 24 + t * 8, z + (k * 2048 >> 4), id_z, h > 0 || t + k > 0);
+                    tcl_commit(&B.y_free[h]);
                     if (h == 1) {
                         tcl_commit(&B.update);
-                        if (OUT) tcl_commit(&B.empty[mx % kSlots]);
-                        tcl_commit(&B.empty[my % kSlots]);
-                        if (!OUT) tcl_commit(&B.empty[mz % kSlots]);
+                        // (four arrivals free a tile: z's, with outputs, come from the warps that use its memory last)
+                        for (int m = OUT ? mx : my; m <= (OUT ? my : mz); ++m) {
+                            mbar_arrive_n(&B.empty[m % kSlots], 3);
+                            tcl_commit(&B.empty[m % kSlots]);
+                        }
                     }
                 }
                 __syncwarp();
             }
             if (!go) break;
             if constexpr (OUT) {
-                if (!wait(&B.p_ready, i)) break;
+                if (!wait(&B.z_ok[i & 1], i >> 1) || !wait(&B.p_ready, i)) break;
                 tcl_fence_after();
                 if (lane == 0) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int t = 0; t < NP; ++t)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t a = tmem + kScores + (k >> 1) * 32 + t * 16 + (k & 1) * 8;
-                            tcl_mma_ts(tmem + kOut, a, tc_desc(tz + k * 2048, kBlock), id_z, true);
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            tcl_mma_ts(tmem + kOut, tmem + kScores + k * 16 + t * 8, tz + (k * 2048 >> 4), id_z, true);
                     tcl_commit(&B.out);
-                    tcl_commit(&B.empty[mz % kSlots]);
                 }
                 __syncwarp();
             }
@@ -347,22 +407,26 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         constexpr int ZC = ZP / 2;
         const bool active = (warp & 3) * 32 < YP;     // (YP = 64: lanes 64 .. 127 of Y are zero)
         const float z_inv = 1.f / p.z_scale;
-        float S[ZC];
+        const int sy = (int)p.sy, sz = (int)p.sz;
+        f2 S[ZC / 2];
         {
             const float *from = nullptr;
-            if (OUT && !skip) {
+            if (OUT) {
                 if (!whole) from = P.local + item_at;
                 else if (p.start) from = p.start + state_at;
             }
+            const int left = from && y < p.DY ? p.DZ - half * ZC : 0;             // columns there are to load
+            from += y * sy + half * ZC * sz;
 #pragma unroll
-            for (int c = 0; c < ZC; ++c) {
-                const int z = half * ZC + c;
-                S[c] = from && y < p.DY && z < p.DZ ? from[y * p.sy + z * p.sz] * z_inv : 0.f;
-            }
+            for (int c = 0; c < ZC / 2; ++c)
+                S[c] = pair(2 * c < left ? from[2 * c * sz] * z_inv : 0.f, 2 * c + 1 < left ? from[(2 * c + 1) * sz] * z_inv : 0.f);
         }
         if (!active) {
-            uint32_t zero[16] = {};
-            for (int k = 0; k < 3; ++k) tcl_st16(tmem + lanes + kY + half * 48 + k * 16, zero);
+            uint32_t zero[8] = {};
+            for (int k = 0; k < 6; ++k) {
+                tcl_st8(tmem + lanes + kY + half * 48 + k * 8, zero);
+                if (!OUT) tcl_st8(tmem + lanes + kY2 + half * 48 + k * 8, zero);
+            }
             tcl_wait_st();
         }
         const auto put_state = [&]() {
@@ -371,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             for (int c = 0; c < ZC; c += 8) {
                 uint32_t w[4][NS];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) split<NS>(S[c + 2 * j], S[c + 2 * j + 1], w[j]);
+                for (int j = 0; j < 4; ++j) split<NS>(S[c / 2 + j], w[j]);
                 const int z = half * ZC + c;
                 const uint32_t to = sbase + M::kStates + (z >> 6) * (YP * 128) + y * 128 + ((((z & 63) >> 3) ^ (y & 7)) << 4);
 #pragma unroll
@@ -385,61 +449,90 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             mbar_arrive(&B.state_ready);
         }
         for (int i = 0; i < chunks; ++i) {
-            const int b = i & 1, m = i * TILES + YI, slot = m % kSlots;
-            if (!wait(&B.decays[b], i >> 1) || !wait(&B.full[slot], m / kSlots)) break;
-            const float2 end = decays[b][kRows - 1];
+            const int m = i * TILES + YI, slot = m % kSlots;
+            const int c0 = p.reverse ? chunks - 1 - i : i, at = it.begin + c0 * kRows;
+            const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 128);
+            if (!wait(&B.decays, i) || !wait(&B.full[slot], m / kSlots)) break;
+            if (OUT && p.chunk_dot) {
+                // the product of this state's gradient, as it reaches the chunk's last row, and the state behind that row
+                float d = 0.f;
+                const int next = at + min(kRows, n - c0 * kRows);
+                if (active) {
+#pragma unroll
+                    for (int c = 0; c < ZC / 2; ++c) {
+                        const float2 v = unpair(S[c]);
+                        d = fmaf(v.x, p.chunk_states[chunk + 512 * c], fmaf(v.y, p.chunk_states[chunk + 512 * c + 256], d));
+                    }
+                    d *= exp2_wide(linear_decay(P, hv, next - 1, it.seq_end, 1)) * p.z_scale;
+                }
+                d = group_sum<32>(d);
+                if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 4] = d;
+            }
+            const int last = p.reverse ? 0 : kRows - 1;
+            const float decay = ex2(-decays.nhi[last]) * ex2(-decays.nlo[last]);
+            const int rows = min(kRows, n - c0 * kRows);
             bool go = true;
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                const int s0 = 64 * h + 32 * half;
-                const float2 d = decays[b][s0 + lane];
-                const float weight = ex2(end.x - d.x) * ex2(end.y - d.y);
-                if (2 * i + h > 0 && !wait(&B.y_free, 2 * i + h - 1)) {
+                // the half before has been used (without outputs: the same one, a chunk before)
+                const bool used = OUT ? (2 * i + h == 0 || wait(&B.y_free[h ^ 1], h ? i : i - 1)) : (i == 0 || wait(&B.y_free[h], i - 1));
+                if (!used) {
                     go = false;
                     break;
                 }
                 tcl_fence_after();
                 if (active) {
-                    const uint16_t *ty = reinterpret_cast<const uint16_t *>(sm + slot * kTile + (y >> 6) * kBlock);
-                    uint32_t w[3][16];
+                    const uint16_t *ty = reinterpret_cast<const uint16_t *>(sm + slot * kTile + (y >> 6) * kBlock) + (y & 7);
+                    const int yc = (y & 63) >> 3;
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        const int s0 = 64 * h + 32 * half + 16 * k;              // 16 tokens: one step of the product
+                        uint32_t w[3][8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float v[2];
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&decays.weight[s0 + 4 * j]);
+                            uint32_t raw[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int s = s0 + 2 * j + e;
-                            const uint32_t raw = ty[s * 64 + ((((y & 63) >> 3) ^ (s & 7)) << 3) + (y & 7)];
-                            v[e] = __uint_as_float(raw << 16) * __shfl_sync(kAll, weight, 2 * j + e);
+                            for (int e = 0; e < 4; ++e) {
+                                const int s = s0 + 4 * j + e;
+                                raw[e] = ty[s * 64 + ((yc ^ ((4 * j + e) & 7)) << 3)];
+                                raw[e] = s < rows ? raw[e] << 16 : 0;          // rows behind belong to no one or another sequence
+                            }
+                            uint32_t t[3];
+                            split<3>(mul2(pair(raw[0], raw[1]), pair(f.x, f.y)), t);
+                            w[0][2 * j] = t[0], w[1][2 * j] = t[1], w[2][2 * j] = t[2];
+                            split<3>(mul2(pair(raw[2], raw[3]), pair(f.z, f.w)), t);
+                            w[0][2 * j + 1] = t[0], w[1][2 * j + 1] = t[1], w[2][2 * j + 1] = t[2];
                         }
-                        uint32_t t[3];
-                        split<3>(v[0], v[1], t);
-                        w[0][j] = t[0], w[1][j] = t[1], w[2][j] = t[2];
-                    }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) tcl_st16(tmem + lanes + kY + half * 48 + k * 16, w[k]);
+                        for (int t = 0; t < 3; ++t) tcl_st8(tmem + lanes + (!OUT && h ? kY2 : kY) + (2 * half + k) * 24 + t * 8, w[t]);
+                    }
                     tcl_wait_st();
                 }
                 tcl_fence_before();
-                mbar_arrive(&B.y_ready);
+                mbar_arrive(&B.y_ready[h]);
             }
+            mbar_arrive(&B.decays_free);
             if (!go || !wait(&B.update, i)) break;
             tcl_fence_after();
-            const float decay = ex2(end.x) * ex2(end.y);
-            const bool bad = *(volatile int *)&B.bad[b];
             if (active) {
+                const f2 decay2 = pair(decay, decay);
 #pragma unroll
-                for (int c = 0; c < ZC; c += 32) {
-                    float u[32];
-                    tcl_ld32(tmem + lanes + kUpdate + half * ZC + c, u);
+                for (int c = 0; c < ZC; c += 16) {
+                    uint32_t u[16];
+                    tcl_ld16(tmem + lanes + kUpdate + half * ZC + c, u);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) S[c + j] = fmaf(S[c + j], decay, u[j]);
-                    if (bad)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (first_bad[b][half * ZC + c + j] < kRows) S[c + j] = __int_as_float(0x7fc00000);
+                    for (int j = 0; j < 8; ++j) S[c / 2 + j] = fma2(S[c / 2 + j], decay2, pair(u[2 * j], u[2 * j + 1]));
                 }
+                if (OUT && p.chunk_states && !p.chunk_dot)
+#pragma unroll
+                    for (int c = 0; c < ZC / 2; ++c) {
+                        const float2 v = unpair(S[c]);
+                        p.chunk_states[chunk + 512 * c] = v.x;
+                        p.chunk_states[chunk + 512 * c + 256] = v.y;
+                    }
             }
             tcl_fence_before();
-            mbar_arrive(&B.decays_free[b]);
             if (OUT && i + 1 < chunks) {
                 if (!wait(&B.inter, i)) break;        // the product with the state before has read it
                 put_state();
@@ -450,152 +543,220 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const bool ends = p.reverse ? it.index == 0 : it.begin + n == it.seq_end;
         float *to = nullptr;
         if (!OUT) to = P.local + item_at;
-        else if (ends && !skip && p.end) to = p.end + state_at;
+        else if (ends && p.end) to = p.end + state_at;
         if (ok && to) {
             const float pass = OUT && p.reverse && it.seq_end > it.seq_begin ? exp2_wide(linear_log2(P.a.g[it.seq_begin * P.a.g_stride + hv])) : 1.f;
             const float f = pass * p.z_scale;
+            const int left = y < p.DY ? p.DZ - half * ZC : 0;
+            to += y * sy + half * ZC * sz;
 #pragma unroll
-            for (int c = 0; c < ZC; ++c) {
-                const int z = half * ZC + c;
-                if (y < p.DY && z < p.DZ) to[y * p.sy + z * p.sz] = S[c] * f;
+            for (int c = 0; c < ZC / 2; ++c) {
+                const float2 v = unpair(S[c]);
+                if (2 * c < left) to[2 * c * sz] = v.x * f;
+                if (2 * c + 1 < left) to[(2 * c + 1) * sz] = v.y * f;
             }
-        }
-        if (OUT && p.with_end && ends) {
-            float d = 0.f;
-            if (!skip) {
-                const float *w = p.with_end + state_at;
-#pragma unroll
-                for (int c = 0; c < ZC; ++c) {
-                    const int z = half * ZC + c;
-                    if (y < p.DY && z < p.DZ) d = fmaf(S[c] * p.z_scale, w[y * p.sy + z * p.sz], d);
-                }
-            }
-            d = group_sum<32>(d);
-            if (lane == 0) B.sums[warp - 4] = d;
         }
     } else if constexpr (OUT) {
         // ---------------------------------------------------------------- P, inter's decays, outputs
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         const int r = tid;
         const float f = p.x_scale * p.z_scale;
+        constexpr int CH = 2 * ZP / 16;               // 16-byte chunks of an output row in bf16
         for (int i = 0; i < chunks; ++i) {
-            const int b = i & 1;
-            if (!wait(&B.decays[b], i >> 1)) break;
-            const float2 G = decays[b][r];
+            const int b = i & 1, c0 = p.reverse ? chunks - 1 - i : i, rows = min(kRows, n - c0 * kRows);
+            if (!wait(&B.decays, i)) break;
+            const float hi = -decays.nhi[r], lo = -decays.nlo[r];
+            const float er = ex2(hi) * ex2(lo);
             if (!wait(&B.scores, i)) break;
             tcl_fence_after();
+            // Sixteen columns s at a time, over which P's two terms are laid. In the row's own 32 the decay is taken for each
+            // element, and the columns it does not see (s > r; backwards s < r and rows behind the sequence) are zero; the
+            // columns of other 32s have theirs as a factor of the column times one of the row.
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w[32] = {};
-                if (c <= warp) {
-                    float v[32];
-                    tcl_ld32(tmem + lanes + kScores + c * 32, v);
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t at = tmem + lanes + kScores + c * 16;
+                uint32_t w[16];
+                if (p.reverse ? (c >> 1) < warp : (c >> 1) > warp) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int s = c * 32 + 2 * j;
-                        const float4 d = *reinterpret_cast<const float4 *>(&decays[b][s]);
-                        const float p0 = s <= r ? v[2 * j] * ex2((G.x - d.x) + (G.y - d.y)) : 0.f;
-                        const float p1 = s + 1 <= r ? v[2 * j + 1] * ex2((G.x - d.z) + (G.y - d.w)) : 0.f;
-                        uint32_t t[2];
-                        split<2>(p0, p1, t);
-                        w[j] = t[0], w[16 + j] = t[1];
+                    for (int j = 0; j < 16; ++j) w[j] = 0;
+                } else {
+                    uint32_t v[16];
+                    tcl_ld16(at, v);
+                    f2 q[8];
+                    if ((c >> 1) == warp || (p.reverse && rows < c * 16 + 16)) {
+                        const int from = p.reverse ? r : 0, to = p.reverse ? rows : r + 1;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int s = c * 16 + 2 * j;
+                            const f2 d = add2(add2(pair(hi, hi), *reinterpret_cast<const f2 *>(&decays.nhi[s])),
+                                              add2(pair(lo, lo), *reinterpret_cast<const f2 *>(&decays.nlo[s])));
+                            const float2 e = unpair(d);
+                            const float p0 = __uint_as_float(v[2 * j]) * ex2(e.x), p1 = __uint_as_float(v[2 * j + 1]) * ex2(e.y);
+                            q[j] = pair(s >= from && s < to ? p0 : 0.f, s + 1 >= from && s + 1 < to ? p1 : 0.f);
+                        }
+                    } else {
+                        const int end = p.reverse ? (c >> 1) * 32 : (c >> 1) * 32 + 31;
+                        const float f = ex2(hi + decays.nhi[end]) * ex2(lo + decays.nlo[end]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            q[j] = mul2(pair(v[2 * j], v[2 * j + 1]),
+                                        mul2(*reinterpret_cast<const f2 *>(&decays.col[c * 16 + 2 * j]), pair(f, f)));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t t[NP];
+                        split<NP>(q[j], t);
+                        w[j] = t[0], w[8 + j] = NP > 1 ? t[NP - 1] : 0;
                     }
                 }
-                tcl_st32(tmem + lanes + kScores + c * 32, w);
+                if constexpr (NP > 1) {
+                    tcl_st16(at, w);
+                } else {
+                    const uint32_t w8[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+                    tcl_st8(at, w8);
+                }
             }
-            const float er = ex2(G.x) * ex2(G.y);
+            mbar_arrive(&B.decays_free);
             if (!wait(&B.inter, i)) break;
             tcl_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < ZP; c += 32) {
-                float v[32];
-                tcl_ld32(tmem + lanes + kOut + c, v);
-                uint32_t w[32];
+            for (int c = 0; c < ZP; c += 16) {
+                uint32_t v[16];
+                tcl_ld16(tmem + lanes + kOut + c, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] * er);
-                tcl_st32(tmem + lanes + kOut + c, w);
+                for (int j = 0; j < 8; ++j) {
+                    const float2 q = unpair(mul2(pair(v[2 * j], v[2 * j + 1]), pair(er, er)));
+                    v[2 * j] = __float_as_uint(q.x), v[2 * j + 1] = __float_as_uint(q.y);
+                }
+                tcl_st16(tmem + lanes + kOut + c, v);
             }
             tcl_wait_st();
             tcl_fence_before();
             mbar_arrive(&B.p_ready);
             if (!wait(&B.out, i)) break;
             tcl_fence_after();
+            // The products have read z's tile; its memory takes this warp's 32 output rows, so that global memory is
+            // written (and dot_with read) in whole rows. Row q's chunk c lies at q * 2 ZP + ((c ^ (q & 7)) << 4).
+            const int slot = (i * TILES + ZI) % kSlots;
+            unsigned char *stage = sm + slot * kTile + warp * (64 * ZP);
+            const int row0 = 32 * warp, mine = min(32, rows - row0);         // rows of this warp there are
+            const int64_t t0 = it.begin + c0 * kRows + row0;
             const bool bad = *(volatile int *)&B.bad[b];
-            const bool mine = i * kRows + r < n;
-            const int64_t t = first + (int64_t)dir * (i * kRows + r);
-            const bf16 *with = p.dot && mine ? static_cast<const bf16 *>(p.dot_with) + t * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head : nullptr;
+            if (p.dot) {
+                const bf16 *with = static_cast<const bf16 *>(p.dot_with) + t0 * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head;
+                for (int e = lane; e < 32 * CH; e += 32) {
+                    const int q = e / CH, c = e % CH;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (q < mine) {
+                        if (wide & 8) {
+                            if (c * 8 < p.DZ) v = *reinterpret_cast<const uint4 *>(with + q * p.dot_stride + c * 8);
+                        } else {
+                            uint16_t h[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                h[k] = c * 8 + k < p.DZ ? reinterpret_cast<const uint16_t *>(with)[q * p.dot_stride + c * 8 + k] : 0;
+                            v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(stage + q * (2 * ZP) + ((c ^ (q & 7)) << 4)) = v;
+                }
+                __syncwarp();
+            }
             float dot = 0.f;
+            if (bad) {
+                // columns whose z is not finite from a row on: NaN from there
 #pragma unroll 1
-            for (int c = 0; c < ZP; c += 32) {
-                float v[32];
-                tcl_ld32(tmem + lanes + kOut + c, v);
-                if (c + 32 >= ZP) {
+                for (int c = 0; c < ZP; ++c) {
+                    const int fb = first_bad[b][c];
+                    if (fb == 255) continue;          // the same in every lane
+                    uint32_t v;
+                    const uint32_t at = tmem + lanes + kOut + c;
+                    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(v) : "r"(at) : "memory");
+                    if (p.reverse ? r <= fb : r >= fb) v = 0x7fc00000u;
+                    __syncwarp();
+                    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(at), "r"(v) : "memory");
+                }
+            }
+            const uint32_t row = lane * (2 * ZP);
+#pragma unroll 1
+            for (int c = 0; c < ZP; c += 16) {
+                uint32_t u[16];
+                tcl_ld16(tmem + lanes + kOut + c, u);
+                if (c + 16 >= ZP) {
                     tcl_fence_before();
                     mbar_arrive(&B.out_read);
                 }
-                if (mine) {
+                f2 v[8];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = skip ? 0.f : v[j] * f;
-                    if (bad)
+                for (int j = 0; j < 8; ++j) v[j] = mul2(pair(u[2 * j], u[2 * j + 1]), pair(f, f));
+                uint4 *at[2] = {reinterpret_cast<uint4 *>(stage + row + (((c >> 3) ^ (lane & 7)) << 4)),
+                                reinterpret_cast<uint4 *>(stage + row + (((c >> 3) + 1 ^ (lane & 7)) << 4))};
+                if (p.dot) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (first_bad[b][c + j] <= r && !skip) v[j] = __int_as_float(0x7fc00000);
-                    const int left = p.DZ - c;            // columns there are
-                    if (with) {
-                        if ((wide & 8) && left >= 32) {
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 q = *at[j];
+                        const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                const uint4 q = *reinterpret_cast<const uint4 *>(with + c + j);
-                                const uint32_t e[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) dot = fmaf(v[j + 2 * k], low_bf16(e[k]), fmaf(v[j + 2 * k + 1], high_bf16(e[k]), dot));
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j < left) dot = fmaf(v[j], to_f32(with[c + j]), dot);
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 o = unpair(v[4 * j + k]);
+                            dot = fmaf(o.x, low_bf16(e[k]), fmaf(o.y, high_bf16(e[k]), dot));
                         }
                     }
-                    if (p.out) {
-                        const int64_t to = t * p.out_stride + (int64_t)hv * p.out_head + c;
-                        if (p.out_f32) {
-                            float *o = static_cast<float *>(p.out) + to;
-                            if ((wide & 16) && left >= 32) {
+                }
+                if (!p.out) continue;
+                if (!p.out_f32) {
 #pragma unroll
-                                for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4 *>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                            } else {
+                    for (int j = 0; j < 2; ++j)
+                        *at[j] = make_uint4(pack_bf16(v[4 * j]), pack_bf16(v[4 * j + 1]), pack_bf16(v[4 * j + 2]), pack_bf16(v[4 * j + 3]));
+                    continue;
+                }
+                if (lane < mine) {
+                    float *o = static_cast<float *>(p.out) + (t0 + lane) * p.out_stride + (int64_t)hv * p.out_head + c;
+                    const int left = p.DZ - c;
+                    if ((wide & 16) && left >= 16) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (j < left) o[j] = v[j];
-                            }
-                        } else {
-                            bf16 *o = static_cast<bf16 *>(p.out) + to;
-                            if ((wide & 16) && left >= 32) {
+                        for (int j = 0; j < 8; j += 2) {
+                            const float2 e = unpair(v[j]), g = unpair(v[j + 1]);
+                            *reinterpret_cast<float4 *>(o + 2 * j) = make_float4(e.x, e.y, g.x, g.y);
+                        }
+                    } else {
 #pragma unroll
-                                for (int j = 0; j < 32; j += 8)
-                                    *reinterpret_cast<uint4 *>(o + j) = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                                                                                   pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (j < left) o[j] = __float2bfloat16_rn(v[j]);
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 e = unpair(v[j]);
+                            if (2 * j < left) o[2 * j] = e.x;
+                            if (2 * j + 1 < left) o[2 * j + 1] = e.y;
                         }
                     }
                 }
                 __syncwarp();
             }
-            mbar_arrive(&B.decays_free[b]);
-            if (with) p.dot[t * P.a.HV + hv] = dot;
+            if (p.out && !p.out_f32) {
+                __syncwarp();
+                bf16 *o = static_cast<bf16 *>(p.out) + t0 * p.out_stride + (int64_t)hv * p.out_head;
+                if ((wide & 16) && p.DZ % 8 == 0) {
+#pragma unroll 4
+                    for (int e = lane; e < 32 * CH; e += 32) {
+                        const int q = e / CH, c = e % CH;
+                        if (q < mine && c * 8 < p.DZ)
+                            *reinterpret_cast<uint4 *>(o + q * p.out_stride + c * 8) =
+                                *reinterpret_cast<const uint4 *>(stage + q * (2 * ZP) + ((c ^ (q & 7)) << 4));
+                    }
+                } else {
+                    for (int q = 0; q < mine; ++q)
+                        for (int c = lane; c < p.DZ; c += 32)
+                            o[q * p.out_stride + c] =
+                                *reinterpret_cast<const bf16 *>(stage + q * (2 * ZP) + (((c >> 3) ^ (q & 7)) << 4) + (c & 7) * 2);
+                }
+            }
+            if (p.dot && lane < mine) p.dot[(t0 + lane) * P.a.HV + hv] = dot;
+            mbar_arrive(&B.bad_read[b]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.empty[slot]);
         }
     }
     tcl_fence_before();
     __syncthreads();
-    if (OUT && p.with_end && tid == 0 && (p.reverse ? it.index == 0 : it.begin + n == it.seq_end)) {
-        float s = 0.f;
-        for (int w = 0; w < 8; ++w) s += B.sums[w];
-        p.end_dot[(size_t)it.seq * P.a.HV + hv] = s;
-    }
     if (warp == 12) {
         tcl_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -605,7 +766,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 constexpr int kMaxDevices = 64;
 
 template <int YB, int ZB, int NS, bool OUT>
-int launch(const LinearLaunch &P, const LinearSweep &p, int wide, cudaStream_t stream)
+int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, int wide, cudaStream_t stream)
 {
     const auto kernel = linear_chunk_kernel<YB, ZB, NS, OUT>;
     static std::mutex lock;
@@ -619,15 +780,18 @@ int launch(const LinearLaunch &P, const LinearSweep &p, int wide, cudaStream_t s
             raised[dev] = true;
         }
     }
-    kernel<<<dim3((unsigned)P.items, (unsigned)P.a.HV), kThreadsChunk, Smem<NS>::kBytes, stream>>>(P, p, wide);
+    kernel<<<dim3((unsigned)P.items, (unsigned)P.a.HV), kThreadsChunk, Smem<NS>::kBytes, stream>>>(P, p, maps, wide);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSweep &p, bool outputs, int wide, cudaStream_t stream)
+template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSweep &p, bool outputs, const ChunkMaps &maps, int wide, cudaStream_t stream)
 {
-    if (!outputs) return launch<YB, ZB, 2, false>(P, p, wide, stream);
-    // what dg is summed from keeps the state whole
-    return p.dot ? launch<YB, ZB, 3, true>(P, p, wide, stream) : launch<YB, ZB, 2, true>(P, p, wide, stream);
+    if (!outputs) return launch<YB, ZB, 2, false>(P, p, maps, wide, stream);
+    // Terms of the state and of P: one for bf16 outputs (their error against 64 bits grows by at most the square root of
+    // two: each of P, the state and the output is rounded once to bf16), two for fp32 outputs; what dg is summed from keeps the
+    // state whole.
+    if (!p.dot && !p.exact) return launch<YB, ZB, 1, true>(P, p, maps, wide, stream);
+    return p.dot ? launch<YB, ZB, 3, true>(P, p, maps, wide, stream) : launch<YB, ZB, 2, true>(P, p, maps, wide, stream);
 }
 
 }  // namespace
@@ -638,13 +802,16 @@ int launch_linear_chunk(const LinearLaunch &P, const LinearSweep &p, bool output
         return q && reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0 && head * es % 16 == 0 && n * es % 16 == 0;
     };
     int wide = 0;
-    if (wide_rows(p.x, p.x_stride, p.x_head, p.DY, 2)) wide |= 1;
-    if (wide_rows(p.y, p.y_stride, p.y_head, p.DY, 2)) wide |= 2;
-    if (wide_rows(p.z, p.z_stride, p.z_head, p.DZ, 2)) wide |= 4;
+    ChunkMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const int HV = P.a.HV;
+    if (outputs && encode_head_rows(&maps.x, p.x, P.a.T, HV / p.x_group, p.DY, p.x_stride, p.x_head, kRows)) wide |= 1;
+    if (encode_head_rows(&maps.y, p.y, P.a.T, HV / p.y_group, p.DY, p.y_stride, p.y_head, kRows)) wide |= 2;
+    if (encode_head_rows(&maps.z, p.z, P.a.T, HV / p.z_group, p.DZ, p.z_stride, p.z_head, kRows)) wide |= 4;
     if (wide_rows(p.dot_with, p.dot_stride, p.dot_head, p.DZ, 2)) wide |= 8;
     if (wide_rows(p.out, p.out_stride, p.out_head, 8, p.out_f32 ? 4 : 2)) wide |= 16;
-    if (p.DY <= 64) return p.DZ <= 64 ? launch_size<1, 1>(P, p, outputs, wide, stream) : launch_size<1, 2>(P, p, outputs, wide, stream);
-    return p.DZ <= 64 ? launch_size<2, 1>(P, p, outputs, wide, stream) : launch_size<2, 2>(P, p, outputs, wide, stream);
+    if (p.DY <= 64) return p.DZ <= 64 ? launch_size<1, 1>(P, p, outputs, maps, wide, stream) : launch_size<1, 2>(P, p, outputs, maps, wide, stream);
+    return p.DZ <= 64 ? launch_size<2, 1>(P, p, outputs, maps, wide, stream) : launch_size<2, 2>(P, p, outputs, maps, wide, stream);
 }
 
 }  // namespace gdn

@@ -25,6 +25,7 @@ struct LinearSweep {
     int64_t sy, sz;                    // strides of the state's memory [V, K] along y and z
     const float *start;                // [num_states, HV, V, K] states to start from, or null: zero
     float *end;                        // [num_states, HV, V, K] states to end with, or null
+    // of the fp32 kernel:
     const float *with_end;             // [num_states, HV, V, K] or null: its product with the end state goes to
     float *end_dot;                    // [S, HV, parts of z]
     // of the tensor-core kernel:
@@ -32,6 +33,11 @@ struct LinearSweep {
     const void *dot_with;
     int64_t dot_stride, dot_head;
     int dot_group;
+    int exact;                         // outputs to more than bf16
+    // for dg, per chunk (chunk c of sequence s: its first row / 128 + s) and value head:
+    float *chunk_states;               // [chunks, HV, 128 x 64 or 128] the state behind it, in the kernel's own order
+    float *chunk_dot;                  // [chunks, HV, 8]: given, chunk_states is read, and the parts of its product with
+                                       // the state the sweep comes with are written
 };
 
 struct LinearLaunch {
@@ -75,5 +81,9 @@ int launch_linear_fold(const LinearLaunch &P, const LinearFold &f, cudaStream_t 
 size_t linear_dg_part_floats(int S, int HV);
 int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, const float *end_dot, int parts, float *dg,
                      int64_t dg_stride, float *part, cudaStream_t stream);
+
+// The same from products per token and chunk (chunk_dot), of the tensor-core kernel.
+int launch_linear_dg_chunks(const LinearLaunch &P, const float *qdq, const float *kdk, const float *chunk_dot, float *dg,
+                            int64_t dg_stride, float *part, cudaStream_t stream);
 
 }  // namespace gdn
