@@ -61,11 +61,18 @@ void plan(LinearLaunch &P, bool uniform, bool backward)
     const gdn_linear_args &a = P.a;
     P.Ls = uniform ? a.T / a.S : 0;
     P.tc = a.in_dtype == GDN_BF16;
+    const int64_t longest = uniform ? P.Ls : a.T;
     if (P.tc) {
-        // one CTA an SM; whole chunks
-        int64_t seg = ((int64_t)a.T * a.HV + 2 * kSms - 1) / (2 * kSms);
-        seg = (seg + kLinearChunk - 1) / kLinearChunk * kLinearChunk;
-        if (seg < 2 * kLinearChunk) seg = 2 * kLinearChunk;
+        // One CTA an SM, whole chunks. Sequences are cut where they are too few to fill the SMs; a cut sequence's keys and
+        // values are read twice.
+        int64_t seg = longest;
+        if ((int64_t)a.S * a.HV < kSms || !uniform) {
+            const int64_t ctas = (int64_t)a.T * a.HV;
+            seg = (ctas + 2 * kSms - 1) / (2 * kSms);
+            if (!uniform) seg = (ctas + kSms - 1) / kSms;
+            seg = (seg + kLinearChunk - 1) / kLinearChunk * kLinearChunk;
+            if (seg < 2 * kLinearChunk) seg = 2 * kLinearChunk;
+        }
         set_segments(P, uniform, seg);
         return;
     }

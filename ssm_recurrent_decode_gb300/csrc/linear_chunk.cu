@@ -13,14 +13,18 @@
 // tensor memory is a row y of it, the columns z are shared by two warpgroups), a product's sum is added to it in fp32
 // once a chunk. Two terms keep 16 bits of what leads to a token's bf16 output; the update's three keep all 24.
 //
-// One CTA owns a segment of a sequence and a value head. Warps 0-3: P, inter's decays and the outputs (a thread a row
-// r); warps 4-7 and 8-11: Y and the state; 12: issues the MMAs; 13: decays, and z's non-finite values; 14:
-// copies x, y and z by TMA into a ring of 32 KB tiles (with 15, by plain loads, what is not aligned to 16 bytes). A tile may end
-// in another sequence's rows: their y's weigh nothing, their scores are not looked at, their outputs are not written.
+// One CTA owns a segment of a sequence and a value head. Its 24 warps are groups of four, which take turns on a chunk so that
+// each one's latencies are covered by the others' work:
+//   0, 1   P, blocks of 32 columns in turn; then a quarter of Y each     2   inter's decays and the outputs (a thread a row r)
+//   3, 4   a quarter of Y each; the state                               5   a warp each: MMAs of scores, inter and out; MMAs of
+//          the update; decays and z's non-finite values; copies of x, y and z by TMA into a ring of 32 KB tiles (by plain
+//          loads what is not aligned to 16 bytes)
+// A tile may end in another sequence's rows: their y's weigh nothing, their scores are not looked at, their outputs are not
+// written.
 //
-// A product with a zero of P would carry a later token's NaN to earlier ones; warp 13 looks z's tile over (one
-// multiply-add a pair), and in the rare tile that has a non-finite value sets it to zero, notes the column's first
-// such row, and the outputs and the state get their NaN from there.
+// A product with a zero of P would carry a later token's NaN to earlier ones; z's tile is looked over (one multiply-add a
+// pair), and in the rare tile that has a non-finite value the outputs' product takes it as zero, the column's first such
+// row is noted, and the outputs get their NaN from there.
 //
 // Every wait is bounded; a wait that gives up raises GDN_DEVERR_TIMEOUT and ends the CTA, its MMAs and copies done.
 #include <cstring>
@@ -38,16 +42,25 @@ namespace {
 constexpr int kRows = 128;                            // tokens per chunk
 constexpr uint32_t kBlock = 16384;                    // 128 rows of 64 columns
 constexpr uint32_t kTile = 2 * kBlock;
-constexpr int kThreadsChunk = 512;
-constexpr int kLoaders = 64;
+constexpr int kThreadsChunk = 768;
+constexpr int kLoaders = 32;
+// Registers a thread: 80 at launch; the groups that hold the state take more of them, the others give some up
+// (2 x 128 + 4 x 56 = 6 x 80 for each of 128 threads). All four warps of a group execute the same of the two.
+constexpr int kStateRegisters = 128, kOtherRegisters = 56;
+static_assert(2 * kStateRegisters + 4 * kOtherRegisters <= 6 * 80, "more registers than the CTA has");
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters)); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters)); }
 constexpr long long kWaitLimit = 1LL << 31;           // SM clock cycles, about one second
 
 // columns of tensor memory
-constexpr uint32_t kScores = 0, kOut = 128, kUpdate = 256, kY = 384, kY2 = 0;    // (kY2: without outputs)
+constexpr uint32_t kScores = 0, kOut = 128, kUpdate = 256, kY = 384;
+// Y: 48 columns for 32 tokens (16 tokens: three terms of eight columns); two buffers behind the others, two more where there are
+// no outputs
+__host__ __device__ constexpr uint32_t y_column(bool outputs, int buffer) { return outputs || buffer < 2 ? kY + 48 * buffer : 48 * (buffer - 2); }
 
-constexpr int kSlots = 4;                             // tiles of x, y and z in shared memory
+constexpr int kMostSlots = 7;
 
-// what warp 13 says of a chunk's rows; G: sum of the log decays up to and with the row in the sweep's order, as a
+// what the decays' warp says of a chunk's rows; G: sum of the log decays up to and with the row in the sweep's order, as a
 // power of two, hi + lo with hi in steps of 1/256 (differences of hi are exact, lo is small)
 struct Decays {
     float nhi[kRows], nlo[kRows];                     // -hi, -lo
@@ -55,13 +68,14 @@ struct Decays {
     float weight[kRows];                              // e^{(G at the chunk's end) - G}; 0 for rows behind the sequence
 };
 
-template <int NS> struct Smem {                       // NS: bf16 terms of the state
+template <int NS> struct Smem {                       // NS: bf16 terms of the state (0: no outputs)
+    static constexpr int kSlots = 7 - NS;             // tiles of x, y and z: what the state leaves
     static constexpr uint32_t kStates = kSlots * kTile;
     static constexpr uint32_t kDecays = kStates + NS * kTile;
     static constexpr uint32_t kBad = kDecays + sizeof(Decays);        // uint8 [2][128]: first non-finite row of a column of z
     static constexpr uint32_t kBars = kBad + 2 * kRows;
     static constexpr uint32_t kBytes = kBars + 512;
-    static_assert(kBytes <= 232448, "more than an SM's shared memory");
+    static_assert(kSlots <= kMostSlots && kBytes <= 232448, "more than an SM's shared memory");
 };
 
 struct ChunkMaps {
@@ -69,16 +83,15 @@ struct ChunkMaps {
 };
 
 struct Bars {
-    uint64_t full[kSlots], empty[kSlots];             // tiles
+    uint64_t full[kMostSlots], empty[kMostSlots];     // tiles
     uint64_t decays, decays_free;
-    uint64_t z_raw[2], z_ok[2], bad_read[2];          // z's tile may be used for the update; for the outputs; first_bad was read
-    uint64_t y_ready[2], y_free[2];                   // the halves of Y
-    uint64_t scores, p_ready, inter, out, out_read, update, state_ready, done;
+    uint64_t z_raw[4], z_ok[2], bad_read[2];          // z's tile may be used for the update; for the outputs; first_bad was read
+    uint64_t y_ready[4], y_free[4];                   // quarters of Y: written; used
+    uint64_t scores, p_ready, inter, out, out_read, update[2], update_read, state_ready, done[2];
     LinearItem item;
     uint32_t tmem;
     int abort_flag, zero, bad[2];
     long long limit;
-    int32_t *err;
 };
 static_assert(sizeof(Bars) <= 512, "");
 
@@ -103,35 +116,63 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t
     }
 }
 
-// Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. The clock is read once
-// in a while only, since the warps that wait share their scheduler with those that work, and the code is kept out of the
-// loops for the sake of the instruction caches.
-__device__ __noinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B)
+// Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. The clock and the flag are
+// looked at once in a while only, since the warps that wait share their scheduler with those that work.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B)
 {
     bool done = mbar_try_wait(bar, parity & 1u);
-    for (long long t0 = 0; !done;) {
-#pragma unroll 1
-        for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(bar, parity & 1u);
-        if (done) break;
-        const long long t = clock64();
-        if (!t0) t0 = t;
-        if (*(volatile int *)&B->abort_flag) break;
-        if (t - t0 > B->limit) {
-            *(volatile int *)&B->abort_flag = 1;
-            raise_flag(B->err, GDN_DEVERR_TIMEOUT);
-            break;
+    if (!__all_sync(kAll, done)) {
+        const long long t0 = clock64();
+        for (uint32_t i = 1; !done; ++i) {
+            done = mbar_try_wait(bar, parity & 1u);
+            if ((i & 63) == 0 && !done && (*(volatile int *)&B->abort_flag || clock64() - t0 > B->limit)) break;
         }
+        done = __all_sync(kAll, done);
+        if (!done) *(volatile int *)&B->abort_flag = 1;
     }
-    return __all_sync(kAll, done);
+    return done;
 }
 
-// YB, ZB: blocks of 64 columns of x and y, of z. NS: bf16 terms of the state. OUT: outputs (else the state a segment ends with from zero).
-template <int YB, int ZB, int NS, bool OUT>
+// 32 tokens of Y, from row s0 of y's tile, into the buffer at taddr: lane y of tensor memory takes column y.
+__device__ __forceinline__ void make_y(const unsigned char *tile, int y, int s0, int rows, const Decays &decays, uint32_t taddr)
+{
+    const uint16_t *ty = reinterpret_cast<const uint16_t *>(tile + (y >> 6) * kBlock) + (y & 7);
+    const int yc = (y & 63) >> 3;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k, s0 += 16) {           // 16 tokens: one step of the product
+        uint32_t w[3][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 f = *reinterpret_cast<const float4 *>(&decays.weight[s0 + 4 * j]);
+            uint32_t raw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int s = s0 + 4 * j + e;
+                raw[e] = ty[s * 64 + ((yc ^ ((4 * j + e) & 7)) << 3)];
+                raw[e] = s < rows ? raw[e] << 16 : 0;              // rows behind belong to no one or another sequence
+            }
+            uint32_t t[3];
+            split<3>(mul2(pair(raw[0], raw[1]), pair(f.x, f.y)), t);
+            w[0][2 * j] = t[0], w[1][2 * j] = t[1], w[2][2 * j] = t[2];
+            split<3>(mul2(pair(raw[2], raw[3]), pair(f.z, f.w)), t);
+            w[0][2 * j + 1] = t[0], w[1][2 * j + 1] = t[1], w[2][2 * j + 1] = t[2];
+        }
+#pragma unroll
+        for (int t = 0; t < 3; ++t) tcl_st8(taddr + k * 24 + t * 8, w[t]);
+    }
+    tcl_wait_st();
+}
+
+// YB, ZB: blocks of 64 columns of x and y, of z. NS: bf16 terms of the state; 0: no outputs, only the state a segment ends
+// with from zero.
+template <int YB, int ZB, int NS>
 __global__ void __launch_bounds__(kThreadsChunk, 1)
     linear_chunk_kernel(const __grid_constant__ LinearLaunch P, const __grid_constant__ LinearSweep p,
                         const __grid_constant__ ChunkMaps maps, const int wide)
 {
     using M = Smem<NS>;
+    constexpr bool OUT = NS > 0;
+    constexpr int kSlots = M::kSlots;
     constexpr int YP = 64 * YB, ZP = 64 * ZB;
     constexpr int NP = NS == 1 ? 1 : 2;               // terms of P
     constexpr int TILES = OUT ? 3 : 2;                // x, y, z (x only with outputs)
@@ -145,20 +186,17 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     const int hv = blockIdx.y;
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 4);
-        mbar_init(&B.decays, 32), mbar_init(&B.decays_free, OUT ? 384 : 256);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&B.z_raw[i], 32), mbar_init(&B.z_ok[i], 32), mbar_init(&B.bad_read[i], 128);
-            mbar_init(&B.y_ready[i], 256), mbar_init(&B.y_free[i], 1);
-        }
-        mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.update, 1), mbar_init(&B.done, 1);
-        mbar_init(&B.p_ready, 128), mbar_init(&B.out_read, 128), mbar_init(&B.state_ready, 256);
+        for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 6);
+        mbar_init(&B.decays, 32), mbar_init(&B.decays_free, OUT ? 640 : 512);
+        for (int i = 0; i < 2; ++i) mbar_init(&B.z_ok[i], 32), mbar_init(&B.bad_read[i], 128), mbar_init(&B.done[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&B.y_ready[i], 128), mbar_init(&B.y_free[i], 1), mbar_init(&B.z_raw[i], 32);
+        mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.update[0], 1), mbar_init(&B.update[1], 1);
+        mbar_init(&B.p_ready, 384), mbar_init(&B.out_read, 128), mbar_init(&B.state_ready, 256), mbar_init(&B.update_read, 256);
         B.abort_flag = B.zero = B.bad[0] = B.bad[1] = 0;
         B.limit = P.wait_limit > 0 ? P.wait_limit : kWaitLimit;
-        B.err = P.a.err_flags;
         fence_barrier_init();
     }
-    if (warp == 13) {
+    if (warp == 22) {
         const LinearItem it = linear_item(P, blockIdx.x, OUT && hv == 0);
         if (lane == 0) B.item = it;
     }
@@ -176,7 +214,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         }
         return;
     }
-    if (warp == 12) {
+    if (warp == 20) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&B.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -184,150 +222,161 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     __syncthreads();
     tcl_fence_after();
     const uint32_t tmem = B.tmem;
+    if (YB == 1 && warp < 4 && warp >= 2) {           // lanes 64 .. 127 of Y are zero
+        const uint32_t zero[16] = {};
+        for (int b = 0; b < (OUT ? 2 : 4); ++b)
+            for (int k = 0; k < 48; k += 16) tcl_st16(tmem + ((uint32_t)(32 * warp) << 16) + y_column(OUT, b) + k, zero);
+        tcl_wait_st();
+    }
+    if (YB == 1) {
+        tcl_fence_before();
+        __syncthreads();
+        tcl_fence_after();
+    }
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &B); };
     const size_t state_at = ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     const size_t item_at = ((size_t)blockIdx.x * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
 
-    if (warp >= 14) {
-        // ---------------------------------------------------------------- copies
-        const int t = tid - 14 * 32;
-        const int hx = OUT ? hv / p.x_group : 0, hy = hv / p.y_group, hz = hv / p.z_group;
-        int issued = 0;
-        for (int i = 0; i < chunks && ok; ++i) {
-            const int at = it.begin + kRows * (p.reverse ? chunks - 1 - i : i);
+    if (warp >= 20) {
+        give_registers();
+        if (warp == 23) {
+            // ---------------------------------------------------------------- copies
+            const int hx = OUT ? hv / p.x_group : 0, hy = hv / p.y_group, hz = hv / p.z_group;
+            int issued = 0;
+            for (int i = 0; i < chunks && ok; ++i) {
+                const int at = it.begin + kRows * (p.reverse ? chunks - 1 - i : i);
 #pragma unroll 1
-            for (int k = 0; k < TILES; ++k) {
-                const int m = i * TILES + k, slot = m % kSlots;
-                const int which = k + 3 - TILES;      // 0: x, 1: y, 2: z
-                const bool tma = wide >> which & 1;
-                if (tma && warp != 14) continue;
-                if (m >= kSlots && !wait(&B.empty[slot], m / kSlots - 1)) break;
-                const uint32_t dst = sbase + slot * kTile;
-                if (tma) {
-                    if (lane == 0) {
-                        const CUtensorMap *map = which == 0 ? &maps.x : which == 1 ? &maps.y : &maps.z;
-                        const int head = which == 0 ? hx : which == 1 ? hy : hz, blocks = which == 2 ? ZB : YB;
-                        mbar_arrive_expect_tx(&B.full[slot], blocks * kBlock);
-                        mbar_arrive_n(&B.full[slot], kLoaders - 1);
-                        for (int c = 0; c < blocks; ++c) tma_rows(dst + c * kBlock, map, 64 * c, head, at, &B.full[slot]);
-                    }
-                    __syncwarp();
-                } else {
-                    const int rows = min(kRows, it.begin + n - at);
-                    if (which == 2)
-                        load_tile<ZB>(dst, static_cast<const bf16 *>(p.z) + hz * p.z_head + at * p.z_stride, p.z_stride, rows, p.DZ, t);
-                    else if (which == 1)
-                        load_tile<YB>(dst, static_cast<const bf16 *>(p.y) + hy * p.y_head + at * p.y_stride, p.y_stride, rows, p.DY, t);
-                    else
-                        load_tile<YB>(dst, static_cast<const bf16 *>(p.x) + hx * p.x_head + at * p.x_stride, p.x_stride, rows, p.DY, t);
-                    fence_proxy_async();
-                    mbar_arrive(&B.full[slot]);
-                }
-                issued = m + 1;
-            }
-        }
-        if (!ok && warp == 14)                        // copies in flight land before the CTA ends
-            for (int m = max(0, issued - kSlots); m < issued; ++m)
-                if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
-    } else if (warp == 13) {
-        // ---------------------------------------------------------------- decays; z's non-finite values
-        double all = 0.0;
-        for (int i = 0; i < chunks; ++i) {
-            const int b = i & 1, c = p.reverse ? chunks - 1 - i : i, at = it.begin + c * kRows, rows = min(kRows, n - c * kRows);
-            // lane l takes the rows 4 l .. 4 l + 3 in the sweep's order
-            double s[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
-                const double d = r < rows ? linear_decay(P, hv, at + r, it.seq_end, p.reverse) : 0.0;
-                s[j] = j ? s[j - 1] + d : d;
-            }
-            double sum = s[3];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(kAll, sum, o);
-                if (lane >= o) sum += v;
-            }
-            double before = __shfl_up_sync(kAll, sum, 1);
-            if (lane == 0) before = 0.0;
-            all += __shfl_sync(kAll, sum, 31);
-            float hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const double G = before + s[j], h = rint(G * 256.0) * (1.0 / 256.0);
-                hi[j] = (float)h;
-                lo[j] = (float)(G - h);
-            }
-            const float hi32 = __shfl_sync(kAll, hi[3], lane | 7), lo32 = __shfl_sync(kAll, lo[3], lane | 7);
-            const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
-            if (i > 0 && !wait(&B.decays_free, i - 1)) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
-                decays.nhi[r] = -hi[j];
-                decays.nlo[r] = -lo[j];
-                decays.col[r] = ex2(hi32 - hi[j]) * ex2(lo32 - lo[j]);
-                decays.weight[r] = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
-            }
-            mbar_arrive(&B.decays);
-            const int m = i * TILES + ZI, slot = m % kSlots;
-            if (!wait(&B.full[slot], m / kSlots)) break;
-            uint4 *z = reinterpret_cast<uint4 *>(sm + slot * kTile);
-            const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
-            __nv_bfloat162 acc[4] = {none, none, none, none};
-#pragma unroll 4
-            for (int e = lane; e < ZB * (int)kBlock / 16; e += 32) {
-                const uint4 v = z[e];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), none, acc[j]);
-            }
-            acc[0] = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
-            const bool bad = __any_sync(kAll, __hisnan(acc[0].x) || __hisnan(acc[0].y));
-            if (bad && rows < kRows) {
-                // rows behind the sequence (or before it, none) are another's: zero
-                for (int e = lane; e < ZB * kRows * 8; e += 32)
-                    if ((e >> 3) % kRows >= rows) z[e] = make_uint4(0, 0, 0, 0);
-                fence_proxy_async();
-            }
-            __syncwarp();
-            mbar_arrive(&B.z_raw[b]);
-            if (!OUT) continue;
-            if (i >= 2 && !wait(&B.bad_read[b], (i >> 1) - 1)) break;
-            if (bad) {
-                // the update has its NaN; the outputs' product takes zeros, and the column's first row is noted
-                if (!wait(&B.update, i)) break;
-                uint16_t *e = reinterpret_cast<uint16_t *>(z);
-                for (int k = lane; k < ZP; k += 32) {
-                    int from = 255;
-                    for (int j = 0; j < rows; ++j) {
-                        const int r = p.reverse ? rows - 1 - j : j;
-                        uint16_t &v = e[(k >> 6) * (kBlock / 2) + r * 64 + ((((k & 63) >> 3) ^ (r & 7)) << 3) + (k & 7)];
-                        if ((v & 0x7F80) == 0x7F80) {
-                            if (from == 255) from = r;
-                            v = 0;
+                for (int k = 0; k < TILES; ++k) {
+                    const int m = i * TILES + k, slot = m % kSlots;
+                    const int which = k + 3 - TILES;      // 0: x, 1: y, 2: z
+                    const bool tma = wide >> which & 1;
+                    if (m >= kSlots && !wait(&B.empty[slot], m / kSlots - 1)) break;
+                    const uint32_t dst = sbase + slot * kTile;
+                    if (tma) {
+                        if (lane == 0) {
+                            const CUtensorMap *map = which == 0 ? &maps.x : which == 1 ? &maps.y : &maps.z;
+                            const int head = which == 0 ? hx : which == 1 ? hy : hz, blocks = which == 2 ? ZB : YB;
+                            mbar_arrive_expect_tx(&B.full[slot], blocks * kBlock);
+                            mbar_arrive_n(&B.full[slot], kLoaders - 1);
+                            for (int c = 0; c < blocks; ++c) tma_rows(dst + c * kBlock, map, 64 * c, head, at, &B.full[slot]);
                         }
+                        __syncwarp();
+                    } else {
+                        const int rows = min(kRows, it.begin + n - at);
+                        if (which == 2)
+                            load_tile<ZB>(dst, static_cast<const bf16 *>(p.z) + hz * p.z_head + at * p.z_stride, p.z_stride, rows, p.DZ, lane);
+                        else if (which == 1)
+                            load_tile<YB>(dst, static_cast<const bf16 *>(p.y) + hy * p.y_head + at * p.y_stride, p.y_stride, rows, p.DY, lane);
+                        else
+                            load_tile<YB>(dst, static_cast<const bf16 *>(p.x) + hx * p.x_head + at * p.x_stride, p.x_stride, rows, p.DY, lane);
+                        fence_proxy_async();
+                        mbar_arrive(&B.full[slot]);
                     }
-                    first_bad[b][k] = (uint8_t)from;
+                    issued = m + 1;
                 }
-                fence_proxy_async();
             }
-            if (lane == 0) B.bad[b] = bad;
-            __syncwarp();
-            mbar_arrive(&B.z_ok[b]);
-        }
-        if (!OUT && lane == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = (float)all;
-    } else if (warp == 12) {
-        // ---------------------------------------------------------------- MMAs
-        constexpr uint32_t id_scores = tc_idesc(128, 128, false), id_z = tc_idesc(128, ZP, true);
-        const uint64_t state = tc_desc(sbase + M::kStates, YP * 128);
-        for (int i = 0; i < chunks; ++i) {
-            const int mx = i * TILES, my = mx + YI, mz = mx + ZI;
-            const uint64_t tx = tc_desc(sbase + (mx % kSlots) * kTile, 16), ty = tc_desc(sbase + (my % kSlots) * kTile, 16);
-            const uint64_t tz = tc_desc(sbase + (mz % kSlots) * kTile, kBlock);
-            // (descriptors step in units of 16 bytes)
-            if constexpr (OUT) {
+            if (!ok)                                      // copies in flight land before the CTA ends
+                for (int m = max(0, issued - kSlots); m < issued; ++m)
+                    if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
+        } else if (warp == 22) {
+            // ---------------------------------------------------------------- decays; z's non-finite values
+            double all = 0.0;
+            for (int i = 0; i < chunks; ++i) {
+                const int c = p.reverse ? chunks - 1 - i : i, at = it.begin + c * kRows, rows = min(kRows, n - c * kRows);
+                // lane l takes the rows 4 l .. 4 l + 3 in the sweep's order
+                double s[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
+                    const double d = r < rows ? linear_decay(P, hv, at + r, it.seq_end, p.reverse) : 0.0;
+                    s[j] = j ? s[j - 1] + d : d;
+                }
+                double sum = s[3];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double v = __shfl_up_sync(kAll, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                double before = __shfl_up_sync(kAll, sum, 1);
+                if (lane == 0) before = 0.0;
+                all += __shfl_sync(kAll, sum, 31);
+                float hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const double G = before + s[j], h = rint(G * 256.0) * (1.0 / 256.0);
+                    hi[j] = (float)h;
+                    lo[j] = (float)(G - h);
+                }
+                const float hi32 = __shfl_sync(kAll, hi[3], lane | 7), lo32 = __shfl_sync(kAll, lo[3], lane | 7);
+                const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
+                if (i > 0 && !wait(&B.decays_free, i - 1)) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
+                    decays.nhi[r] = -hi[j];
+                    decays.nlo[r] = -lo[j];
+                    decays.col[r] = ex2(hi32 - hi[j]) * ex2(lo32 - lo[j]);
+                    decays.weight[r] = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
+                }
+                mbar_arrive(&B.decays);
+                const int b = i & 1;
+                const int m = i * TILES + ZI, slot = m % kSlots;
+                if (!wait(&B.full[slot], m / kSlots)) break;
+                uint4 *z = reinterpret_cast<uint4 *>(sm + slot * kTile);
+                const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
+                __nv_bfloat162 acc[4] = {none, none, none, none};
+#pragma unroll 8
+                for (int e = lane; e < ZB * (int)kBlock / 16; e += 32) {
+                    const uint4 v = z[e];
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[j] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), none, acc[j]);
+                }
+                acc[0] = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+                const bool bad = __any_sync(kAll, __hisnan(acc[0].x) || __hisnan(acc[0].y));
+                if (bad && rows < kRows) {
+                    // rows behind the sequence (or before it, none) are another's: zero
+                    for (int e = lane; e < ZB * kRows * 8; e += 32)
+                        if ((e >> 3) % kRows >= rows) z[e] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();
+                }
+                __syncwarp();
+                mbar_arrive(&B.z_raw[i & 3]);
+                if (!OUT) continue;
+                if (i >= 2 && !wait(&B.bad_read[b], (i >> 1) - 1)) break;
+                if (bad) {
+                    // the update has its NaN; the outputs' product takes zeros, and the column's first row is noted
+                    if (!wait(&B.update[i & 1], i >> 1)) break;
+                    uint16_t *e = reinterpret_cast<uint16_t *>(z);
+                    for (int k = lane; k < ZP; k += 32) {
+                        int from = 255;
+                        for (int j = 0; j < rows; ++j) {
+                            const int r = p.reverse ? rows - 1 - j : j;
+                            uint16_t &v = e[(k >> 6) * (kBlock / 2) + r * 64 + ((((k & 63) >> 3) ^ (r & 7)) << 3) + (k & 7)];
+                            if ((v & 0x7F80) == 0x7F80) {
+                                if (from == 255) from = r;
+                                v = 0;
+                            }
+                        }
+                        first_bad[b][k] = (uint8_t)from;
+                    }
+                    fence_proxy_async();
+                }
+                if (lane == 0) B.bad[b] = bad;
+                __syncwarp();
+                mbar_arrive(&B.z_ok[b]);
+            }
+            if (!OUT && lane == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = (float)all;
+        } else if (warp == 20) {
+            // ---------------------------------------------------------------- MMAs: scores, inter, out
+            constexpr uint32_t id_scores = tc_idesc(128, 128, false), id_z = tc_idesc(128, ZP, true);
+            const uint64_t state = tc_desc(sbase + M::kStates, YP * 128);
+            for (int i = 0; OUT && i < chunks; ++i) {
+                const int mx = i * TILES, my = mx + YI, mz = mx + ZI;
+                const uint64_t tx = tc_desc(sbase + (mx % kSlots) * kTile, 16), ty = tc_desc(sbase + (my % kSlots) * kTile, 16);
+                const uint64_t tz = tc_desc(sbase + (mz % kSlots) * kTile, kBlock);
+                // (descriptors step in units of 16 bytes; six arrivals free a tile: those that no one else makes come from here)
                 if (!wait(&B.full[mx % kSlots], mx / kSlots) || !wait(&B.full[my % kSlots], my / kSlots)) break;
                 tcl_fence_after();
                 if (lane == 0) {
@@ -337,6 +386,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         tcl_mma_ss(tmem + kScores, tx + o, ty + o, id_scores, k > 0);
                     }
                     tcl_commit(&B.scores);
+                    tcl_commit(&B.empty[my % kSlots]);
                 }
                 __syncwarp();
                 if (!wait(&B.state_ready, i) || (i > 0 && !wait(&B.out_read, i - 1))) break;
@@ -349,38 +399,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                             tcl_mma_ss(tmem + kOut, tx + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), state + ((t * kTile + k * 2048) >> 4), id_z,
                                        t + k > 0);
                     tcl_commit(&B.inter);
+                    mbar_arrive_n(&B.empty[mx % kSlots], 5);
+                    tcl_commit(&B.empty[mx % kSlots]);
                 }
                 __syncwarp();
-            }
-            if (!wait(&B.z_raw[i & 1], i >> 1)) break;
-            bool go = true;
-#pragma unroll 1
-            for (int h = 0; h < 2 && go; ++h) {
-                go = wait(&B.y_ready[h], i);
-                if (!go) break;
-                tcl_fence_after();
-                if (lane == 0) {
-                    const uint32_t y = tmem + (!OUT && h ? kY2 : kY);
-                    const uint64_t z = tz + h * (8192 >> 4);
-#pragma unroll
-                    for (int t = 0; t < 3; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tcl_mma_ts(tmem + kUpdate, y + k * 24 + t * 8, z + (k * 2048 >> 4), id_z, h > 0 || t + k > 0);
-                    tcl_commit(&B.y_free[h]);
-                    if (h == 1) {
-                        tcl_commit(&B.update);
-                        // (four arrivals free a tile: z's, with outputs, come from the warps that use its memory last)
-                        for (int m = OUT ? mx : my; m <= (OUT ? my : mz); ++m) {
-                            mbar_arrive_n(&B.empty[m % kSlots], 3);
-                            tcl_commit(&B.empty[m % kSlots]);
-                        }
-                    }
-                }
-                __syncwarp();
-            }
-            if (!go) break;
-            if constexpr (OUT) {
                 if (!wait(&B.z_ok[i & 1], i >> 1) || !wait(&B.p_ready, i)) break;
                 tcl_fence_after();
                 if (lane == 0) {
@@ -393,16 +415,56 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 }
                 __syncwarp();
             }
+            // every MMA has completed before the tensor memory is freed
+            if (lane == 0) {
+                tcl_commit(&B.done[0]);
+                mbar_wait(&B.done[0], 0u, &B.zero, kWaitLimit);
+            }
+            __syncwarp();
+        } else if (warp == 21) {
+            // ---------------------------------------------------------------- MMAs: update
+            constexpr uint32_t id_z = tc_idesc(128, ZP, true);
+            for (int i = 0; i < chunks; ++i) {
+                const int my = i * TILES + YI, mz = i * TILES + ZI;
+                const uint64_t tz = tc_desc(sbase + (mz % kSlots) * kTile, kBlock);
+                if (!wait(&B.z_raw[i & 3], i >> 2) || (i > 0 && !wait(&B.update_read, i - 1))) break;
+                bool go = true;
+#pragma unroll 1
+                for (int u = 0; u < 4 && go; ++u) {       // 32 tokens each
+                        go = wait(&B.y_ready[u], i);
+                    if (!go) break;
+                    tcl_fence_after();
+                    if (lane == 0) {
+                        const uint32_t y = tmem + y_column(OUT, OUT ? u & 1 : u);
+                        const uint64_t z = tz + u * (4096 >> 4);
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                tcl_mma_ts(tmem + kUpdate, y + k * 24 + t * 8, z + (k * 2048 >> 4), id_z, u > 0 || t + k > 0);
+                        tcl_commit(&B.y_free[u]);
+                        if (u == 3) {
+                            tcl_commit(&B.update[i & 1]);
+                            mbar_arrive_n(&B.empty[my % kSlots], OUT ? 4 : 5);
+                            tcl_commit(&B.empty[my % kSlots]);
+                            mbar_arrive_n(&B.empty[mz % kSlots], OUT ? 1 : 5);
+                            tcl_commit(&B.empty[mz % kSlots]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!go) break;
+            }
+            if (lane == 0) {
+                tcl_commit(&B.done[1]);
+                mbar_wait(&B.done[1], 0u, &B.zero, kWaitLimit);
+            }
+            __syncwarp();
         }
-        // every MMA has completed before the tensor memory is freed
-        if (lane == 0) {
-            tcl_commit(&B.done);
-            mbar_wait(&B.done, 0u, &B.zero, kWaitLimit);
-        }
-        __syncwarp();
-    } else if (warp >= 4) {
-        // ---------------------------------------------------------------- Y and the state
-        const int half = warp >= 8, y = tid & 127;    // this thread's row of the state; columns half * ZP / 2 ..
+    } else if (warp >= 12) {
+        take_registers();
+        // ---------------------------------------------------------------- a quarter of Y; the state
+        const int half = warp >= 16, y = tid & 127;    // this thread's row of the state; columns half * ZP / 2 ..
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         constexpr int ZC = ZP / 2;
         const bool active = (warp & 3) * 32 < YP;     // (YP = 64: lanes 64 .. 127 of Y are zero)
@@ -421,21 +483,13 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             for (int c = 0; c < ZC / 2; ++c)
                 S[c] = pair(2 * c < left ? from[2 * c * sz] * z_inv : 0.f, 2 * c + 1 < left ? from[(2 * c + 1) * sz] * z_inv : 0.f);
         }
-        if (!active) {
-            uint32_t zero[8] = {};
-            for (int k = 0; k < 6; ++k) {
-                tcl_st8(tmem + lanes + kY + half * 48 + k * 8, zero);
-                if (!OUT) tcl_st8(tmem + lanes + kY2 + half * 48 + k * 8, zero);
-            }
-            tcl_wait_st();
-        }
         const auto put_state = [&]() {
             if (!active) return;
 #pragma unroll
             for (int c = 0; c < ZC; c += 8) {
-                uint32_t w[4][NS];
+                uint32_t w[4][NS > 0 ? NS : 1];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) split<NS>(S[c / 2 + j], w[j]);
+                for (int j = 0; j < 4; ++j) split(S[c / 2 + j], w[j]);
                 const int z = half * ZC + c;
                 const uint32_t to = sbase + M::kStates + (z >> 6) * (YP * 128) + y * 128 + ((((z & 63) >> 3) ^ (y & 7)) << 4);
 #pragma unroll
@@ -451,7 +505,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < chunks; ++i) {
             const int m = i * TILES + YI, slot = m % kSlots;
             const int c0 = p.reverse ? chunks - 1 - i : i, at = it.begin + c0 * kRows;
-            const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 128);
+            const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 384);
             if (!wait(&B.decays, i) || !wait(&B.full[slot], m / kSlots)) break;
             if (OUT && p.chunk_dot) {
                 // the product of this state's gradient, as it reaches the chunk's last row, and the state behind that row
@@ -466,54 +520,22 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     d *= exp2_wide(linear_decay(P, hv, next - 1, it.seq_end, 1)) * p.z_scale;
                 }
                 d = group_sum<32>(d);
-                if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 4] = d;
+                if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
             }
             const int last = p.reverse ? 0 : kRows - 1;
             const float decay = ex2(-decays.nhi[last]) * ex2(-decays.nlo[last]);
             const int rows = min(kRows, n - c0 * kRows);
-            bool go = true;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                // the half before has been used (without outputs: the same one, a chunk before)
-                const bool used = OUT ? (2 * i + h == 0 || wait(&B.y_free[h ^ 1], h ? i : i - 1)) : (i == 0 || wait(&B.y_free[h], i - 1));
-                if (!used) {
-                    go = false;
-                    break;
-                }
+            // (with outputs the buffer is that of the quarter two behind, a chunk before)
+            const int u = OUT ? half : 2 + half;
+            const bool go = i == 0 || wait(&B.y_free[2 + half], i - 1);
+            if (go) {
                 tcl_fence_after();
-                if (active) {
-                    const uint16_t *ty = reinterpret_cast<const uint16_t *>(sm + slot * kTile + (y >> 6) * kBlock) + (y & 7);
-                    const int yc = (y & 63) >> 3;
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        const int s0 = 64 * h + 32 * half + 16 * k;              // 16 tokens: one step of the product
-                        uint32_t w[3][8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&decays.weight[s0 + 4 * j]);
-                            uint32_t raw[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int s = s0 + 4 * j + e;
-                                raw[e] = ty[s * 64 + ((yc ^ ((4 * j + e) & 7)) << 3)];
-                                raw[e] = s < rows ? raw[e] << 16 : 0;          // rows behind belong to no one or another sequence
-                            }
-                            uint32_t t[3];
-                            split<3>(mul2(pair(raw[0], raw[1]), pair(f.x, f.y)), t);
-                            w[0][2 * j] = t[0], w[1][2 * j] = t[1], w[2][2 * j] = t[2];
-                            split<3>(mul2(pair(raw[2], raw[3]), pair(f.z, f.w)), t);
-                            w[0][2 * j + 1] = t[0], w[1][2 * j + 1] = t[1], w[2][2 * j + 1] = t[2];
-                        }
-#pragma unroll
-                        for (int t = 0; t < 3; ++t) tcl_st8(tmem + lanes + (!OUT && h ? kY2 : kY) + (2 * half + k) * 24 + t * 8, w[t]);
-                    }
-                    tcl_wait_st();
-                }
+                if (active) make_y(sm + slot * kTile, y, 32 * u, rows, decays, tmem + lanes + y_column(OUT, u));
                 tcl_fence_before();
-                mbar_arrive(&B.y_ready[h]);
+                mbar_arrive(&B.y_ready[u]);
             }
             mbar_arrive(&B.decays_free);
-            if (!go || !wait(&B.update, i)) break;
+            if (!go || !wait(&B.update[i & 1], i >> 1)) break;
             tcl_fence_after();
             if (active) {
                 const f2 decay2 = pair(decay, decay);
@@ -533,6 +555,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     }
             }
             tcl_fence_before();
+            mbar_arrive(&B.update_read);
             if (OUT && i + 1 < chunks) {
                 if (!wait(&B.inter, i)) break;        // the product with the state before has read it
                 put_state();
@@ -556,91 +579,152 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (2 * c + 1 < left) to[(2 * c + 1) * sz] = v.y * f;
             }
         }
-    } else if constexpr (OUT) {
-        // ---------------------------------------------------------------- P, inter's decays, outputs
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const int r = tid;
+    } else if (warp < 8) {
+        give_registers();
+        // ---------------------------------------------------------------- P; a quarter of Y
+        const int group = warp >> 2, quad = warp & 3, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        for (int i = 0; i < chunks; ++i) {
+            const int m = i * TILES + YI, slot = m % kSlots;
+            const int rows = min(kRows, n - kRows * (p.reverse ? chunks - 1 - i : i));
+            if (!wait(&B.decays, i)) break;
+            if constexpr (OUT) {
+                const float hi = -decays.nhi[r], lo = -decays.nlo[r];
+                if (!wait(&B.scores, i)) break;
+                tcl_fence_after();
+                // Blocks of 32 columns s, every other one, over which P's terms are laid (16 columns: eight of the first term,
+                // eight of the second). In the row's own 32 the decay is taken for each element, and the columns it does not
+                // see (s > r; backwards s < r and rows behind the sequence) are zero; the columns of other 32s have theirs as
+                // a factor of the column times one of the row.
+                const int from = p.reverse ? r : 0, to = p.reverse ? rows : r + 1;
+#pragma unroll 1
+                for (int c = group; c < 4; c += 2) {
+                    const bool none = p.reverse ? c < quad : c > quad;
+                    const bool each = c == quad || (p.reverse && rows < c * 32 + 32);
+                    float f = 0.f;
+                    if (!none && !each) {
+                        const int end = p.reverse ? c * 32 : c * 32 + 31;
+                        f = ex2(hi + decays.nhi[end]) * ex2(lo + decays.nlo[end]);
+                    }
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t at = tmem + lanes + kScores + c * 32 + h * 16;
+                        const int s0 = c * 32 + h * 16;
+                        uint32_t w[NP][8] = {};
+                        if (!none) {
+                            uint32_t v[16];
+                            tcl_ld16(at, v);
+                            if (each) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const int s = s0 + 2 * j;
+                                    const f2 d = add2(add2(pair(hi, hi), *reinterpret_cast<const f2 *>(&decays.nhi[s])),
+                                                      add2(pair(lo, lo), *reinterpret_cast<const f2 *>(&decays.nlo[s])));
+                                    const float2 e = unpair(d);
+                                    const float p0 = __uint_as_float(v[2 * j]) * ex2(e.x), p1 = __uint_as_float(v[2 * j + 1]) * ex2(e.y);
+                                    uint32_t t[NP];
+                                    split(pair(s >= from && s < to ? p0 : 0.f, s + 1 >= from && s + 1 < to ? p1 : 0.f), t);
+#pragma unroll
+                                    for (int k = 0; k < NP; ++k) w[k][j] = t[k];
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    uint32_t t[NP];
+                                    split(mul2(pair(v[2 * j], v[2 * j + 1]), mul2(*reinterpret_cast<const f2 *>(&decays.col[s0 + 2 * j]), pair(f, f))), t);
+#pragma unroll
+                                    for (int k = 0; k < NP; ++k) w[k][j] = t[k];
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) tcl_st8(at + k * 8, w[k]);
+                    }
+                }
+                tcl_wait_st();
+                tcl_fence_before();
+                mbar_arrive(&B.p_ready);
+            }
+            // (with outputs the buffer is the one of the quarter two before, which has been used)
+            const int u = OUT ? 2 + group : group, buffer = group;
+            if (!wait(&B.full[slot], m / kSlots)) break;
+            if (OUT ? !wait(&B.y_free[group], i) : i > 0 && !wait(&B.y_free[u], i - 1)) break;
+            tcl_fence_after();
+            if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays, tmem + lanes + y_column(OUT, buffer));
+            tcl_fence_before();
+            mbar_arrive(&B.y_ready[u]);
+            mbar_arrive(&B.decays_free);
+        }
+    } else {
+        give_registers();
+        if constexpr (OUT) {
+        // ---------------------------------------------------------------- inter's decays, outputs
+        const int quad = warp & 3, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         const float f = p.x_scale * p.z_scale;
         constexpr int CH = 2 * ZP / 16;               // 16-byte chunks of an output row in bf16
-        for (int i = 0; i < chunks; ++i) {
-            const int b = i & 1, c0 = p.reverse ? chunks - 1 - i : i, rows = min(kRows, n - c0 * kRows);
-            if (!wait(&B.decays, i)) break;
-            const float hi = -decays.nhi[r], lo = -decays.nlo[r];
-            const float er = ex2(hi) * ex2(lo);
-            if (!wait(&B.scores, i)) break;
-            tcl_fence_after();
-            // Sixteen columns s at a time, over which P's two terms are laid. In the row's own 32 the decay is taken for each
-            // element, and the columns it does not see (s > r; backwards s < r and rows behind the sequence) are zero; the
-            // columns of other 32s have theirs as a factor of the column times one of the row.
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t at = tmem + lanes + kScores + c * 16;
-                uint32_t w[16];
-                if (p.reverse ? (c >> 1) < warp : (c >> 1) > warp) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = 0;
-                } else {
-                    uint32_t v[16];
-                    tcl_ld16(at, v);
-                    f2 q[8];
-                    if ((c >> 1) == warp || (p.reverse && rows < c * 16 + 16)) {
-                        const int from = p.reverse ? r : 0, to = p.reverse ? rows : r + 1;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int s = c * 16 + 2 * j;
-                            const f2 d = add2(add2(pair(hi, hi), *reinterpret_cast<const f2 *>(&decays.nhi[s])),
-                                              add2(pair(lo, lo), *reinterpret_cast<const f2 *>(&decays.nlo[s])));
-                            const float2 e = unpair(d);
-                            const float p0 = __uint_as_float(v[2 * j]) * ex2(e.x), p1 = __uint_as_float(v[2 * j + 1]) * ex2(e.y);
-                            q[j] = pair(s >= from && s < to ? p0 : 0.f, s + 1 >= from && s + 1 < to ? p1 : 0.f);
-                        }
-                    } else {
-                        const int end = p.reverse ? (c >> 1) * 32 : (c >> 1) * 32 + 31;
-                        const float f = ex2(hi + decays.nhi[end]) * ex2(lo + decays.nlo[end]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            q[j] = mul2(pair(v[2 * j], v[2 * j + 1]),
-                                        mul2(*reinterpret_cast<const f2 *>(&decays.col[c * 16 + 2 * j]), pair(f, f)));
-                    }
+        // Chunk i's outputs are taken from tensor memory in turn i and written to global memory in turn i + 1, while its
+        // products run.
+        int slot = 0, mine = 0;
+        int64_t t0 = 0;
+        unsigned char *stage = sm;
+        for (int i = 0; i <= chunks; ++i) {
+            if (i < chunks) {
+                if (!wait(&B.decays, i)) break;
+                const float er = ex2(-decays.nhi[r]) * ex2(-decays.nlo[r]);
+                mbar_arrive(&B.decays_free);
+                if (!wait(&B.inter, i)) break;
+                tcl_fence_after();
+                const f2 er2 = pair(er, er);
+#pragma unroll 2
+                for (int c = 0; c < ZP; c += 16) {
+                    uint32_t u[16];
+                    tcl_ld16(tmem + lanes + kOut + c, u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        uint32_t t[NP];
-                        split<NP>(q[j], t);
-                        w[j] = t[0], w[8 + j] = NP > 1 ? t[NP - 1] : 0;
+                        const float2 q = unpair(mul2(pair(u[2 * j], u[2 * j + 1]), er2));
+                        u[2 * j] = __float_as_uint(q.x), u[2 * j + 1] = __float_as_uint(q.y);
+                    }
+                    tcl_st16(tmem + lanes + kOut + c, u);
+                }
+                tcl_wait_st();
+                tcl_fence_before();
+                mbar_arrive(&B.p_ready);
+            }
+            if (i > 0) {
+                // the outputs of the chunk before, as whole rows
+                if (p.out && !p.out_f32) {
+                    __syncwarp();
+                    bf16 *o = static_cast<bf16 *>(p.out) + t0 * p.out_stride + (int64_t)hv * p.out_head;
+                    if ((wide & 16) && p.DZ % 8 == 0) {
+#pragma unroll 4
+                        for (int e = lane; e < 32 * CH; e += 32) {
+                            const int q = e / CH, c = e % CH;
+                            if (q < mine && c * 8 < p.DZ)
+                                *reinterpret_cast<uint4 *>(o + q * p.out_stride + c * 8) =
+                                    *reinterpret_cast<const uint4 *>(stage + q * (2 * ZP) + ((c ^ (q & 7)) << 4));
+                        }
+                    } else {
+                        for (int q = 0; q < mine; ++q)
+                            for (int c = lane; c < p.DZ; c += 32)
+                                o[q * p.out_stride + c] =
+                                    *reinterpret_cast<const bf16 *>(stage + q * (2 * ZP) + (((c >> 3) ^ (q & 7)) << 4) + (c & 7) * 2);
                     }
                 }
-                if constexpr (NP > 1) {
-                    tcl_st16(at, w);
-                } else {
-                    const uint32_t w8[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
-                    tcl_st8(at, w8);
-                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.empty[slot]);
             }
-            mbar_arrive(&B.decays_free);
-            if (!wait(&B.inter, i)) break;
+            // (the update reads z's tile too)
+            if (i == chunks || !wait(&B.out, i) || !wait(&B.update[i & 1], i >> 1)) break;
             tcl_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < ZP; c += 16) {
-                uint32_t v[16];
-                tcl_ld16(tmem + lanes + kOut + c, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 q = unpair(mul2(pair(v[2 * j], v[2 * j + 1]), pair(er, er)));
-                    v[2 * j] = __float_as_uint(q.x), v[2 * j + 1] = __float_as_uint(q.y);
-                }
-                tcl_st16(tmem + lanes + kOut + c, v);
-            }
-            tcl_wait_st();
-            tcl_fence_before();
-            mbar_arrive(&B.p_ready);
-            if (!wait(&B.out, i)) break;
-            tcl_fence_after();
+            const int b = i & 1, c0 = p.reverse ? chunks - 1 - i : i, rows = min(kRows, n - c0 * kRows);
             // The products have read z's tile; its memory takes this warp's 32 output rows, so that global memory is
             // written (and dot_with read) in whole rows. Row q's chunk c lies at q * 2 ZP + ((c ^ (q & 7)) << 4).
-            const int slot = (i * TILES + ZI) % kSlots;
-            unsigned char *stage = sm + slot * kTile + warp * (64 * ZP);
-            const int row0 = 32 * warp, mine = min(32, rows - row0);         // rows of this warp there are
-            const int64_t t0 = it.begin + c0 * kRows + row0;
+            slot = (i * TILES + ZI) % kSlots;
+            stage = sm + slot * kTile + quad * (64 * ZP);
+            mine = min(32, rows - 32 * quad);         // rows of this warp there are
+            t0 = it.begin + c0 * kRows + 32 * quad;
             const bool bad = *(volatile int *)&B.bad[b];
             if (p.dot) {
                 const bf16 *with = static_cast<const bf16 *>(p.dot_with) + t0 * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head;
@@ -730,34 +814,15 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 }
                 __syncwarp();
             }
-            if (p.out && !p.out_f32) {
-                __syncwarp();
-                bf16 *o = static_cast<bf16 *>(p.out) + t0 * p.out_stride + (int64_t)hv * p.out_head;
-                if ((wide & 16) && p.DZ % 8 == 0) {
-#pragma unroll 4
-                    for (int e = lane; e < 32 * CH; e += 32) {
-                        const int q = e / CH, c = e % CH;
-                        if (q < mine && c * 8 < p.DZ)
-                            *reinterpret_cast<uint4 *>(o + q * p.out_stride + c * 8) =
-                                *reinterpret_cast<const uint4 *>(stage + q * (2 * ZP) + ((c ^ (q & 7)) << 4));
-                    }
-                } else {
-                    for (int q = 0; q < mine; ++q)
-                        for (int c = lane; c < p.DZ; c += 32)
-                            o[q * p.out_stride + c] =
-                                *reinterpret_cast<const bf16 *>(stage + q * (2 * ZP) + (((c >> 3) ^ (q & 7)) << 4) + (c & 7) * 2);
-                }
-            }
             if (p.dot && lane < mine) p.dot[(t0 + lane) * P.a.HV + hv] = dot;
             mbar_arrive(&B.bad_read[b]);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B.empty[slot]);
+        }
         }
     }
     tcl_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (tid == 0 && B.abort_flag) raise_flag(P.a.err_flags, GDN_DEVERR_TIMEOUT);
+    if (warp == 20) {
         tcl_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -765,10 +830,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 
 constexpr int kMaxDevices = 64;
 
-template <int YB, int ZB, int NS, bool OUT>
+template <int YB, int ZB, int NS>
 int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, int wide, cudaStream_t stream)
 {
-    const auto kernel = linear_chunk_kernel<YB, ZB, NS, OUT>;
+    const auto kernel = linear_chunk_kernel<YB, ZB, NS>;
     static std::mutex lock;
     static bool raised[kMaxDevices] = {};             // the shared-memory limit, a function attribute of each device
     int dev = 0;
@@ -786,12 +851,12 @@ int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, i
 
 template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSweep &p, bool outputs, const ChunkMaps &maps, int wide, cudaStream_t stream)
 {
-    if (!outputs) return launch<YB, ZB, 2, false>(P, p, maps, wide, stream);
+    if (!outputs) return launch<YB, ZB, 0>(P, p, maps, wide, stream);
     // Terms of the state and of P: one for bf16 outputs (their error against 64 bits grows by at most the square root of
     // two: each of P, the state and the output is rounded once to bf16), two for fp32 outputs; what dg is summed from keeps the
     // state whole.
-    if (!p.dot && !p.exact) return launch<YB, ZB, 1, true>(P, p, maps, wide, stream);
-    return p.dot ? launch<YB, ZB, 3, true>(P, p, maps, wide, stream) : launch<YB, ZB, 2, true>(P, p, maps, wide, stream);
+    if (!p.dot && !p.exact) return launch<YB, ZB, 1>(P, p, maps, wide, stream);
+    return p.dot ? launch<YB, ZB, 3>(P, p, maps, wide, stream) : launch<YB, ZB, 2>(P, p, maps, wide, stream);
 }
 
 }  // namespace
