@@ -65,17 +65,8 @@ constexpr int kMostSlots = 7;
 struct Decays {
     float nhi[kRows], nlo[kRows];                     // -hi, -lo
     float col[kRows];                                 // e^{(G at the end of the row's 32) - G}
-    float weight[kRows];                              // e^{(G at the chunk's end) - G}; 0 for rows behind the sequence
-};
-
-template <int NS> struct Smem {                       // NS: bf16 terms of the state (0: no outputs)
-    static constexpr int kSlots = 7 - NS;             // tiles of x, y and z: what the state leaves
-    static constexpr uint32_t kStates = kSlots * kTile;
-    static constexpr uint32_t kDecays = kStates + NS * kTile;
-    static constexpr uint32_t kBad = kDecays + sizeof(Decays);        // uint8 [2][128]: first non-finite row of a column of z
-    static constexpr uint32_t kBars = kBad + 2 * kRows;
-    static constexpr uint32_t kBytes = kBars + 512;
-    static_assert(kSlots <= kMostSlots && kBytes <= 232448, "more than an SM's shared memory");
+    float weight[2][kRows];                           // e^{(G at the chunk's end) - G}; 0 for rows behind the sequence. Two, since
+                                                      // the state's warps come to a chunk last
 };
 
 struct ChunkMaps {
@@ -84,16 +75,27 @@ struct ChunkMaps {
 
 struct Bars {
     uint64_t full[kMostSlots], empty[kMostSlots];     // tiles
-    uint64_t decays, decays_free;
-    uint64_t z_raw[4], z_ok[2], bad_read[2];          // z's tile may be used for the update; for the outputs; first_bad was read
+    uint64_t decays[2], rows_free, weight_free[2];
+    uint64_t z_raw[3], z_ok[2], bad_read[2];          // z's tile may be used for the update; for the outputs; first_bad was read
     uint64_t y_ready[4], y_free[4];                   // quarters of Y: written; used
     uint64_t scores, p_ready, inter, out, out_read, update[2], update_read, state_ready, done[2];
-    LinearItem item;
+    float decay[2];                                   // e^{G at the chunk's end}
     uint32_t tmem;
-    int abort_flag, zero, bad[2];
-    long long limit;
+    int abort_flag, zero;
+    uint8_t bad[2];
 };
-static_assert(sizeof(Bars) <= 512, "");
+
+// Seven tiles of shared memory: NS for the state's bf16 terms (0: no outputs), the others for x, y and z; and what the
+// 227 KB leave besides.
+template <int NS> struct Smem {
+    static constexpr int kSlots = 7 - NS;
+    static constexpr uint32_t kStates = kSlots * kTile;
+    static constexpr uint32_t kDecays = 7 * kTile;
+    static constexpr uint32_t kBad = kDecays + sizeof(Decays);        // uint8 [128]: first non-finite row of a column of z
+    static constexpr uint32_t kBars = kBad + kRows;
+    static constexpr uint32_t kBytes = kBars + sizeof(Bars);
+    static_assert(kSlots <= kMostSlots && kBytes <= 232448 && sizeof(LinearItem) <= sizeof(Decays), "more than an SM's shared memory");
+};
 
 // A tile by plain loads, for rows that TMA cannot copy (not 16-byte aligned): zeros behind n rows and dim columns.
 template <int BLOCKS>
@@ -118,14 +120,14 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t
 
 // Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. The clock and the flag are
 // looked at once in a while only, since the warps that wait share their scheduler with those that work.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B)
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B, long long limit)
 {
     bool done = mbar_try_wait(bar, parity & 1u);
     if (!__all_sync(kAll, done)) {
         const long long t0 = clock64();
         for (uint32_t i = 1; !done; ++i) {
             done = mbar_try_wait(bar, parity & 1u);
-            if ((i & 63) == 0 && !done && (*(volatile int *)&B->abort_flag || clock64() - t0 > B->limit)) break;
+            if ((i & 63) == 0 && !done && (*(volatile int *)&B->abort_flag || clock64() - t0 > limit)) break;
         }
         done = __all_sync(kAll, done);
         if (!done) *(volatile int *)&B->abort_flag = 1;
@@ -134,31 +136,35 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars 
 }
 
 // 32 tokens of Y, from row s0 of y's tile, into the buffer at taddr: lane y of tensor memory takes column y.
-__device__ __forceinline__ void make_y(const unsigned char *tile, int y, int s0, int rows, const Decays &decays, uint32_t taddr)
+__device__ __forceinline__ void make_y(const unsigned char *tile, int y, int s0, int rows, const float *weight, uint32_t taddr)
 {
     const uint16_t *ty = reinterpret_cast<const uint16_t *>(tile + (y >> 6) * kBlock) + (y & 7);
     const int yc = (y & 63) >> 3;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k, s0 += 16) {           // 16 tokens: one step of the product
-        uint32_t w[3][8];
+        // (step by step for all of them, so that the steps' latencies overlap)
+        uint32_t raw[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 f = *reinterpret_cast<const float4 *>(&decays.weight[s0 + 4 * j]);
-            uint32_t raw[4];
+        for (int j = 0; j < 16; ++j) raw[j] = ty[(s0 + j) * 64 + ((yc ^ (j & 7)) << 3)];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int s = s0 + 4 * j + e;
-                raw[e] = ty[s * 64 + ((yc ^ ((4 * j + e) & 7)) << 3)];
-                raw[e] = s < rows ? raw[e] << 16 : 0;              // rows behind belong to no one or another sequence
-            }
-            uint32_t t[3];
-            split<3>(mul2(pair(raw[0], raw[1]), pair(f.x, f.y)), t);
-            w[0][2 * j] = t[0], w[1][2 * j] = t[1], w[2][2 * j] = t[2];
-            split<3>(mul2(pair(raw[2], raw[3]), pair(f.z, f.w)), t);
-            w[0][2 * j + 1] = t[0], w[1][2 * j + 1] = t[1], w[2][2 * j + 1] = t[2];
+        for (int j = 0; j < 16; ++j) raw[j] <<= 16;
+        if (rows < s0 + 16) {                         // rows behind belong to no one or another sequence
+#pragma unroll
+            for (int j = 0; j < 16; ++j) raw[j] = s0 + j < rows ? raw[j] : 0;
         }
+        f2 v[8];
 #pragma unroll
-        for (int t = 0; t < 3; ++t) tcl_st8(taddr + k * 24 + t * 8, w[t]);
+        for (int j = 0; j < 8; ++j) v[j] = mul2(pair(raw[2 * j], raw[2 * j + 1]), *reinterpret_cast<const f2 *>(&weight[s0 + 2 * j]));
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[j]);
+            tcl_st8(taddr + k * 24 + t * 8, w);
+            if (t < 2)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = fma2(pair(w[j] << 16, w[j] & 0xFFFF0000u), pair(-1.f, -1.f), v[j]);
+        }
     }
     tcl_wait_st();
 }
@@ -181,27 +187,28 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     Bars &B = *reinterpret_cast<Bars *>(sm + M::kBars);
     const uint32_t sbase = smem_u32(sm);
     Decays &decays = *reinterpret_cast<Decays *>(sm + M::kDecays);
-    uint8_t(*first_bad)[kRows] = reinterpret_cast<uint8_t(*)[kRows]>(sm + M::kBad);
+    uint8_t *first_bad = sm + M::kBad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hv = blockIdx.y;
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 6);
-        mbar_init(&B.decays, 32), mbar_init(&B.decays_free, OUT ? 640 : 512);
+        for (int i = 0; i < 2; ++i) mbar_init(&B.decays[i], 32), mbar_init(&B.weight_free[i], 512);
+        mbar_init(&B.rows_free, 384);
         for (int i = 0; i < 2; ++i) mbar_init(&B.z_ok[i], 32), mbar_init(&B.bad_read[i], 128), mbar_init(&B.done[i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&B.y_ready[i], 128), mbar_init(&B.y_free[i], 1), mbar_init(&B.z_raw[i], 32);
+        for (int i = 0; i < 4; ++i) mbar_init(&B.y_ready[i], 128), mbar_init(&B.y_free[i], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&B.z_raw[i], 32);
         mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.update[0], 1), mbar_init(&B.update[1], 1);
         mbar_init(&B.p_ready, 384), mbar_init(&B.out_read, 128), mbar_init(&B.state_ready, 256), mbar_init(&B.update_read, 256);
         B.abort_flag = B.zero = B.bad[0] = B.bad[1] = 0;
-        B.limit = P.wait_limit > 0 ? P.wait_limit : kWaitLimit;
         fence_barrier_init();
     }
     if (warp == 22) {
         const LinearItem it = linear_item(P, blockIdx.x, OUT && hv == 0);
-        if (lane == 0) B.item = it;
+        if (lane == 0) *reinterpret_cast<LinearItem *>(sm + M::kDecays) = it;   // (the decays come later)
     }
     __syncthreads();
-    const LinearItem it = B.item;
+    const LinearItem it = *reinterpret_cast<const LinearItem *>(sm + M::kDecays);
     if (it.seq < 0 || (sbase & 1023u)) return;
     const bool whole = it.seq_end - it.seq_begin <= P.seg;
     if (!OUT && (whole || it.state < 0)) return;
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         tcl_fence_after();
     }
     bool ok = true;
-    const auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &B); };
+    const auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &B, P.wait_limit); };
     const size_t state_at = ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     const size_t item_at = ((size_t)blockIdx.x * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
 
@@ -281,45 +288,63 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
         } else if (warp == 22) {
             // ---------------------------------------------------------------- decays; z's non-finite values
+            // Sums as 64-bit integers in steps of 2^-40 (fp64 runs at two operations a clock and SM, and this warp is on every
+            // chunk's path); lane l takes the rows 4 l .. 4 l + 3 in the sweep's order, the next chunk's already loaded.
             double all = 0.0;
-            for (int i = 0; i < chunks; ++i) {
+            float g[4];
+            const auto fetch = [&](int i) {
                 const int c = p.reverse ? chunks - 1 - i : i, at = it.begin + c * kRows, rows = min(kRows, n - c * kRows);
-                // lane l takes the rows 4 l .. 4 l + 3 in the sweep's order
-                double s[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
-                    const double d = r < rows ? linear_decay(P, hv, at + r, it.seq_end, p.reverse) : 0.0;
+                    const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j, t = at + r + (p.reverse ? 1 : 0);
+                    g[j] = r < rows && t < it.seq_end ? P.a.g[t * P.a.g_stride + hv] : 0.f;
+                }
+            };
+            if (chunks > 0) fetch(0);
+            for (int i = 0; i < chunks; ++i) {
+                const int rows = min(kRows, n - kRows * (p.reverse ? chunks - 1 - i : i));
+                long long s[4];
+                bool nan[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    nan[j] = (j && nan[j - 1]) || !(g[j] < INFINITY);
+                    const float x = fminf(fmaxf(g[j], -200.f), 200.f);
+                    // x log2(e) as the sum of two fp32 numbers
+                    const float q = x * 1.44269502f, e = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -q));
+                    const long long d = __float2ll_rn(q * 0x1p40f) + __float2ll_rn(e * 0x1p40f);
                     s[j] = j ? s[j - 1] + d : d;
                 }
-                double sum = s[3];
+                if (i + 1 < chunks) fetch(i + 1);
+                long long sum = s[3];
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const double v = __shfl_up_sync(kAll, sum, o);
+                    const long long v = __shfl_up_sync(kAll, sum, o);
                     if (lane >= o) sum += v;
                 }
-                double before = __shfl_up_sync(kAll, sum, 1);
-                if (lane == 0) before = 0.0;
-                all += __shfl_sync(kAll, sum, 31);
+                const bool nan_before = (__ballot_sync(kAll, nan[3]) & ((1u << lane) - 1)) != 0;
+                const long long before = sum - s[3];
                 float hi[4], lo[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const double G = before + s[j], h = rint(G * 256.0) * (1.0 / 256.0);
-                    hi[j] = (float)h;
-                    lo[j] = (float)(G - h);
+                    const long long G = before + s[j], h = (G + (1ll << 31)) >> 32;            // hi: steps of 1/256
+                    hi[j] = (float)(int)h * 0x1p-8f;
+                    lo[j] = nan_before || nan[j] ? __int_as_float(0x7fc00000) : (float)(int)(G - (h << 32)) * 0x1p-40f;
                 }
                 const float hi32 = __shfl_sync(kAll, hi[3], lane | 7), lo32 = __shfl_sync(kAll, lo[3], lane | 7);
                 const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
-                if (i > 0 && !wait(&B.decays_free, i - 1)) break;
+                if (!OUT) all += (double)hi_end + (double)lo_end;
+                if (i >= 2 && !wait(&B.weight_free[i & 1], (i >> 1) - 1)) break;
+                if (OUT && i > 0 && !wait(&B.rows_free, i - 1)) break;
+                if (lane == 0) B.decay[i & 1] = ex2(hi_end) * ex2(lo_end);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
                     decays.nhi[r] = -hi[j];
                     decays.nlo[r] = -lo[j];
                     decays.col[r] = ex2(hi32 - hi[j]) * ex2(lo32 - lo[j]);
-                    decays.weight[r] = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
+                    decays.weight[i & 1][r] = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
                 }
-                mbar_arrive(&B.decays);
+                mbar_arrive(&B.decays[i & 1]);
                 const int b = i & 1;
                 const int m = i * TILES + ZI, slot = m % kSlots;
                 if (!wait(&B.full[slot], m / kSlots)) break;
@@ -341,10 +366,13 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         if ((e >> 3) % kRows >= rows) z[e] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                 }
+                // (a phase is waited for only when the one before it is known to be complete: parities repeat)
+                if (OUT && bad && i >= 2 && !wait(&B.update[b], (i >> 1) - 1)) break;
                 __syncwarp();
-                mbar_arrive(&B.z_raw[i & 3]);
+                mbar_arrive(&B.z_raw[i % 3]);
                 if (!OUT) continue;
                 if (i >= 2 && !wait(&B.bad_read[b], (i >> 1) - 1)) break;
+                if (bad && i >= 1 && !wait(&B.bad_read[b ^ 1], (i - 1) >> 1)) break;       // (there is one first_bad)
                 if (bad) {
                     // the update has its NaN; the outputs' product takes zeros, and the column's first row is noted
                     if (!wait(&B.update[i & 1], i >> 1)) break;
@@ -359,7 +387,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                                 v = 0;
                             }
                         }
-                        first_bad[b][k] = (uint8_t)from;
+                        first_bad[k] = (uint8_t)from;
                     }
                     fence_proxy_async();
                 }
@@ -427,7 +455,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             for (int i = 0; i < chunks; ++i) {
                 const int my = i * TILES + YI, mz = i * TILES + ZI;
                 const uint64_t tz = tc_desc(sbase + (mz % kSlots) * kTile, kBlock);
-                if (!wait(&B.z_raw[i & 3], i >> 2) || (i > 0 && !wait(&B.update_read, i - 1))) break;
+                if (!wait(&B.z_raw[i % 3], i / 3) || (i > 0 && !wait(&B.update_read, i - 1))) break;
                 bool go = true;
 #pragma unroll 1
                 for (int u = 0; u < 4 && go; ++u) {       // 32 tokens each
@@ -506,7 +534,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int m = i * TILES + YI, slot = m % kSlots;
             const int c0 = p.reverse ? chunks - 1 - i : i, at = it.begin + c0 * kRows;
             const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 384);
-            if (!wait(&B.decays, i) || !wait(&B.full[slot], m / kSlots)) break;
+            if (!wait(&B.decays[i & 1], i >> 1) || !wait(&B.full[slot], m / kSlots)) break;
             if (OUT && p.chunk_dot) {
                 // the product of this state's gradient, as it reaches the chunk's last row, and the state behind that row
                 float d = 0.f;
@@ -522,19 +550,19 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 d = group_sum<32>(d);
                 if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
             }
-            const int last = p.reverse ? 0 : kRows - 1;
-            const float decay = ex2(-decays.nhi[last]) * ex2(-decays.nlo[last]);
+            const float decay = B.decay[i & 1];
             const int rows = min(kRows, n - c0 * kRows);
-            // (with outputs the buffer is that of the quarter two behind, a chunk before)
-            const int u = OUT ? half : 2 + half;
-            const bool go = i == 0 || wait(&B.y_free[2 + half], i - 1);
+            // (the second half, made last, since these warps are the last to get to a chunk; with outputs its buffers are
+            // those of the first)
+            const int u = 2 + half;
+            const bool go = OUT ? wait(&B.y_free[half], i) : i == 0 || wait(&B.y_free[u], i - 1);
             if (go) {
                 tcl_fence_after();
-                if (active) make_y(sm + slot * kTile, y, 32 * u, rows, decays, tmem + lanes + y_column(OUT, u));
+                if (active) make_y(sm + slot * kTile, y, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, OUT ? half : u));
                 tcl_fence_before();
                 mbar_arrive(&B.y_ready[u]);
             }
-            mbar_arrive(&B.decays_free);
+            mbar_arrive(&B.weight_free[i & 1]);
             if (!go || !wait(&B.update[i & 1], i >> 1)) break;
             tcl_fence_after();
             if (active) {
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < chunks; ++i) {
             const int m = i * TILES + YI, slot = m % kSlots;
             const int rows = min(kRows, n - kRows * (p.reverse ? chunks - 1 - i : i));
-            if (!wait(&B.decays, i)) break;
+            if (!wait(&B.decays[i & 1], i >> 1)) break;
             if constexpr (OUT) {
                 const float hi = -decays.nhi[r], lo = -decays.nlo[r];
                 if (!wait(&B.scores, i)) break;
@@ -641,19 +669,19 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         for (int k = 0; k < NP; ++k) tcl_st8(at + k * 8, w[k]);
                     }
                 }
+                mbar_arrive(&B.rows_free);
                 tcl_wait_st();
                 tcl_fence_before();
                 mbar_arrive(&B.p_ready);
             }
-            // (with outputs the buffer is the one of the quarter two before, which has been used)
-            const int u = OUT ? 2 + group : group, buffer = group;
-            if (!wait(&B.full[slot], m / kSlots)) break;
-            if (OUT ? !wait(&B.y_free[group], i) : i > 0 && !wait(&B.y_free[u], i - 1)) break;
+            // (the first half: with outputs its buffers are those of the second half, a chunk before)
+            const int u = group;
+            if (!wait(&B.full[slot], m / kSlots) || (i > 0 && !wait(&B.y_free[OUT ? 2 + u : u], i - 1))) break;
             tcl_fence_after();
-            if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays, tmem + lanes + y_column(OUT, buffer));
+            if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, u));
             tcl_fence_before();
             mbar_arrive(&B.y_ready[u]);
-            mbar_arrive(&B.decays_free);
+            mbar_arrive(&B.weight_free[i & 1]);
         }
     } else {
         give_registers();
@@ -670,9 +698,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         unsigned char *stage = sm;
         for (int i = 0; i <= chunks; ++i) {
             if (i < chunks) {
-                if (!wait(&B.decays, i)) break;
+                if (!wait(&B.decays[i & 1], i >> 1)) break;
                 const float er = ex2(-decays.nhi[r]) * ex2(-decays.nlo[r]);
-                mbar_arrive(&B.decays_free);
+                mbar_arrive(&B.rows_free);
                 if (!wait(&B.inter, i)) break;
                 tcl_fence_after();
                 const f2 er2 = pair(er, er);
@@ -725,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             stage = sm + slot * kTile + quad * (64 * ZP);
             mine = min(32, rows - 32 * quad);         // rows of this warp there are
             t0 = it.begin + c0 * kRows + 32 * quad;
-            const bool bad = *(volatile int *)&B.bad[b];
+            const bool bad = *(volatile uint8_t *)&B.bad[b];
             if (p.dot) {
                 const bf16 *with = static_cast<const bf16 *>(p.dot_with) + t0 * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head;
                 for (int e = lane; e < 32 * CH; e += 32) {
@@ -751,7 +779,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 // columns whose z is not finite from a row on: NaN from there
 #pragma unroll 1
                 for (int c = 0; c < ZP; ++c) {
-                    const int fb = first_bad[b][c];
+                    const int fb = first_bad[c];
                     if (fb == 255) continue;          // the same in every lane
                     uint32_t v;
                     const uint32_t at = tmem + lanes + kOut + c;
@@ -861,8 +889,10 @@ template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSwe
 
 }  // namespace
 
-int launch_linear_chunk(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream)
+int launch_linear_chunk(const LinearLaunch &launch, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
+    LinearLaunch P = launch;
+    if (P.wait_limit <= 0) P.wait_limit = kWaitLimit;
     const auto wide_rows = [](const void *q, int64_t stride, int64_t head, int n, int es) {
         return q && reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0 && head * es % 16 == 0 && n * es % 16 == 0;
     };
