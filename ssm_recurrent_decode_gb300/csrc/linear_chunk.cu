@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     const int hv = blockIdx.y;
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 6);
+        for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 2);
         for (int i = 0; i < 2; ++i) mbar_init(&B.decays[i], 32), mbar_init(&B.weight_free[i], 512);
         mbar_init(&B.rows_free, 384);
         for (int i = 0; i < 2; ++i) mbar_init(&B.z_ok[i], 32), mbar_init(&B.bad_read[i], 128), mbar_init(&B.done[i], 1);
@@ -351,12 +351,29 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 uint4 *z = reinterpret_cast<uint4 *>(sm + slot * kTile);
                 const __nv_bfloat162 none = __float2bfloat162_rn(0.f);
                 __nv_bfloat162 acc[4] = {none, none, none, none};
-#pragma unroll 8
-                for (int e = lane; e < ZB * (int)kBlock / 16; e += 32) {
-                    const uint4 v = z[e];
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const auto look = [&](const uint4 (&v)[4]) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[j] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), none, acc[j]);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[j] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]), none, acc[j]);
+                    }
+                };
+                {
+                    uint4 v[2][4];
+                    const uint4 *from = z + lane;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[0][k] = from[32 * k];
+#pragma unroll 1
+                    for (int e = 0; e < ZB * (int)kBlock / 16 / 32; e += 8, from += 256) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[1][k] = from[128 + 32 * k];
+                        look(v[0]);
+                        if (e + 8 < ZB * (int)kBlock / 16 / 32)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) v[0][k] = from[256 + 32 * k];
+                        look(v[1]);
+                    }
                 }
                 acc[0] = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
                 const bool bad = __any_sync(kAll, __hisnan(acc[0].x) || __hisnan(acc[0].y));
@@ -404,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const int mx = i * TILES, my = mx + YI, mz = mx + ZI;
                 const uint64_t tx = tc_desc(sbase + (mx % kSlots) * kTile, 16), ty = tc_desc(sbase + (my % kSlots) * kTile, 16);
                 const uint64_t tz = tc_desc(sbase + (mz % kSlots) * kTile, kBlock);
-                // (descriptors step in units of 16 bytes; six arrivals free a tile: those that no one else makes come from here)
+                // (descriptors step in units of 16 bytes; two arrivals free a tile: of two products, or one with a plain one)
                 if (!wait(&B.full[mx % kSlots], mx / kSlots) || !wait(&B.full[my % kSlots], my / kSlots)) break;
                 tcl_fence_after();
                 if (lane == 0) {
@@ -427,7 +444,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                             tcl_mma_ss(tmem + kOut, tx + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), state + ((t * kTile + k * 2048) >> 4), id_z,
                                        t + k > 0);
                     tcl_commit(&B.inter);
-                    mbar_arrive_n(&B.empty[mx % kSlots], 5);
+                    mbar_arrive(&B.empty[mx % kSlots]);
                     tcl_commit(&B.empty[mx % kSlots]);
                 }
                 __syncwarp();
@@ -440,6 +457,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         for (int k = 0; k < 8; ++k)
                             tcl_mma_ts(tmem + kOut, tmem + kScores + k * 16 + t * 8, tz + (k * 2048 >> 4), id_z, true);
                     tcl_commit(&B.out);
+                    tcl_commit(&B.empty[mz % kSlots]);
                 }
                 __syncwarp();
             }
@@ -473,10 +491,12 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         tcl_commit(&B.y_free[u]);
                         if (u == 3) {
                             tcl_commit(&B.update[i & 1]);
-                            mbar_arrive_n(&B.empty[my % kSlots], OUT ? 4 : 5);
                             tcl_commit(&B.empty[my % kSlots]);
-                            mbar_arrive_n(&B.empty[mz % kSlots], OUT ? 1 : 5);
                             tcl_commit(&B.empty[mz % kSlots]);
+                            if (!OUT) {
+                                mbar_arrive(&B.empty[my % kSlots]);
+                                mbar_arrive(&B.empty[mz % kSlots]);
+                            }
                         }
                     }
                     __syncwarp();
@@ -567,12 +587,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             tcl_fence_after();
             if (active) {
                 const f2 decay2 = pair(decay, decay);
+                const uint32_t from = tmem + lanes + kUpdate + half * ZC;
+                uint32_t u[2][16];
+                tcl_ld16_start(from, u[0]);
 #pragma unroll
                 for (int c = 0; c < ZC; c += 16) {
-                    uint32_t u[16];
-                    tcl_ld16(tmem + lanes + kUpdate + half * ZC + c, u);
+                    uint32_t(&v)[16] = u[(c >> 4) & 1];
+                    tcl_ld16_wait(v);
+                    if (c + 16 < ZC) tcl_ld16_start(from + c + 16, u[((c >> 4) & 1) ^ 1]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) S[c / 2 + j] = fma2(S[c / 2 + j], decay2, pair(u[2 * j], u[2 * j + 1]));
+                    for (int j = 0; j < 8; ++j) S[c / 2 + j] = fma2(S[c / 2 + j], decay2, pair(v[2 * j], v[2 * j + 1]));
                 }
                 if (OUT && p.chunk_states && !p.chunk_dot)
 #pragma unroll
@@ -634,39 +658,48 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         const int end = p.reverse ? c * 32 : c * 32 + 31;
                         f = ex2(hi + decays.nhi[end]) * ex2(lo + decays.nlo[end]);
                     }
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t at = tmem + lanes + kScores + c * 32 + h * 16;
+                    const uint32_t at = tmem + lanes + kScores + c * 32;
+                    if (none) {
+                        const uint32_t zero[16] = {};
+                        tcl_st16(at, zero);
+                        tcl_st16(at + 16, zero);
+                        continue;
+                    }
+                    const auto convert = [&](int h, const uint32_t (&v)[16]) {
                         const int s0 = c * 32 + h * 16;
-                        uint32_t w[NP][8] = {};
-                        if (!none) {
-                            uint32_t v[16];
-                            tcl_ld16(at, v);
-                            if (each) {
+                        f2 q[8];
+                        if (each) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int s = s0 + 2 * j;
-                                    const f2 d = add2(add2(pair(hi, hi), *reinterpret_cast<const f2 *>(&decays.nhi[s])),
-                                                      add2(pair(lo, lo), *reinterpret_cast<const f2 *>(&decays.nlo[s])));
-                                    const float2 e = unpair(d);
-                                    const float p0 = __uint_as_float(v[2 * j]) * ex2(e.x), p1 = __uint_as_float(v[2 * j + 1]) * ex2(e.y);
-                                    uint32_t t[NP];
-                                    split(pair(s >= from && s < to ? p0 : 0.f, s + 1 >= from && s + 1 < to ? p1 : 0.f), t);
-#pragma unroll
-                                    for (int k = 0; k < NP; ++k) w[k][j] = t[k];
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    uint32_t t[NP];
-                                    split(mul2(pair(v[2 * j], v[2 * j + 1]), mul2(*reinterpret_cast<const f2 *>(&decays.col[s0 + 2 * j]), pair(f, f))), t);
-#pragma unroll
-                                    for (int k = 0; k < NP; ++k) w[k][j] = t[k];
-                                }
+                            for (int j = 0; j < 8; ++j) {
+                                const int s = s0 + 2 * j;
+                                const f2 d = add2(add2(pair(hi, hi), *reinterpret_cast<const f2 *>(&decays.nhi[s])),
+                                                  add2(pair(lo, lo), *reinterpret_cast<const f2 *>(&decays.nlo[s])));
+                                const float2 e = unpair(d);
+                                const float p0 = __uint_as_float(v[2 * j]) * ex2(e.x), p1 = __uint_as_float(v[2 * j + 1]) * ex2(e.y);
+                                q[j] = pair(s >= from && s < to ? p0 : 0.f, s + 1 >= from && s + 1 < to ? p1 : 0.f);
                             }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) q[j] = mul2(*reinterpret_cast<const f2 *>(&decays.col[s0 + 2 * j]), pair(f, f));
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) q[j] = mul2(pair(v[2 * j], v[2 * j + 1]), q[j]);
                         }
 #pragma unroll
-                        for (int k = 0; k < NP; ++k) tcl_st8(at + k * 8, w[k]);
+                        for (int k = 0; k < NP; ++k) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(q[j]);
+                            tcl_st8(at + h * 16 + k * 8, w);
+                            if (k + 1 < NP)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) q[j] = fma2(pair(w[j] << 16, w[j] & 0xFFFF0000u), pair(-1.f, -1.f), q[j]);
+                        }
+                    };
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[16];
+                        tcl_ld16(at + h * 16, v);
+                        convert(h, v);
                     }
                 }
                 mbar_arrive(&B.rows_free);
@@ -690,90 +723,45 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const int quad = warp & 3, r = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         const float f = p.x_scale * p.z_scale;
-        constexpr int CH = 2 * ZP / 16;               // 16-byte chunks of an output row in bf16
-        // Chunk i's outputs are taken from tensor memory in turn i and written to global memory in turn i + 1, while its
-        // products run.
-        int slot = 0, mine = 0;
-        int64_t t0 = 0;
-        unsigned char *stage = sm;
-        for (int i = 0; i <= chunks; ++i) {
-            if (i < chunks) {
+        for (int i = 0; i < chunks; ++i) {
+            {
                 if (!wait(&B.decays[i & 1], i >> 1)) break;
                 const float er = ex2(-decays.nhi[r]) * ex2(-decays.nlo[r]);
                 mbar_arrive(&B.rows_free);
                 if (!wait(&B.inter, i)) break;
                 tcl_fence_after();
                 const f2 er2 = pair(er, er);
-#pragma unroll 2
-                for (int c = 0; c < ZP; c += 16) {
-                    uint32_t u[16];
-                    tcl_ld16(tmem + lanes + kOut + c, u);
+                const uint32_t at = tmem + lanes + kOut;
+                const auto scale = [&](int c, uint32_t (&u)[16]) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float2 q = unpair(mul2(pair(u[2 * j], u[2 * j + 1]), er2));
                         u[2 * j] = __float_as_uint(q.x), u[2 * j + 1] = __float_as_uint(q.y);
                     }
-                    tcl_st16(tmem + lanes + kOut + c, u);
+                    tcl_st16(at + c, u);
+                };
+                uint32_t u[2][16];
+                tcl_ld16_start(at, u[0]);
+#pragma unroll 1
+                for (int c = 0; c < ZP; c += 32) {
+                    tcl_ld16_wait(u[0]);
+                    tcl_ld16_start(at + c + 16, u[1]);
+                    scale(c, u[0]);
+                    tcl_ld16_wait(u[1]);
+                    if (c + 32 < ZP) tcl_ld16_start(at + c + 32, u[0]);
+                    scale(c + 16, u[1]);
                 }
                 tcl_wait_st();
                 tcl_fence_before();
                 mbar_arrive(&B.p_ready);
             }
-            if (i > 0) {
-                // the outputs of the chunk before, as whole rows
-                if (p.out && !p.out_f32) {
-                    __syncwarp();
-                    bf16 *o = static_cast<bf16 *>(p.out) + t0 * p.out_stride + (int64_t)hv * p.out_head;
-                    if ((wide & 16) && p.DZ % 8 == 0) {
-#pragma unroll 4
-                        for (int e = lane; e < 32 * CH; e += 32) {
-                            const int q = e / CH, c = e % CH;
-                            if (q < mine && c * 8 < p.DZ)
-                                *reinterpret_cast<uint4 *>(o + q * p.out_stride + c * 8) =
-                                    *reinterpret_cast<const uint4 *>(stage + q * (2 * ZP) + ((c ^ (q & 7)) << 4));
-                        }
-                    } else {
-                        for (int q = 0; q < mine; ++q)
-                            for (int c = lane; c < p.DZ; c += 32)
-                                o[q * p.out_stride + c] =
-                                    *reinterpret_cast<const bf16 *>(stage + q * (2 * ZP) + (((c >> 3) ^ (q & 7)) << 4) + (c & 7) * 2);
-                    }
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B.empty[slot]);
-            }
-            // (the update reads z's tile too)
-            if (i == chunks || !wait(&B.out, i) || !wait(&B.update[i & 1], i >> 1)) break;
+            if (!wait(&B.out, i)) break;
             tcl_fence_after();
             const int b = i & 1, c0 = p.reverse ? chunks - 1 - i : i, rows = min(kRows, n - c0 * kRows);
-            // The products have read z's tile; its memory takes this warp's 32 output rows, so that global memory is
-            // written (and dot_with read) in whole rows. Row q's chunk c lies at q * 2 ZP + ((c ^ (q & 7)) << 4).
-            slot = (i * TILES + ZI) % kSlots;
-            stage = sm + slot * kTile + quad * (64 * ZP);
-            mine = min(32, rows - 32 * quad);         // rows of this warp there are
-            t0 = it.begin + c0 * kRows + 32 * quad;
             const bool bad = *(volatile uint8_t *)&B.bad[b];
-            if (p.dot) {
-                const bf16 *with = static_cast<const bf16 *>(p.dot_with) + t0 * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head;
-                for (int e = lane; e < 32 * CH; e += 32) {
-                    const int q = e / CH, c = e % CH;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (q < mine) {
-                        if (wide & 8) {
-                            if (c * 8 < p.DZ) v = *reinterpret_cast<const uint4 *>(with + q * p.dot_stride + c * 8);
-                        } else {
-                            uint16_t h[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                h[k] = c * 8 + k < p.DZ ? reinterpret_cast<const uint16_t *>(with)[q * p.dot_stride + c * 8 + k] : 0;
-                            v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(stage + q * (2 * ZP) + ((c ^ (q & 7)) << 4)) = v;
-                }
-                __syncwarp();
-            }
+            const bool mine = r < rows;
+            const int64_t t = it.begin + c0 * kRows + r;
+            const bf16 *with = p.dot && mine ? static_cast<const bf16 *>(p.dot_with) + t * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head : nullptr;
             float dot = 0.f;
             if (bad) {
                 // columns whose z is not finite from a row on: NaN from there
@@ -789,60 +777,80 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(at), "r"(v) : "memory");
                 }
             }
-            const uint32_t row = lane * (2 * ZP);
-#pragma unroll 1
-            for (int c = 0; c < ZP; c += 16) {
-                uint32_t u[16];
-                tcl_ld16(tmem + lanes + kOut + c, u);
-                if (c + 16 >= ZP) {
-                    tcl_fence_before();
-                    mbar_arrive(&B.out_read);
-                }
+            const auto take = [&](int c, const uint32_t (&u)[16]) {
                 f2 v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = mul2(pair(u[2 * j], u[2 * j + 1]), pair(f, f));
-                uint4 *at[2] = {reinterpret_cast<uint4 *>(stage + row + (((c >> 3) ^ (lane & 7)) << 4)),
-                                reinterpret_cast<uint4 *>(stage + row + (((c >> 3) + 1 ^ (lane & 7)) << 4))};
-                if (p.dot) {
+                if (!mine) return;
+                const int left = p.DZ - c;            // columns there are
+                if (with) {
+                    if ((wide & 8) && left >= 16) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 q = *at[j];
-                        const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 q = *reinterpret_cast<const uint4 *>(with + c + 8 * j);
+                            const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 o = unpair(v[4 * j + k]);
-                            dot = fmaf(o.x, low_bf16(e[k]), fmaf(o.y, high_bf16(e[k]), dot));
-                        }
-                    }
-                }
-                if (!p.out) continue;
-                if (!p.out_f32) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *at[j] = make_uint4(pack_bf16(v[4 * j]), pack_bf16(v[4 * j + 1]), pack_bf16(v[4 * j + 2]), pack_bf16(v[4 * j + 3]));
-                    continue;
-                }
-                if (lane < mine) {
-                    float *o = static_cast<float *>(p.out) + (t0 + lane) * p.out_stride + (int64_t)hv * p.out_head + c;
-                    const int left = p.DZ - c;
-                    if ((wide & 16) && left >= 16) {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            const float2 e = unpair(v[j]), g = unpair(v[j + 1]);
-                            *reinterpret_cast<float4 *>(o + 2 * j) = make_float4(e.x, e.y, g.x, g.y);
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 o = unpair(v[4 * j + k]);
+                                dot = fmaf(o.x, low_bf16(e[k]), fmaf(o.y, high_bf16(e[k]), dot));
+                            }
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float2 e = unpair(v[j]);
-                            if (2 * j < left) o[2 * j] = e.x;
-                            if (2 * j + 1 < left) o[2 * j + 1] = e.y;
+                            const float2 o = unpair(v[j]);
+                            if (2 * j < left) dot = fmaf(o.x, to_f32(with[c + 2 * j]), dot);
+                            if (2 * j + 1 < left) dot = fmaf(o.y, to_f32(with[c + 2 * j + 1]), dot);
                         }
                     }
                 }
-                __syncwarp();
+                if (!p.out) return;
+                const int64_t to = t * p.out_stride + (int64_t)hv * p.out_head + c;
+                if ((wide & 16) && left >= 16) {
+                    // whole sectors of 32 bytes
+                    uint32_t w[16];
+                    if (p.out_f32) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 e = unpair(v[j]);
+                            w[2 * j] = __float_as_uint(e.x), w[2 * j + 1] = __float_as_uint(e.y);
+                        }
+                        st_global32(static_cast<float *>(p.out) + to, w);
+                        st_global32(static_cast<float *>(p.out) + to + 8, w + 8);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[j]);
+                        st_global32(static_cast<bf16 *>(p.out) + to, w);
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 e = unpair(v[j]);
+                    if (p.out_f32) {
+                        if (2 * j < left) static_cast<float *>(p.out)[to + 2 * j] = e.x;
+                        if (2 * j + 1 < left) static_cast<float *>(p.out)[to + 2 * j + 1] = e.y;
+                    } else {
+                        if (2 * j < left) static_cast<bf16 *>(p.out)[to + 2 * j] = __float2bfloat16_rn(e.x);
+                        if (2 * j + 1 < left) static_cast<bf16 *>(p.out)[to + 2 * j + 1] = __float2bfloat16_rn(e.y);
+                    }
+                }
+            };
+            {
+                const uint32_t at = tmem + lanes + kOut;
+#pragma unroll 1
+                for (int c = 0; c < ZP; c += 16) {
+                    uint32_t u[16];
+                    tcl_ld16(at + c, u);
+                    if (c + 16 >= ZP) {
+                        tcl_fence_before();
+                        mbar_arrive(&B.out_read);
+                    }
+                    take(c, u);
+                    __syncwarp();
+                }
             }
-            if (p.dot && lane < mine) p.dot[(t0 + lane) * P.a.HV + hv] = dot;
+            if (with) p.dot[t * P.a.HV + hv] = dot;
             mbar_arrive(&B.bad_read[b]);
         }
         }
@@ -904,7 +912,7 @@ int launch_linear_chunk(const LinearLaunch &launch, const LinearSweep &p, bool o
     if (encode_head_rows(&maps.y, p.y, P.a.T, HV / p.y_group, p.DY, p.y_stride, p.y_head, kRows)) wide |= 2;
     if (encode_head_rows(&maps.z, p.z, P.a.T, HV / p.z_group, p.DZ, p.z_stride, p.z_head, kRows)) wide |= 4;
     if (wide_rows(p.dot_with, p.dot_stride, p.dot_head, p.DZ, 2)) wide |= 8;
-    if (wide_rows(p.out, p.out_stride, p.out_head, 8, p.out_f32 ? 4 : 2)) wide |= 16;
+    if (reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_stride * (p.out_f32 ? 4 : 2) % 32 == 0 && p.out_head * (p.out_f32 ? 4 : 2) % 32 == 0) wide |= 16;
     if (p.DY <= 64) return p.DZ <= 64 ? launch_size<1, 1>(P, p, outputs, maps, wide, stream) : launch_size<1, 2>(P, p, outputs, maps, wide, stream);
     return p.DZ <= 64 ? launch_size<2, 1>(P, p, outputs, maps, wide, stream) : launch_size<2, 2>(P, p, outputs, maps, wide, stream);
 }
