@@ -15,7 +15,7 @@
 //
 // One CTA owns a segment of a sequence and a value head. Its 24 warps are groups of four, which take turns on a chunk so that
 // each one's latencies are covered by the others' work:
-//   0, 1   P, blocks of 32 columns in turn; then a quarter of Y each     2   inter's decays and the outputs (a thread a row r)
+//   0, 1   a quarter of Y each, then P, blocks of 32 columns in turn      2   inter's decays and the outputs (a thread a row r)
 //   3, 4   a quarter of Y each; the state                               5   a warp each: MMAs of scores, inter and out; MMAs of
 //          the update; decays and z's non-finite values; copies of x, y and z by TMA into a ring of 32 KB tiles (by plain
 //          loads what is not aligned to 16 bytes)
@@ -50,7 +50,7 @@ constexpr int kStateRegisters = 128, kOtherRegisters = 56;
 static_assert(2 * kStateRegisters + 4 * kOtherRegisters <= 6 * 80, "more registers than the CTA has");
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters)); }
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters)); }
-constexpr long long kWaitLimit = 1LL << 31;           // SM clock cycles, about one second
+constexpr uint32_t kWaitLimit = 1u << 30;              // SM clock cycles, about half a second
 
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kOut = 128, kUpdate = 256, kY = 384;
@@ -118,20 +118,26 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t
     }
 }
 
-// Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. The clock and the flag are
-// looked at once in a while only, since the warps that wait share their scheduler with those that work.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B, long long limit)
+// Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. A try suspends the warp
+// for up to a millisecond, so that warps that wait leave the scheduler to those that work.
+__device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity)
 {
-    bool done = mbar_try_wait(bar, parity & 1u);
-    if (!__all_sync(kAll, done)) {
-        const long long t0 = clock64();
-        for (uint32_t i = 1; !done; ++i) {
-            done = mbar_try_wait(bar, parity & 1u);
-            if ((i & 63) == 0 && !done && (*(volatile int *)&B->abort_flag || clock64() - t0 > limit)) break;
-        }
-        done = __all_sync(kAll, done);
-        if (!done) *(volatile int *)&B->abort_flag = 1;
-    }
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+                 : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars *B, uint32_t limit)
+{
+    const uint32_t t0 = clock();
+    bool done;
+    do {
+        done = try_phase(bar, parity & 1u);
+    } while (!done && !*(volatile int *)&B->abort_flag && (uint32_t)clock() - t0 < limit);
+    done = __all_sync(kAll, done);
+    if (!done) *(volatile int *)&B->abort_flag = 1;
     return done;
 }
 
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (!wait(&B.full[mx % kSlots], mx / kSlots) || !wait(&B.full[my % kSlots], my / kSlots)) break;
                 tcl_fence_after();
                 if (lane == 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < YP / 16; ++k) {
                         const uint32_t o = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
                         tcl_mma_ss(tmem + kScores, tx + o, ty + o, id_scores, k > 0);
@@ -437,9 +443,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (!wait(&B.state_ready, i) || (i > 0 && !wait(&B.out_read, i - 1))) break;
                 tcl_fence_after();
                 if (lane == 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int t = 0; t < NS; ++t)
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < YP / 16; ++k)
                             tcl_mma_ss(tmem + kOut, tx + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), state + ((t * kTile + k * 2048) >> 4), id_z,
                                        t + k > 0);
@@ -451,9 +457,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (!wait(&B.z_ok[i & 1], i >> 1) || !wait(&B.p_ready, i)) break;
                 tcl_fence_after();
                 if (lane == 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int t = 0; t < NP; ++t)
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < 8; ++k)
                             tcl_mma_ts(tmem + kOut, tmem + kScores + k * 16 + t * 8, tz + (k * 2048 >> 4), id_z, true);
                     tcl_commit(&B.out);
@@ -551,11 +557,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             mbar_arrive(&B.state_ready);
         }
         for (int i = 0; i < chunks; ++i) {
-            const int m = i * TILES + YI, slot = m % kSlots;
             const int c0 = p.reverse ? chunks - 1 - i : i, at = it.begin + c0 * kRows;
             const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 384);
-            if (!wait(&B.decays[i & 1], i >> 1) || !wait(&B.full[slot], m / kSlots)) break;
-            if (OUT && p.chunk_dot) {
+            if (!wait(&B.decays[i & 1], i >> 1)) break;
+            if (NS == 3 && p.chunk_dot) {
                 // the product of this state's gradient, as it reaches the chunk's last row, and the state behind that row
                 float d = 0.f;
                 const int next = at + min(kRows, n - c0 * kRows);
@@ -571,19 +576,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
             }
             const float decay = B.decay[i & 1];
-            const int rows = min(kRows, n - c0 * kRows);
-            // (the second half, made last, since these warps are the last to get to a chunk; with outputs its buffers are
-            // those of the first)
-            const int u = 2 + half;
-            const bool go = OUT ? wait(&B.y_free[half], i) : i == 0 || wait(&B.y_free[u], i - 1);
-            if (go) {
-                tcl_fence_after();
-                if (active) make_y(sm + slot * kTile, y, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, OUT ? half : u));
-                tcl_fence_before();
-                mbar_arrive(&B.y_ready[u]);
-            }
             mbar_arrive(&B.weight_free[i & 1]);
-            if (!go || !wait(&B.update[i & 1], i >> 1)) break;
+            if (!wait(&B.update[i & 1], i >> 1)) break;
             tcl_fence_after();
             if (active) {
                 const f2 decay2 = pair(decay, decay);
@@ -598,7 +592,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) S[c / 2 + j] = fma2(S[c / 2 + j], decay2, pair(v[2 * j], v[2 * j + 1]));
                 }
-                if (OUT && p.chunk_states && !p.chunk_dot)
+                if (NS == 3 && p.chunk_states && !p.chunk_dot)
 #pragma unroll
                     for (int c = 0; c < ZC / 2; ++c) {
                         const float2 v = unpair(S[c]);
@@ -633,13 +627,28 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         }
     } else if (warp < 8) {
         give_registers();
-        // ---------------------------------------------------------------- P; a quarter of Y
+        // ---------------------------------------------------------------- a quarter of Y; P
         const int group = warp >> 2, quad = warp & 3, r = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         for (int i = 0; i < chunks; ++i) {
             const int m = i * TILES + YI, slot = m % kSlots;
             const int rows = min(kRows, n - kRows * (p.reverse ? chunks - 1 - i : i));
             if (!wait(&B.decays[i & 1], i >> 1)) break;
+            if (!wait(&B.full[slot], m / kSlots)) break;
+            bool go = true;
+#pragma unroll 1
+            for (int k = 0; k < 2 && go; ++k) {
+                // quarters group and 2 + group; with outputs both in the same buffer
+                const int u = 2 * k + group;
+                go = OUT ? k ? wait(&B.y_free[group], i) : i == 0 || wait(&B.y_free[2 + group], i - 1) : i == 0 || wait(&B.y_free[u], i - 1);
+                if (!go) break;
+                tcl_fence_after();
+                if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, OUT ? group : u));
+                tcl_fence_before();
+                mbar_arrive(&B.y_ready[u]);
+            }
+            if (!go) break;
+            mbar_arrive(&B.weight_free[i & 1]);
             if constexpr (OUT) {
                 const float hi = -decays.nhi[r], lo = -decays.nlo[r];
                 if (!wait(&B.scores, i)) break;
@@ -707,14 +716,6 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 tcl_fence_before();
                 mbar_arrive(&B.p_ready);
             }
-            // (the first half: with outputs its buffers are those of the second half, a chunk before)
-            const int u = group;
-            if (!wait(&B.full[slot], m / kSlots) || (i > 0 && !wait(&B.y_free[OUT ? 2 + u : u], i - 1))) break;
-            tcl_fence_after();
-            if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, u));
-            tcl_fence_before();
-            mbar_arrive(&B.y_ready[u]);
-            mbar_arrive(&B.weight_free[i & 1]);
         }
     } else {
         give_registers();
@@ -732,24 +733,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 tcl_fence_after();
                 const f2 er2 = pair(er, er);
                 const uint32_t at = tmem + lanes + kOut;
-                const auto scale = [&](int c, uint32_t (&u)[16]) {
+#pragma unroll 1
+                for (int c = 0; c < ZP; c += 16) {
+                    uint32_t u[16];
+                    tcl_ld16(at + c, u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float2 q = unpair(mul2(pair(u[2 * j], u[2 * j + 1]), er2));
                         u[2 * j] = __float_as_uint(q.x), u[2 * j + 1] = __float_as_uint(q.y);
                     }
                     tcl_st16(at + c, u);
-                };
-                uint32_t u[2][16];
-                tcl_ld16_start(at, u[0]);
-#pragma unroll 1
-                for (int c = 0; c < ZP; c += 32) {
-                    tcl_ld16_wait(u[0]);
-                    tcl_ld16_start(at + c + 16, u[1]);
-                    scale(c, u[0]);
-                    tcl_ld16_wait(u[1]);
-                    if (c + 32 < ZP) tcl_ld16_start(at + c + 32, u[0]);
-                    scale(c + 16, u[1]);
                 }
                 tcl_wait_st();
                 tcl_fence_before();
@@ -761,7 +754,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const bool bad = *(volatile uint8_t *)&B.bad[b];
             const bool mine = r < rows;
             const int64_t t = it.begin + c0 * kRows + r;
-            const bf16 *with = p.dot && mine ? static_cast<const bf16 *>(p.dot_with) + t * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head : nullptr;
+            const bf16 *with = NS == 3 && p.dot && mine ? static_cast<const bf16 *>(p.dot_with) + t * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head : nullptr;
             float dot = 0.f;
             if (bad) {
                 // columns whose z is not finite from a row on: NaN from there
@@ -783,7 +776,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 for (int j = 0; j < 8; ++j) v[j] = mul2(pair(u[2 * j], u[2 * j + 1]), pair(f, f));
                 if (!mine) return;
                 const int left = p.DZ - c;            // columns there are
-                if (with) {
+                if (NS == 3 && with) {
                     if ((wide & 8) && left >= 16) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -850,7 +843,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     __syncwarp();
                 }
             }
-            if (with) p.dot[t * P.a.HV + hv] = dot;
+            if (NS == 3 && with) p.dot[t * P.a.HV + hv] = dot;
             mbar_arrive(&B.bad_read[b]);
         }
         }
@@ -900,7 +893,7 @@ template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSwe
 int launch_linear_chunk(const LinearLaunch &launch, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
     LinearLaunch P = launch;
-    if (P.wait_limit <= 0) P.wait_limit = kWaitLimit;
+    if (P.wait_limit == 0) P.wait_limit = kWaitLimit;
     const auto wide_rows = [](const void *q, int64_t stride, int64_t head, int n, int es) {
         return q && reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0 && head * es % 16 == 0 && n * es % 16 == 0;
     };
