@@ -75,8 +75,8 @@ struct ChunkMaps {
 
 struct Bars {
     uint64_t full[kMostSlots], empty[kMostSlots];     // tiles
-    uint64_t decays[2], rows_free, weight_free[2];
-    uint64_t z_raw[3], z_ok[2], bad_read[2];          // z's tile may be used for the update; for the outputs; first_bad was read
+    uint64_t weights[2], weight_free[2], rows, rows_free;              // Decays: its weights; the rest of it
+    uint64_t z_raw[3], z_ok[2], bad_read;             // z's tile may be used for the update; for the outputs; first_bad was read
     uint64_t y_ready[4], y_free[4];                   // quarters of Y: written; used
     uint64_t scores, p_ready, inter, out, out_read, update[2], update_read, state_ready, done[2];
     float decay[2];                                   // e^{G at the chunk's end}
@@ -199,9 +199,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 2);
-        for (int i = 0; i < 2; ++i) mbar_init(&B.decays[i], 32), mbar_init(&B.weight_free[i], 512);
-        mbar_init(&B.rows_free, 384);
-        for (int i = 0; i < 2; ++i) mbar_init(&B.z_ok[i], 32), mbar_init(&B.bad_read[i], 128), mbar_init(&B.done[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&B.weights[i], 32), mbar_init(&B.weight_free[i], 512);
+        mbar_init(&B.rows, 32), mbar_init(&B.rows_free, 384), mbar_init(&B.bad_read, 128);
+        for (int i = 0; i < 2; ++i) mbar_init(&B.z_ok[i], 32), mbar_init(&B.done[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&B.y_ready[i], 128), mbar_init(&B.y_free[i], 1);
         for (int i = 0; i < 3; ++i) mbar_init(&B.z_raw[i], 32);
         mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.update[0], 1), mbar_init(&B.update[1], 1);
@@ -340,17 +340,24 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
                 if (!OUT) all += (double)hi_end + (double)lo_end;
                 if (i >= 2 && !wait(&B.weight_free[i & 1], (i >> 1) - 1)) break;
-                if (OUT && i > 0 && !wait(&B.rows_free, i - 1)) break;
                 if (lane == 0) B.decay[i & 1] = ex2(hi_end) * ex2(lo_end);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
-                    decays.nhi[r] = -hi[j];
-                    decays.nlo[r] = -lo[j];
-                    decays.col[r] = ex2(hi32 - hi[j]) * ex2(lo32 - lo[j]);
                     decays.weight[i & 1][r] = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
                 }
-                mbar_arrive(&B.decays[i & 1]);
+                mbar_arrive(&B.weights[i & 1]);
+                if (OUT) {
+                    if (i > 0 && !wait(&B.rows_free, i - 1)) break;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
+                        decays.nhi[r] = -hi[j];
+                        decays.nlo[r] = -lo[j];
+                        decays.col[r] = ex2(hi32 - hi[j]) * ex2(lo32 - lo[j]);
+                    }
+                    mbar_arrive(&B.rows);
+                }
                 const int b = i & 1;
                 const int m = i * TILES + ZI, slot = m % kSlots;
                 if (!wait(&B.full[slot], m / kSlots)) break;
@@ -394,8 +401,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 __syncwarp();
                 mbar_arrive(&B.z_raw[i % 3]);
                 if (!OUT) continue;
-                if (i >= 2 && !wait(&B.bad_read[b], (i >> 1) - 1)) break;
-                if (bad && i >= 1 && !wait(&B.bad_read[b ^ 1], (i - 1) >> 1)) break;       // (there is one first_bad)
+                if (i >= 1 && !wait(&B.bad_read, i - 1)) break;
                 if (bad) {
                     // the update has its NaN; the outputs' product takes zeros, and the column's first row is noted
                     if (!wait(&B.update[i & 1], i >> 1)) break;
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < chunks; ++i) {
             const int c0 = p.reverse ? chunks - 1 - i : i, at = it.begin + c0 * kRows;
             const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 384);
-            if (!wait(&B.decays[i & 1], i >> 1)) break;
+            if (!wait(&B.weights[i & 1], i >> 1)) break;
             if (NS == 3 && p.chunk_dot) {
                 // the product of this state's gradient, as it reaches the chunk's last row, and the state behind that row
                 float d = 0.f;
@@ -633,8 +639,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < chunks; ++i) {
             const int m = i * TILES + YI, slot = m % kSlots;
             const int rows = min(kRows, n - kRows * (p.reverse ? chunks - 1 - i : i));
-            if (!wait(&B.decays[i & 1], i >> 1)) break;
-            if (!wait(&B.full[slot], m / kSlots)) break;
+            if (!wait(&B.weights[i & 1], i >> 1) || !wait(&B.full[slot], m / kSlots)) break;
             bool go = true;
 #pragma unroll 1
             for (int k = 0; k < 2 && go; ++k) {
@@ -646,12 +651,11 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, OUT ? group : u));
                 tcl_fence_before();
                 mbar_arrive(&B.y_ready[u]);
-            }
-            if (!go) break;
-            mbar_arrive(&B.weight_free[i & 1]);
-            if constexpr (OUT) {
+                if (!OUT || k == 1) continue;
+                // P, while the first half is being used
+                go = wait(&B.rows, i) && wait(&B.scores, i);
+                if (!go) break;
                 const float hi = -decays.nhi[r], lo = -decays.nlo[r];
-                if (!wait(&B.scores, i)) break;
                 tcl_fence_after();
                 // Blocks of 32 columns s, every other one, over which P's terms are laid (16 columns: eight of the first term,
                 // eight of the second). In the row's own 32 the decay is taken for each element, and the columns it does not
@@ -716,6 +720,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 tcl_fence_before();
                 mbar_arrive(&B.p_ready);
             }
+            if (!go) break;
+            mbar_arrive(&B.weight_free[i & 1]);
         }
     } else {
         give_registers();
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const float f = p.x_scale * p.z_scale;
         for (int i = 0; i < chunks; ++i) {
             {
-                if (!wait(&B.decays[i & 1], i >> 1)) break;
+                if (!wait(&B.rows, i)) break;
                 const float er = ex2(-decays.nhi[r]) * ex2(-decays.nlo[r]);
                 mbar_arrive(&B.rows_free);
                 if (!wait(&B.inter, i)) break;
@@ -844,7 +850,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 }
             }
             if (NS == 3 && with) p.dot[t * P.a.HV + hv] = dot;
-            mbar_arrive(&B.bad_read[b]);
+            mbar_arrive(&B.bad_read);
         }
         }
     }
