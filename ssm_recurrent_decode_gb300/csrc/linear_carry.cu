@@ -26,13 +26,26 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant
     if (at >= KV) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.start) run = *reinterpret_cast<const float4 *>(p.start + ((size_t)state * P.a.HV + hv) * KV + at);
-    for (int j = 0; j < segs; ++j) {
-        const size_t item = (size_t)(item0 + (p.reverse ? segs - 1 - j : j)) * P.a.HV + hv;
-        float4 *l = reinterpret_cast<float4 *>(P.local + item * KV + at);
-        const float f = exp2_wide(P.total[item]);
-        const float4 own = *l;
-        *l = run;
-        run = make_float4(fmaf(f, run.x, own.x), fmaf(f, run.y, own.y), fmaf(f, run.z, own.z), fmaf(f, run.w, own.w));
+    // four segments' states at a time on their way
+    for (int j0 = 0; j0 < segs; j0 += 4) {
+        float4 own[4];
+        float f[4];
+        float4 *l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = min(j0 + j, segs - 1);
+            const size_t item = (size_t)(item0 + (p.reverse ? segs - 1 - k : k)) * P.a.HV + hv;
+            l[j] = reinterpret_cast<float4 *>(P.local + item * KV + at);
+            own[j] = *l[j];
+            f[j] = P.total[item];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j0 + j >= segs) break;
+            const float g = exp2f(f[j]);
+            *l[j] = run;
+            run = make_float4(fmaf(g, run.x, own[j].x), fmaf(g, run.y, own[j].y), fmaf(g, run.z, own[j].z), fmaf(g, run.w, own[j].w));
+        }
     }
 }
 

@@ -313,11 +313,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 bool nan[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    nan[j] = (j && nan[j - 1]) || !(g[j] < INFINITY);
-                    const float x = fminf(fmaxf(g[j], -200.f), 200.f);
-                    // x log2(e) as the sum of two fp32 numbers
-                    const float q = x * 1.44269502f, e = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -q));
-                    const long long d = __float2ll_rn(q * 0x1p40f) + __float2ll_rn(e * 0x1p40f);
+                    const long long d = linear_fixed(g[j], nan[j]);
+                    if (j) nan[j] |= nan[j - 1];
                     s[j] = j ? s[j - 1] + d : d;
                 }
                 if (i + 1 < chunks) fetch(i + 1);
@@ -332,9 +329,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 float hi[4], lo[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const long long G = before + s[j], h = (G + (1ll << 31)) >> 32;            // hi: steps of 1/256
-                    hi[j] = (float)(int)h * 0x1p-8f;
-                    lo[j] = nan_before || nan[j] ? __int_as_float(0x7fc00000) : (float)(int)(G - (h << 32)) * 0x1p-40f;
+                    linear_parts(before + s[j], hi[j], lo[j]);
+                    if (nan_before || nan[j]) lo[j] = __int_as_float(0x7fc00000);
                 }
                 const float hi32 = __shfl_sync(kAll, hi[3], lane | 7), lo32 = __shfl_sync(kAll, lo[3], lane | 7);
                 const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
@@ -539,9 +535,19 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
             const int left = from && y < p.DY ? p.DZ - half * ZC : 0;             // columns there are to load
             from += y * sy + half * ZC * sz;
+            float v[ZC];
+            if (left >= ZC && sz == 1) {
 #pragma unroll
-            for (int c = 0; c < ZC / 2; ++c)
-                S[c] = pair(2 * c < left ? from[2 * c * sz] * z_inv : 0.f, 2 * c + 1 < left ? from[(2 * c + 1) * sz] * z_inv : 0.f);
+                for (int c = 0; c < ZC; c += 4) *reinterpret_cast<float4 *>(&v[c]) = *reinterpret_cast<const float4 *>(from + c);
+            } else if (left >= ZC) {
+#pragma unroll
+                for (int c = 0; c < ZC; ++c, from += sz) v[c] = *from;
+            } else {
+#pragma unroll
+                for (int c = 0; c < ZC; ++c) v[c] = c < left ? from[c * sz] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < ZC / 2; ++c) S[c] = pair(v[2 * c] * z_inv, v[2 * c + 1] * z_inv);
         }
         const auto put_state = [&]() {
             if (!active) return;
@@ -624,11 +630,26 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const float f = pass * p.z_scale;
             const int left = y < p.DY ? p.DZ - half * ZC : 0;
             to += y * sy + half * ZC * sz;
+            if (left >= ZC && sz == 1) {
 #pragma unroll
-            for (int c = 0; c < ZC / 2; ++c) {
-                const float2 v = unpair(S[c]);
-                if (2 * c < left) to[2 * c * sz] = v.x * f;
-                if (2 * c + 1 < left) to[(2 * c + 1) * sz] = v.y * f;
+                for (int c = 0; c < ZC / 2; c += 2) {
+                    const float2 v = unpair(S[c]), w = unpair(S[c + 1]);
+                    *reinterpret_cast<float4 *>(to + 2 * c) = make_float4(v.x * f, v.y * f, w.x * f, w.y * f);
+                }
+            } else if (left >= ZC) {
+#pragma unroll
+                for (int c = 0; c < ZC / 2; ++c, to += 2 * sz) {
+                    const float2 v = unpair(S[c]);
+                    to[0] = v.x * f;
+                    to[sz] = v.y * f;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < ZC / 2; ++c) {
+                    const float2 v = unpair(S[c]);
+                    if (2 * c < left) to[2 * c * sz] = v.x * f;
+                    if (2 * c + 1 < left) to[(2 * c + 1) * sz] = v.y * f;
+                }
             }
         }
     } else if (warp < 8) {

@@ -134,6 +134,30 @@ __device__ __forceinline__ float exp2_wide(double a)
     return ldexpf(exp2f((float)(a - n)), (int)n);
 }
 
+// The same sums as 64-bit integers in steps of 2^-40, for the kernels whose path they are on (fp64 runs at two operations
+// a clock and SM). A NaN is kept apart.
+__device__ __forceinline__ long long linear_fixed(float g, bool &nan)
+{
+    nan = !(g < INFINITY);
+    const float x = nan ? 0.f : fminf(fmaxf(g, -200.f), 200.f);
+    // x log2(e) as the sum of two fp32 numbers
+    const float q = x * 1.44269502f, e = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -q));
+    return __float2ll_rn(q * 0x1p40f) + __float2ll_rn(e * 0x1p40f);
+}
+// such a sum as hi + lo, hi in steps of 1/256; and 2 to its power
+__device__ __forceinline__ void linear_parts(long long G, float &hi, float &lo)
+{
+    const long long h = (G + (1ll << 31)) >> 32;
+    hi = (float)(int)h * 0x1p-8f;
+    lo = (float)(int)(G - (h << 32)) * 0x1p-40f;
+}
+__device__ __forceinline__ float linear_exp2(long long G)
+{
+    float hi, lo;
+    linear_parts(G, hi, lo);
+    return exp2f(hi) * exp2f(lo);
+}
+
 // decay that a sweep applies before it takes token t (in its own direction)
 __device__ __forceinline__ double linear_decay(const LinearLaunch &P, int hv, int t, int seq_end, int reverse)
 {

@@ -105,27 +105,37 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             sz[b][e / kLinearZ][e % kLinearZ] = rz[i];
         }
     };
-    // warp 0: the factors of a block's tokens; held: log2 of the decay since the reference token
-    double held = 0.0, all = 0.0;
+    // warp 0: the factors of a block's tokens; held: log2 of the decay since the reference token (steps of 2^-40)
+    constexpr long long kOne = 1ll << 40;
+    long long held = 0, all = 0;
+    bool lost = false;                                                         // a NaN came
     const auto factors = [&](int block, int b) {
         const int r = block * kBlock + lane;
-        double s = lane < kBlock && r < n ? linear_decay(P, hv, first + dir * r, it.seq_end, p.reverse) : 0.0;
-        const double own = s;
+        bool nan = false;
+        long long s = 0;
+        if (lane < kBlock && r < n) {
+            const int t = first + dir * r + (p.reverse ? 1 : 0);
+            if (t < it.seq_end) s = linear_fixed(P.a.g[t * P.a.g_stride + hv], nan);
+        }
+        const long long own = s;
 #pragma unroll
         for (int o = 1; o < kBlock; o <<= 1) {
-            const double v = __shfl_up_sync(kAll, s, o);
+            const long long v = __shfl_up_sync(kAll, s, o);
             if (lane >= o) s += v;
         }
-        const double span = __shfl_sync(kAll, s, kBlock - 1);
-        const bool each = __any_sync(kAll, fabs(s) > 60.0);                    // (a NaN leaves the tokens before it alone)
+        const unsigned nans = __ballot_sync(kAll, nan);
+        const bool gone = lost || (nans & ((2u << lane) - 1));                  // (it leaves the tokens before it alone)
+        const long long span = __shfl_sync(kAll, s, kBlock - 1);
+        const bool each = __any_sync(kAll, s > 60 * kOne || s < -60 * kOne);
         float f = 1.f;
-        if (each || !(fabs(held) <= 20.0)) {
-            f = exp2_wide(held);
-            held = 0.0;
+        if (each || held > 20 * kOne || held < -20 * kOne) {
+            f = linear_exp2(held);
+            held = 0;
         }
+        const float none = __int_as_float(0x7fc00000);
         if (lane < kBlock) {
-            s_in[b][lane] = each ? exp2_wide(own) : exp2_wide(-(held + s));
-            s_out[b][lane] = each ? 1.f : exp2_wide(held + s);
+            s_in[b][lane] = gone ? none : each ? linear_exp2(own) : linear_exp2(-(held + s));
+            s_out[b][lane] = each ? 1.f : linear_exp2(held + s);
         }
         if (lane == 0) {
             s_first[b] = f;
@@ -133,6 +143,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
         }
         if (!each) held += span;
         all += span;
+        lost = lost || nans;
     };
 
     const int blocks = (n + kBlock - 1) / kBlock;
@@ -220,14 +231,14 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     }
 
     // the state as it is: times the decay since the reference token
-    if (tid == 0) s_last = exp2_wide(held);
+    if (tid == 0) s_last = lost ? __int_as_float(0x7fc00000) : linear_exp2(held);
     __syncthreads();
     float f = s_last;
     const bool ends = p.reverse ? it.index == 0 : it.begin + n == it.seq_end;  // the sequence's last segment, in the sweep's order
     float *to = nullptr;
     if (!OUT) {
         to = P.local + item_state;
-        if (tid == 0 && zpart == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = (float)all;
+        if (tid == 0 && zpart == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = lost ? __int_as_float(0x7fc00000) : (float)((double)all * 0x1p-40);
     } else if (ends && !skip && p.end) {
         to = p.end + ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     }

@@ -24,30 +24,42 @@ struct LinearStepLaunch {
     int wide;             // q and k may be read four elements at a time
 };
 
-// four channels of a q or k head, turned by the row's position
-template <typename Tin>
-__device__ __forceinline__ float4 head4(const gdn_linear_step_args &a, const Tin *x, int col, bool wide, const float (*cs)[2])
+// four channels of a q or k head, and the other members of their pairs
+struct Head4 {
+    float v[4], other[4];
+};
+template <typename Tin> __device__ __forceinline__ Head4 load_head(const gdn_linear_step_args &a, const Tin *x, int col, bool wide)
 {
-    float v[4];
+    Head4 h;
     if (wide) {
         const float4 x4 = load4(x + col);
-        v[0] = x4.x, v[1] = x4.y, v[2] = x4.z, v[3] = x4.w;
+        h.v[0] = x4.x, h.v[1] = x4.y, h.v[2] = x4.z, h.v[3] = x4.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = to_f32(x[col + i]);
+        for (int i = 0; i < 4; ++i) h.v[i] = to_f32(x[col + i]);
     }
     const int half = a.rotary_dim / 2;
-    if (half > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = col + i;
-            if (c >= a.rotary_dim) continue;
-            const int pair = a.interleaved ? c >> 1 : c < half ? c : c - half;
-            const bool second = a.interleaved ? c & 1 : c >= half;
-            const int other = a.interleaved ? c ^ 1 : second ? c - half : c + half;
-            const float o = to_f32(x[other]);
-            v[i] = second ? fmaf(o, cs[pair][1], v[i] * cs[pair][0]) : fmaf(-o, cs[pair][1], v[i] * cs[pair][0]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int c = col + i;
+        const int other = a.interleaved ? c ^ 1 : c >= half ? c - half : c + half;
+        h.other[i] = c < a.rotary_dim ? to_f32(x[other]) : 0.f;
+    }
+    return h;
+}
+// turned by the row's position
+__device__ __forceinline__ float4 turn_head(const gdn_linear_step_args &a, const Head4 &h, int col, const float (*cs)[2])
+{
+    float v[4];
+    const int half = a.rotary_dim / 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = col + i;
+        v[i] = h.v[i];
+        if (c >= a.rotary_dim) continue;
+        const int pair = a.interleaved ? c >> 1 : c < half ? c : c - half;
+        const bool second = a.interleaved ? c & 1 : c >= half;
+        v[i] = fmaf(second ? h.other[i] : -h.other[i], cs[pair][1], v[i] * cs[pair][0]);
     }
     return make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -65,6 +77,13 @@ __global__ void __launch_bounds__(kThreads, 4) linear_step_kernel(const __grid_c
     const int first_row = blk * TL::ROWS_PASS, row_step = splits * TL::ROWS_PASS;
     __shared__ float cs[K / 2][2];
     ordinary_launch_start();
+    // (asked for before the state: their chain of loads is the longer one)
+    int position = 0;
+    uint64_t turns = 0;
+    if ((int)threadIdx.x < a.rotary_dim / 2) {
+        position = a.positions[b];
+        turns = rotary_turns(a.frequencies[threadIdx.x]);
+    }
 
     int slot = b;
     if (P.idx) {
@@ -82,21 +101,22 @@ __global__ void __launch_bounds__(kThreads, 4) linear_step_kernel(const __grid_c
     TL t;
     t.init();
     t.load(S, V, first_row);
-    if (a.rotary_dim > 0) {
-        const int i = threadIdx.x;
-        if (i < a.rotary_dim / 2) {
-            rotary_cos_sin(a.positions[b], rotary_turns(a.frequencies[i]), cs[i][0], cs[i][1]);
-            cs[i][0] *= P.magnitude;
-            cs[i][1] *= P.magnitude;
-        }
-        __syncthreads();
-    }
     const Tin *qp = static_cast<const Tin *>(a.q) + b * a.q_stride + h * a.q_head_stride;
     const Tin *kp = static_cast<const Tin *>(a.k) + b * a.k_stride + h * a.k_head_stride;
     const Tin *vp = static_cast<const Tin *>(a.v) + b * a.v_stride + hv * a.v_head_stride;
-    const float4 q4 = scale4(head4<Tin>(a, qp, t.col, P.wide, cs), P.scale), k4 = head4<Tin>(a, kp, t.col, P.wide, cs);
-    const float kq = group_sum<TL::LPR>(dot4(k4, q4));
+    const Head4 qh = load_head<Tin>(a, qp, t.col, P.wide), kh = load_head<Tin>(a, kp, t.col, P.wide);
     const float e = expf(a.g[b * a.g_stride + hv]);
+    if (a.rotary_dim > 0) {
+        if ((int)threadIdx.x < a.rotary_dim / 2) {
+            float c, s;
+            rotary_cos_sin(position, turns, c, s);
+            cs[threadIdx.x][0] = c * P.magnitude;
+            cs[threadIdx.x][1] = s * P.magnitude;
+        }
+        __syncthreads();
+    }
+    const float4 q4 = scale4(turn_head(a, qh, t.col, cs), P.scale), k4 = turn_head(a, kh, t.col, cs);
+    const float kq = group_sum<TL::LPR>(dot4(k4, q4));
 
     for (int row0 = first_row; row0 < V; row0 += row_step) {
         if (row0 != first_row) t.load(S, V, row0);

@@ -54,34 +54,47 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
         }
     }
     const int last = min(a.H + a.HK, (group + 1) * R.heads);
-#pragma unroll 4
-    for (int head = group * R.heads; head < last; ++head) {
-        const bool isq = head < a.H;
-        const T *in = isq ? static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)head * a.q_head_stride
-                          : static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(head - a.H) * a.k_head_stride;
-        T *out = isq ? static_cast<T *>(a.q_out) + t * a.q_out_stride + (int64_t)head * a.q_out_head_stride
-                     : static_cast<T *>(a.k_out) + t * a.k_out_stride + (int64_t)(head - a.H) * a.k_out_head_stride;
-        W x = *reinterpret_cast<const W *>(in + c0);
-        if (turn) {
-            if constexpr (INTER && VEC > 1) {
+    // four heads' vectors are asked for before any is written (an output may be its input's memory, so the compiler keeps
+    // the order: 16384 tokens x 48 heads of 128 in bf16 100 us one at a time, SUBST four)
+    constexpr int NH = 4;
+    constexpr bool kTwo = !(INTER && VEC > 1);
+    for (int head0 = group * R.heads; head0 < last; head0 += NH) {
+        W x[NH], y[kTwo ? NH : 1];
+        T *out[NH];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const float p = to_f32(x.v[2 * i]), q = to_f32(x.v[2 * i + 1]);
-                    x.v[2 * i] = from_f32<T>(p * cs[i] - q * sn[i]);
-                    x.v[2 * i + 1] = from_f32<T>(q * cs[i] + p * sn[i]);
-                }
-            } else {
-                W y = *reinterpret_cast<const W *>(in + c1);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const float p = to_f32(x.v[i]), q = to_f32(y.v[i]);
-                    x.v[i] = from_f32<T>(p * cs[i] - q * sn[i]);
-                    y.v[i] = from_f32<T>(q * cs[i] + p * sn[i]);
-                }
-                *reinterpret_cast<W *>(out + c1) = y;
-            }
+        for (int k = 0; k < NH; ++k) {
+            const int head = min(head0 + k, last - 1);
+            const bool isq = head < a.H;
+            const T *in = isq ? static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)head * a.q_head_stride
+                              : static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(head - a.H) * a.k_head_stride;
+            out[k] = isq ? static_cast<T *>(a.q_out) + t * a.q_out_stride + (int64_t)head * a.q_out_head_stride
+                         : static_cast<T *>(a.k_out) + t * a.k_out_stride + (int64_t)(head - a.H) * a.k_out_head_stride;
+            x[k] = *reinterpret_cast<const W *>(in + c0);
+            if (kTwo && turn) y[kTwo ? k : 0] = *reinterpret_cast<const W *>(in + c1);
         }
-        *reinterpret_cast<W *>(out + c0) = x;
+#pragma unroll
+        for (int k = 0; k < NH; ++k) {
+            if (head0 + k >= last) break;
+            if (turn) {
+                if constexpr (!kTwo) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const float p = to_f32(x[k].v[2 * i]), q = to_f32(x[k].v[2 * i + 1]);
+                        x[k].v[2 * i] = from_f32<T>(p * cs[i] - q * sn[i]);
+                        x[k].v[2 * i + 1] = from_f32<T>(q * cs[i] + p * sn[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const float p = to_f32(x[k].v[i]), q = to_f32(y[k].v[i]);
+                        x[k].v[i] = from_f32<T>(p * cs[i] - q * sn[i]);
+                        y[k].v[i] = from_f32<T>(q * cs[i] + p * sn[i]);
+                    }
+                    *reinterpret_cast<W *>(out[k] + c1) = y[k];
+                }
+            }
+            *reinterpret_cast<W *>(out[k] + c0) = x[k];
+        }
     }
 }
 
