@@ -23,8 +23,8 @@
  *
  * Sequences are packed end to end: token rows 0 .. T-1. With cu_seqlens sequence s owns rows
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 (it may be empty: its final state is then its initial one); without,
- * T rows are S sequences of T / S tokens each. Rows that cu_seqlens gives to no sequence are neither read
- * nor written. Two sequences of a call may not name the same state row (the result is then undefined).
+ * T rows are S sequences of T / S tokens each. Rows that cu_seqlens gives to no sequence may hold
+ * anything and are not written. Two sequences of a call may not name the same state row (the result is then undefined).
  */
 #ifndef GDN_LINEAR_H
 #define GDN_LINEAR_H
@@ -137,8 +137,8 @@ size_t gdn_linear_workspace_bytes(int32_t T, int32_t S, int32_t H, int32_t HV, i
  * workspace where one is needed), GDN_ERR_SHAPE (sizes out of range, T not a multiple of S without cu_seqlens,
  * a stride that makes heads or rows of an output overlap, a workspace that is too small), GDN_ERR_DTYPE,
  * GDN_ERR_ALIGN (a pointer not aligned to its element, a state buffer or the workspace not to 16 bytes) or
- * GDN_ERR_LAUNCH. Any row and head strides are accepted; rows that are 16-byte aligned (pointers, strides
- * and head sizes) are copied faster. Outputs may not overlap inputs, one another or the workspace, but for
+ * GDN_ERR_LAUNCH. Any row and head strides are accepted; bf16 rows that are 16-byte aligned (pointers,
+ * strides and head sizes) are read faster, and where V is not a multiple of 8 the workspace takes a copy of the others. Outputs may not overlap inputs, one another or the workspace, but for
  * final_state on initial_state (not checked).
  */
 int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream);

@@ -28,9 +28,14 @@ bool sizes_ok(const gdn_linear_args &a, bool uniform)
 struct BackwardSpace {
     float *part;                       // [T, HV, K] dq, then dk of every value head
     float *qdq, *kdk;                  // [T, HV]
-    float *end_dot;                    // [S, HV, parts]
     float *dg_part;
-    float *chunk_states, *chunk_dot;   // of the tensor-core kernel
+    float *chunk_states, *chunk_dot;   // see LinearSweep
+};
+
+// Copies of inputs whose rows TMA cannot take, for value sizes that are not a multiple of eight (other rows that are not
+// aligned to 16 bytes, which dense tensors and views of them have not, are read by plain loads instead).
+struct PackedSpace {
+    void *q, *k, *v, *d_o;
 };
 
 struct Carver {
@@ -80,13 +85,22 @@ void plan(LinearLaunch &P, bool uniform, bool backward)
     int64_t seg = ((int64_t)a.T * ctas + 4 * kSms - 1) / (4 * kSms);
     seg = (seg + 15) / 16 * 16;
     if (seg < 48) seg = 48;
+    if (backward && seg > 128) seg = 128;                // dg's sums run no longer than a segment
     set_segments(P, uniform, seg);
 }
 
-size_t carve(LinearLaunch &P, BackwardSpace *B, unsigned char *base)
+size_t carve(LinearLaunch &P, BackwardSpace *B, PackedSpace &packed, unsigned char *base)
 {
     Carver w{base};
     const gdn_linear_args &a = P.a;
+    packed = PackedSpace{};
+    if (P.tc && a.V % 8) {
+        const size_t qk = (size_t)a.T * a.H * a.K / 2, v = (size_t)a.T * a.HV * ((a.V + 7) / 8 * 4);      // in words
+        packed.q = w.take(qk);
+        packed.k = w.take(qk);
+        packed.v = w.take(v);
+        if (B) packed.d_o = w.take(v);
+    }
     if (P.carried) {
         P.local = w.take((size_t)P.items * a.HV * a.K * a.V);
         P.total = w.take((size_t)P.items * a.HV);
@@ -102,8 +116,10 @@ size_t carve(LinearLaunch &P, BackwardSpace *B, unsigned char *base)
             B->chunk_dot = w.take(chunks * 8);
             B->dg_part = w.take(chunks * 8);
         } else {
-            B->end_dot = w.take((size_t)a.S * a.HV * z_parts(a.K));
-            B->dg_part = w.take(linear_dg_part_floats(a.S, a.HV));
+            const size_t parts = (size_t)P.items * a.HV * z_parts(a.K);
+            B->chunk_states = w.take(parts * kLinearZ * (a.V <= 16 ? 16 : a.V <= 32 ? 32 : a.V <= 64 ? 64 : 128));
+            B->chunk_dot = w.take(parts);
+            B->dg_part = w.take(linear_dg_part_floats(P.items, a.HV));
         }
     }
     return w.used;
@@ -168,6 +184,26 @@ int run(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream)
     return P.tc ? launch_linear_chunk(P, p, true, stream) : launch_linear_recurrent(P, p, true, stream);
 }
 
+// An input's rows, copied where they need it.
+int pack(const LinearLaunch &P, const void *&p, int64_t &stride, int64_t &head, int heads, int n, void *to, cudaStream_t stream)
+{
+    if (!to || P.a.T == 0 || (n % 8 == 0 && aligned(p, 16) && stride % 8 == 0 && (head % 8 == 0 || heads == 1))) return GDN_OK;
+    const int rc = launch_linear_pack(p, stride, head, P.a.T, heads, n, to, stream);
+    p = to;
+    head = (n + 7) / 8 * 8;
+    stride = heads * head;
+    return rc;
+}
+
+int pack_inputs(LinearLaunch &P, const PackedSpace &packed, cudaStream_t stream)
+{
+    gdn_linear_args &a = P.a;
+    int rc = pack(P, a.q, a.q_stride, a.q_head_stride, a.H, a.K, packed.q, stream);
+    if (rc == GDN_OK) rc = pack(P, a.k, a.k_stride, a.k_head_stride, a.H, a.K, packed.k, stream);
+    if (rc == GDN_OK) rc = pack(P, a.v, a.v_stride, a.v_head_stride, a.HV, a.V, packed.v, stream);
+    return rc;
+}
+
 struct Rows {
     const void *p;
     int64_t stride, head;
@@ -221,7 +257,8 @@ size_t gdn_linear_workspace_bytes(int32_t T, int32_t S, int32_t H, int32_t HV, i
     if (!gdn::sizes_ok(P.a, uniform != 0)) return 0;
     gdn::plan(P, uniform != 0, backward != 0);
     gdn::BackwardSpace B;
-    return gdn::carve(P, backward ? &B : nullptr, nullptr);
+    gdn::PackedSpace packed;
+    return gdn::carve(P, backward ? &B : nullptr, packed, nullptr);
 }
 
 int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream)
@@ -236,10 +273,13 @@ int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream)
     rc = gdn::check_output(a.o, a.o_stride, a.o_head_stride, a.T, a.HV, a.V, a.out_dtype == GDN_BF16 ? 2 : 4);
     if (rc != GDN_OK || (a.T == 0 && !a.final_state)) return rc;
     gdn::LinearLaunch P = gdn::make(a, false, states);
-    rc = gdn::check_workspace(a, gdn::carve(P, nullptr, nullptr));
+    gdn::PackedSpace packed;
+    rc = gdn::check_workspace(a, gdn::carve(P, nullptr, packed, nullptr));
     if (rc != GDN_OK) return rc;
-    gdn::carve(P, nullptr, static_cast<unsigned char *>(a.workspace));
+    gdn::carve(P, nullptr, packed, static_cast<unsigned char *>(a.workspace));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    rc = gdn::pack_inputs(P, packed, s);
+    if (rc != GDN_OK) return rc;
     gdn::LinearSweep p = gdn::forward_sweep(P);
     p.start = a.initial_state;
     p.end = a.final_state;
@@ -251,29 +291,34 @@ int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream)
 int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t stream)
 {
     if (!args) return GDN_ERR_NULL;
-    const gdn_linear_grad_args &q = *args;
-    const gdn_linear_args &a = q.s;
-    const bool states = a.initial_state || q.d_final_state || q.d_initial_state;
-    gdn_linear_args in = a;
+    const gdn_linear_grad_args &given = *args;
+    const bool states = given.s.initial_state || given.d_final_state || given.d_initial_state;
+    gdn_linear_args in = given.s;
     in.final_state = nullptr;
     int rc = gdn::check(in, states);
     if (rc != GDN_OK) return rc;
-    if (a.T > 0 && !q.d_o) return GDN_ERR_NULL;
-    const size_t es = a.in_dtype == GDN_BF16 ? 2 : 4, pool = states ? (size_t)a.num_states * a.HV * a.K * a.V * 4 : 0;
-    for (int r : {gdn::check_rows(q.d_o, q.do_stride, q.do_head_stride, es),
-                  q.dq ? gdn::check_output(q.dq, q.dq_stride, q.dq_head_stride, a.T, a.H, a.K, es) : (int)GDN_OK,
-                  q.dk ? gdn::check_output(q.dk, q.dk_stride, q.dk_head_stride, a.T, a.H, a.K, es) : (int)GDN_OK,
-                  q.dv ? gdn::check_output(q.dv, q.dv_stride, q.dv_head_stride, a.T, a.HV, a.V, es) : (int)GDN_OK,
-                  q.dg && a.g_stride ? gdn::check_output(q.dg, q.dg_stride, a.HV, a.T, 1, a.HV, 4) : (int)GDN_OK})
+    if (in.T > 0 && !given.d_o) return GDN_ERR_NULL;
+    const size_t es = in.in_dtype == GDN_BF16 ? 2 : 4, pool = states ? (size_t)in.num_states * in.HV * in.K * in.V * 4 : 0;
+    for (int r : {gdn::check_rows(given.d_o, given.do_stride, given.do_head_stride, es),
+                  given.dq ? gdn::check_output(given.dq, given.dq_stride, given.dq_head_stride, in.T, in.H, in.K, es) : (int)GDN_OK,
+                  given.dk ? gdn::check_output(given.dk, given.dk_stride, given.dk_head_stride, in.T, in.H, in.K, es) : (int)GDN_OK,
+                  given.dv ? gdn::check_output(given.dv, given.dv_stride, given.dv_head_stride, in.T, in.HV, in.V, es) : (int)GDN_OK,
+                  given.dg && in.g_stride ? gdn::check_output(given.dg, given.dg_stride, in.HV, in.T, 1, in.HV, 4) : (int)GDN_OK})
         if (r != GDN_OK) return r;
-    if (!gdn::aligned(q.dg, 4) || !gdn::aligned(q.d_final_state, 16) || !gdn::aligned(q.d_initial_state, 16)) return GDN_ERR_ALIGN;
-    if (gdn::overlap(q.d_initial_state, q.d_final_state, pool) || gdn::overlap(q.d_initial_state, a.initial_state, pool)) return GDN_ERR_ARG;
+    if (!gdn::aligned(given.dg, 4) || !gdn::aligned(given.d_final_state, 16) || !gdn::aligned(given.d_initial_state, 16)) return GDN_ERR_ALIGN;
+    if (gdn::overlap(given.d_initial_state, given.d_final_state, pool) || gdn::overlap(given.d_initial_state, in.initial_state, pool)) return GDN_ERR_ARG;
     gdn::LinearLaunch P = gdn::make(in, true, states);
     gdn::BackwardSpace B;
-    rc = gdn::check_workspace(a, gdn::carve(P, &B, nullptr));
+    gdn::PackedSpace packed;
+    rc = gdn::check_workspace(in, gdn::carve(P, &B, packed, nullptr));
     if (rc != GDN_OK) return rc;
-    gdn::carve(P, &B, static_cast<unsigned char *>(a.workspace));
+    gdn::carve(P, &B, packed, static_cast<unsigned char *>(in.workspace));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    gdn_linear_grad_args q = *args;
+    rc = gdn::pack_inputs(P, packed, s);
+    if (rc == GDN_OK) rc = gdn::pack(P, q.d_o, q.do_stride, q.do_head_stride, in.HV, in.V, packed.d_o, s);
+    if (rc != GDN_OK) return rc;
+    const gdn_linear_args &a = P.a;
     const int G = a.HV / a.H;
 
     // forward: dq from the states
@@ -286,8 +331,7 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
         p.y = a.v, p.y_stride = a.v_stride, p.y_head = a.v_head_stride, p.y_group = 1;
         p.z = a.k, p.z_stride = a.k_stride, p.z_head = a.k_head_stride, p.z_group = G;
         p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
-        if (q.dg && P.tc) p.chunk_states = B.chunk_states;
-        if (q.dg && !P.tc && q.d_final_state) p.with_end = q.d_final_state, p.end_dot = B.end_dot;
+        if (q.dg) p.chunk_states = B.chunk_states;
         rc = gdn::run_heads(P, p, B.part, {q.dq, q.dq_stride, q.dq_head_stride}, {a.q, a.q_stride, a.q_head_stride}, q.dg ? B.qdq : nullptr, s);
         if (rc != GDN_OK) return rc;
     }
@@ -314,14 +358,14 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
             p.y = q.d_o, p.y_stride = q.do_stride, p.y_head = q.do_head_stride, p.y_group = 1;
             p.z = a.q, p.z_stride = a.q_stride, p.z_head = a.q_head_stride, p.z_group = G;
             p.DY = a.V, p.DZ = a.K, p.sy = a.K, p.sz = 1;
-            if (q.dg && P.tc) p.chunk_states = B.chunk_states, p.chunk_dot = B.chunk_dot;
+            if (q.dg) p.chunk_states = B.chunk_states, p.chunk_dot = B.chunk_dot;
             rc = gdn::run_heads(P, p, B.part, {q.dk, q.dk_stride, q.dk_head_stride}, {a.k, a.k_stride, a.k_head_stride}, q.dg ? B.kdk : nullptr, s);
             if (rc != GDN_OK) return rc;
         }
     }
     if (!q.dg) return GDN_OK;
     if (P.tc) return gdn::launch_linear_dg_chunks(P, B.qdq, B.kdk, B.chunk_dot, q.dg, q.dg_stride, B.dg_part, s);
-    return gdn::launch_linear_dg(P, B.qdq, B.kdk, q.d_final_state ? B.end_dot : nullptr, gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
+    return gdn::launch_linear_dg(P, B.qdq, B.kdk, B.chunk_dot, gdn::z_parts(a.K), q.dg, q.dg_stride, B.dg_part, s);
 }
 
 }  // extern "C"

@@ -104,21 +104,19 @@ struct Pair {
     __device__ __forceinline__ float value() const { return hi + lo; }
 };
 
-// A CTA per sequence and eight heads; 64 ranges of tokens, each summed, then taken again from
-// behind with the sum of the ranges behind it.
+// A CTA per segment and eight heads; 64 ranges of tokens, each summed, then taken again from behind with the sum of the
+// ranges behind it.
 constexpr int kDgHeads = 8, kDgRanges = 64;
 __global__ void __launch_bounds__(kDgHeads *kDgRanges) linear_dg_kernel(const __grid_constant__ LinearLaunch P, const float *qdq,
-                                                                     const float *kdk, const float *end_dot, int parts,
+                                                                     const float *kdk, const float *segment_dot, int parts,
                                                                      float *dg, int64_t dg_stride, float *part)
 {
-    const int s = blockIdx.x, i = threadIdx.x % kDgHeads, range = threadIdx.x / kDgHeads;
+    const int i = threadIdx.x % kDgHeads, range = threadIdx.x / kDgHeads;
     const int hv = blockIdx.y * kDgHeads + i, HV = P.a.HV;
     __shared__ float hi[kDgRanges][kDgHeads], lo[kDgRanges][kDgHeads];
-    int b, e;
-    bool bad;
-    linear_rows(P, s, b, e, bad);
-    const int state = P.states && P.a.state_indices ? P.a.state_indices[s] : s;
-    const bool skip = bad || (P.states && (state < 0 || state >= P.a.num_states));
+    const LinearItem it = linear_item(P, blockIdx.x, false);
+    const bool skip = it.seq < 0 || it.state < 0;
+    const int b = it.begin, e = it.seq < 0 ? b : b + it.n;
     const int per = (e - b + kDgRanges - 1) / kDgRanges;
     const int first = b + range * per, last = min(e, first + per);
     const bool mine = hv < HV;
@@ -133,8 +131,8 @@ __global__ void __launch_bounds__(kDgHeads *kDgRanges) linear_dg_kernel(const __
     __syncthreads();
     if (!mine) return;
     Pair run, total;
-    if (!skip && end_dot)
-        for (int k = 0; k < parts; ++k) run.add(end_dot[((size_t)s * HV + hv) * parts + k]);
+    if (!skip)
+        for (int k = 0; k < parts; ++k) run.add(segment_dot[((size_t)blockIdx.x * HV + hv) * parts + k]);
     for (int r = kDgRanges - 1; r > range; --r) {
         run.add(hi[r][i]);
         run.add(lo[r][i]);
@@ -149,10 +147,10 @@ __global__ void __launch_bounds__(kDgHeads *kDgRanges) linear_dg_kernel(const __
         if (fixed) total.add(v);
         else dg[t * dg_stride + hv] = v;
     }
-    if (fixed) part[((size_t)s * kDgRanges + range) * HV + hv] = total.value();
+    if (fixed) part[((size_t)blockIdx.x * kDgRanges + range) * HV + hv] = total.value();
 }
 
-// dg of one decay a head: the ranges' sums of every sequence, in order
+// dg of one decay a head: the ranges' sums of every segment, in order
 __global__ void __launch_bounds__(256) linear_dg_fixed_kernel(const float *part, int rows, int HV, float *dg)
 {
     const int hv = blockIdx.x;
@@ -233,11 +231,37 @@ __global__ void __launch_bounds__(256) linear_dg_chunk_fixed_kernel(const __grid
     }
 }
 
+// A thread per eight values.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const uint16_t *from, int64_t stride, int64_t head, int64_t count, int heads,
+                                                       int n, int vectors, uint4 *to)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= count) return;
+    const int c = (int)(i % vectors) * 8;
+    const int64_t th = i / vectors, t = th / heads;
+    const uint16_t *p = from + t * stride + (th - t * heads) * head;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = (c + 2 * j < n ? p[c + 2 * j] : 0u) | (c + 2 * j + 1 < n ? (uint32_t)p[c + 2 * j + 1] << 16 : 0u);
+    to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 int status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
 
 }  // namespace
 
-size_t linear_dg_part_floats(int S, int HV) { return (size_t)S * kDgRanges * HV; }
+size_t linear_dg_part_floats(int items, int HV) { return (size_t)items * kDgRanges * HV; }
+
+int launch_linear_pack(const void *from, int64_t stride, int64_t head, int T, int heads, int n, void *to, cudaStream_t stream)
+{
+    const int vectors = (n + 7) / 8;
+    const int64_t count = (int64_t)T * heads * vectors, grid = (count + 255) / 256;
+    if (grid > INT32_MAX) return GDN_ERR_SHAPE;
+    linear_pack_kernel<<<(unsigned)grid, 256, 0, stream>>>(static_cast<const uint16_t *>(from), stride, head, count, heads, n, vectors,
+                                                         static_cast<uint4 *>(to));
+    return status();
+}
 
 int launch_linear_carry(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream)
 {
@@ -254,12 +278,12 @@ int launch_linear_fold(const LinearLaunch &P, const LinearFold &f, cudaStream_t 
     return status();
 }
 
-int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, const float *end_dot, int parts, float *dg,
+int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, const float *segment_dot, int parts, float *dg,
                      int64_t dg_stride, float *part, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)P.a.S, (unsigned)((P.a.HV + kDgHeads - 1) / kDgHeads));
-    linear_dg_kernel<<<grid, kDgHeads * kDgRanges, 0, stream>>>(P, qdq, kdk, end_dot, parts, dg, dg_stride, part);
-    if (P.a.g_stride == 0) linear_dg_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(part, P.a.S * kDgRanges, P.a.HV, dg);
+    const dim3 grid((unsigned)P.items, (unsigned)((P.a.HV + kDgHeads - 1) / kDgHeads));
+    linear_dg_kernel<<<grid, kDgHeads * kDgRanges, 0, stream>>>(P, qdq, kdk, segment_dot, parts, dg, dg_stride, part);
+    if (P.a.g_stride == 0) linear_dg_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(part, P.items * kDgRanges, P.a.HV, dg);
     return status();
 }
 

@@ -25,19 +25,16 @@ struct LinearSweep {
     int64_t sy, sz;                    // strides of the state's memory [V, K] along y and z
     const float *start;                // [num_states, HV, V, K] states to start from, or null: zero
     float *end;                        // [num_states, HV, V, K] states to end with, or null
-    // of the fp32 kernel:
-    const float *with_end;             // [num_states, HV, V, K] or null: its product with the end state goes to
-    float *end_dot;                    // [S, HV, parts of z]
     // of the tensor-core kernel:
     float *dot;                        // [T, HV] or null: sum_z out_t[z] dot_with_t[z], before rounding
     const void *dot_with;
     int64_t dot_stride, dot_head;
     int dot_group;
     int exact;                         // outputs to more than bf16
-    // for dg, per chunk (chunk c of sequence s: its first row / 128 + s) and value head:
-    float *chunk_states;               // [chunks, HV, 128 x 64 or 128] the state behind it, in the kernel's own order
-    float *chunk_dot;                  // [chunks, HV, 8]: given, chunk_states is read, and the parts of its product with
-                                       // the state the sweep comes with are written
+    // for dg, per chunk (chunk c of sequence s: its first row / 128 + s; of the fp32 kernel per segment) and value head:
+    float *chunk_states;               // the state behind it, in the kernel's own order
+    float *chunk_dot;                  // given, chunk_states is read, and the parts of its product with the state the
+                                       // sweep comes with are written (8, or one per part of z)
 };
 
 struct LinearLaunch {
@@ -63,6 +60,9 @@ int launch_linear_recurrent(const LinearLaunch &P, const LinearSweep &p, bool ou
 int launch_linear_chunk(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);
 constexpr int kLinearChunk = 128;      // its tokens per chunk
 
+// bf16 rows [T, heads, n] copied to dense rows of n rounded up to eight, zeros behind
+int launch_linear_pack(const void *from, int64_t stride, int64_t head, int T, int heads, int n, void *to, cudaStream_t stream);
+
 // Between the two: local from end states to start states.
 int launch_linear_carry(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream);
 
@@ -77,9 +77,10 @@ struct LinearFold {
 };
 int launch_linear_fold(const LinearLaunch &P, const LinearFold &f, cudaStream_t stream);
 
-// dg from the products per token: dg_t = sum_{s >= t} (q.dq - k.dk)_s + <d_final, S_last>
-size_t linear_dg_part_floats(int S, int HV);
-int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, const float *end_dot, int parts, float *dg,
+// dg from the products per token and segment: dg_t = sum over the rows from t to the segment's end of (q.dq - k.dk), plus
+// the segment's products (parts of them).
+size_t linear_dg_part_floats(int items, int HV);
+int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, const float *segment_dot, int parts, float *dg,
                      int64_t dg_stride, float *part, cudaStream_t stream);
 
 // The same from products per token and chunk (chunk_dot), of the tensor-core kernel.

@@ -71,6 +71,29 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             }
     }
 
+    // dg's boundary terms: the product of the state's gradient, as it reaches the segment's last row, and the state behind it
+    const size_t kept = (((size_t)blockIdx.x * P.a.HV + hv) * gridDim.z + zpart) * (32 * NT) + tid;
+    if (OUT && p.chunk_dot) {
+        float d = 0.f;
+        if (!skip)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) d = fmaf(S[i][j], p.chunk_states[kept + (2 * i + j) * NT], d);
+        d = group_sum<32>(d);
+        if (lane == 0) so[0][warp] = d;
+        __syncthreads();
+        if (tid == 0) {
+            float sum = 0.f;
+            for (int w = 0; w < NT / 32; ++w) sum += so[0][w];
+            bool nan = false;
+            const int next = it.begin + n;
+            const float g = next < it.seq_end ? linear_exp2(linear_fixed(P.a.g[next * P.a.g_stride + hv], nan)) : 1.f;
+            p.chunk_dot[((size_t)blockIdx.x * P.a.HV + hv) * gridDim.z + zpart] = nan ? __int_as_float(0x7fc00000) : sum * g;
+        }
+        __syncthreads();
+    }
+
     const Tin *xp = OUT ? static_cast<const Tin *>(p.x) + (int64_t)(hv / p.x_group) * p.x_head : nullptr;
     const Tin *yp = static_cast<const Tin *>(p.y) + (int64_t)(hv / p.y_group) * p.y_head;
     const Tin *zp = static_cast<const Tin *>(p.z) + (int64_t)(hv / p.z_group) * p.z_head;
@@ -253,28 +276,11 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
                 if (y < p.DY && z < p.DZ) to[y * p.sy + z * p.sz] = S[i][j] * f * pass;
             }
     }
-    if (OUT && p.with_end && ends) {
-        float d = 0.f;
-        if (!skip) {
-            const float *w = p.with_end + ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
+    if (OUT && p.chunk_states && !p.chunk_dot)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int y = y_of(i), z = z0 + col + j;
-                    if (y < p.DY && z < p.DZ) d = fmaf(S[i][j] * f, w[y * p.sy + z * p.sz], d);
-                }
-        }
-        d = group_sum<32>(d);
-        __syncthreads();
-        if (lane == 0) so[0][warp] = d;
-        __syncthreads();
-        if (tid == 0) {
-            float s = 0.f;
-            for (int w = 0; w < NT / 32; ++w) s += so[0][w];
-            p.end_dot[((size_t)it.seq * P.a.HV + hv) * gridDim.z + zpart] = s;
-        }
-    }
+            for (int j = 0; j < 2; ++j) p.chunk_states[kept + (2 * i + j) * NT] = S[i][j] * f;
 }
 
 template <typename Tin, int NY>
