@@ -220,7 +220,12 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     }
     __syncthreads();
     const LinearItem it = *reinterpret_cast<const LinearItem *>(sm + M::kDecays);
-    if (it.seq < 0 || (sbase & 1023u)) return;
+    if (OUT && p.before_next && tid == 0) grid_launch_dependents();
+    // (a CTA of a launch that may have started early ends behind the launch before it, on every path)
+    const auto leave = [&]() {
+        if (OUT && p.early && tid == 0) grid_dependency_wait();
+    };
+    if (it.seq < 0 || (sbase & 1023u)) return leave();
     const bool whole = it.seq_end - it.seq_begin <= P.seg;
     if (!OUT && (whole || it.state < 0)) return;
     const int n = it.n, chunks = (n + kRows - 1) / kRows;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             if (p.out_f32) static_cast<float *>(p.out)[at] = 0.f;
             else static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(0.f);
         }
-        return;
+        return leave();
     }
     if (warp == 20) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&B.tmem)) : "memory");
@@ -890,6 +895,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         tcl_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+    leave();
 }
 
 constexpr int kMaxDevices = 64;
@@ -909,8 +915,15 @@ int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, i
             raised[dev] = true;
         }
     }
-    kernel<<<dim3((unsigned)P.items, (unsigned)P.a.HV), kThreadsChunk, Smem<NS>::kBytes, stream>>>(P, p, maps, wide);
-    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)P.items, (unsigned)P.a.HV);
+    cfg.blockDim = dim3(kThreadsChunk);
+    cfg.dynamicSmemBytes = Smem<NS>::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (p.early) set_programmatic(attr[cfg.numAttrs++]);
+    return cudaLaunchKernelEx(&cfg, kernel, P, p, maps, wide) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSweep &p, bool outputs, const ChunkMaps &maps, int wide, cudaStream_t stream)

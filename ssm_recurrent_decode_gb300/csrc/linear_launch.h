@@ -35,6 +35,10 @@ struct LinearSweep {
     float *chunk_states;               // the state behind it, in the kernel's own order
     float *chunk_dot;                  // given, chunk_states is read, and the parts of its product with the state the
                                        // sweep comes with are written (8, or one per part of z)
+    // Two sweeps that need nothing of each other: the second one's CTAs take the SMs that the first one's last CTAs leave empty
+    // (programmatic dependent launch), and end behind them.
+    int before_next;                   // the launch behind this one may start early
+    int early;                         // this one may
 };
 
 struct LinearLaunch {

@@ -1,9 +1,9 @@
 // rotary.cu -- rotary positions of q and k (gdn_rotary).
 //
-// A thread owns a vector of pairs (16 bytes of each channel range where pointers, strides and sizes allow, else single
-// pairs) of one token and walks over heads, so that a pair's cosine and sine are computed once for all its heads. Memory-bound:
-// each element is read and written once. The channels behind rotary_dim are copied by threads of their own, unless
-// the call works in place.
+// A CTA takes a few tokens: their cosines and sines go to shared memory, once for all heads, then its threads walk over the
+// tokens' heads in the order of memory, a vector of pairs each (16 bytes of each channel range where pointers, strides and sizes
+// allow, else two elements, else one). Memory-bound: each element is read and written once. The channels behind rotary_dim are
+// copied, unless the call works in place.
 #include "gdn_chain.cuh"
 #include "gdn_common.cuh"
 #include "gdn_rotary.h"
@@ -13,88 +13,84 @@ namespace gdn {
 
 namespace {
 
+// One vector a thread at a time and six CTAs an SM (16384 tokens x 48 heads of 128 in bf16, 403 MB: 70 us, 0.85 of the copy rate;
+// two vectors and four CTAs 81, four and two 115; a thread that kept its pairs' angles in registers and walked over the heads,
+// whose warps touch rows 4 KB apart, 100 to 115).
+constexpr int kThreads = 256, kResident = 6;
+
 struct RotaryLaunch {
     gdn_rotary_args a;
     float magnitude;
-    int pairs;            // threads of a token and head group that turn; behind them those that copy
-    int threads;          // both
-    int heads;            // heads per thread
-    int groups;           // head groups (of q and k together) per token
+    int pairs;            // vectors of a head that turn; behind them those that are copied
+    int units;            // both
+    int tokens;           // tokens per CTA
+    int parts;            // CTAs (blockIdx.y) that share the tokens' vectors
 };
 
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Vec { T v[VEC]; };
 
-// VEC elements a vector; halves: a pair's members lie in two vectors, interleaved: side by side in one
+// VEC elements a vector; halves: a pair's members lie in two vectors, interleaved: side by side in one (unless VEC is 1)
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryLaunch R)
+__global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __grid_constant__ RotaryLaunch R)
 {
     using W = Vec<T, VEC>;
-    constexpr int NP = INTER ? (VEC + 1) / 2 : VEC;                // pairs a thread turns
+    constexpr bool kTwo = !(INTER && VEC > 1);                     // two vectors
+    constexpr int NP = kTwo ? VEC : VEC / 2;                       // pairs
+    extern __shared__ float2 turned[];                             // [tokens, rotary_dim / 2] cosine, sine
     const gdn_rotary_args &a = R.a;
     ordinary_launch_start();
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t tg = u / R.threads;
-    const int j = (int)(u - tg * R.threads);
-    const int64_t t = tg / R.groups;
-    const int group = (int)(tg - t * R.groups);
-    if (t >= a.T) return;
-    const bool turn = j < R.pairs;
-    // first channel of this thread's vector, and of its pairs' other members
-    const int half = a.rotary_dim / 2;
-    const int c0 = turn ? (INTER ? (VEC == 1 ? 2 * j : VEC * j) : VEC * j) : a.rotary_dim + VEC * (j - R.pairs);
-    const int c1 = INTER ? c0 + 1 : c0 + half;                      // (interleaved: only where VEC is 1)
-    float cs[NP], sn[NP];
-    if (turn) {
-        const int pos = a.positions[t];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            rotary_cos_sin(pos, rotary_turns(a.frequencies[(INTER ? c0 / 2 : c0) + i]), cs[i], sn[i]);
-            cs[i] *= R.magnitude;
-            sn[i] *= a.inverse ? -R.magnitude : R.magnitude;
-        }
+    const int half = a.rotary_dim / 2, heads = a.H + a.HK;
+    const int64_t t0 = (int64_t)blockIdx.x * R.tokens;
+    const int tokens = (int)min((int64_t)R.tokens, a.T - t0);
+    // this thread's next vector, and the step to the one behind it
+    const int first = blockIdx.y * kThreads + threadIdx.x, step = R.parts * kThreads;
+    int u = first % R.units, head = first / R.units % heads, tk = first / R.units / heads;
+    const int du = step % R.units, dh = step / R.units % heads, dt = step / R.units / heads;
+    W x, y;
+    T *out;
+    int c0, at;                                                    // first channel; its place in `turned`, or -1: copied
+    const auto load = [&]() {
+        out = nullptr;
+        if (tk >= tokens) return;
+        const int64_t t = t0 + tk;
+        const bool turn = u < R.pairs, isq = head < a.H;
+        const int h = isq ? head : head - a.H;
+        c0 = turn ? (INTER && VEC == 1 ? 2 * u : VEC * u) : a.rotary_dim + VEC * (u - R.pairs);
+        at = turn ? tk * half + NP * u : -1;
+        const T *in = isq ? static_cast<const T *>(a.q) + t * a.q_stride + h * a.q_head_stride
+                          : static_cast<const T *>(a.k) + t * a.k_stride + h * a.k_head_stride;
+        out = isq ? static_cast<T *>(a.q_out) + t * a.q_out_stride + h * a.q_out_head_stride
+                  : static_cast<T *>(a.k_out) + t * a.k_out_stride + h * a.k_out_head_stride;
+        x = *reinterpret_cast<const W *>(in + c0);
+        if (kTwo && turn) y = *reinterpret_cast<const W *>(in + c0 + (INTER ? 1 : half));
+        u += du;
+        head += dh;
+        tk += dt;
+        if (u >= R.units) u -= R.units, ++head;
+        if (head >= heads) head -= heads, ++tk;
+    };
+    load();                                                        // on its way while the angles are taken
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int k = i / half;
+        float c, s;
+        rotary_cos_sin(a.positions[t0 + k], rotary_turns(a.frequencies[i - k * half]), c, s);
+        turned[i] = make_float2(c * R.magnitude, a.inverse ? -R.magnitude * s : R.magnitude * s);
     }
-    const int last = min(a.H + a.HK, (group + 1) * R.heads);
-    // four heads' vectors are asked for before any is written (an output may be its input's memory, so the compiler keeps
-    // the order: 16384 tokens x 48 heads of 128 in bf16 100 us one at a time, SUBST four)
-    constexpr int NH = 4;
-    constexpr bool kTwo = !(INTER && VEC > 1);
-    for (int head0 = group * R.heads; head0 < last; head0 += NH) {
-        W x[NH], y[kTwo ? NH : 1];
-        T *out[NH];
+    __syncthreads();
+    while (out) {
+        if (at >= 0) {
 #pragma unroll
-        for (int k = 0; k < NH; ++k) {
-            const int head = min(head0 + k, last - 1);
-            const bool isq = head < a.H;
-            const T *in = isq ? static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)head * a.q_head_stride
-                              : static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(head - a.H) * a.k_head_stride;
-            out[k] = isq ? static_cast<T *>(a.q_out) + t * a.q_out_stride + (int64_t)head * a.q_out_head_stride
-                         : static_cast<T *>(a.k_out) + t * a.k_out_stride + (int64_t)(head - a.H) * a.k_out_head_stride;
-            x[k] = *reinterpret_cast<const W *>(in + c0);
-            if (kTwo && turn) y[kTwo ? k : 0] = *reinterpret_cast<const W *>(in + c1);
-        }
-#pragma unroll
-        for (int k = 0; k < NH; ++k) {
-            if (head0 + k >= last) break;
-            if (turn) {
-                if constexpr (!kTwo) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const float p = to_f32(x[k].v[2 * i]), q = to_f32(x[k].v[2 * i + 1]);
-                        x[k].v[2 * i] = from_f32<T>(p * cs[i] - q * sn[i]);
-                        x[k].v[2 * i + 1] = from_f32<T>(q * cs[i] + p * sn[i]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const float p = to_f32(x[k].v[i]), q = to_f32(y[k].v[i]);
-                        x[k].v[i] = from_f32<T>(p * cs[i] - q * sn[i]);
-                        y[k].v[i] = from_f32<T>(q * cs[i] + p * sn[i]);
-                    }
-                    *reinterpret_cast<W *>(out[k] + c1) = y[k];
-                }
+            for (int j = 0; j < NP; ++j) {
+                T &p = kTwo ? x.v[j] : x.v[kTwo ? 0 : 2 * j], &q = kTwo ? y.v[j] : x.v[kTwo ? 0 : 2 * j + 1];
+                const float2 cs = turned[at + j];
+                const float f = to_f32(p), h = to_f32(q);
+                p = from_f32<T>(f * cs.x - h * cs.y);
+                q = from_f32<T>(h * cs.x + f * cs.y);
             }
-            *reinterpret_cast<W *>(out[k] + c0) = x[k];
+            if (kTwo) *reinterpret_cast<W *>(out + c0 + (INTER ? 1 : half)) = y;
         }
+        *reinterpret_cast<W *>(out + c0) = x;
+        load();
     }
 }
 
@@ -102,26 +98,33 @@ template <typename T, int VEC, bool INTER> int launch(RotaryLaunch &R, cudaStrea
 {
     const gdn_rotary_args &a = R.a;
     const bool in_place = a.q == a.q_out && (a.HK == 0 || a.k == a.k_out);
-    R.pairs = INTER ? (VEC == 1 ? a.rotary_dim / 2 : a.rotary_dim / VEC) : a.rotary_dim / 2 / VEC;
-    R.threads = R.pairs + (in_place ? 0 : (a.D - a.rotary_dim) / VEC);
-    // Heads per thread: as many as leave every SM a full complement of threads, so that few threads repeat a pair's
-    // cosine and sine.
-    const int heads = a.H + a.HK;
-    R.heads = 1;
-    while (R.heads < 16 && R.heads < heads && (int64_t)a.T * R.threads * ((heads + 2 * R.heads - 1) / (2 * R.heads)) >= 152 * 2048) R.heads *= 2;
-    R.groups = (heads + R.heads - 1) / R.heads;
-    const int64_t n = (int64_t)a.T * R.groups * R.threads;
-    const int64_t grid = (n + 255) / 256;
-    if (grid > INT32_MAX) return GDN_ERR_SHAPE;
-    return launch_ordinary(rotary_kernel<T, VEC, INTER>, dim3((unsigned)grid), dim3(256), 0, stream, R) == cudaSuccess ? GDN_OK
-                                                                                                                    : GDN_ERR_LAUNCH;
+    R.pairs = INTER && VEC > 1 ? a.rotary_dim / VEC : a.rotary_dim / 2 / VEC;
+    R.units = R.pairs + (in_place ? 0 : (a.D - a.rotary_dim) / VEC);
+    // Tokens of a CTA: up to four, as long as two rounds of CTAs remain (16384 tokens of 48 bf16 heads: 70 us at four, 72 at two,
+    // 72 at eight; 4999 of 24 fp32 heads: 19.7 at two, 20.7 at four, 21.1 at one); few tokens are shared by CTAs, a vector a thread.
+    constexpr int kCtas = kResident * 152, kTokens = 4;
+    const int tokens = a.T / (2 * kCtas);
+    R.tokens = tokens < 1 ? 1 : tokens > kTokens ? kTokens : tokens;
+    const int64_t grid = ((int64_t)a.T + R.tokens - 1) / R.tokens;
+    const int64_t vectors = (int64_t)R.tokens * (a.H + a.HK) * R.units;
+    const int64_t parts = grid >= kCtas ? 1 : (vectors + kThreads - 1) / kThreads;
+    R.parts = (int)(parts < 65535 ? parts : 65535);
+    return launch_ordinary(rotary_kernel<T, VEC, INTER>, dim3((unsigned)grid, (unsigned)R.parts), dim3(kThreads),
+                           (size_t)R.tokens * (a.rotary_dim / 2) * sizeof(float2), stream, R) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_LAUNCH;
 }
 
-template <typename T> int launch_t(RotaryLaunch &R, bool vec, cudaStream_t stream)
+template <typename T, bool INTER> int launch_vec(RotaryLaunch &R, int bytes, cudaStream_t stream)
 {
     constexpr int N = 16 / sizeof(T);
-    if (R.a.interleaved) return vec ? launch<T, N, true>(R, stream) : launch<T, 1, true>(R, stream);
-    return vec ? launch<T, N, false>(R, stream) : launch<T, 1, false>(R, stream);
+    if (bytes >= 16) return launch<T, N, INTER>(R, stream);
+    return bytes >= 2 * (int)sizeof(T) ? launch<T, 2, INTER>(R, stream) : launch<T, 1, INTER>(R, stream);
+}
+
+template <typename T> int launch_t(RotaryLaunch &R, int bytes, cudaStream_t stream)
+{
+    return R.a.interleaved ? launch_vec<T, true>(R, bytes, stream) : launch_vec<T, false>(R, bytes, stream);
 }
 
 }  // namespace
@@ -140,7 +143,13 @@ extern "C" int gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream)
     const int es = a.dtype == GDN_BF16 ? 2 : 4;
     const auto aligned = [](const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
     if (!aligned(a.positions, 4) || !aligned(a.frequencies, 8)) return GDN_ERR_ALIGN;
-    bool vec = a.D * es % 16 == 0 && a.rotary_dim * es % (a.interleaved ? 16 : 32) == 0;
+    // bytes of a vector: 16, two elements or one
+    int vec = 16;
+    const auto limit = [&](int64_t bytes) {
+        if (bytes % vec) vec = bytes % (2 * es) ? es : 2 * es;
+    };
+    limit((int64_t)a.D * es);
+    limit((int64_t)a.rotary_dim * es / (a.interleaved ? 1 : 2));
     const auto tensor = [&](const void *p, int64_t stride, int64_t head, bool output, int heads) {
         if (!aligned(p, es)) return GDN_ERR_ALIGN;
         if (stride < 0 || head < 0) return GDN_ERR_SHAPE;
@@ -150,7 +159,9 @@ extern "C" int gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream)
             const bool planes = heads == 1 || head >= (a.T - 1) * stride + a.D, in_plane = a.T == 1 || stride >= a.D;
             if (!(rows && in_row) && !(planes && in_plane)) return GDN_ERR_SHAPE;
         }
-        if (!aligned(p, 16) || (a.T > 1 && stride * es % 16) || (heads > 1 && head * es % 16)) vec = false;
+        limit((int64_t)(reinterpret_cast<uintptr_t>(p) % 16));
+        if (a.T > 1) limit(stride * es);
+        if (heads > 1) limit(head * es);
         return GDN_OK;
     };
     int rc = tensor(a.q, a.q_stride, a.q_head_stride, false, a.H);
