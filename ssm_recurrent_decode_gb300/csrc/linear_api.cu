@@ -60,8 +60,8 @@ void set_segments(LinearLaunch &P, bool uniform, int64_t seg)
     P.items = (int)(uniform ? (int64_t)P.a.S * (P.Ls > 0 ? (P.Ls + seg - 1) / seg : 1) : P.a.S + P.a.T / seg);
 }
 
-// Rows of a segment of equal sequences: as many segments as make the shortest run of rounds of CTAs, in units of a chunk's 2 us.
-// 1 x 32768 x 32 heads: nine segments (288 CTAs, two rounds of 29 chunks) SUBST us, ten (320 CTAs, three rounds) 513.
+// Rows of a segment of equal sequences: as many segments as make the shortest run of rounds of CTAs, in units of a chunk's 4.4 us.
+// 1 x 32768 x 32 heads: nine segments (288 CTAs, two rounds of 29 chunks) 436 us, ten (320 CTAs, three rounds) 513.
 int64_t uniform_segment(const gdn_linear_args &a, int64_t length, bool backward)
 {
     const int64_t chunks = (length + kLinearChunk - 1) / kLinearChunk, tiles = (int64_t)a.S * a.HV;
@@ -70,10 +70,10 @@ int64_t uniform_segment(const gdn_linear_args &a, int64_t length, bool backward)
     for (int64_t n = 1; n <= 8 * kSms && (n == 1 || 2 * n <= chunks); ++n) {
         const int64_t per = (chunks + n - 1) / n;
         if (n > 1 && (n - 1) * per >= chunks) continue;          // as good as fewer
-        // a CTA starts and ends in the time of one and a half chunks; the pass for the segments' states takes two thirds of one with
+        // a CTA starts and ends in the time of a chunk; the pass for the segments' states takes two thirds of one with
         // outputs, two of them beside the three of the gradients a quarter; a state of the carry 4 K V floats of traffic at 5 TB/s
-        double cost = (double)((tiles * n + kSms - 1) / kSms) * (per + 1.5);
-        if (n > 1) cost = cost * (backward ? 1.27 : 1.65) + 1.6e-6 * (double)(tiles * n) * a.K * a.V + 0.1 * n;
+        double cost = (double)((tiles * n + kSms - 1) / kSms) * (per + 1);
+        if (n > 1) cost = cost * (backward ? 1.27 : 1.65) + 0.7e-6 * (double)(tiles * n) * a.K * a.V + 0.1 * n;
         if (n == 1 || cost < best) best = cost, seg = n == 1 ? length : per * kLinearChunk;
     }
     return seg;
@@ -92,9 +92,11 @@ void plan(LinearLaunch &P, bool uniform, bool backward)
         int64_t seg = longest;
         if (uniform || a.S == 1) seg = uniform_segment(a, longest, backward);
         else {
-            // (the lengths are on the device: no segment longer than an SM's share)
-            seg = ((int64_t)a.T * a.HV + kSms - 1) / kSms;
-            seg = (seg + kLinearChunk - 1) / kLinearChunk * kLinearChunk;
+            // The lengths are on the device; the longest sequences start first. No segment is longer than what an SM has to do in
+            // all: its share of the tokens and, where that order is kept, of the sequences' starts and last chunks (a chunk and
+            // a half each). 24 sequences of 8000 tokens, 32 heads: 136 us, 147 by the
+            // share of the tokens alone.
+            seg = ((int64_t)a.T + (a.S <= kLinearSorted ? 3 * kLinearChunk / 2 * (int64_t)a.S : 0)) * a.HV / kSms / kLinearChunk * kLinearChunk;
             if (seg < 2 * kLinearChunk) seg = 2 * kLinearChunk;
         }
         set_segments(P, uniform, seg);

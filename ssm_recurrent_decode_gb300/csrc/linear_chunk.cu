@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     Decays &decays = *reinterpret_cast<Decays *>(sm + M::kDecays);
     uint8_t *first_bad = sm + M::kBad;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = blockIdx.y;
+    const int hv = blockIdx.x % P.a.HV;               // (a token's heads lie side by side in memory)
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&B.full[i], kLoaders), mbar_init(&B.empty[i], 2);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         fence_barrier_init();
     }
     if (warp == 22) {
-        const LinearItem it = linear_item(P, blockIdx.x, OUT && hv == 0);
+        const LinearItem it = linear_item(P, linear_turn(P, blockIdx.x / P.a.HV), OUT && hv == 0);
         if (lane == 0) *reinterpret_cast<LinearItem *>(sm + M::kDecays) = it;   // (the decays come later)
     }
     __syncthreads();
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &B, P.wait_limit); };
     const size_t state_at = ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
-    const size_t item_at = ((size_t)blockIdx.x * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
+    const size_t item_at = ((size_t)it.id * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
 
     if (warp >= 20) {
         give_registers();
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 __syncwarp();
                 mbar_arrive(&B.z_ok[b]);
             }
-            if (!OUT && lane == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = (float)all;
+            if (!OUT && lane == 0) P.total[(size_t)it.id * P.a.HV + hv] = (float)all;
         } else if (warp == 20) {
             // ---------------------------------------------------------------- MMAs: scores, inter, out
             constexpr uint32_t id_scores = tc_idesc(128, 128, false), id_z = tc_idesc(128, ZP, true);
@@ -917,7 +917,8 @@ int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, i
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)P.items, (unsigned)P.a.HV);
+    if ((int64_t)P.items * P.a.HV > INT32_MAX) return GDN_ERR_SHAPE;
+    cfg.gridDim = dim3((unsigned)(P.items * P.a.HV));
     cfg.blockDim = dim3(kThreadsChunk);
     cfg.dynamicSmemBytes = Smem<NS>::kBytes;
     cfg.stream = stream;

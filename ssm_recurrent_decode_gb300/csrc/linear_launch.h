@@ -56,6 +56,7 @@ struct LinearLaunch {
     long long wait_limit;
 };
 
+constexpr int kLinearSorted = 64;      // up to so many sequences, the longest start first
 constexpr int kLinearZ = 64;           // columns of z per CTA of the fp32 kernel
 
 // The sweep on the CUDA cores in fp32 (any type, size, stride); outputs: p.x given. Without: local and total.
