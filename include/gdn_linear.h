@@ -69,8 +69,9 @@ typedef struct gdn_linear_args {
     size_t workspace_bytes;
     int32_t *err_flags;           /* optional device word: GDN_DEVERR_BAD_INDEX is ORed in for a state index
                                      outside [0, num_states) and for a sequence whose cu_seqlens leave 0 .. T or
-                                     decrease (its rows are neither read nor written; rows that two
-                                     other sequences of such a table claim hold either one's outputs); where the state index
+                                     decrease (its rows are not written; of such a table, rows that two
+                                     other sequences claim hold either one's outputs, and sequences of more
+                                     than T rows together may be left out whole); where the state index
                                      is bad, the sequence's outputs and gradients are zeroed and its states left
                                      out. GDN_DEVERR_TIMEOUT when a bounded wait gave up (that CTA's
                                      remaining outputs are not written) */
@@ -138,8 +139,9 @@ size_t gdn_linear_workspace_bytes(int32_t T, int32_t S, int32_t H, int32_t HV, i
  * a stride that makes heads or rows of an output overlap, a workspace that is too small), GDN_ERR_DTYPE,
  * GDN_ERR_ALIGN (a pointer not aligned to its element, a state buffer or the workspace not to 16 bytes) or
  * GDN_ERR_LAUNCH. Any row and head strides are accepted; bf16 rows that are 16-byte aligned (pointers,
- * strides and head sizes) are read faster, and where V is not a multiple of 8 the workspace takes a copy of the others. Outputs may not overlap inputs, one another or the workspace, but for
- * final_state on initial_state (not checked).
+ * strides and head sizes) are read faster, and where V is not a multiple of 8 the workspace takes a copy of
+ * the others. Outputs may not overlap inputs, one another or the workspace, but for final_state on
+ * initial_state (not checked).
  */
 int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream);
 

@@ -46,7 +46,8 @@ typedef struct gdn_rotary_args {
 } gdn_rotary_args;
 
 /* gdn_rotary -- turns q and k. Returns GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN (a
- * pointer not aligned to its element) or GDN_ERR_LAUNCH. Outputs may not overlap the inputs but for in place. */
+ * pointer not aligned to its element) or GDN_ERR_LAUNCH. Outputs may not overlap the inputs but for in place, nor
+ * one another (not checked). */
 int gdn_rotary(const gdn_rotary_args *args, gdn_stream_t stream);
 
 #ifdef __cplusplus

@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant
         if (state < 0 || state >= P.a.num_states) return;
     }
     const int item0 = linear_first_item(P, s);
+    if (item0 + segs > P.items) return;              // (left out, as in linear_item)
     const int KV = P.a.K * P.a.V, at = (blockIdx.z * 256 + threadIdx.x) * 4;
     if (at >= KV) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -6,19 +6,26 @@
 //     State <- e^{G_last} State + sum_s e^{G_last - G_s} y_s z_s^T
 // Four products a chunk, each with fp32 sums in tensor memory:
 //     scores  [r, s] = x y^T                      both operands as loaded
-//     inter   [r, z] = x State                    State from registers through shared memory, as two bf16 terms
-//     out     [r, z] = inter e^{G_r} + P z        P = scores times decays, two bf16 terms, in tensor memory over the scores
-//     update  [y, z] = Y^T z                      Y = y e^{G_last - G_s}, three bf16 terms, in tensor memory, 64 tokens at a time
-// The terms are what keeps fp32: x, y and z are bf16 and exact, the state itself stays in fp32 registers (a lane of
-// tensor memory is a row y of it, the columns z are shared by two warpgroups), a product's sum is added to it in fp32
-// once a chunk. Two terms keep 16 bits of what leads to a token's bf16 output; the update's three keep all 24.
+//     inter   [r, z] = x State                    State from registers through shared memory, as one to three bf16 terms
+//     out     [r, z] = inter e^{G_r} + P z        P = scores times decays, one or two bf16 terms, in tensor memory over the scores
+//     update  [y, z] = Y^T z                      Y = y e^{G_last - G_s}, three bf16 terms, in tensor memory, 32 tokens at a time
+// The terms are what keeps fp32: x, y and z are bf16 and exact, the state itself stays in fp32 registers (a lane of tensor
+// memory is a row y of it, the columns z are shared by two warpgroups), a product's sum is added to it in fp32 once a chunk. The
+// update's three terms keep 24 bits of the state; how many the outputs need is said at launch_size.
 //
 // One CTA owns a segment of a sequence and a value head. Its 24 warps are groups of four, which take turns on a chunk so that
 // each one's latencies are covered by the others' work:
 //   0, 1   a quarter of Y each, then P, blocks of 32 columns in turn      2   inter's decays and the outputs (a thread a row r)
 //   3, 4   a quarter of Y each; the state                               5   a warp each: MMAs of scores, inter and out; MMAs of
-//          the update; decays and z's non-finite values; copies of x, y and z by TMA into a ring of 32 KB tiles (by plain
+//          the update; the decays, and z's non-finite values; copies of x, y and z by TMA into a ring of 32 KB tiles (by plain
 //          loads what is not aligned to 16 bytes)
+// What a chunk takes (4.4 us with one term of the state, 8 to 9 with three and dg) is set by no one unit: the tensor pipe is
+// active 21 to 29% of the time, 29 to 41% of the issue slots are used. A chunk's stages follow one another, and the seven tiles
+// and 512 columns of tensor memory hold the operands of two chunks. The steps there, for 1 x 32768 tokens of 32 heads (both
+// passes): 16 warps in step 1073 us; tiles by TMA, decays as factors of rows and of columns, one term for bf16 outputs 747;
+// groups of warps with registers of their own (24 ragged prompts 316 -> 260) and outputs stored from registers as whole
+// sectors 666; the update's weights apart from the other decays 597; states loaded as whole rows, decays in integers 513; whole
+// rounds of CTAs 436; a token's heads side by side 423.
 // A tile may end in another sequence's rows: their y's weigh nothing, their scores are not looked at, their outputs are not
 // written.
 //
@@ -40,7 +47,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 128;                            // tokens per chunk
-// The tensor cores cut a sum's bits off towards zero at each step of 16 products: 2^-24 of it at most, 4.4e-8 on average
+// The tensor cores cut a sum's bits off towards zero at each step of 16 products: 2^-23 of it at most, 4.4e-8 on average
 // (measured as 3.5e-7 after the eight steps of a chunk's update). Over many chunks that would add up, and where a difference of
 // such sums counts (dg) it shows; so the update's weights and the sums behind dg carry the average back (dg's error over 8 x
 // 2048 tokens 1.1e-6 -> 7.7e-7).

@@ -89,11 +89,13 @@ __device__ __forceinline__ LinearItem linear_item(const LinearLaunch &P, int i, 
             if (who) {
                 const int src = __ffs(who) - 1;
                 it.seq = s0 + src;
-                it.index = i - (before + __shfl_sync(0xFFFFFFFFu, sum - m, src));
+                const int first = before + __shfl_sync(0xFFFFFFFFu, sum - m, src);
+                it.index = i - first;
                 it.seq_begin = __shfl_sync(0xFFFFFFFFu, b, src);
                 it.seq_end = __shfl_sync(0xFFFFFFFFu, e, src);
+                // (only borders that decrease can make more segments than there is room for)
                 const int wrong = __shfl_sync(0xFFFFFFFFu, (int)bad, src);
-                if (wrong) {
+                if (wrong || first + linear_segments(P, it.seq_end - it.seq_begin) > P.items) {
                     if (report && lane == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
                     it.seq = -1;
                     return it;

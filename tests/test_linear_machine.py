@@ -242,3 +242,54 @@ def test_the_debug_build_agrees(S, L, H, HV, K, V, dtype):
             results.append(run())
     for a, b in zip(*results):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("repeat", [1, 2, 40])
+def test_a_table_that_claims_rows_again_and_again(repeat, dtype):
+    """Borders that decrease can name more segments than the workspace has room for: nothing behind it is touched, the flag is
+    raised, and the first sequence, which is in order, has its outputs."""
+    T, H, HV, K, V = 2000, 2, 4, 64, 32
+    x = _random(1, T, H, HV, K, V, dtype, 61)
+    table = torch.tensor([0, T] + [0, T] * repeat, dtype=torch.int32, device="cuda")
+    S = len(table) - 1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    guards = []
+
+    def space(backward):
+        ws = gdn.linear_attention_workspace(T, H, HV, K, V, sequences=S, uniform=False, backward=backward, dtype=lc.TYPES[dtype])
+        guards.append(Guarded(ws.fill_(0xFF)))
+        return guards[-1].t
+
+    o = torch.empty_like(x["v"])
+    args = (x["q"], x["k"], x["v"], x["g"])
+    gdn.gdn_linear_attention(*args, o, cu_seqlens=table, workspace=space(False), err_flags=err)
+    grads = {n: torch.empty_like(x[i]) for n, i in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"))}
+    gdn.gdn_linear_attention_backward(*args, x["do"], cu_seqlens=table, workspace=space(True), **grads)
+    torch.cuda.synchronize()
+    assert int(err) == gdn.GDN_DEVERR_BAD_INDEX
+    assert all(g.intact() for g in guards)
+    d = lambda t: t.double().cpu().numpy()
+    c = {"q": d(x["q"]), "k": d(x["k"]), "v": d(x["v"]), "do": d(x["do"]), "g": d(x["g"]), "initial": None, "d_final": None,
+         "lengths": [T], "scale": K ** -0.5, "dtype": dtype}
+    lc.check(c, "o", o, lc.forward(c)["o"], lc._magnitudes(c)["o"], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_broadcast_inputs(dtype):
+    """Strides of zero: one q for all heads, one v for all tokens."""
+    c = lc.make([200, 90], 2, 4, 32, 40, dtype, 88, states=False)
+    c["q"] = np.broadcast_to(c["q"][:, :1], c["q"].shape).copy()
+    c["v"] = np.broadcast_to(c["v"][:1], c["v"].shape).copy()
+    q = lc.put(c["q"][:, :1], dtype, "dense").expand(-1, 2, -1)
+    v = lc.put(c["v"][:1], dtype, "dense").expand(290, -1, -1)
+    k, do, g = lc.put(c["k"], dtype, "dense"), lc.put(c["do"], dtype, "dense"), lc.f32(c["g"])
+    space = lambda b: gdn.linear_attention_workspace(290, 2, 4, 32, 40, sequences=2, uniform=False, backward=b, dtype=lc.TYPES[dtype])
+    full = lambda t: torch.full_like(t.contiguous(), float("nan"))
+    o, grads = full(v), {"dq": full(q), "dk": full(k), "dv": full(v), "dg": full(g)}
+    gdn.gdn_linear_attention(q, k, v, g, o, cu_seqlens=lc.cu(c["lengths"]), workspace=space(False))
+    gdn.gdn_linear_attention_backward(q, k, v, g, do, cu_seqlens=lc.cu(c["lengths"]), workspace=space(True), **grads)
+    torch.cuda.synchronize()
+    ref, mag = lc.references(c)
+    for n, t in {"o": o, **grads}.items():
+        lc.check(c, n, t, ref[n], mag[n], dtype if n != "dg" else "f32")
