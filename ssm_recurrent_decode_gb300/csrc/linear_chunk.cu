@@ -110,6 +110,8 @@ template <int NS> struct Smem {
 };
 
 // A tile by plain loads, for rows that TMA cannot copy (not 16-byte aligned): zeros behind n rows and dim columns.
+// (2048 tokens of 8 heads of 128 x 128: 180 us, 33 by TMA; with 4-byte loads, 16 on their way a lane, 131 where rows are aligned
+// to that, 342 where not, and ten ragged sequences' gradients, which never come here, 232 against 224 by its registers.)
 template <int BLOCKS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t stride, int n, int dim, int tid)
 {

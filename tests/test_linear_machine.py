@@ -293,3 +293,31 @@ def test_broadcast_inputs(dtype):
     ref, mag = lc.references(c)
     for n, t in {"o": o, **grads}.items():
         lc.check(c, n, t, ref[n], mag[n], dtype if n != "dg" else "f32")
+
+
+@pytest.mark.parametrize("offset", [1, 2, 4, 8])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 72), (16, 24)])
+def test_rows_at_any_address(K, V, offset):
+    """bf16 rows that start 2, 4, 8 or 16 bytes past their alignment, at strides that keep them there."""
+    c = lc.make([140, 75], 2, 4, K, V, "bf16", 90 + offset)
+    T, H, HV = 215, 2, 4
+
+    def put(a):
+        heads, n = a.shape[1:]
+        rows = torch.full((T, offset + heads * n), float("nan"), dtype=torch.bfloat16, device="cuda")
+        view = rows[:, offset:].unflatten(1, (heads, n))
+        view.copy_(torch.from_numpy(a))
+        return view
+
+    q, k, v, do, g = put(c["q"]), put(c["k"]), put(c["v"]), put(c["do"]), lc.f32(c["g"])
+    o, grads = torch.empty_like(v), {"dq": put(c["q"]), "dk": put(c["k"]), "dv": put(c["v"]), "dg": torch.empty_like(g)}
+    space = lambda b: gdn.linear_attention_workspace(T, H, HV, K, V, sequences=2, uniform=False, backward=b)
+    start, end = lc.f32(c["initial"]), lc.f32(c["d_final"])
+    final, d0 = torch.empty_like(start), torch.empty_like(start)
+    gdn.gdn_linear_attention(q, k, v, g, o, initial_state=start, final_state=final, cu_seqlens=lc.cu(c["lengths"]), workspace=space(False))
+    gdn.gdn_linear_attention_backward(q, k, v, g, do, initial_state=start, d_final_state=end, d_initial_state=d0,
+                                      cu_seqlens=lc.cu(c["lengths"]), workspace=space(True), **grads)
+    torch.cuda.synchronize()
+    ref, mag = lc.references(c)
+    for n, t in {"o": o, "final": final, "d_initial": d0, **grads}.items():
+        lc.check(c, n, t, ref[n], mag[n], "bf16" if n in ("o", "dq", "dk", "dv") else "f32")
