@@ -321,3 +321,60 @@ def test_rows_at_any_address(K, V, offset):
     ref, mag = lc.references(c)
     for n, t in {"o": o, "final": final, "d_initial": d0, **grads}.items():
         lc.check(c, n, t, ref[n], mag[n], "bf16" if n in ("o", "dq", "dk", "dv") else "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_and_states_gigabytes_apart(dtype):
+    """Offsets beyond 32 bits: token rows 2^30 elements apart, and the last slots of a pool of 9 GB."""
+    T, H, HV, K, V = 5, 2, 4, 128, 128
+    c = lc.make([T], H, HV, K, V, dtype, 77)
+    c["d_final"] = None
+    gap = 1 << 30
+    memory = torch.empty((T - 1) * gap + 16384, dtype=lc.TYPES[dtype], device="cuda")
+    used = [0]
+
+    def far(a=None, heads=None, n=None):
+        heads, n = (a.shape[1], a.shape[2]) if a is not None else (heads, n)
+        t = memory[used[0]:].as_strided((T, heads, n), (gap, n, 1))
+        used[0] += heads * n
+        if a is not None:
+            t.copy_(torch.from_numpy(np.ascontiguousarray(a)))
+        return t
+
+    q, k, v, do = (far(c[n]) for n in ("q", "k", "v", "do"))
+    o, dq, dk, dv = far(None, HV, V), far(None, H, K), far(None, H, K), far(None, HV, V)
+    g = lc.f32(c["g"])
+    slots, num = torch.tensor([4290], dtype=torch.int32, device="cuda"), 4300
+    pool = torch.empty(num, HV, V, K, device="cuda")
+    pool[4290] = lc.f32(c["initial"][0])
+    gdn.gdn_linear_attention(q, k, v, g, o, sequences=1, state_indices=slots, initial_state=pool, final_state=pool)
+    final = pool[4290:4291].clone()
+    pool[4290] = lc.f32(c["initial"][0])
+    dg = torch.empty_like(g)
+    ws = gdn.linear_attention_workspace(T, H, HV, K, V, backward=True, dtype=lc.TYPES[dtype])
+    gdn.gdn_linear_attention_backward(q, k, v, g, do, sequences=1, state_indices=slots, initial_state=pool, dq=dq, dk=dk, dv=dv, dg=dg,
+                                      workspace=ws)
+    torch.cuda.synchronize()
+    ref, mag = lc.references(c)
+    for n, t in {"o": o, "final": final, "dq": dq, "dk": dk, "dv": dv, "dg": dg}.items():
+        lc.check(c, n, t, ref[n], mag[n], dtype if n in ("o", "dq", "dk", "dv") else "f32")
+    # rotary positions there and on dense copies
+    near, positions, table = q.contiguous(), torch.arange(T, dtype=torch.int32, device="cuda"), gdn.rotary_frequencies(K)
+    gdn.gdn_rotary(q, None, positions, table)
+    gdn.gdn_rotary(near, None, positions, table)
+    assert torch.equal(q, near)
+    del memory, q, k, v, do, o, dq, dk, dv, pool
+    # a pool of more than 2^31 entries: the last slot gives what a slot of a small pool gives
+    HV = 33
+    big, small = torch.empty(4300, HV, V, K, device="cuda"), torch.randn(1, HV, V, K, device="cuda")
+    big[4290] = small[0]
+    x = [torch.randn(1, n, K, device="cuda").to(lc.TYPES[dtype]) for n in (HV, HV, HV)]
+    decay, idx = -torch.rand(1, HV, device="cuda"), torch.tensor([4290], dtype=torch.int32, device="cuda")
+    outs = [torch.empty(1, HV, V, device="cuda") for _ in range(2)]
+    gdn.gdn_linear_attention_step(*x, decay, big, outs[0], idx)
+    gdn.gdn_linear_attention_step(*x, decay, small, outs[1])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(big[4290], small[0])
+    gdn.gdn_linear_attention(*x, decay, outs[0], sequences=1, state_indices=idx, initial_state=big, final_state=big)
+    gdn.gdn_linear_attention(*x, decay, outs[1], sequences=1, initial_state=small, final_state=small)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(big[4290], small[0])
