@@ -17,7 +17,10 @@
  * with dq and dk summed over the value heads that share them, and dg over tokens where g is one per head.
  *
  * Arithmetic and states are fp32 whatever the inputs' type (states are stored in fp32, for the step also in
- * bf16). A log decay below -200 counts as -200 (a factor of 0 in fp32); infinite inputs count as NaN, and a
+ * bf16). With bf16 inputs the sequences' products take what is not bf16 already as a sum of bf16 numbers: the states carried
+ * from token to token keep 24 bits; where a token's output or gradient is summed, the state that it meets and its
+ * score times decay keep 16 bits, so that the sum is off by at most 2^-16 of the sum of its terms' magnitudes beside what fp32
+ * sums lose. Where dg is asked for, the states that dq and dk meet keep 24 bits: their last bits may depend on it. A log decay below -200 counts as -200 (a factor of 0 in fp32); infinite inputs count as NaN, and a
  * NaN reaches what the formulas say it reaches: outputs of its own token and of later ones (gradients of k, v
  * and g: of earlier ones), and no other sequence.
  *

@@ -315,7 +315,7 @@ int gdn_linear_attention(const gdn_linear_args *args, gdn_stream_t stream)
     gdn::LinearSweep p = gdn::forward_sweep(P);
     p.start = a.initial_state;
     p.end = a.final_state;
-    p.out = a.o, p.out_stride = a.o_stride, p.out_head = a.o_head_stride, p.out_f32 = p.exact = a.out_dtype == GDN_F32;
+    p.out = a.o, p.out_stride = a.o_stride, p.out_head = a.o_head_stride, p.out_f32 = a.out_dtype == GDN_F32;
     rc = gdn::run_states(P, p, s);
     return rc != GDN_OK ? rc : gdn::run(P, p, s);
 }

@@ -6,8 +6,8 @@
 //     State <- e^{G_last} State + sum_s e^{G_last - G_s} y_s z_s^T
 // Four products a chunk, each with fp32 sums in tensor memory:
 //     scores  [r, s] = x y^T                      both operands as loaded
-//     inter   [r, z] = x State                    State from registers through shared memory, as one to three bf16 terms
-//     out     [r, z] = inter e^{G_r} + P z        P = scores times decays, one or two bf16 terms, in tensor memory over the scores
+//     inter   [r, z] = x State                    State from registers through shared memory, as two or three bf16 terms
+//     out     [r, z] = inter e^{G_r} + P z        P = scores times decays, two bf16 terms, in tensor memory over the scores
 //     update  [y, z] = Y^T z                      Y = y e^{G_last - G_s}, three bf16 terms, in tensor memory, 32 tokens at a time
 // The terms are what keeps fp32: x, y and z are bf16 and exact, the state itself stays in fp32 registers (a lane of tensor
 // memory is a row y of it, the columns z are shared by two warpgroups), a product's sum is added to it in fp32 once a chunk. The
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     constexpr bool OUT = NS > 0;
     constexpr int kSlots = M::kSlots;
     constexpr int YP = 64 * YB, ZP = 64 * ZB;
-    constexpr int NP = NS == 1 ? 1 : 2;               // terms of P
+    constexpr int NP = 2;                             // terms of P
     constexpr int TILES = OUT ? 3 : 2;                // x, y, z (x only with outputs)
     constexpr int YI = OUT ? 1 : 0, ZI = OUT ? 2 : 1;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -939,10 +939,11 @@ int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, i
 template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSweep &p, bool outputs, const ChunkMaps &maps, int wide, cudaStream_t stream)
 {
     if (!outputs) return launch<YB, ZB, 0>(P, p, maps, wide, stream);
-    // Terms of the state and of P: one for bf16 outputs (their error against 64 bits grows by at most the square root of
-    // two: each of P, the state and the output is rounded once to bf16), two for fp32 outputs; what dg is summed from keeps the
-    // state whole.
-    if (!p.dot && !p.exact) return launch<YB, ZB, 1>(P, p, maps, wide, stream);
+    // Terms of the state and of P: two of each, whose remainder is at most 2^-16 of a term of the outputs' sums. One would do where
+    // the sums' terms do not cancel (zero-mean inputs: 0.0023 of the norm off, 0.0017 with two as by rounding the exact result to bf16),
+    // but keys or values with a common mean leave outputs far below their terms: 1024 tokens of mean 1 and spread 0.1, q
+    // orthogonal to the mean: 0.38 off with one term, 0.0017 with two. (32768 tokens of 32 heads: 455 us, 423 with one; 24 ragged
+    // prompts 148 and 136; gradients of 8 x 2048 816 and 790.) What dg is summed from keeps the state whole, as three.
     return p.dot ? launch<YB, ZB, 3>(P, p, maps, wide, stream) : launch<YB, ZB, 2>(P, p, maps, wide, stream);
 }
 

@@ -30,7 +30,6 @@ struct LinearSweep {
     const void *dot_with;
     int64_t dot_stride, dot_head;
     int dot_group;
-    int exact;                         // outputs to more than bf16
     // for dg, per chunk (chunk c of sequence s: its first row / 128 + s; of the fp32 kernel per segment) and value head:
     float *chunk_states;               // the state behind it, in the kernel's own order
     float *chunk_dot;                  // given, chunk_states is read, and the parts of its product with the state the
