@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     };
     // warp 0: the factors of a block's tokens; held: log2 of the decay since the reference token (steps of 2^-40)
     constexpr long long kOne = 1ll << 40;
-    long long held = 0, all = 0;
+    long long held = 0;
+    double all = 0.0;                                                          // of the whole segment: its steps would pass 64 bits after 29000
+                                                                               // tokens of the largest decay
     bool lost = false;                                                         // a NaN came
     const auto factors = [&](int block, int b) {
         const int r = block * kBlock + lane;
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             s_each[b] = each;
         }
         if (!each) held += span;
-        all += span;
+        if (!OUT) all += (double)span * 0x1p-40;
         lost = lost || nans;
     };
 
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     float *to = nullptr;
     if (!OUT) {
         to = P.local + item_state;
-        if (tid == 0 && zpart == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = lost ? __int_as_float(0x7fc00000) : (float)((double)all * 0x1p-40);
+        if (tid == 0 && zpart == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = lost ? __int_as_float(0x7fc00000) : (float)all;
     } else if (ends && !skip && p.end) {
         to = p.end + ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     }
