@@ -2,10 +2,13 @@
 //
 // A CTA owns one segment of a sequence, one value head and 64 columns of z; a thread keeps 16 x 2 entries of the state
 // State[y, z] in registers: DY / 16 lanes side by side share two columns. A token costs every entry two multiply-adds,
-// State += y z and out += State x; the decay costs none: the state is kept divided by the decay since a reference
-// token, z is divided by it as it is staged and out multiplied. The reference moves up when that decay falls below
-// 2^-20, and a block of 16 tokens that decays by more than 2^-60 in itself is taken with one more product an entry
-// and token instead. Log decays are summed in 64 bits, so a long memory loses nothing to rounded factors near one.
+// State += y z and out += State x; the decay costs none: the state is kept times the decay up to a reference token ahead
+// (2^-held, held >= 0), z is multiplied by it as it is staged and out divided. So what is kept is never above the state itself, and
+// below it by no more than 2^40, in a block of 16 tokens that decays by less than 16 octaves no more than 2^21: neither end of
+// fp32's range comes nearer than that. (Kept divided by the decay since a token behind, products above 2^48 overflowed.)
+// The reference moves by whole octaves, which is exact, and a block that decays by more than 28 octaves in itself, or grows by
+// more than five, is taken with one more product an entry and token instead. Log decays are summed in 64 bits, so a
+// long memory loses nothing to rounded factors near one.
 // x, y (broadcast within a column pair's lanes) and z come from shared memory, 16 tokens at a time, the next 16
 // already on their way in registers.
 //
@@ -33,7 +36,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     constexpr int EX = kBlock * NY / NT, EZ = kBlock * kLinearZ / NT;          // elements staged by a thread
     __shared__ __align__(16) float sx[2][kBlock][NY], sy[2][kBlock][NY], sz[2][kBlock][kLinearZ];
     __shared__ float so[OUT ? kBlock : 1][kLinearZ];
-    __shared__ float s_in[2][kBlock], s_out[2][kBlock], s_first[2];
+    __shared__ float s_in[2][kBlock], s_out[2][kBlock], s_first[2], s_z[2];
     __shared__ int s_each[2];
     __shared__ LinearItem s_item;
     __shared__ float s_last;
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             sz[b][e / kLinearZ][e % kLinearZ] = rz[i];
         }
     };
-    // warp 0: the factors of a block's tokens; held: log2 of the decay since the reference token (steps of 2^-40)
+    // warp 0: the factors of a block's tokens; held: -log2 of the decay up to the reference token (steps of 2^-40)
     constexpr long long kOne = 1ll << 40;
     long long held = 0;
     double all = 0.0;                                                          // of the whole segment: its steps would pass 64 bits after 29000
@@ -151,19 +154,22 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
         const unsigned nans = __ballot_sync(kAll, nan);
         const bool gone = lost || (nans & ((2u << lane) - 1));                  // (it leaves the tokens before it alone)
         const long long span = __shfl_sync(kAll, s, kBlock - 1);
-        const bool each = __any_sync(kAll, s > 60 * kOne || s < -60 * kOne);
-        float f = 1.f;
-        if (each || held > 20 * kOne || held < -20 * kOne) {
-            f = linear_exp2(held);
-            held = 0;
-        }
+        // the lowest and highest sum in octaves (the highest to the next one)
+        const int octaves = lane < kBlock ? (int)(s >> 40) : 0;
+        const int low = min(0, __reduce_min_sync(kAll, octaves)), high = max(0, __reduce_max_sync(kAll, octaves)) + 1;
+        const bool each = low < -28 || high > 5;
+        int move = 0;                                                          // of the reference, in octaves
+        if (each) move = -(int)(held >> 40);
+        else if (held + low * kOne < 0 || held + high * kOne > 40 * kOne) move = (int)(((4 - low) * kOne - held + kOne - 1) >> 40);
+        held += move * kOne;
         const float none = __int_as_float(0x7fc00000);
         if (lane < kBlock) {
-            s_in[b][lane] = gone ? none : each ? linear_exp2(own) : linear_exp2(-(held + s));
-            s_out[b][lane] = each ? 1.f : linear_exp2(held + s);
+            s_in[b][lane] = gone ? none : linear_exp2(each ? own : -(held + s));
+            s_out[b][lane] = linear_exp2(each ? held : held + s);
         }
         if (lane == 0) {
-            s_first[b] = f;
+            s_first[b] = __int_as_float((127 - move) << 23);
+            s_z[b] = linear_exp2(-held);
             s_each[b] = each;
         }
         if (!each) held += span;
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
         const int b = k & 1, rows = min(kBlock, n - k * kBlock);
         if (k + 1 < blocks) fetch(k + 1);
         const bool each = s_each[b];
-        const float f = s_first[b];
+        const float f = s_first[b], block_z = s_z[b];
         if (f != 1.f)
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i][0] *= f, S[i][1] *= f;
@@ -192,10 +198,10 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             if (each) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[i][0] *= fin, S[i][1] *= fin;
-            } else {
-                z.x *= fin;
-                z.y *= fin;
             }
+            const float fz = each ? block_z : fin;
+            z.x *= fz;
+            z.y *= fz;
             float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
         }
     }
 
-    // the state as it is: times the decay since the reference token
+    // the state as it is: divided by the decay up to the reference token
     if (tid == 0) s_last = lost ? __int_as_float(0x7fc00000) : linear_exp2(held);
     __syncthreads();
     float f = s_last;
