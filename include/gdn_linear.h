@@ -76,8 +76,8 @@ typedef struct gdn_linear_args {
                                      other sequences claim hold either one's outputs, and sequences of more
                                      than T rows together may be left out whole); where the state index
                                      is bad, the sequence's outputs and gradients are zeroed and its states left
-                                     out. GDN_DEVERR_TIMEOUT when a bounded wait gave up (that CTA's
-                                     remaining outputs are not written) */
+                                     out. GDN_DEVERR_TIMEOUT when a bounded wait gave up: the outputs,
+                                     states and gradients that needed what it waited for are NaN */
 } gdn_linear_args;
 
 /* The gradients. s holds the forward call's inputs (s.o, s.final_state and s.out_dtype are not used,
@@ -158,6 +158,15 @@ int gdn_linear_attention_backward(const gdn_linear_grad_args *args, gdn_stream_t
  * index is outside [0, num_slots) as well, and raises GDN_DEVERR_BAD_INDEX. Two rows may not name one slot. */
 int gdn_linear_attention_step(const gdn_linear_step_args *args, const int32_t *cache_indices, int32_t pad_slot_id,
                               gdn_stream_t stream);
+
+/*
+ * gdn_linear_set_wait_limit -- test hook, not for production use: sets, for the whole process, the number of SM clock cycles
+ * after which a wait of the bf16 sequences' kernel gives up; 0 restores the default (2^30 cycles, about half a second).
+ * With a limit below a copy's latency a test can make the waits run out and check that the call returns normally, reports
+ * GDN_DEVERR_TIMEOUT and leaves NaN. The waits that let copies and MMAs in flight finish keep the default limit.
+ * Returns the previous setting. Launches nothing.
+ */
+int64_t gdn_linear_set_wait_limit(int64_t cycles);
 
 #ifdef __cplusplus
 }

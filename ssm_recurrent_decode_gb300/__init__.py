@@ -67,7 +67,7 @@ EXPORTS = ("gdn_decode_step", "gdn_decode_step_indexed", "gdn_decode_buffered", 
            "mamba_selective_scan", "mamba_selective_scan_backward", "mamba_scan_workspace_bytes",
            "gdn_beam_select", "gdn_beam_select_workspace_bytes", "gdn_beam_reorder",
            "gdn_linear_attention", "gdn_linear_attention_backward", "gdn_linear_attention_step",
-           "gdn_linear_workspace_bytes", "gdn_rotary")
+           "gdn_linear_workspace_bytes", "gdn_linear_set_wait_limit", "gdn_rotary")
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -241,6 +241,8 @@ def _load(path: str):
     L.gdn_linear_attention_step.restype = ctypes.c_int
     L.gdn_linear_workspace_bytes.argtypes = [_i32] * 9
     L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_linear_set_wait_limit.argtypes = [_i64]
+    L.gdn_linear_set_wait_limit.restype = _i64
     L.gdn_rotary.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
     L.gdn_rotary.restype = ctypes.c_int
     L.gdn_selftest_bounded_wait.argtypes = [_vp, _i64, _i32, _vp]

@@ -33,7 +33,9 @@
 // pair), and in the rare tile that has a non-finite value the outputs' product takes it as zero, the column's first such
 // row is noted, and the outputs get their NaN from there.
 //
-// Every wait is bounded; a wait that gives up raises GDN_DEVERR_TIMEOUT and ends the CTA, its MMAs and copies done.
+// Every wait is bounded; a wait that gives up raises GDN_DEVERR_TIMEOUT and ends the CTA once its MMAs and copies are done. The outputs
+// of its segment and head are NaN then, what other kernels read of it too.
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -63,6 +65,9 @@ static_assert(2 * kStateRegisters + 4 * kOtherRegisters <= 6 * 80, "more registe
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters)); }
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters)); }
 constexpr uint32_t kWaitLimit = 1u << 30;              // SM clock cycles, about half a second
+// The limit of the waits that can give up (0: kWaitLimit); set only by the test hook below. The waits for copies and MMAs in
+// flight always use kWaitLimit.
+std::atomic<uint32_t> g_wait_limit{0};
 
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kOut = 128, kUpdate = 256, kY = 384;
@@ -133,13 +138,13 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t
 }
 
 // Waits for a barrier's phase, every lane of a warp with one answer; false once the CTA gives up. A try suspends the warp
-// for up to a millisecond, so that warps that wait leave the scheduler to those that work.
-__device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity)
+// for up to a millisecond (`suspend` ns), so that warps that wait leave the scheduler to those that work.
+__device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity, uint32_t suspend)
 {
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done)
-                 : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+                 : "r"(smem_u32(bar)), "r"(parity), "r"(suspend)
                  : "memory");
     return done != 0;
 }
@@ -148,7 +153,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars 
     const uint32_t t0 = clock();
     bool done;
     do {
-        done = try_phase(bar, parity & 1u);
+        done = try_phase(bar, parity & 1u, min(limit, 1000000u));
     } while (!done && !*(volatile int *)&B->abort_flag && (uint32_t)clock() - t0 < limit);
     done = __all_sync(kAll, done);
     if (!done) *(volatile int *)&B->abort_flag = 1;
@@ -234,16 +239,20 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     const auto leave = [&]() {
         if (OUT && p.early && tid == 0) grid_dependency_wait();
     };
-    if (it.seq < 0 || (sbase & 1023u)) return leave();
+    if (it.seq < 0) return leave();
     const bool whole = it.seq_end - it.seq_begin <= P.seg;
     if (!OUT && (whole || it.state < 0)) return;
     const int n = it.n, chunks = (n + kRows - 1) / kRows;
+    const auto fill = [&](float v, int first, int warps) {         // the segment's outputs, a warp a row
+        for (int r = first; p.out && r < n; r += warps)
+            for (int c = lane; c < p.DZ; c += 32) {
+                const int64_t at = (int64_t)(it.begin + r) * p.out_stride + (int64_t)hv * p.out_head + c;
+                if (p.out_f32) static_cast<float *>(p.out)[at] = v;
+                else static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(v);
+            }
+    };
     if (it.state < 0) {                               // a bad state index: zeros
-        for (int e = tid; p.out && e < n * p.DZ; e += kThreadsChunk) {
-            const int64_t at = (int64_t)(it.begin + e / p.DZ) * p.out_stride + (int64_t)hv * p.out_head + e % p.DZ;
-            if (p.out_f32) static_cast<float *>(p.out)[at] = 0.f;
-            else static_cast<bf16 *>(p.out)[at] = __float2bfloat16_rn(0.f);
-        }
+        fill(0.f, warp, kThreadsChunk / 32);
         return leave();
     }
     if (warp == 20) {
@@ -308,9 +317,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     issued = m + 1;
                 }
             }
-            if (!ok)                                      // copies in flight land before the CTA ends
-                for (int m = max(0, issued - kSlots); m < issued; ++m)
-                    if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
+            // Copies in flight land before the CTA ends (whether this warp gave up or another one will: nobody else may look
+            // for the last tiles then).
+            for (int m = max(0, issued - kSlots); m < issued; ++m)
+                if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
         } else if (warp == 22) {
             // ---------------------------------------------------------------- decays; z's non-finite values
             // Sums as 64-bit integers in steps of 2^-40 (fp64 runs at two operations a clock and SM, and this warp is on every
@@ -899,7 +909,19 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     }
     tcl_fence_before();
     __syncthreads();
-    if (tid == 0 && B.abort_flag) raise_flag(P.a.err_flags, GDN_DEVERR_TIMEOUT);
+    if (B.abort_flag && warp >= 12 && warp < 20) {    // (warps with registers to spare)
+        const float none = __int_as_float(0x7fc00000);
+        if (tid == 384) raise_flag(P.a.err_flags, GDN_DEVERR_TIMEOUT);
+        if (!OUT) {
+            if (tid == 384) P.total[(size_t)it.id * P.a.HV + hv] = none;          // and with it the states of the segments behind
+        } else {
+            fill(none, warp - 12, 8);
+            if (NS == 3 && p.dot)
+                for (int r = tid - 384; r < n; r += 256) p.dot[(size_t)(it.begin + r) * P.a.HV + hv] = none;
+            if (p.end && (p.reverse ? it.index == 0 : it.begin + n == it.seq_end))
+                for (int e = tid - 384; e < P.a.K * P.a.V; e += 256) p.end[state_at + e] = none;
+        }
+    }
     if (warp == 20) {
         tcl_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -952,7 +974,8 @@ template <int YB, int ZB> int launch_size(const LinearLaunch &P, const LinearSwe
 int launch_linear_chunk(const LinearLaunch &launch, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
     LinearLaunch P = launch;
-    if (P.wait_limit == 0) P.wait_limit = kWaitLimit;
+    const uint32_t limit = g_wait_limit.load(std::memory_order_relaxed);
+    P.wait_limit = limit ? limit : kWaitLimit;
     const auto wide_rows = [](const void *q, int64_t stride, int64_t head, int n, int es) {
         return q && reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride * es % 16 == 0 && head * es % 16 == 0 && n * es % 16 == 0;
     };
@@ -970,3 +993,8 @@ int launch_linear_chunk(const LinearLaunch &launch, const LinearSweep &p, bool o
 }
 
 }  // namespace gdn
+
+extern "C" int64_t gdn_linear_set_wait_limit(int64_t cycles)
+{
+    return gdn::g_wait_limit.exchange(cycles <= 0 ? 0u : cycles < gdn::kWaitLimit ? (uint32_t)cycles : gdn::kWaitLimit);
+}

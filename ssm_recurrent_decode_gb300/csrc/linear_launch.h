@@ -52,7 +52,7 @@ struct LinearLaunch {
     // workspace
     float *local;       // [items, HV, V, K] the state that a segment ends with from zero; then the one it starts with
     float *total;       // [items, HV] log2 of the segment's decay
-    long long wait_limit;
+    uint32_t wait_limit;  // SM clock cycles of a wait that can give up
 };
 
 constexpr int kLinearSorted = 64;      // up to so many sequences, the longest start first
