@@ -73,8 +73,8 @@ typedef struct gdn_linear_args {
     int32_t *err_flags;           /* optional device word: GDN_DEVERR_BAD_INDEX is ORed in for a state index
                                      outside [0, num_states) and for a sequence whose cu_seqlens leave 0 .. T or
                                      decrease (its rows are not written; of such a table, rows that two
-                                     other sequences claim hold either one's outputs, and sequences of more
-                                     than T rows together may be left out whole); where the state index
+                                     other sequences claim hold either one's outputs, dg is undefined, and
+                                     sequences of more than T rows together may be left out whole); where the state index
                                      is bad, the sequence's outputs and gradients are zeroed and its states left
                                      out. GDN_DEVERR_TIMEOUT when a bounded wait gave up: the outputs,
                                      states and gradients that needed what it waited for are NaN */
@@ -132,7 +132,7 @@ typedef struct gdn_linear_step_args {
 } gdn_linear_step_args;
 
 /* Bytes of workspace that a call with these sizes needs; uniform: non-zero when cu_seqlens is NULL. 0 for
- * sizes that the calls refuse. */
+ * sizes that the calls refuse. It goes by how the sequences are cut: fewer tokens or sequences may need more. */
 size_t gdn_linear_workspace_bytes(int32_t T, int32_t S, int32_t H, int32_t HV, int32_t K, int32_t V, int32_t in_dtype,
                                   int32_t uniform, int32_t backward);
 

@@ -989,7 +989,8 @@ def _log_decays(g, rows, heads):
 def linear_attention_workspace(T, H, HV, K, V, *, sequences=1, uniform=True, backward=False, dtype=None, device=None):
     """A workspace tensor for gdn_linear_attention (or its backward pass) over T token rows of `sequences` sequences,
     of equal lengths (uniform) or given by cu_seqlens, with inputs of `dtype` (default bfloat16); None when the call
-    needs none. Calls that may run at the same time need one each."""
+    needs none. It is for these sizes: fewer tokens or sequences, cut otherwise, may need more. Calls that may run at the
+    same time need one each."""
     torch = _torch()
     code = GDN_F32 if dtype == torch.float32 else GDN_BF16
     nbytes = lib().gdn_linear_workspace_bytes(int(T), int(sequences), int(H), int(HV), int(K), int(V), code, int(uniform),

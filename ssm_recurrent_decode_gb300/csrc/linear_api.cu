@@ -1,4 +1,5 @@
 // linear_api.cu -- host checks, workspace layout and dispatch of linear attention.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -20,7 +21,7 @@ bool overlap(const void *p, const void *q, size_t bytes)
 
 bool sizes_ok(const gdn_linear_args &a, bool uniform)
 {
-    return a.T >= 0 && a.S >= 1 && a.H >= 1 && a.HV >= 1 && a.HV <= 65535 && a.HV % a.H == 0 && a.V >= 1 && a.V <= 128 &&
+    return a.T >= 0 && a.S >= 1 && (int64_t)a.S + a.T / 16 <= INT32_MAX && a.H >= 1 && a.HV >= 1 && a.HV <= 65535 && a.HV % a.H == 0 && a.V >= 1 && a.V <= 128 &&
            (a.K == 16 || a.K == 32 || a.K == 64 || a.K == 128) && (!uniform || a.T % a.S == 0);
 }
 
@@ -58,6 +59,8 @@ void set_segments(LinearLaunch &P, bool uniform, int64_t seg)
     P.seg = (int)seg;
     P.carried = longest > seg;
     P.items = (int)(uniform ? (int64_t)P.a.S * (P.Ls > 0 ? (P.Ls + seg - 1) / seg : 1) : P.a.S + P.a.T / seg);
+    // (a sequence that is cut has more than seg rows, and at most twice as many segments as whole ones)
+    P.cut_items = uniform || P.a.S <= kLinearSorted ? P.items : (int)std::min<int64_t>(P.items, 2 * (P.a.T / seg));
 }
 
 // Rows of a segment of equal sequences: as many segments as make the shortest run of rounds of CTAs, in units of a chunk's 4.4 us.
@@ -123,8 +126,8 @@ size_t carve(LinearLaunch &P, BackwardSpace *B, PackedSpace &packed, unsigned ch
         if (B) packed.d_o = w.take(v);
     }
     if (P.carried) {
-        P.local = w.take((size_t)P.items * a.HV * a.K * a.V);
-        P.total = w.take((size_t)P.items * a.HV);
+        P.local = w.take((size_t)P.cut_items * a.HV * a.K * a.V);
+        P.total = w.take((size_t)P.cut_items * a.HV);
     }
     if (B) {
         const size_t th = (size_t)a.T * a.HV;

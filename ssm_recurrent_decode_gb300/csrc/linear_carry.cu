@@ -10,19 +10,28 @@ namespace {
 // entries of a sequence's states over all its segments; memory-bound, 8 K V bytes a segment and head.
 __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant__ LinearLaunch P, const __grid_constant__ LinearSweep p)
 {
-    const int s = blockIdx.x, hv = blockIdx.y;
-    int b, e;
-    bool bad;
-    linear_rows(P, s, b, e, bad);
-    const int segs = linear_segments(P, e - b);
-    if (bad || segs == 1) return;
-    int state = s;
-    if (P.states) {
-        if (P.a.state_indices) state = P.a.state_indices[s];
-        if (state < 0 || state >= P.a.num_states) return;
+    const int hv = blockIdx.y;
+    int state, item0, segs;
+    if (linear_many(P)) {                            // CTAs for the segments of sequences that are cut; the first one's work
+        __shared__ LinearItem s_item;
+        __shared__ LinearScan s_scan;
+        linear_find<256>(P, blockIdx.x, true, false, 0, s_scan, &s_item);
+        const LinearItem it = s_item;
+        if (it.seq < 0 || it.index > 0 || it.state < 0) return;
+        state = it.state;
+        item0 = it.slot;
+        segs = linear_segments(P, it.seq_end - it.seq_begin);
+    } else {
+        const int s = blockIdx.x;
+        int b, e;
+        bool bad;
+        linear_rows(P, s, b, e, bad);
+        segs = linear_segments(P, e - b);
+        if (bad || segs == 1) return;
+        state = linear_state(P, s, false);
+        item0 = linear_first_item(P, s);
+        if (state < 0 || item0 + segs > P.items) return;     // (left out, as in linear_item)
     }
-    const int item0 = linear_first_item(P, s);
-    if (item0 + segs > P.items) return;              // (left out, as in linear_item)
     const int KV = P.a.K * P.a.V, at = (blockIdx.z * 256 + threadIdx.x) * 4;
     if (at >= KV) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -50,17 +59,34 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant
     }
 }
 
-// A warp per token and q/k head: the sum over the value heads that share it, and each one's product with `with`.
-constexpr int kFoldRows = 64;          // token rows of a segment per CTA
+// A warp per token and q/k head: the sum over the value heads that share it, and each one's product with `with`. A CTA takes
+// kFoldRows token rows, those among them that some sequence has. (A grid of segments x the longest segment's rows, whose CTAs each
+// count all sequences, grows with the square of their number: gradients of 2048 documents of 256 tokens, 32 heads of 128 x 128,
+// took 1757 ms, 34 so; of 64 documents 1.39 and 1.30.)
+constexpr int kFoldRows = 64;
 template <typename Tin>
 __global__ void __launch_bounds__(256) linear_fold_kernel(const __grid_constant__ LinearLaunch P, const __grid_constant__ LinearFold f)
 {
     const int lane = threadIdx.x & 31, h = blockIdx.y, K = P.a.K, G = P.a.HV / P.a.H;
-    const LinearItem it = linear_item(P, blockIdx.x, false);
-    if (it.seq < 0) return;
-    const int last = min(it.n, ((int)blockIdx.z + 1) * kFoldRows);
-    for (int r = blockIdx.z * kFoldRows + (threadIdx.x >> 5); r < last; r += 8) {
-        const int64_t t = it.begin + r;
+    const int64_t t0 = (int64_t)blockIdx.x * kFoldRows;
+    __shared__ unsigned long long s_mine;
+    __shared__ LinearScan s_scan;
+    unsigned long long mine = ~0ull;
+    static_assert(kFoldRows == 64, "a bit a row");
+    if (P.a.cu_seqlens) {
+        if (threadIdx.x == 0) s_mine = 0;
+        __syncthreads();
+        linear_each<256>(P, s_scan, [&](int, int b, int e, bool bad, long long, long long) {
+            const int from = (int)max((int64_t)0, b - t0), to = (int)min((int64_t)kFoldRows, e - t0);
+            if (!bad && from < to) atomicOr(&s_mine, (~0ull >> (64 - (to - from))) << from);
+        });
+        __syncthreads();
+        mine = s_mine;
+    }
+    const int last = (int)min((int64_t)kFoldRows, P.a.T - t0);
+    for (int r = threadIdx.x >> 5; r < last; r += 8) {
+        if (!(mine >> r & 1)) continue;
+        const int64_t t = t0 + r;
         float sum[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -115,7 +141,10 @@ __global__ void __launch_bounds__(kDgHeads *kDgRanges) linear_dg_kernel(const __
     const int i = threadIdx.x % kDgHeads, range = threadIdx.x / kDgHeads;
     const int hv = blockIdx.y * kDgHeads + i, HV = P.a.HV;
     __shared__ float hi[kDgRanges][kDgHeads], lo[kDgRanges][kDgHeads];
-    const LinearItem it = linear_item(P, blockIdx.x, false);
+    __shared__ LinearItem s_item;
+    __shared__ LinearScan s_scan;
+    linear_find<kDgHeads * kDgRanges>(P, blockIdx.x, false, false, 0, s_scan, &s_item);
+    const LinearItem it = s_item;
     const bool skip = it.seq < 0 || it.state < 0;
     const int b = it.begin, e = it.seq < 0 ? b : b + it.n;
     const int per = (e - b + kDgRanges - 1) / kDgRanges;
@@ -151,13 +180,13 @@ __global__ void __launch_bounds__(kDgHeads *kDgRanges) linear_dg_kernel(const __
     if (fixed) part[((size_t)blockIdx.x * kDgRanges + range) * HV + hv] = total.value();
 }
 
-// dg of one decay a head: the ranges' sums of every segment, in order
-__global__ void __launch_bounds__(256) linear_dg_fixed_kernel(const float *part, int rows, int HV, float *dg)
+// dg of one decay a head: the ranges' sums of every segment (eight of every chunk), in order
+__global__ void __launch_bounds__(256) linear_dg_fixed_kernel(const float *part, int64_t rows, int HV, float *dg)
 {
     const int hv = blockIdx.x;
     __shared__ double sums[8];
     double s = 0.0;
-    for (int r = threadIdx.x; r < rows; r += 256) s += part[(size_t)r * HV + hv];
+    for (int64_t r = threadIdx.x; r < rows; r += 256) s += part[(size_t)r * HV + hv];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
@@ -169,17 +198,44 @@ __global__ void __launch_bounds__(256) linear_dg_fixed_kernel(const float *part,
 }
 
 // Of the tensor-core kernel: no sum is longer than a chunk. A CTA per chunk and 32 heads, eight ranges of 16 rows.
+struct DgChunk {
+    int seq, at, rows;
+};
 __global__ void __launch_bounds__(256) linear_dg_chunk_kernel(const __grid_constant__ LinearLaunch P, const float *qdq, const float *kdk,
                                                            const float *chunk_dot, float *dg, int64_t dg_stride, float *part)
 {
-    const int i = threadIdx.x & 31, range = threadIdx.x >> 5, hv = blockIdx.z * 32 + i, HV = P.a.HV;
+    const int i = threadIdx.x & 31, range = threadIdx.x >> 5, hv = blockIdx.y * 32 + i, HV = P.a.HV;
+    const int id = blockIdx.x;                        // first row / 128 + sequence
     __shared__ float sums[8][32];
-    const LinearItem it = linear_item(P, blockIdx.x, false);
-    const int at = it.begin + blockIdx.y * kLinearChunk, rows = min(kLinearChunk, it.begin + it.n - at);
-    if (it.seq < 0 || rows <= 0) return;
-    const bool mine = hv < HV && it.state >= 0;
+    __shared__ DgChunk s_chunk;
+    __shared__ LinearScan s_scan;
+    if (threadIdx.x == 0) s_chunk.seq = -1;
+    __syncthreads();
+    const auto take = [&](int s, int b, int e) {
+        const int j = id - s - b / kLinearChunk;
+        if (j < 0 || (int64_t)j * kLinearChunk >= e - b) return;
+        const int at = b + j * kLinearChunk;
+        s_chunk = {s, at, min(kLinearChunk, e - at)};
+    };
+    if (P.a.cu_seqlens) {
+        linear_each<256>(P, s_scan, [&](int s, int b, int e, bool bad, long long, long long) {
+            if (!bad) take(s, b, e);                  // (one sequence, or of borders that decrease any of them)
+        });
+    } else if (threadIdx.x < 2) {
+        // s L / 128 + s <= id, the last such s: 128 id / (L + 128), or the one behind it
+        const int64_t s = (int64_t)id * kLinearChunk / (P.Ls + kLinearChunk) + threadIdx.x;
+        if (s < P.a.S) take((int)s, (int)s * P.Ls, (int)s * P.Ls + P.Ls);
+    }
+    __syncthreads();
+    const DgChunk it = s_chunk;
+    const int at = it.at, rows = it.seq < 0 ? 0 : it.rows;
+    const bool fixed = P.a.g_stride == 0;
+    if (it.seq < 0) {                                 // nobody's
+        if (fixed && hv < HV) part[((size_t)id * 8 + range) * HV + hv] = 0.f;
+        return;
+    }
+    const bool mine = hv < HV && linear_state(P, it.seq, false) >= 0;
     const int first = 16 * range, last = min(rows, first + 16);
-    const size_t chunk = (size_t)(at / kLinearChunk + it.seq) * HV + hv;
     float d[16], sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -193,9 +249,8 @@ __global__ void __launch_bounds__(256) linear_dg_chunk_kernel(const __grid_const
     if (hv >= HV) return;
     float run = 0.f, total = 0.f;
     if (mine)
-        for (int k = 0; k < 8; ++k) run += chunk_dot[chunk * 8 + k];
+        for (int k = 0; k < 8; ++k) run += chunk_dot[((size_t)id * HV + hv) * 8 + k];
     for (int r = 7; r > range; --r) run += sums[r][i];
-    const bool fixed = P.a.g_stride == 0;
 #pragma unroll
     for (int k = 15; k >= 0; --k) {
         run += d[k];
@@ -205,30 +260,7 @@ __global__ void __launch_bounds__(256) linear_dg_chunk_kernel(const __grid_const
     }
     if (fixed) {
         __syncwarp();
-        part[chunk * 8 + range] = total;
-    }
-}
-
-// dg of one decay a head: every chunk's parts, in order
-__global__ void __launch_bounds__(256) linear_dg_chunk_fixed_kernel(const __grid_constant__ LinearLaunch P, const float *part, float *dg)
-{
-    const int hv = blockIdx.x;
-    __shared__ double sums[8];
-    double sum = 0.0;
-    for (int s = 0; s < P.a.S; ++s) {
-        int b, e;
-        bool bad;
-        linear_rows(P, s, b, e, bad);
-        for (int k = threadIdx.x; k < (e - b + kLinearChunk - 1) / kLinearChunk * 8; k += 256)
-            sum += part[((size_t)((b + (k >> 3) * kLinearChunk) / kLinearChunk + s) * P.a.HV + hv) * 8 + (k & 7)];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) sum += sums[w];
-        dg[hv] = (float)sum;
+        part[((size_t)id * 8 + range) * HV + hv] = total;
     }
 }
 
@@ -266,14 +298,15 @@ int launch_linear_pack(const void *from, int64_t stride, int64_t head, int T, in
 
 int launch_linear_carry(const LinearLaunch &P, const LinearSweep &p, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)P.a.S, (unsigned)P.a.HV, (unsigned)((P.a.K * P.a.V + 1023) / 1024));
+    const dim3 grid((unsigned)(P.a.cu_seqlens && P.a.S > kLinearSorted ? P.cut_items : P.a.S), (unsigned)P.a.HV, (unsigned)((P.a.K * P.a.V + 1023) / 1024));
     linear_carry_kernel<<<grid, 256, 0, stream>>>(P, p);
     return status();
 }
 
 int launch_linear_fold(const LinearLaunch &P, const LinearFold &f, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)P.items, (unsigned)P.a.H, (unsigned)((P.seg + kFoldRows - 1) / kFoldRows));
+    if (P.a.T == 0) return GDN_OK;
+    const dim3 grid((unsigned)(((int64_t)P.a.T + kFoldRows - 1) / kFoldRows), (unsigned)P.a.H);
     if (P.a.in_dtype == GDN_BF16) linear_fold_kernel<bf16><<<grid, 256, 0, stream>>>(P, f);
     else linear_fold_kernel<float><<<grid, 256, 0, stream>>>(P, f);
     return status();
@@ -284,16 +317,16 @@ int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, 
 {
     const dim3 grid((unsigned)P.items, (unsigned)((P.a.HV + kDgHeads - 1) / kDgHeads));
     linear_dg_kernel<<<grid, kDgHeads * kDgRanges, 0, stream>>>(P, qdq, kdk, segment_dot, parts, dg, dg_stride, part);
-    if (P.a.g_stride == 0) linear_dg_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(part, P.items * kDgRanges, P.a.HV, dg);
+    if (P.a.g_stride == 0) linear_dg_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(part, (int64_t)P.items * kDgRanges, P.a.HV, dg);
     return status();
 }
 
 int launch_linear_dg_chunks(const LinearLaunch &P, const float *qdq, const float *kdk, const float *chunk_dot, float *dg,
                             int64_t dg_stride, float *part, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)P.items, (unsigned)((P.seg + kLinearChunk - 1) / kLinearChunk), (unsigned)((P.a.HV + 31) / 32));
-    linear_dg_chunk_kernel<<<grid, 256, 0, stream>>>(P, qdq, kdk, chunk_dot, dg, dg_stride, part);
-    if (P.a.g_stride == 0) linear_dg_chunk_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(P, part, dg);
+    const int ids = P.a.T / kLinearChunk + P.a.S;
+    linear_dg_chunk_kernel<<<dim3((unsigned)ids, (unsigned)((P.a.HV + 31) / 32)), 256, 0, stream>>>(P, qdq, kdk, chunk_dot, dg, dg_stride, part);
+    if (P.a.g_stride == 0) linear_dg_fixed_kernel<<<P.a.HV, 256, 0, stream>>>(part, (int64_t)ids * 8, P.a.HV, dg);
     return status();
 }
 

@@ -111,7 +111,7 @@ template <int NS> struct Smem {
     static constexpr uint32_t kBad = kDecays + sizeof(Decays);        // uint8 [128]: first non-finite row of a column of z
     static constexpr uint32_t kBars = kBad + kRows;
     static constexpr uint32_t kBytes = kBars + sizeof(Bars);
-    static_assert(kSlots <= kMostSlots && kBytes <= 232448 && sizeof(LinearItem) <= sizeof(Decays), "more than an SM's shared memory");
+    static_assert(kSlots <= kMostSlots && kBytes <= 232448 && sizeof(LinearItem) <= 64 && 64 + sizeof(LinearScan) <= sizeof(Decays), "more than an SM's shared memory");
 };
 
 // A tile by plain loads, for rows that TMA cannot copy (not 16-byte aligned): zeros behind n rows and dim columns.
@@ -228,12 +228,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         B.abort_flag = B.zero = B.bad[0] = B.bad[1] = 0;
         fence_barrier_init();
     }
-    if (warp == 22) {
-        const LinearItem it = linear_item(P, linear_turn(P, blockIdx.x / P.a.HV), OUT && hv == 0);
-        if (lane == 0) *reinterpret_cast<LinearItem *>(sm + M::kDecays) = it;   // (the decays come later)
-    }
-    __syncthreads();
-    const LinearItem it = *reinterpret_cast<const LinearItem *>(sm + M::kDecays);
+    LinearItem *found = reinterpret_cast<LinearItem *>(sm + M::kDecays);       // (the decays come later)
+    const int turn = warp == 22 ? linear_turn(P, blockIdx.x / P.a.HV) : blockIdx.x / P.a.HV;
+    linear_find<kThreadsChunk>(P, turn, !OUT, OUT && hv == 0, 22, *reinterpret_cast<LinearScan *>(sm + M::kDecays + 64), found);
+    const LinearItem it = *found;
     if (OUT && p.before_next && tid == 0) grid_launch_dependents();
     // (a CTA of a launch that may have started early ends behind the launch before it, on every path)
     const auto leave = [&]() {
@@ -277,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     bool ok = true;
     const auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &B, P.wait_limit); };
     const size_t state_at = ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
-    const size_t item_at = ((size_t)it.id * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
+    const size_t item_at = ((size_t)it.slot * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
 
     if (warp >= 20) {
         give_registers();
@@ -450,7 +448,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 __syncwarp();
                 mbar_arrive(&B.z_ok[b]);
             }
-            if (!OUT && lane == 0) P.total[(size_t)it.id * P.a.HV + hv] = (float)all;
+            if (!OUT && lane == 0) P.total[(size_t)it.slot * P.a.HV + hv] = (float)all;
         } else if (warp == 20) {
             // ---------------------------------------------------------------- MMAs: scores, inter, out
             constexpr uint32_t id_scores = tc_idesc(128, 128, false), id_z = tc_idesc(128, ZP, true);
@@ -913,7 +911,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const float none = __int_as_float(0x7fc00000);
         if (tid == 384) raise_flag(P.a.err_flags, GDN_DEVERR_TIMEOUT);
         if (!OUT) {
-            if (tid == 384) P.total[(size_t)it.id * P.a.HV + hv] = none;          // and with it the states of the segments behind
+            if (tid == 384) P.total[(size_t)it.slot * P.a.HV + hv] = none;          // and with it the states of the segments behind
         } else {
             fill(none, warp - 12, 8);
             if (NS == 3 && p.dot)
@@ -948,8 +946,9 @@ int launch(const LinearLaunch &P, const LinearSweep &p, const ChunkMaps &maps, i
     }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    if ((int64_t)P.items * P.a.HV > INT32_MAX) return GDN_ERR_SHAPE;
-    cfg.gridDim = dim3((unsigned)(P.items * P.a.HV));
+    const int64_t ctas = (int64_t)(NS > 0 ? P.items : P.cut_items) * P.a.HV;
+    if (ctas > INT32_MAX) return GDN_ERR_SHAPE;
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreadsChunk);
     cfg.dynamicSmemBytes = Smem<NS>::kBytes;
     cfg.stream = stream;

@@ -13,7 +13,8 @@ struct LinearItem {
     int seq_begin, seq_end;
     int state;          // row in the state buffers; -1: a bad index (no states, outputs zeroed)
     int index;          // of the segment in the sequence
-    int id;             // of the segment among all: its place in the workspace
+    int id;             // of the segment among all
+    int slot;           // its place in local and total
 };
 
 // rows of sequence s; a sequence whose borders leave 0 .. T or decrease has none (bad)
@@ -31,12 +32,25 @@ __device__ __forceinline__ void linear_rows(const LinearLaunch &P, int s, int &b
     }
 }
 
+// row of sequence s in the state buffers; -1: a bad index
+__device__ __forceinline__ int linear_state(const LinearLaunch &P, int s, bool report)
+{
+    if (!P.states) return s;
+    const int state = P.a.state_indices ? P.a.state_indices[s] : s;
+    if (state >= 0 && state < P.a.num_states) return state;
+    if (report) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
+    return -1;
+}
+
 __device__ __forceinline__ int linear_segments(const LinearLaunch &P, int rows)
 {
     return rows <= P.seg ? 1 : (rows + P.seg - 1) / P.seg;
 }
 
-// The first segment of sequence s, and the sequence's rows; all 32 lanes of a warp call it.
+// whether a block looks for its segment, not a warp
+__device__ __forceinline__ bool linear_many(const LinearLaunch &P) { return P.a.cu_seqlens && P.a.S > kLinearSorted; }
+
+// The first segment of sequence s; all 32 lanes of a warp call it.
 __device__ __forceinline__ int linear_first_item(const LinearLaunch &P, int s)
 {
     if (!P.a.cu_seqlens) return s * linear_segments(P, P.Ls);
@@ -58,7 +72,7 @@ __device__ __forceinline__ LinearItem linear_item(const LinearLaunch &P, int i, 
     LinearItem it;
     it.seq = -1;
     it.begin = it.n = it.seq_begin = it.seq_end = it.state = it.index = 0;
-    it.id = i;
+    it.id = it.slot = i;
     const int lane = threadIdx.x & 31;
     if (!P.a.cu_seqlens) {
         const int per = linear_segments(P, P.Ls);
@@ -108,14 +122,7 @@ __device__ __forceinline__ LinearItem linear_item(const LinearLaunch &P, int i, 
     }
     it.begin = it.seq_begin + it.index * P.seg;
     it.n = min(P.seg, it.seq_end - it.begin);
-    it.state = it.seq;
-    if (P.states) {
-        if (P.a.state_indices) it.state = P.a.state_indices[it.seq];
-        if (it.state < 0 || it.state >= P.a.num_states) {
-            if (report && lane == 0) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
-            it.state = -1;
-        }
-    }
+    it.state = linear_state(P, it.seq, report && lane == 0);
     return it;
 }
 
@@ -152,6 +159,96 @@ __device__ __forceinline__ int linear_turn(const LinearLaunch &P, int i)
         if (who) item = __shfl_sync(0xFFFFFFFFu, first[h] + i - at[h], __ffs(who) - 1);
     }
     return item;
+}
+
+// What a block of threads adds up over many sequences: every warp's segments, and those of sequences that have several.
+struct LinearScan {
+    long long all[32], cut[32];
+};
+
+// Calls f(s, b, e, bad, first, cut) for all sequences: each thread for a range of its own, in order. first: segments of the
+// sequences before; cut: of those among them that have several. bad: no rows, or segments that there is no room for (which
+// only borders that decrease can make). All NT threads of a block call it; `w` is free again behind the caller's next barrier.
+template <int NT, typename F> __device__ __forceinline__ void linear_each(const LinearLaunch &P, LinearScan &w, F &&f)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t per = ((int64_t)P.a.S + NT - 1) / NT;
+    const int s0 = (int)min((int64_t)P.a.S, per * threadIdx.x), s1 = (int)min((int64_t)P.a.S, per * (threadIdx.x + 1));
+    long long own[2] = {0, 0};
+    for (int s = s0; s < s1; ++s) {
+        int b, e;
+        bool bad;
+        linear_rows(P, s, b, e, bad);
+        const int m = linear_segments(P, e - b);
+        own[0] += m;
+        if (m > 1) own[1] += m;
+    }
+    long long sum[2] = {own[0], own[1]};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, sum[k], o);
+            if (lane >= o) sum[k] += v;
+        }
+    if (lane == 31) w.all[warp] = sum[0], w.cut[warp] = sum[1];
+    __syncthreads();
+    long long first = sum[0] - own[0], cut = sum[1] - own[1];
+    for (int i = 0; i < warp; ++i) first += w.all[i], cut += w.cut[i];
+    for (int s = s0; s < s1; ++s) {
+        int b, e;
+        bool bad;
+        linear_rows(P, s, b, e, bad);
+        const int m = linear_segments(P, e - b);
+        f(s, b, e, bad || first + m > P.items || (m > 1 && cut + m > P.cut_items), first, cut);
+        first += m;
+        if (m > 1) cut += m;
+    }
+}
+
+// The search of linear_find among many sequences (apart, so that the others' kernels do not carry its code between theirs).
+template <int NT>
+__device__ __noinline__ void linear_find_block(const LinearLaunch &P, int i, bool cut, bool report, LinearScan &w, LinearItem *to)
+{
+    if (threadIdx.x == 0) to->seq = -1, to->begin = to->n = 0;      // (linear_each has a barrier before it calls)
+    linear_each<NT>(P, w, [&](int s, int b, int e, bool bad, long long first, long long before) {
+        const int m = linear_segments(P, e - b);
+        const long long j = i - (cut ? before : first);
+        if (j < 0 || j >= m || (cut && m == 1)) return;
+        if (bad) {
+            if (report) raise_flag(P.a.err_flags, GDN_DEVERR_BAD_INDEX);
+            return;
+        }
+        LinearItem it;
+        it.seq = s;
+        it.index = (int)j;
+        it.seq_begin = b;
+        it.seq_end = e;
+        it.begin = b + it.index * P.seg;
+        it.n = min(P.seg, e - it.begin);
+        it.state = linear_state(P, s, report);
+        it.id = (int)(first + j);
+        it.slot = (int)(before + j);
+        *to = it;
+    });
+}
+
+// linear_item for a block of NT threads, into *to in shared memory; up to kLinearSorted sequences by warp `by` alone. `i` counts
+// the segments of sequences with several where only those are asked for (`cut`; not up to kLinearSorted sequences). Ends with a
+// barrier. (A warp that counts 2048 sequences takes 64 steps, one behind the other.)
+template <int NT>
+__device__ __forceinline__ void linear_find(const LinearLaunch &P, int i, bool cut, bool report, int by, LinearScan &w, LinearItem *to)
+{
+    const int lane = threadIdx.x & 31;
+    if (!linear_many(P)) {
+        if ((int)(threadIdx.x >> 5) == by) {
+            const LinearItem it = linear_item(P, i, report);
+            if (lane == 0) *to = it;
+        }
+    } else {
+        linear_find_block<NT>(P, i, cut, report, w, to);
+    }
+    __syncthreads();
 }
 
 // ---- decays ------------------------------------------------------------------------------------

@@ -46,16 +46,17 @@ struct LinearLaunch {
     int Ls;             // rows per sequence without cu_seqlens
     int seg;            // rows per segment of a sequence
     int items;          // most segments (of all sequences) there can be; every sequence has at least one
+    int cut_items;      // most segments of sequences that have several: the CTAs of the pass without outputs
     int carried;        // a sequence may have several segments
     int states;         // state indices are checked
     int tc;             // the tensor-core kernel
     // workspace
-    float *local;       // [items, HV, V, K] the state that a segment ends with from zero; then the one it starts with
-    float *total;       // [items, HV] log2 of the segment's decay
+    float *local;       // [cut_items, HV, V, K] the state that a segment ends with from zero; then the one it starts with
+    float *total;       // [cut_items, HV] log2 of the segment's decay
     uint32_t wait_limit;  // SM clock cycles of a wait that can give up
 };
 
-constexpr int kLinearSorted = 64;      // up to so many sequences, the longest start first
+constexpr int kLinearSorted = 64;      // up to so many sequences, the longest start first, and a warp finds a segment; a block beyond
 constexpr int kLinearZ = 64;           // columns of z per CTA of the fp32 kernel
 
 // The sweep on the CUDA cores in fp32 (any type, size, stride); outputs: p.x given. Without: local and total.
@@ -87,7 +88,7 @@ size_t linear_dg_part_floats(int items, int HV);
 int launch_linear_dg(const LinearLaunch &P, const float *qdq, const float *kdk, const float *segment_dot, int parts, float *dg,
                      int64_t dg_stride, float *part, cudaStream_t stream);
 
-// The same from products per token and chunk (chunk_dot), of the tensor-core kernel.
+// The same from products per token and chunk (chunk_dot), of the tensor-core kernel. `part`: 8 a chunk and head.
 int launch_linear_dg_chunks(const LinearLaunch &P, const float *qdq, const float *kdk, const float *chunk_dot, float *dg,
                             int64_t dg_stride, float *part, cudaStream_t stream);
 

@@ -39,20 +39,17 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     __shared__ float s_in[2][kBlock], s_out[2][kBlock], s_first[2], s_z[2];
     __shared__ int s_each[2];
     __shared__ LinearItem s_item;
+    __shared__ LinearScan s_scan;
     __shared__ float s_last;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hv = blockIdx.y, zpart = blockIdx.z, z0 = zpart * kLinearZ;
-    if (warp == 0) {
-        const LinearItem it = linear_item(P, blockIdx.x, OUT && hv == 0 && zpart == 0);
-        if (lane == 0) s_item = it;
-    }
-    __syncthreads();
+    linear_find<NT>(P, blockIdx.x, !OUT, OUT && hv == 0 && zpart == 0, 0, s_scan, &s_item);
     const LinearItem it = s_item;
     if (it.seq < 0) return;
     const bool whole = it.seq_end - it.seq_begin <= P.seg;                     // the sequence's only segment
     if (!OUT && (whole || it.state < 0)) return;
-    const size_t item_state = ((size_t)blockIdx.x * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
+    const size_t item_state = ((size_t)it.slot * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     const int n = it.n;
     const bool skip = it.state < 0;                                            // a bad state index: outputs zeroed
 
@@ -269,7 +266,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     float *to = nullptr;
     if (!OUT) {
         to = P.local + item_state;
-        if (tid == 0 && zpart == 0) P.total[(size_t)blockIdx.x * P.a.HV + hv] = lost ? __int_as_float(0x7fc00000) : (float)all;
+        if (tid == 0 && zpart == 0) P.total[(size_t)it.slot * P.a.HV + hv] = lost ? __int_as_float(0x7fc00000) : (float)all;
     } else if (ends && !skip && p.end) {
         to = p.end + ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     }
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
 template <typename Tin, int NY>
 cudaError_t launch(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)P.items, (unsigned)P.a.HV, (unsigned)((p.DZ + kLinearZ - 1) / kLinearZ));
+    const dim3 grid((unsigned)(outputs ? P.items : P.cut_items), (unsigned)P.a.HV, (unsigned)((p.DZ + kLinearZ - 1) / kLinearZ));
     if (outputs) linear_recurrent_kernel<Tin, NY, true><<<grid, Geometry<NY>::kThreads, 0, stream>>>(P, p);
     else linear_recurrent_kernel<Tin, NY, false><<<grid, Geometry<NY>::kThreads, 0, stream>>>(P, p);
     return cudaGetLastError();
