@@ -49,11 +49,15 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 128;                            // tokens per chunk
-// The tensor cores cut a sum's bits off towards zero at each step of 16 products: 2^-23 of it at most, 4.4e-8 on average
-// (measured as 3.5e-7 after the eight steps of a chunk's update). Over many chunks that would add up, and where a difference of
-// such sums counts (dg) it shows; so the update's weights and the sums behind dg carry the average back (dg's error over 8 x
-// 2048 tokens 1.1e-6 -> 7.7e-7).
-constexpr float kCut = 4.4e-8f;
+// The tensor cores cut off what a sum's step has below its largest term's last bit, towards zero. Measured on zero-mean inputs, in the
+// states after a chunk: what 32 tokens bring is low by 0.4 to 1.2e-7 from their own steps and by 1.5e-7 more for every 32 tokens
+// behind them whose share is not lost beside theirs (uncorrected: 1.1e-7 after 32 tokens, 3.4e-7 after 128, 2.2e-7
+// under decays of 0.01 a token, 0.6e-7 of 0.5). Over many chunks that would add up, and where a difference of such sums counts (dg) it
+// shows; so the update's weights carry it back, 32 tokens at a time in the sweep's order (states are then off by -0.9 to 1.3e-7
+// on average, 0.7 to 2.0e-7 in norm, forwards and backwards, over decays of 0 to 2 a token; with one constant for all 128 it was -1.9e-7 for
+// long memories and 3.2e-7 for short ones, and rows in one order for both sweeps would be low by 6.6e-7 backwards under 0.03).
+// Outputs are low by 1.2 to 2.4e-7. (In the weights' exponents it costs nothing; as a factor of its own 3% of 1 x 32768 tokens.)
+constexpr float kCutOwn = 0.9e-7f, kCutLater = 1.5e-7f, kCutOut = 2e-7f;
 constexpr uint32_t kBlock = 16384;                    // 128 rows of 64 columns
 constexpr uint32_t kTile = 2 * kBlock;
 constexpr int kThreadsChunk = 768;
@@ -96,7 +100,7 @@ struct Bars {
     uint64_t z_raw[3], z_ok[2], bad_read;             // z's tile may be used for the update; for the outputs; first_bad was read
     uint64_t y_ready[4], y_free[4];                   // quarters of Y: written; used
     uint64_t scores, p_ready, inter, out, out_read, update[2], update_read, state_ready, done[2];
-    float decay[2];                                   // e^{G at the chunk's end}
+    float end[2];                                     // G at the chunk's end
     uint32_t tmem;
     int abort_flag, zero;
     uint8_t bad[2];
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // Sums as 64-bit integers in steps of 2^-40 (fp64 runs at two operations a clock and SM, and this warp is on every
             // chunk's path); lane l takes the rows 4 l .. 4 l + 3 in the sweep's order, the next chunk's already loaded.
             double all = 0.0;
+            const float cut = 1.44269504f * (kCutOwn + kCutLater * (3 - (lane >> 3)));   // (a lane's four rows lie in the same 32)
             float g[4];
             const auto fetch = [&](int i) {
                 const int c = p.reverse ? chunks - 1 - i : i, at = it.begin + c * kRows, rows = min(kRows, n - c * kRows);
@@ -363,12 +368,14 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
                 if (!OUT) all += (double)hi_end + (double)lo_end;
                 if (i >= 2 && !wait(&B.weight_free[i & 1], (i >> 1) - 1)) break;
-                if (lane == 0) B.decay[i & 1] = ex2(hi_end) * ex2(lo_end);
+                if (lane == 0) B.end[i & 1] = hi_end + lo_end;    // (the state's warps take its factor: this one's steps are on every chunk's path)
+                float lo_cut = lo_end + cut;                  // what the weights carry back is a factor too
+                if (rows < kRows && !p.reverse) lo_cut += 1.44269504f * kCutLater * (((rows - 1) >> 5) - 3);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = p.reverse ? kRows - 1 - lane * 4 - j : lane * 4 + j;
-                    const float w = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_end - lo[j]) : 0.f;
-                    decays.weight[i & 1][r] = fmaf(w, kCut * ((rows + 15) >> 4), w);
+                    const float w = r < rows ? ex2(hi_end - hi[j]) * ex2(lo_cut - lo[j]) : 0.f;
+                    decays.weight[i & 1][r] = w;
                 }
                 mbar_arrive(&B.weights[i & 1]);
                 if (OUT) {
@@ -512,13 +519,13 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (!wait(&B.z_raw[i % 3], i / 3) || (i > 0 && !wait(&B.update_read, i - 1))) break;
                 bool go = true;
 #pragma unroll 1
-                for (int u = 0; u < 4 && go; ++u) {       // 32 tokens each
+                for (int u = 0; u < 4 && go; ++u) {       // 32 tokens each, in the sweep's order
                     go = wait(&B.y_ready[u], i);
                     if (!go) break;
                     tcl_fence_after();
                     if (lane == 0) {
                         const uint32_t y = tmem + y_column(OUT, OUT ? u & 1 : u);
-                        const uint64_t z = tz + u * (4096 >> 4);
+                        const uint64_t z = tz + (p.reverse ? 3 - u : u) * (4096 >> 4);
 #pragma unroll
                         for (int t = 2; t >= 0; --t)
 #pragma unroll
@@ -615,8 +622,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 d = group_sum<32>(d);
                 if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
             }
-            const float decay = B.decay[i & 1];
+            const float end = B.end[i & 1];
             mbar_arrive(&B.weight_free[i & 1]);
+            const float decay = linear_decay_factor(end);
             if (!wait(&B.update[i & 1], i >> 1)) break;
             tcl_fence_after();
             if (active) {
@@ -692,12 +700,12 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             bool go = true;
 #pragma unroll 1
             for (int k = 0; k < 2 && go; ++k) {
-                // quarters group and 2 + group; with outputs both in the same buffer
+                // quarters group and 2 + group, in the sweep's order; with outputs both in the same buffer
                 const int u = 2 * k + group;
                 go = OUT ? k ? wait(&B.y_free[group], i) : i == 0 || wait(&B.y_free[2 + group], i - 1) : i == 0 || wait(&B.y_free[u], i - 1);
                 if (!go) break;
                 tcl_fence_after();
-                if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * u, rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, OUT ? group : u));
+                if (32 * quad < YP) make_y(sm + slot * kTile, r, 32 * (p.reverse ? 3 - u : u), rows, decays.weight[i & 1], tmem + lanes + y_column(OUT, OUT ? group : u));
                 tcl_fence_before();
                 mbar_arrive(&B.y_ready[u]);
                 if (!OUT || k == 1) continue;
@@ -778,7 +786,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         // ---------------------------------------------------------------- inter's decays, outputs
         const int quad = warp & 3, r = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const float f = p.x_scale * p.z_scale * (NS == 3 ? 1.f + 7 * kCut : 1.f);
+        const float f = p.x_scale * p.z_scale * (1.f + kCutOut);
         for (int i = 0; i < chunks; ++i) {
             {
                 if (!wait(&B.rows, i)) break;
