@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant
         if (state < 0 || item0 + segs > P.items) return;     // (left out, as in linear_item)
     }
     const int KV = P.a.K * P.a.V, at = (blockIdx.z * 256 + threadIdx.x) * 4;
-    if (at >= KV) return;
+    if (at >= KV || !GDN_IN(P.a.err_flags, item0 + segs - 1, P.cut_items)) return;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.start) run = *reinterpret_cast<const float4 *>(p.start + ((size_t)state * P.a.HV + hv) * KV + at);
     // four segments' states at a time on their way
@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(256) linear_fold_kernel(const __grid_constant_
     }
     const int last = (int)min((int64_t)kFoldRows, P.a.T - t0);
     for (int r = threadIdx.x >> 5; r < last; r += 8) {
-        if (!(mine >> r & 1)) continue;
         const int64_t t = t0 + r;
+        if (!(mine >> r & 1) || !GDN_IN(P.a.err_flags, t, P.a.T)) continue;
         float sum[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kDgHeads *kDgRanges) linear_dg_kernel(const __
     __shared__ LinearScan s_scan;
     linear_find<kDgHeads * kDgRanges>(P, blockIdx.x, false, false, 0, s_scan, &s_item);
     const LinearItem it = s_item;
+    if (it.seq >= 0 && !linear_in(P, it)) return;
     const bool skip = it.seq < 0 || it.state < 0;
     const int b = it.begin, e = it.seq < 0 ? b : b + it.n;
     const int per = (e - b + kDgRanges - 1) / kDgRanges;
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(256) linear_dg_chunk_kernel(const __grid_const
         if (fixed && hv < HV) part[((size_t)id * 8 + range) * HV + hv] = 0.f;
         return;
     }
+    if (!GDN_IN(P.a.err_flags, at, P.a.T) || !GDN_IN(P.a.err_flags, rows, P.a.T - at + 1)) return;
     const bool mine = hv < HV && linear_state(P, it.seq, false) >= 0;
     const int first = 16 * range, last = min(rows, first + 16);
     float d[16], sum = 0.f;

@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         if (OUT && p.early && tid == 0) grid_dependency_wait();
     };
     if (it.seq < 0) return leave();
+    // (the tiles' swizzle needs the 1024 bytes that the declaration asks for)
+    if (!linear_in(P, it) || !GDN_IN(P.a.err_flags, sbase & 1023u, 1)) return leave();
     const bool whole = it.seq_end - it.seq_begin <= P.seg;
     if (!OUT && (whole || it.state < 0)) return;
     const int n = it.n, chunks = (n + kRows - 1) / kRows;
@@ -606,12 +608,13 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < chunks; ++i) {
             const int c0 = p.reverse ? chunks - 1 - i : i, at = it.begin + c0 * kRows;
             const size_t chunk = ((size_t)(at / kRows + it.seq) * P.a.HV + hv) * (128 * ZP) + (tid - 384);
+            const bool mine = NS != 3 || GDN_IN(P.a.err_flags, at / kRows + it.seq, P.a.T / kRows + P.a.S);
             if (!wait(&B.weights[i & 1], i >> 1)) break;
             if (NS == 3 && p.chunk_dot) {
                 // the product of this state's gradient, as it reaches the chunk's last row, and the state behind that row
                 float d = 0.f;
                 const int next = at + min(kRows, n - c0 * kRows);
-                if (active) {
+                if (active && mine) {
 #pragma unroll
                     for (int c = 0; c < ZC / 2; ++c) {
                         const float2 v = unpair(S[c]);
@@ -620,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     d *= exp2_wide(linear_decay(P, hv, next - 1, it.seq_end, 1)) * p.z_scale;
                 }
                 d = group_sum<32>(d);
-                if (lane == 0) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
+                if (lane == 0 && mine) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
             }
             const float end = B.end[i & 1];
             mbar_arrive(&B.weight_free[i & 1]);
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) S[c / 2 + j] = fma2(S[c / 2 + j], decay2, pair(v[2 * j], v[2 * j + 1]));
                 }
-                if (NS == 3 && p.chunk_states && !p.chunk_dot)
+                if (NS == 3 && p.chunk_states && !p.chunk_dot && mine)
 #pragma unroll
                     for (int c = 0; c < ZC / 2; ++c) {
                         const float2 v = unpair(S[c]);
@@ -815,8 +818,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             tcl_fence_after();
             const int b = i & 1, c0 = p.reverse ? chunks - 1 - i : i, rows = min(kRows, n - c0 * kRows);
             const bool bad = *(volatile uint8_t *)&B.bad[b];
-            const bool mine = r < rows;
             const int64_t t = it.begin + c0 * kRows + r;
+            const bool mine = r < rows && linear_in(P, (int)t, hv, P.a.HV);
             const bf16 *with = NS == 3 && p.dot && mine ? static_cast<const bf16 *>(p.dot_with) + t * p.dot_stride + (int64_t)(hv / p.dot_group) * p.dot_head : nullptr;
             float dot = 0.f;
             if (bad) {

@@ -315,7 +315,14 @@ __device__ __forceinline__ double linear_decay(const LinearLaunch &P, int hv, in
     return at < seq_end ? linear_log2(P.a.g[at * P.a.g_stride + hv]) : 0.0;
 }
 
-// debug build: element (t, head, c) of a tensor with T rows lies inside it
+// debug build: a segment's rows, state and workspace lie inside their buffers
+__device__ __forceinline__ bool linear_in(const LinearLaunch &P, const LinearItem &it)
+{
+    return GDN_IN(P.a.err_flags, it.begin, (int64_t)P.a.T + 1) && GDN_IN(P.a.err_flags, it.n, (int64_t)P.a.T - it.begin + 1) &&
+           GDN_IN(P.a.err_flags, it.id, P.items) && (it.seq_end - it.seq_begin <= P.seg || GDN_IN(P.a.err_flags, it.slot, P.cut_items)) &&
+           (!P.states || it.state < 0 || GDN_IN(P.a.err_flags, it.state, P.a.num_states));
+}
+// token row t of value head hv
 __device__ __forceinline__ bool linear_in(const LinearLaunch &P, int t, int head, int heads)
 {
     return GDN_IN(P.a.err_flags, t, P.a.T) && GDN_IN(P.a.err_flags, head, heads);

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     const int hv = blockIdx.y, zpart = blockIdx.z, z0 = zpart * kLinearZ;
     linear_find<NT>(P, blockIdx.x, !OUT, OUT && hv == 0 && zpart == 0, 0, s_scan, &s_item);
     const LinearItem it = s_item;
-    if (it.seq < 0) return;
+    if (it.seq < 0 || !linear_in(P, it)) return;
     const bool whole = it.seq_end - it.seq_begin <= P.seg;                     // the sequence's only segment
     if (!OUT && (whole || it.state < 0)) return;
     const size_t item_state = ((size_t)it.slot * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);

@@ -61,6 +61,11 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __gri
                           : static_cast<const T *>(a.k) + t * a.k_stride + h * a.k_head_stride;
         out = isq ? static_cast<T *>(a.q_out) + t * a.q_out_stride + h * a.q_out_head_stride
                   : static_cast<T *>(a.k_out) + t * a.k_out_stride + h * a.k_out_head_stride;
+        if (!GDN_IN(nullptr, t, a.T) || !GDN_IN(nullptr, c0 + VEC - 1, a.D) || (turn && !GDN_IN(nullptr, at + NP - 1, R.tokens * half)) ||
+            (turn && kTwo && !GDN_IN(nullptr, c0 + (INTER ? 1 : half) + VEC - 1, a.rotary_dim))) {
+            out = nullptr;
+            return;
+        }
         x = *reinterpret_cast<const W *>(in + c0);
         if (kTwo && turn) y = *reinterpret_cast<const W *>(in + c0 + (INTER ? 1 : half));
         u += du;
