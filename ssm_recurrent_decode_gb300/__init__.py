@@ -1094,6 +1094,8 @@ def gdn_linear_attention_step(q, k, v, g, state, out, cache_indices=None, *, pad
     updated in place; out: [B, HV, V] dense. Row b is on slot cache_indices[b] (int32; default b); rows whose index is
     pad_slot_id are skipped (out zeroed). With frequencies (see gdn_rotary) q and k are turned to positions [B] first."""
     torch = _torch()
+    if float(magnitude) == 0.0:
+        raise ValueError("magnitude must not be 0")
     a = LinearStepArgs()
     a.in_dtype, a.out_dtype, a.state_dtype = _dtype_code(q), _dtype_code(out), _dtype_code(state)
     a.B, a.H, a.K = _put_rows(a, "q", q, "q")
