@@ -127,7 +127,7 @@ size_t carve(LinearLaunch &P, BackwardSpace *B, PackedSpace &packed, unsigned ch
     }
     if (P.carried) {
         P.local = w.take((size_t)P.cut_items * a.HV * a.K * a.V);
-        P.total = w.take((size_t)P.cut_items * a.HV);
+        P.total = reinterpret_cast<float2 *>(w.take((size_t)P.cut_items * a.HV * 2));
     }
     if (B) {
         const size_t th = (size_t)a.T * a.HV;

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant
     // four segments' states at a time on their way
     for (int j0 = 0; j0 < segs; j0 += 4) {
         float4 own[4];
-        float f[4];
+        float2 f[4];
         float4 *l[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const __grid_constant
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j0 + j >= segs) break;
-            const float g = linear_decay_factor(f[j]);
+            const float g = linear_decay_factor(f[j].x, f[j].y);
             *l[j] = run;
             run = make_float4(fmaf(g, run.x, own[j].x), fmaf(g, run.y, own[j].y), fmaf(g, run.z, own[j].z), fmaf(g, run.w, own[j].w));
         }

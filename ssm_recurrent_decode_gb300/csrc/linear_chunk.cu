@@ -100,10 +100,9 @@ struct Bars {
     uint64_t z_raw[3], z_ok[2], bad_read;             // z's tile may be used for the update; for the outputs; first_bad was read
     uint64_t y_ready[4], y_free[4];                   // quarters of Y: written; used
     uint64_t scores, p_ready, inter, out, out_read, update[2], update_read, state_ready, done[2];
-    float end[2];                                     // G at the chunk's end
+    float end_hi[2], end_lo[2];                       // G at the chunk's end
     uint32_t tmem;
-    int abort_flag, zero;
-    uint8_t bad[2];
+    uint8_t abort_flag, bad[2];
 };
 
 // Seven tiles of shared memory: NS for the state's bf16 terms (0: no outputs), the others for x, y and z; and what the
@@ -158,10 +157,15 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, Bars 
     bool done;
     do {
         done = try_phase(bar, parity & 1u, min(limit, 1000000u));
-    } while (!done && !*(volatile int *)&B->abort_flag && (uint32_t)clock() - t0 < limit);
+    } while (!done && !*(volatile uint8_t *)&B->abort_flag && (uint32_t)clock() - t0 < limit);
     done = __all_sync(kAll, done);
-    if (!done) *(volatile int *)&B->abort_flag = 1;
+    if (!done) *(volatile uint8_t *)&B->abort_flag = 1;
     return done;
+}
+// Waits for what is in flight, whether or not the CTA has given up.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
+{
+    for (const uint32_t t0 = clock(); !try_phase(bar, parity & 1u, 1000000u) && (uint32_t)clock() - t0 < kWaitLimit;);
 }
 
 // 32 tokens of Y, from row s0 of y's tile, into the buffer at taddr: lane y of tensor memory takes column y.
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < 3; ++i) mbar_init(&B.z_raw[i], 32);
         mbar_init(&B.scores, 1), mbar_init(&B.inter, 1), mbar_init(&B.out, 1), mbar_init(&B.update[0], 1), mbar_init(&B.update[1], 1);
         mbar_init(&B.p_ready, 384), mbar_init(&B.out_read, 128), mbar_init(&B.state_ready, 256), mbar_init(&B.update_read, 256);
-        B.abort_flag = B.zero = B.bad[0] = B.bad[1] = 0;
+        B.abort_flag = B.bad[0] = B.bad[1] = 0;
         fence_barrier_init();
     }
     LinearItem *found = reinterpret_cast<LinearItem *>(sm + M::kDecays);       // (the decays come later)
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // Copies in flight land before the CTA ends (whether this warp gave up or another one will: nobody else may look
             // for the last tiles then).
             for (int m = max(0, issued - kSlots); m < issued; ++m)
-                if (wide >> (m % TILES + 3 - TILES) & 1) mbar_wait_warp(&B.full[m % kSlots], (m / kSlots) & 1, &B.zero, kWaitLimit);
+                if (wide >> (m % TILES + 3 - TILES) & 1) drain(&B.full[m % kSlots], m / kSlots);
         } else if (warp == 22) {
             // ---------------------------------------------------------------- decays; z's non-finite values
             // Sums as 64-bit integers in steps of 2^-40 (fp64 runs at two operations a clock and SM, and this warp is on every
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const float hi_end = __shfl_sync(kAll, hi[3], 31), lo_end = __shfl_sync(kAll, lo[3], 31);
                 if (!OUT) all += (double)hi_end + (double)lo_end;
                 if (i >= 2 && !wait(&B.weight_free[i & 1], (i >> 1) - 1)) break;
-                if (lane == 0) B.end[i & 1] = hi_end + lo_end;    // (the state's warps take its factor: this one's steps are on every chunk's path)
+                if (lane == 0) B.end_hi[i & 1] = hi_end, B.end_lo[i & 1] = lo_end;    // (the state's warps take its factor: this one's steps are on every chunk's path)
                 float lo_cut = lo_end + cut;                  // what the weights carry back is a factor too
                 if (rows < kRows && !p.reverse) lo_cut += 1.44269504f * kCutLater * (((rows - 1) >> 5) - 3);
 #pragma unroll
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 __syncwarp();
                 mbar_arrive(&B.z_ok[b]);
             }
-            if (!OUT && lane == 0) P.total[(size_t)it.slot * P.a.HV + hv] = (float)all;
+            if (!OUT && lane == 0) P.total[(size_t)it.slot * P.a.HV + hv] = linear_parts(all);
         } else if (warp == 20) {
             // ---------------------------------------------------------------- MMAs: scores, inter, out
             constexpr uint32_t id_scores = tc_idesc(128, 128, false), id_z = tc_idesc(128, ZP, true);
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // every MMA has completed before the tensor memory is freed
             if (lane == 0) {
                 tcl_commit(&B.done[0]);
-                mbar_wait(&B.done[0], 0u, &B.zero, kWaitLimit);
+                drain(&B.done[0], 0);
             }
             __syncwarp();
         } else if (warp == 21) {
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
             if (lane == 0) {
                 tcl_commit(&B.done[1]);
-                mbar_wait(&B.done[1], 0u, &B.zero, kWaitLimit);
+                drain(&B.done[1], 0);
             }
             __syncwarp();
         }
@@ -625,9 +629,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 d = group_sum<32>(d);
                 if (lane == 0 && mine) p.chunk_dot[((size_t)(at / kRows + it.seq) * P.a.HV + hv) * 8 + warp - 12] = d;
             }
-            const float end = B.end[i & 1];
+            const float end_hi = B.end_hi[i & 1], end_lo = B.end_lo[i & 1];
             mbar_arrive(&B.weight_free[i & 1]);
-            const float decay = linear_decay_factor(end);
+            const float decay = linear_decay_factor(end_hi, end_lo);
             if (!wait(&B.update[i & 1], i >> 1)) break;
             tcl_fence_after();
             if (active) {
@@ -922,7 +926,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const float none = __int_as_float(0x7fc00000);
         if (tid == 384) raise_flag(P.a.err_flags, GDN_DEVERR_TIMEOUT);
         if (!OUT) {
-            if (tid == 384) P.total[(size_t)it.slot * P.a.HV + hv] = none;          // and with it the states of the segments behind
+            if (tid == 384) P.total[(size_t)it.slot * P.a.HV + hv] = make_float2(none, none);          // and with it the states of the segments behind
         } else {
             fill(none, warp - 12, 8);
             if (NS == 3 && p.dot)

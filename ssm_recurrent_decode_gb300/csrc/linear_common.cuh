@@ -294,18 +294,24 @@ __device__ __forceinline__ float linear_exp2(long long G)
     return exp2f(hi) * exp2f(lo);
 }
 
-// 2^x as the factor of a state, chunk by chunk or segment by segment. Near one, where many of them are multiplied, by its series:
+// such a sum in fp64 as the same two numbers (a NaN stays one)
+__device__ __forceinline__ float2 linear_parts(double G)
+{
+    const double hi = rint(G * 256.0) / 256.0;
+    return make_float2((float)hi, (float)(G - hi));
+}
+// 2^(hi + lo) as the factor of a state, chunk by chunk or segment by segment. Near one, where many of them are multiplied, by its series:
 // the hardware's 2^x is low by 2e-8 there on average, 3e-7 after the sixteen chunks of 2048 tokens (and 5e-7 after 31
 // segments of 48).
-__device__ __forceinline__ float linear_decay_factor(float x)
+__device__ __forceinline__ float linear_decay_factor(float hi, float lo)
 {
-    const float y = x * 0.693147182f;
+    const float x = hi + lo, y = x * 0.693147182f;
     float p = fmaf(y, 1.f / 720, 1.f / 120);
     p = fmaf(p, y, 1.f / 24);
     p = fmaf(p, y, 1.f / 6);
     p = fmaf(p, y, 0.5f);
     p = fmaf(p, y, 1.f);
-    return fabsf(x) < 0.25f ? fmaf(p, y, 1.f) : exp2f(x);      // (0.17^7 / 5040 < 2^-29)
+    return fabsf(x) < 0.25f ? fmaf(p, y, 1.f) : exp2f(hi) * exp2f(lo);      // (0.17^7 / 5040 < 2^-29)
 }
 
 // decay that a sweep applies before it takes token t (in its own direction)

@@ -52,7 +52,7 @@ struct LinearLaunch {
     int tc;             // the tensor-core kernel
     // workspace
     float *local;       // [cut_items, HV, V, K] the state that a segment ends with from zero; then the one it starts with
-    float *total;       // [cut_items, HV] log2 of the segment's decay
+    float2 *total;      // [cut_items, HV] log2 of the segment's decay, as two numbers
     uint32_t wait_limit;  // SM clock cycles of a wait that can give up
 };
 

@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
     float *to = nullptr;
     if (!OUT) {
         to = P.local + item_state;
-        if (tid == 0 && zpart == 0) P.total[(size_t)it.slot * P.a.HV + hv] = lost ? __int_as_float(0x7fc00000) : (float)all;
+        if (tid == 0 && zpart == 0) P.total[(size_t)it.slot * P.a.HV + hv] = linear_parts(lost ? (double)__int_as_float(0x7fc00000) : all);
     } else if (ends && !skip && p.end) {
         to = p.end + ((size_t)it.state * P.a.HV + hv) * ((size_t)P.a.K * P.a.V);
     }

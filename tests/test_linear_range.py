@@ -39,3 +39,24 @@ def test_states_of_any_size(size, decay, dtype):
     compare(c, run_forward(c), refs)
     if size > 0:
         compare(c, run_backward(c), refs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["0.01", "0.2", "runs", "tokens", "mixed"])
+def test_log_decays_above_zero(kind, dtype):
+    """States that grow, in all tokens or in some of them, while no sum of the log decays leaves +-87 (fp32's powers of two): by 3
+    and by 60 over the sequence, in runs of eight tokens to and fro, in every other token, at random."""
+    lengths, H, HV, K, V = [300, 77], 1, 2, 64, 48
+    c = lc.make(lengths, H, HV, K, V, dtype, 9)
+    t, T = np.arange(sum(lengths))[:, None] + np.zeros((1, HV)), sum(lengths)
+    g = {"runs": np.where(t // 8 % 2 == 0, -8.0, 8.0), "tokens": np.where(t % 2 == 0, -4.0, 4.0),
+         "mixed": 2.0 * np.random.default_rng(2).normal(size=(T, HV)) - 0.5}.get(kind)
+    c["g"] = (np.full((T, HV), float(kind)) if g is None else g).astype(np.float32).astype(np.float64)
+    refs = lc.references(c)
+    forward, backward = run_forward(c), run_backward(c)
+    compare(c, forward, refs)
+    compare(c, backward, refs)
+    for n, x in (("final", forward["final"]), ("d_initial", backward["d_initial"])):
+        # a power of two of 87 octaves is a product of a few roundings; from one fp32 number its error would be 87 2^-24
+        off = np.linalg.norm(x.double().cpu().numpy() - refs[0][n]) / np.linalg.norm(refs[0][n])
+        assert off < 2.0 ** -20, (n, off)
