@@ -59,7 +59,7 @@ struct LinearLaunch {
 constexpr int kLinearSorted = 64;      // up to so many sequences, the longest start first, and a warp finds a segment; a block beyond
 constexpr int kLinearZ = 64;           // columns of z per CTA of the fp32 kernel
 
-// The sweep on the CUDA cores in fp32 (any type, size, stride); outputs: p.x given. Without: local and total.
+// The sweep on the CUDA cores in fp32 (any size, stride); outputs: p.x given. Without: local and total.
 int launch_linear_recurrent(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);
 // The same for bf16 inputs on the tensor cores, and whether a call takes it.
 int launch_linear_chunk(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);

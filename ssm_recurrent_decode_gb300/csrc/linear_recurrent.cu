@@ -1,4 +1,4 @@
-// linear_recurrent.cu -- linear attention on the CUDA cores, token by token in fp32 (any type, size, stride).
+// linear_recurrent.cu -- linear attention of fp32 inputs on the CUDA cores, token by token.
 //
 // A CTA owns one segment of a sequence, one value head and 64 columns of z; a thread keeps 16 x 2 entries of the state
 // State[y, z] in registers: DY / 16 lanes side by side share two columns. A token costs every entry two multiply-adds,
@@ -27,7 +27,7 @@ template <int NY> struct Geometry {
     static constexpr int kThreads = 32 * kLanes;               // kLinearZ columns, two a lane group
 };
 
-template <typename Tin, int NY, bool OUT>
+template <int NY, bool OUT>
 __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kernel(const __grid_constant__ LinearLaunch P,
                                                                                  const __grid_constant__ LinearSweep p)
 {
@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
         __syncthreads();
     }
 
-    const Tin *xp = OUT ? static_cast<const Tin *>(p.x) + (int64_t)(hv / p.x_group) * p.x_head : nullptr;
-    const Tin *yp = static_cast<const Tin *>(p.y) + (int64_t)(hv / p.y_group) * p.y_head;
-    const Tin *zp = static_cast<const Tin *>(p.z) + (int64_t)(hv / p.z_group) * p.z_head;
+    const float *xp = OUT ? static_cast<const float *>(p.x) + (int64_t)(hv / p.x_group) * p.x_head : nullptr;
+    const float *yp = static_cast<const float *>(p.y) + (int64_t)(hv / p.y_group) * p.y_head;
+    const float *zp = static_cast<const float *>(p.z) + (int64_t)(hv / p.z_group) * p.z_head;
     const int first = p.reverse ? it.begin + n - 1 : it.begin, dir = p.reverse ? -1 : 1;
     float rx[OUT ? EX : 1], ry[EX], rz[EZ];
     const auto fetch = [&](int block) {
@@ -105,14 +105,14 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             const int e = tid + i * NT, r = block * kBlock + e / NY, c = e % NY;
             const int64_t t = first + (int64_t)dir * r;
             const bool in = r < n && c < p.DY && linear_in(P, (int)t, hv, P.a.HV);
-            ry[i] = in ? to_f32(yp[t * p.y_stride + c]) : 0.f;
-            if (OUT) rx[i] = in ? to_f32(xp[t * p.x_stride + c]) * p.x_scale : 0.f;
+            ry[i] = in ? yp[t * p.y_stride + c] : 0.f;
+            if (OUT) rx[i] = in ? xp[t * p.x_stride + c] * p.x_scale : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < EZ; ++i) {
             const int e = tid + i * NT, r = block * kBlock + e / kLinearZ, c = z0 + e % kLinearZ;
             const int64_t t = first + (int64_t)dir * r;
-            rz[i] = r < n && c < p.DZ && linear_in(P, (int)t, hv, P.a.HV) ? to_f32(zp[t * p.z_stride + c]) * p.z_scale : 0.f;
+            rz[i] = r < n && c < p.DZ && linear_in(P, (int)t, hv, P.a.HV) ? zp[t * p.z_stride + c] * p.z_scale : 0.f;
         }
     };
     const auto put = [&](int b) {
@@ -288,29 +288,28 @@ __global__ void __launch_bounds__(Geometry<NY>::kThreads) linear_recurrent_kerne
             for (int j = 0; j < 2; ++j) p.chunk_states[kept + (2 * i + j) * NT] = S[i][j] * f;
 }
 
-template <typename Tin, int NY>
+template <int NY>
 cudaError_t launch(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
     const dim3 grid((unsigned)(outputs ? P.items : P.cut_items), (unsigned)P.a.HV, (unsigned)((p.DZ + kLinearZ - 1) / kLinearZ));
-    if (outputs) linear_recurrent_kernel<Tin, NY, true><<<grid, Geometry<NY>::kThreads, 0, stream>>>(P, p);
-    else linear_recurrent_kernel<Tin, NY, false><<<grid, Geometry<NY>::kThreads, 0, stream>>>(P, p);
+    if (outputs) linear_recurrent_kernel<NY, true><<<grid, Geometry<NY>::kThreads, 0, stream>>>(P, p);
+    else linear_recurrent_kernel<NY, false><<<grid, Geometry<NY>::kThreads, 0, stream>>>(P, p);
     return cudaGetLastError();
 }
 
-template <typename Tin> cudaError_t launch_y(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream)
+cudaError_t launch_y(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
-    if (p.DY <= 16) return launch<Tin, 16>(P, p, outputs, stream);
-    if (p.DY <= 32) return launch<Tin, 32>(P, p, outputs, stream);
-    if (p.DY <= 64) return launch<Tin, 64>(P, p, outputs, stream);
-    return launch<Tin, 128>(P, p, outputs, stream);
+    if (p.DY <= 16) return launch<16>(P, p, outputs, stream);
+    if (p.DY <= 32) return launch<32>(P, p, outputs, stream);
+    if (p.DY <= 64) return launch<64>(P, p, outputs, stream);
+    return launch<128>(P, p, outputs, stream);
 }
 
 }  // namespace
 
 int launch_linear_recurrent(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream)
 {
-    const cudaError_t rc = P.a.in_dtype == GDN_BF16 ? launch_y<bf16>(P, p, outputs, stream) : launch_y<float>(P, p, outputs, stream);
-    return rc == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    return launch_y(P, p, outputs, stream) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // namespace gdn

@@ -12,3 +12,11 @@ def test_a_step_refuses_a_magnitude_of_zero():
     with pytest.raises(ValueError, match="magnitude"):
         gdn.gdn_linear_attention_step(t, t, t, torch.zeros(2), torch.zeros(4, 2, 16, 16), t, positions=torch.zeros(4, dtype=torch.int32),
                                       frequencies=torch.ones(8, dtype=torch.float64), magnitude=0.0)
+
+
+@pytest.mark.gpu
+def test_bf16_outputs_of_fp32_inputs():
+    import linear_cases as lc
+    from test_parity_linear import compare, run_forward
+    c = lc.make([140, 75], 2, 2, 64, 40, "f32", 19)
+    compare(c, run_forward(c, out="bf16"))
