@@ -17,12 +17,16 @@
  * with dq and dk summed over the value heads that share them, and dg over tokens where g is one per head.
  *
  * Arithmetic and states are fp32 whatever the inputs' type (states are stored in fp32, for the step also in
- * bf16). With bf16 inputs the sequences' products take what is not bf16 already as a sum of bf16 numbers: the states carried
- * from token to token keep 24 bits; where a token's output or gradient is summed, the state that it meets and its
- * score times decay keep 16 bits, so that the sum is off by at most 2^-16 of the sum of its terms' magnitudes beside what fp32
- * sums lose. Where dg is asked for, the states that dq and dk meet keep 24 bits: their last bits may depend on it. A log decay below -200 counts as -200 (a factor of 0 in fp32); infinite inputs count as NaN, and a
- * NaN reaches what the formulas say it reaches: outputs of its own token and of later ones (gradients of k, v
- * and g: of earlier ones), and no other sequence.
+ * bf16). With bf16 inputs the sequences' products take what is not bf16 already as a sum of bf16 numbers: the
+ * states carried from token to token keep 24 bits; where a token's output or gradient is summed, the state that it
+ * meets and its scores times decays keep 16 bits, so that the sum is off by at most 2^-16 of the sum of its terms'
+ * magnitudes beside what fp32 sums lose. Where dg is asked for, the states that dq and dk meet keep 24 bits: the last
+ * bits of dq and dk may depend on it.
+ *
+ * A log decay below -200 counts as -200 (a factor of 0 in fp32). Log decays may be positive; no sum of consecutive
+ * ones may then leave +-87 (fp32's powers of two). Infinite inputs count as NaN, and a NaN reaches outputs of its own
+ * token and of later ones (gradients of k and v: of earlier ones; of g, which is summed over tokens: of any token of its
+ * sequence), and no other sequence.
  *
  * Sequences are packed end to end: token rows 0 .. T-1. With cu_seqlens sequence s owns rows
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 (it may be empty: its final state is then its initial one); without,

@@ -9,8 +9,8 @@
  * The other channels are copied. inverse turns by -phi: with the same magnitude that is the transpose, so
  * the gradients of the inputs are the inverse call on the gradients of the outputs. Frequencies are fp64
  * radians a position, so any scaling for long contexts is a choice of that table; angles are taken
- * modulo a turn in 64-bit fixed point (within 1e-9 radians of the exact product at position 10^6, where
- * an fp32 product would be off by 0.03).
+ * modulo a turn in 64-bit fixed point, whose error does not grow with the position, and rounded to fp32: within
+ * 1e-7 radians of the exact product, at position 10^6 too, where an fp32 product would be off by 0.03.
  */
 #ifndef GDN_ROTARY_H
 #define GDN_ROTARY_H

@@ -63,8 +63,9 @@ void set_segments(LinearLaunch &P, bool uniform, int64_t seg)
     P.cut_items = uniform || P.a.S <= kLinearSorted ? P.items : (int)std::min<int64_t>(P.items, 2 * (P.a.T / seg));
 }
 
-// Rows of a segment of equal sequences: as many segments as make the shortest run of rounds of CTAs, in units of a chunk's 4.4 us.
-// 1 x 32768 x 32 heads: nine segments (288 CTAs, two rounds of 29 chunks) 436 us, ten (320 CTAs, three rounds) 513.
+// Rows of a segment of equal sequences: as many segments as make the shortest run of rounds of CTAs, in units of a chunk's time.
+// 1 x 32768 x 32 heads: nine segments (288 CTAs, two rounds of 29 chunks) 436 us, ten (320 CTAs, three rounds) 513 (both measured
+// with outputs of one term; nine take 454 now).
 int64_t uniform_segment(const gdn_linear_args &a, int64_t length, bool backward)
 {
     const int64_t chunks = (length + kLinearChunk - 1) / kLinearChunk, tiles = (int64_t)a.S * a.HV;
@@ -73,7 +74,7 @@ int64_t uniform_segment(const gdn_linear_args &a, int64_t length, bool backward)
     for (int64_t n = 1; n <= 8 * kSms && (n == 1 || 2 * n <= chunks); ++n) {
         const int64_t per = (chunks + n - 1) / n;
         if (n > 1 && (n - 1) * per >= chunks) continue;          // as good as fewer
-        // a CTA starts and ends in the time of a chunk; the pass for the segments' states takes two thirds of one with
+        // a CTA starts and ends in the time of a chunk; the pass for the segments' states takes 0.55 to 0.65 of one with
         // outputs, two of them beside the three of the gradients a quarter; a state of the carry 4 K V floats of traffic at 5 TB/s
         double cost = (double)((tiles * n + kSms - 1) / kSms) * (per + 1);
         if (n > 1) cost = cost * (backward ? 1.27 : 1.65) + 0.7e-6 * (double)(tiles * n) * a.K * a.V + 0.1 * n;

@@ -15,17 +15,19 @@
 //
 // One CTA owns a segment of a sequence and a value head. Its 24 warps are groups of four, which take turns on a chunk so that
 // each one's latencies are covered by the others' work:
-//   0, 1   a quarter of Y each, then P, blocks of 32 columns in turn      2   inter's decays and the outputs (a thread a row r)
-//   3, 4   a quarter of Y each; the state                               5   a warp each: MMAs of scores, inter and out; MMAs of
-//          the update; the decays, and z's non-finite values; copies of x, y and z by TMA into a ring of 32 KB tiles (by plain
-//          loads what is not aligned to 16 bytes)
-// What a chunk takes (4.4 us with one term of the state, 8 to 9 with three and dg) is set by no one unit: the tensor pipe is
-// active 21 to 29% of the time, 29 to 41% of the issue slots are used. A chunk's stages follow one another, and the seven tiles
-// and 512 columns of tensor memory hold the operands of two chunks. The steps there, for 1 x 32768 tokens of 32 heads (both
-// passes): 16 warps in step 1073 us; tiles by TMA, decays as factors of rows and of columns, one term for bf16 outputs 747;
-// groups of warps with registers of their own (24 ragged prompts 316 -> 260) and outputs stored from registers as whole
-// sectors 666; the update's weights apart from the other decays 597; states loaded as whole rows, decays in integers 513; whole
-// rounds of CTAs 436; a token's heads side by side 423.
+//   0, 1   two quarters of Y each, P between them, blocks of 32 columns in turn
+//   2      inter's decays and the outputs (a thread a row r)
+//   3, 4   the state, half its columns each
+//   5      a warp each: MMAs of scores, inter and out; MMAs of the update; the decays, and z's non-finite values; copies of x, y
+//          and z by TMA into a ring of 32 KB tiles (by plain loads what is not aligned to 16 bytes)
+// What a chunk takes (5.5 us with two terms of the state, 10 with three and dg, 3.1 without outputs) is set by no one unit: the
+// tensor pipe is active 24 to 40% of the time, 31 to 47% of the issue slots are used (8 x 2048 and 1 x 16384 tokens of 16 heads). A
+// chunk's stages follow one another, and the seven tiles and 512 columns of tensor memory hold the operands of two chunks. The steps
+// there, for 1 x 32768 tokens of 32 heads (both passes): 16 warps in step 1073 us; tiles by TMA, decays as factors of rows and of
+// columns, one term for bf16 outputs 747; groups of warps with registers of their own (24 ragged prompts 316 -> 260) and outputs
+// stored from registers as whole sectors 666; the update's weights apart from the other decays 597; states loaded as whole rows,
+// decays in integers 513; whole rounds of CTAs 436; a token's heads side by side 423; two terms for bf16 outputs, as their cancelling
+// sums need, 454.
 // A tile may end in another sequence's rows: their y's weigh nothing, their scores are not looked at, their outputs are not
 // written.
 //
@@ -118,7 +120,7 @@ template <int NS> struct Smem {
 };
 
 // A tile by plain loads, for rows that TMA cannot copy (not 16-byte aligned): zeros behind n rows and dim columns.
-// (2048 tokens of 8 heads of 128 x 128: 180 us, 33 by TMA; with 4-byte loads, 16 on their way a lane, 131 where rows are aligned
+// (2048 tokens of 8 heads of 128 x 128: 182 us, 35 by TMA; with 4-byte loads, 16 on their way a lane, 131 where rows are aligned
 // to that, 342 where not, and ten ragged sequences' gradients, which never come here, 232 against 224 by its registers.)
 template <int BLOCKS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *src, int64_t stride, int n, int dim, int tid)
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         }
     } else if (warp >= 12) {
         take_registers();
-        // ---------------------------------------------------------------- a quarter of Y; the state
+        // ---------------------------------------------------------------- the state
         const int half = warp >= 16, y = tid & 127;    // this thread's row of the state; columns half * ZP / 2 ..
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         constexpr int ZC = ZP / 2;
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         }
     } else if (warp < 8) {
         give_registers();
-        // ---------------------------------------------------------------- a quarter of Y; P
+        // ---------------------------------------------------------------- two quarters of Y; P
         const int group = warp >> 2, quad = warp & 3, r = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         for (int i = 0; i < chunks; ++i) {

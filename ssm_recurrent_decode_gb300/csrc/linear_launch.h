@@ -61,7 +61,7 @@ constexpr int kLinearZ = 64;           // columns of z per CTA of the fp32 kerne
 
 // The sweep on the CUDA cores in fp32 (any size, stride); outputs: p.x given. Without: local and total.
 int launch_linear_recurrent(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);
-// The same for bf16 inputs on the tensor cores, and whether a call takes it.
+// The same for bf16 inputs on the tensor cores.
 int launch_linear_chunk(const LinearLaunch &P, const LinearSweep &p, bool outputs, cudaStream_t stream);
 constexpr int kLinearChunk = 128;      // its tokens per chunk
 

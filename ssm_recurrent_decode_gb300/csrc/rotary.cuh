@@ -21,7 +21,7 @@ __device__ __forceinline__ uint64_t rotary_turns(double f)
 }
 
 // cos and sin of position times frequency: the product modulo a turn is the product modulo 2^64, its top 32 bits
-// the angle in [-1/2, 1/2) turns.
+// the angle in [-1/2, 1/2) turns, which fp32 then rounds by up to 2^-25 half turns (9.4e-8 radians).
 __device__ __forceinline__ void rotary_cos_sin(int position, uint64_t turns, float &c, float &s)
 {
     const uint64_t phase = (uint64_t)(int64_t)position * turns;
