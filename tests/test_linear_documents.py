@@ -101,3 +101,66 @@ def test_time_does_not_grow_with_their_number():
         return min(times) / x["q"].shape[0]
 
     assert per_token(1024) < 4.0 * per_token(64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_in_place_and_bad_indices_among_many(dtype):
+    """A pool read and written in place by a hundred sequences, some cut, some empty; two with an index outside the pool have zero
+    outputs and gradients and touch no state, the others are right."""
+    lengths = [4, 0, 300, 1] * 25
+    S, H, HV, K, V = len(lengths), 1, 2, 32, 24
+    c = lc.make(lengths, H, HV, K, V, dtype, 31)
+    refs = lc.references(c)
+    T, bad = sum(lengths), (6, 99)
+    start, rows = lc.pool(c["initial"], S, (HV, V, K), 3)
+    end, _ = lc.pool(c["d_final"], S, (HV, V, K), 3)
+    keep = start.clone()
+    slots = rows.clone()
+    slots[bad[0]], slots[bad[1]] = -7, S + 2
+    q, k, v, do = (lc.put(c[n], dtype, "dense") for n in ("q", "k", "v", "do"))
+    g, err = lc.f32(c["g"]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    space = lambda b: gdn.linear_attention_workspace(T, H, HV, K, V, sequences=S, uniform=False, backward=b, dtype=lc.TYPES[dtype]).fill_(0xFF)
+    grads = {n: torch.full_like(t, float("nan")) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g))}
+    o, d0 = torch.full_like(v, float("nan")), torch.full_like(start, 7.0)
+    kw = {"cu_seqlens": lc.cu(lengths), "state_indices": slots, "initial_state": start}
+    gdn.gdn_linear_attention_backward(q, k, v, g, do, d_final_state=end, d_initial_state=d0, err_flags=err, workspace=space(True), **kw, **grads)
+    assert int(err) == gdn.GDN_DEVERR_BAD_INDEX
+    err.zero_()
+    gdn.gdn_linear_attention(q, k, v, g, o, final_state=start, err_flags=err, workspace=space(False), **kw)
+    torch.cuda.synchronize()
+    assert int(err) == gdn.GDN_DEVERR_BAD_INDEX
+    ends = np.cumsum(lengths)
+    lost = np.zeros(T, dtype=bool)
+    for s in bad:
+        lost[ends[s] - lengths[s]:ends[s]] = True
+    good = [s for s in range(S) if s not in bad]
+    for n, t in {"o": o, **grads}.items():
+        assert bool((t[torch.from_numpy(lost).cuda()] == 0).all()), n
+        at = torch.from_numpy(~lost).cuda()
+        lc.check(c, n, t[at], refs[0][n][~lost], refs[1][n][~lost], dtype if n != "dg" else "f32")
+    used = rows[good].long()
+    for n, p in (("final", start), ("d_initial", d0)):
+        lc.check(c, n, p[used], refs[0][n][good], refs[1][n][good])
+    rest = [i for i in range(S + 2) if i not in used.tolist()]
+    assert torch.equal(start[rest], keep[rest]) and bool((d0[rest] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_debug_build_agrees_over_many(dtype):
+    """Its kernels check the segments, rows, chunks and workspace entries that they compute; the bits are the same."""
+    lengths = [5, 0, 290, 1, 130] * 20
+    c = lc.make(lengths, 2, 4, 64, 40, dtype, 37)
+    runs = []
+    for debug in (False, True):
+        def both(c=c):
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = run_forward(c, uniform=False, err=err) | run_backward(c, uniform=False, err=err)
+            assert int(err) == 0
+            return out
+        if debug:
+            with gdn.using_debug_build():
+                runs.append(both())
+        else:
+            runs.append(both())
+    for n, t in runs[0].items():
+        assert torch.equal(t, runs[1][n]), n
